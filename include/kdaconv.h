@@ -251,6 +251,137 @@ int kdaconv_validate(
 int kdaconv_activation_map(uint32_t first, int64_t count, int activation, int dtype, void* out,
                            kdaconv_stream_t stream);
 
+/*
+ * The gated delta rule: the operator of a KDA layer that reads the convolution's planes.
+ * Per value head h, with a state S of head_dim rows (key channels) by head_dim columns
+ * (value channels), for every token t of a sequence:
+ *     a_t = exp(log decay)             per key channel, from g:
+ *           KDACONV_GATE_LOG           log decay = g
+ *           KDACONV_GATE_SOFTPLUS      log decay = -exp(a_log[h]) * softplus(g + dt_bias[h])
+ *           KDACONV_GATE_BOUNDED       log decay = lower_bound *
+ *                                          sigmoid(exp(a_log[h]) * (g + dt_bias[h]))
+ *     k_t, q_t = k and q of head h / (num_heads / num_qk_heads), each divided by
+ *           sqrt(|.|^2 + l2_eps) when l2_eps >= 0
+ *     b_t = beta, or sigmoid(beta) with beta_logits
+ *     S'  = diag(a_t) S;   u_t = b_t (v_t - S'^T k_t);   S = S' + k_t u_t^T
+ *     out_t = scale * S^T q_t          rounded to the format of q, k and v
+ * Sequences, lines, initial states and the null block are those of
+ * kdaconv_packed_causal_conv1d: sequence s owns rows [qsl[s], qsl[s+1]), starts from
+ * states[cache_indices[s]] when has_initial_state[s] is set (else zeros) and leaves its
+ * last S there; a sequence on the null block, or on a line outside the state array, runs
+ * from zeros and leaves the states alone; a sequence without tokens does nothing. The
+ * arithmetic is FP32 or better than FP16 pairs (22 bits) throughout; only out is rounded.
+ * A log decay below -104 acts as -104 (its exp is zero in FP32, as is -infinity's).
+ *
+ * All strides count elements.
+ */
+typedef enum kdaconv_gate {
+  KDACONV_GATE_LOG = 0,
+  KDACONV_GATE_SOFTPLUS = 1,
+  KDACONV_GATE_BOUNDED = 2
+} kdaconv_gate;
+
+typedef struct kdaconv_rule_args {
+  const void* q;    /* (num_tokens, num_qk_heads, head_dim), last axis contiguous */
+  const void* k;    /* as q */
+  const void* v;    /* (num_tokens, num_heads, head_dim), last axis contiguous */
+  const void* g;    /* (num_tokens, num_heads, head_dim); g_stride2 is 1, or 0 for one
+                       gate per head */
+  const void* beta; /* (num_tokens, num_heads) */
+  const float* a_log;   /* (num_heads), contiguous; NULL with KDACONV_GATE_LOG */
+  const float* dt_bias; /* (num_heads, head_dim), contiguous, or NULL for none */
+  float* states;        /* (num_cache_lines, num_heads, head_dim, head_dim) [key][value];
+                           the last two axes are contiguous */
+  const int32_t* query_start_loc;   /* (num_seqs + 1); ignored by the update */
+  const int32_t* cache_indices;     /* (num_seqs) */
+  const uint8_t* has_initial_state; /* (num_seqs) or NULL (none); the update takes every
+                                       sequence from its stored line */
+  void* out;            /* (num_tokens, num_heads, head_dim), contiguous */
+  int64_t num_tokens, num_seqs, num_heads, num_qk_heads, head_dim;
+  int64_t q_stride0, q_stride1, k_stride0, k_stride1, v_stride0, v_stride1;
+  int64_t g_stride0, g_stride1, g_stride2, beta_stride0, beta_stride1;
+  int64_t num_cache_lines, state_stride0, state_stride1;
+  int64_t cache_indices_stride;
+  int64_t null_block_id;
+  double scale, l2_eps, lower_bound;
+  int32_t dtype;      /* kdaconv_dtype of q, k, v and out */
+  int32_t gate_dtype; /* of g: dtype, or KDACONV_F32 */
+  int32_t beta_dtype; /* of beta: dtype, or KDACONV_F32 */
+  int32_t gate;       /* kdaconv_gate */
+  int32_t beta_logits;
+  int32_t has_null_block;
+} kdaconv_rule_args;
+
+/*
+ * Bytes of device scratch memory that kdaconv_gated_delta_rule needs for these sizes (0
+ * for none). The scratch holds no state between calls; calls that may run at the same
+ * time need scratch memories of their own. Aligned to 256 bytes.
+ */
+int64_t kdaconv_gated_delta_rule_workspace(int64_t num_tokens, int64_t num_seqs,
+                                           int64_t num_heads, int64_t head_dim);
+
+/*
+ * The rule over packed sequences (prefill). head_dim is 64 or 128 and num_heads a
+ * multiple of num_qk_heads (else EUNSUPPORTED and EINVAL). Sizes come from the host
+ * arguments alone, so a call can be captured in a graph. Preconditions on device data as
+ * for kdaconv_packed_causal_conv1d. num_tokens, num_seqs or num_heads of 0: KDACONV_OK
+ * with no launch.
+ */
+int kdaconv_gated_delta_rule(const kdaconv_rule_args* args, void* workspace,
+                             int64_t workspace_bytes, kdaconv_stream_t stream);
+
+/*
+ * The rule for one token per sequence (decode): row s of q, k, v, g, beta and out belongs
+ * to sequence s, num_seqs equals num_tokens (else EINVAL), and every sequence continues
+ * from its stored line (zeros for the null block). query_start_loc and has_initial_state
+ * are not read. No scratch memory.
+ */
+int kdaconv_gated_delta_rule_update(const kdaconv_rule_args* args, kdaconv_stream_t stream);
+
+/* The status either call would return before launching (update != 0: the update's). No
+ * HIP call; device pointers are only compared with NULL and tested for alignment. */
+int kdaconv_gated_delta_rule_validate(const kdaconv_rule_args* args, int update,
+                                      const void* workspace, int64_t workspace_bytes);
+
+typedef enum kdaconv_norm_gate {
+  KDACONV_NORM_GATE_NONE = 0,
+  KDACONV_NORM_GATE_SIGMOID = 1,
+  KDACONV_NORM_GATE_SILU = 2
+} kdaconv_norm_gate;
+
+/*
+ * The norm after the rule: for every token t and head h,
+ *     y = x / sqrt(mean(x^2) + eps) * weight * act(gate)
+ * over the head's `dim` channels, computed in FP32 and rounded once to dtype. act is the
+ * sigmoid, or gate * sigmoid(gate), or absent (gate NULL with KDACONV_NORM_GATE_NONE).
+ *
+ * x, gate   format dtype; (t, h, c) at t * stride0 + h * stride1 + c.
+ * weight    FP32 (dim) contiguous, or NULL for ones.
+ * out       format dtype, (num_tokens, num_heads, dim) contiguous; may be x itself when
+ *           x is laid out like it.
+ * dim       a positive multiple of 8, at most 512 (else EUNSUPPORTED).
+ */
+int kdaconv_gated_rms_norm(const void* x, int dtype, int64_t num_tokens, int64_t num_heads,
+                           int64_t dim, int64_t x_stride0, int64_t x_stride1, const void* gate,
+                           int64_t gate_stride0, int64_t gate_stride1, int activation,
+                           const float* weight, double eps, void* out, kdaconv_stream_t stream);
+
+/*
+ * The residual addition and the norm before a block: for every row t,
+ *     h = residual + residual_scale * x;   y = h / sqrt(mean(h^2) + eps) * weight
+ * with h in FP32; residual is replaced by h rounded to dtype, and out by y rounded once
+ * (y comes from the FP32 h). residual may be NULL: h = residual_scale * x, kept nowhere.
+ *
+ * x, residual  format dtype; row t at t * stride, columns contiguous.
+ * weight       FP32 (hidden) contiguous, or NULL for ones.
+ * out          format dtype, (num_tokens, hidden) contiguous.
+ * hidden       1 to 16384 (else EUNSUPPORTED).
+ */
+int kdaconv_residual_rms_norm(const void* x, int dtype, int64_t num_tokens, int64_t hidden,
+                              int64_t x_stride, void* residual, int64_t residual_stride,
+                              double residual_scale, const float* weight, double eps, void* out,
+                              kdaconv_stream_t stream);
+
 /* Static English text for a status code. Never NULL. */
 const char* kdaconv_status_string(int status);
 

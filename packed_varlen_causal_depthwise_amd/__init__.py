@@ -2,8 +2,9 @@
 
 Python face of libkdaconv (include/kdaconv.h): the two functions of the page
 "vllm.models.kimi_k3.nvidia.ops.kda_conv", ``packed_causal_conv1d_fn`` and
-``packed_causal_conv1d_supported``, with the same arguments. PyTorch supplies the
-device memory and the current stream; every step of the computation runs in the
+``packed_causal_conv1d_supported``, with the same arguments; the decode step; and what
+follows the convolution in a KDA layer: the gated delta rule over its planes (prefill and
+single tokens) and the norms around it. PyTorch supplies the device memory and the current stream; every step of the computation runs in the
 HIP kernels of libkdaconv. There is no CPU path: if the library is not built,
 importing the functions still works but calling them raises.
 """
@@ -15,20 +16,24 @@ from typing import Optional
 import torch
 
 from . import _lib
+from ._host import DTYPE_CODES as _DTYPE_CODES
+from ._host import NULL_BLOCK_ID, _on, _ptr, _stream_handle
+from .delta_rule import gated_delta_rule_fn, gated_delta_rule_supported, gated_delta_rule_update
+from .norms import gated_rms_norm, residual_rms_norm
 
 __all__ = [
     "NULL_BLOCK_ID",
     "packed_causal_conv1d_fn",
     "packed_causal_conv1d_update",
     "packed_causal_conv1d_supported",
+    "gated_delta_rule_fn",
+    "gated_delta_rule_update",
+    "gated_delta_rule_supported",
+    "gated_rms_norm",
+    "residual_rms_norm",
     "activation_map",
     "library_path",
 ]
-
-#: Default null block id. The page names the default (NULL_BLOCK_ID) without
-#: printing its value; 0, the block the paged cache reserves as its null block,
-#: is taken here. Pass the id explicitly (or None) to be independent of this.
-NULL_BLOCK_ID = 0
 
 
 def library_path() -> str:
@@ -44,8 +49,6 @@ def _activation_code(activation) -> int:
     raise ValueError(f"unknown activation {activation!r}: use 'silu', 'swish', True, None or False")
 
 
-# x formats the library takes, with their interface codes (the output takes x's dtype).
-_DTYPE_CODES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.F16, torch.float32: _lib.F32}
 _FORMAT_NAMES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
 
 
@@ -53,48 +56,6 @@ def _dtype_code(dtype: torch.dtype) -> int:
     if dtype not in _DTYPE_CODES:
         raise ValueError(f"x must be bfloat16, float16 or float32 (got {dtype})")
     return _DTYPE_CODES[dtype]
-
-
-# The current stream's raw handle: torch's direct query where it has one (0.1 us against
-# about 2 us for building a Stream object per call), else the public route.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-# The current device, likewise by the direct query where torch has one (a plain call,
-# without the initialisation checks of torch.cuda.current_device()).
-_get_device = getattr(torch._C, "_cuda_getDevice", None)
-
-
-def _current_device() -> int:
-    return _get_device() if _get_device is not None else torch.cuda.current_device()
-
-
-def _stream_handle(device: torch.device) -> int:
-    if _raw_stream is not None:
-        idx = device.index if device.index is not None else _current_device()
-        return _raw_stream(idx)
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-class _NoGuard:
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        return False
-
-
-_NO_GUARD = _NoGuard()
-
-
-def _on(device: torch.device):
-    """The device context for a call on `device`: none when it is already current (the
-    context manager costs more than the launch's own host work)."""
-    if device.index is None or device.index == _current_device():
-        return _NO_GUARD
-    return torch.cuda.device(device)
-
-
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
 
 
 # Shapes and strides are read as whole tuples, once per tensor: torch's t.stride(i) and

@@ -5,15 +5,24 @@
 
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import pathlib
 import shutil
 import subprocess
+import tempfile
 
 PKG = pathlib.Path(__file__).resolve().parent
 ROOT = PKG.parent
-SOURCES = [PKG / "csrc" / "kdaconv.hip"]
-HEADERS = [ROOT / "include" / "kdaconv.h", PKG / "csrc" / "kdaconv_device.h"]
+SOURCES = [PKG / "csrc" / name for name in (
+    "kdaconv.hip",
+    "delta_rule.hip",
+    "delta_rule_bf16.hip",
+    "delta_rule_f16.hip",
+    "delta_rule_f32.hip",
+    "norms.hip",
+)]
+HEADERS = [ROOT / "include" / "kdaconv.h", *sorted((PKG / "csrc").glob("*.h"))]
 LIBRARY = PKG / "libkdaconv.so"
 ARCH = "gfx950"
 
@@ -22,7 +31,6 @@ FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     # Packed FP32 instructions stay off: the compiler must not form them.
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     # Exact IEEE binary32 semantics: no contraction, no flushing of subnormals.
@@ -38,10 +46,19 @@ def hipcc() -> str:
 
 
 def build(output: pathlib.Path = LIBRARY, extra_flags=()) -> pathlib.Path:
+    """Compiles each source to an object, several at a time, and links them."""
     tmp = output.with_name(output.name + f".tmp{os.getpid()}")
-    cmd = [hipcc(), *FLAGS, *extra_flags, "-I", str(ROOT / "include"), "-o", str(tmp),
-           *map(str, SOURCES)]
-    subprocess.run(cmd, check=True)
+    with tempfile.TemporaryDirectory() as work:
+        objects = [pathlib.Path(work) / (src.stem + ".o") for src in SOURCES]
+
+        def compile_one(src, obj):
+            subprocess.run([hipcc(), *FLAGS, *extra_flags, "-I", str(ROOT / "include"), "-c",
+                            "-o", str(obj), str(src)], check=True)
+
+        with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as pool:
+            list(pool.map(compile_one, SOURCES, objects))
+        subprocess.run([hipcc(), f"--offload-arch={ARCH}", "-fPIC", "-shared", "-o", str(tmp),
+                        *map(str, objects)], check=True)
     os.replace(tmp, output)
     return output
 

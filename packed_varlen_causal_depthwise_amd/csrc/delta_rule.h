@@ -1,0 +1,47 @@
+// The gated delta rule: parameters shared by the host code and the kernels.
+#ifndef KDACONV_DELTA_RULE_H_
+#define KDACONV_DELTA_RULE_H_
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kdaconv.h"
+
+namespace kdaconv {
+
+constexpr int kRuleWave = 64;
+
+// One call of the rule. Strides are in elements and bounded by the host checks (a token
+// stride below 2^24), so offsets inside a chunk fit 32 bits.
+struct RuleParams {
+  const char* q;
+  const char* k;
+  const char* v;
+  const char* g;
+  const char* beta;
+  const float* a_log;
+  const float* dt_bias;
+  float* states;
+  const int32_t* qsl;  // null: sequence s owns row s
+  const int32_t* cache_indices;
+  const uint8_t* has_init;
+  char* out;
+  int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, g_ts, g_hs, b_ts, b_hs;
+  int64_t st_line, st_head;
+  int64_t num_cache_lines;
+  int64_t ci_stride;
+  int64_t null_block_id;
+  float scale, l2_eps, lower_bound;
+  int32_t num_tokens, num_seqs, heads, share;  // share: value heads per query and key head
+  int32_t g_cs;  // 1, or 0: one gate per head
+  int32_t gate, beta_logits, beta_f32, has_null_block;
+  int32_t all_init;  // every sequence starts from its line (the update)
+};
+
+// Launchers, one set per format (kF: x, kG: gate), defined where they are instantiated.
+template <int kF, int kG>
+void launch_rule_step(const RuleParams& P, int head_dim, hipStream_t st);
+
+}  // namespace kdaconv
+
+#endif  // KDACONV_DELTA_RULE_H_

@@ -1,0 +1,175 @@
+// The gated delta rule: checks of arguments and the C entry points. include/kdaconv.h
+// states the operator.
+#include "delta_rule.h"
+
+#include <algorithm>
+
+namespace kdaconv {
+namespace {
+
+constexpr int64_t kMaxStride = (int64_t)1 << 24;
+
+bool known_rule_dtype(int d) { return d == KDACONV_BF16 || d == KDACONV_F16 || d == KDACONV_F32; }
+
+bool aligned_to(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+int64_t dtype_size(int d) { return d == KDACONV_F32 ? 4 : 2; }
+
+int validate_rule(const kdaconv_rule_args* a, bool update) {
+  if (a == nullptr) return KDACONV_EINVAL;
+  if (a->num_tokens < 0 || a->num_seqs < 0 || a->num_heads < 0 || a->num_cache_lines < 0)
+    return KDACONV_EINVAL;
+  if (!known_rule_dtype(a->dtype) || !known_rule_dtype(a->gate_dtype) ||
+      !known_rule_dtype(a->beta_dtype))
+    return KDACONV_EINVAL;
+  if (a->gate != KDACONV_GATE_LOG && a->gate != KDACONV_GATE_SOFTPLUS &&
+      a->gate != KDACONV_GATE_BOUNDED)
+    return KDACONV_EINVAL;
+  if (a->head_dim <= 0 || a->num_qk_heads <= 0 || a->num_heads % a->num_qk_heads != 0)
+    return KDACONV_EINVAL;
+  if (a->g_stride2 != 0 && a->g_stride2 != 1) return KDACONV_EINVAL;
+  if (update && a->num_tokens != a->num_seqs) return KDACONV_EINVAL;
+  if (a->lower_bound > 0.0 || a->lower_bound != a->lower_bound) return KDACONV_EINVAL;
+  if (a->head_dim != 64 && a->head_dim != 128) return KDACONV_EUNSUPPORTED;
+  if (a->gate_dtype != a->dtype && a->gate_dtype != KDACONV_F32) return KDACONV_EUNSUPPORTED;
+  if (a->beta_dtype != a->dtype && a->beta_dtype != KDACONV_F32) return KDACONV_EUNSUPPORTED;
+  for (int64_t s : {a->q_stride0, a->q_stride1, a->k_stride0, a->k_stride1, a->v_stride0,
+                    a->v_stride1, a->g_stride0, a->g_stride1, a->beta_stride0, a->beta_stride1})
+    if (s < 0 || s >= kMaxStride) return KDACONV_EUNSUPPORTED;
+  if (a->state_stride0 < 0 || a->state_stride1 < 0 || a->cache_indices_stride < 0)
+    return KDACONV_EUNSUPPORTED;
+  // int32 tokens, sequences and workgroups.
+  if (a->num_tokens > INT32_MAX / 2 || a->num_seqs > INT32_MAX / 2 || a->num_heads > 65535)
+    return KDACONV_EUNSUPPORTED;
+  if ((a->num_tokens + a->num_seqs) * std::max<int64_t>(1, a->num_heads) > INT32_MAX / 4)
+    return KDACONV_EUNSUPPORTED;
+  if (a->num_tokens == 0 || a->num_seqs == 0 || a->num_heads == 0) return KDACONV_OK;
+  if (!a->q || !a->k || !a->v || !a->g || !a->beta || !a->states || !a->cache_indices || !a->out)
+    return KDACONV_EINVAL;
+  if (!update && !a->query_start_loc) return KDACONV_EINVAL;
+  if (a->gate != KDACONV_GATE_LOG && !a->a_log) return KDACONV_EINVAL;
+  const int64_t eb = dtype_size(a->dtype);
+  if (!aligned_to(a->q, eb) || !aligned_to(a->k, eb) || !aligned_to(a->v, eb) ||
+      !aligned_to(a->out, eb) || !aligned_to(a->g, dtype_size(a->gate_dtype)) ||
+      !aligned_to(a->beta, dtype_size(a->beta_dtype)) || !aligned_to(a->states, 4) ||
+      !aligned_to(a->a_log, 4) || !aligned_to(a->dt_bias, 4))
+    return KDACONV_EUNSUPPORTED;
+  return KDACONV_OK;
+}
+
+RuleParams rule_params(const kdaconv_rule_args* a, bool update) {
+  RuleParams P;
+  P.q = static_cast<const char*>(a->q);
+  P.k = static_cast<const char*>(a->k);
+  P.v = static_cast<const char*>(a->v);
+  P.g = static_cast<const char*>(a->g);
+  P.beta = static_cast<const char*>(a->beta);
+  P.a_log = a->a_log;
+  P.dt_bias = a->gate == KDACONV_GATE_LOG ? nullptr : a->dt_bias;
+  P.states = a->states;
+  P.qsl = update ? nullptr : a->query_start_loc;
+  P.cache_indices = a->cache_indices;
+  P.has_init = update ? nullptr : a->has_initial_state;
+  P.out = static_cast<char*>(a->out);
+  P.q_ts = a->q_stride0;
+  P.q_hs = a->q_stride1;
+  P.k_ts = a->k_stride0;
+  P.k_hs = a->k_stride1;
+  P.v_ts = a->v_stride0;
+  P.v_hs = a->v_stride1;
+  P.g_ts = a->g_stride0;
+  P.g_hs = a->g_stride1;
+  P.g_cs = (int32_t)a->g_stride2;
+  P.b_ts = a->beta_stride0;
+  P.b_hs = a->beta_stride1;
+  P.st_line = a->state_stride0;
+  P.st_head = a->state_stride1;
+  P.num_cache_lines = a->num_cache_lines;
+  P.ci_stride = a->cache_indices_stride;
+  P.null_block_id = a->null_block_id;
+  P.scale = (float)a->scale;
+  P.l2_eps = (float)a->l2_eps;
+  P.lower_bound = (float)a->lower_bound;
+  P.num_tokens = (int32_t)a->num_tokens;
+  P.num_seqs = (int32_t)a->num_seqs;
+  P.heads = (int32_t)a->num_heads;
+  P.share = (int32_t)(a->num_heads / a->num_qk_heads);
+  P.gate = a->gate;
+  P.beta_logits = a->beta_logits != 0;
+  P.beta_f32 = a->beta_dtype == KDACONV_F32;
+  P.has_null_block = a->has_null_block != 0;
+  P.all_init = update;
+  return P;
+}
+
+// Calls op.template run<x format, gate format>() for the call's formats.
+template <class Op>
+void for_formats(const kdaconv_rule_args* a, Op op) {
+  if (a->dtype == KDACONV_F32)
+    op.template run<KDACONV_F32, KDACONV_F32>();
+  else if (a->dtype == KDACONV_F16 && a->gate_dtype == KDACONV_F32)
+    op.template run<KDACONV_F16, KDACONV_F32>();
+  else if (a->dtype == KDACONV_F16)
+    op.template run<KDACONV_F16, KDACONV_F16>();
+  else if (a->gate_dtype == KDACONV_F32)
+    op.template run<KDACONV_BF16, KDACONV_F32>();
+  else
+    op.template run<KDACONV_BF16, KDACONV_BF16>();
+}
+
+struct Step {
+  const RuleParams& P;
+  int head_dim;
+  hipStream_t st;
+  template <int kF, int kG>
+  void run() {
+    launch_rule_step<kF, kG>(P, head_dim, st);
+  }
+};
+
+bool nothing(const kdaconv_rule_args* a) {
+  return a->num_tokens == 0 || a->num_seqs == 0 || a->num_heads == 0;
+}
+
+}  // namespace
+}  // namespace kdaconv
+
+using namespace kdaconv;
+
+extern "C" int64_t kdaconv_gated_delta_rule_workspace(int64_t num_tokens, int64_t num_seqs,
+                                                      int64_t num_heads, int64_t head_dim) {
+  (void)num_tokens;
+  (void)num_seqs;
+  (void)num_heads;
+  (void)head_dim;
+  return 0;
+}
+
+extern "C" int kdaconv_gated_delta_rule_validate(const kdaconv_rule_args* args, int update,
+                                                 const void* workspace, int64_t workspace_bytes) {
+  const int rc = validate_rule(args, update != 0);
+  if (rc != KDACONV_OK || update != 0 || nothing(args)) return rc;
+  const int64_t need = kdaconv_gated_delta_rule_workspace(args->num_tokens, args->num_seqs,
+                                                          args->num_heads, args->head_dim);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KDACONV_EINVAL;
+  if (need > 0 && !aligned_to(workspace, 256)) return KDACONV_EUNSUPPORTED;
+  return KDACONV_OK;
+}
+
+extern "C" int kdaconv_gated_delta_rule(const kdaconv_rule_args* args, void* workspace,
+                                        int64_t workspace_bytes, kdaconv_stream_t stream) {
+  const int rc = kdaconv_gated_delta_rule_validate(args, 0, workspace, workspace_bytes);
+  if (rc != KDACONV_OK || nothing(args)) return rc;
+  const RuleParams P = rule_params(args, false);
+  for_formats(args, Step{P, (int)args->head_dim, reinterpret_cast<hipStream_t>(stream)});
+  return hipGetLastError() == hipSuccess ? KDACONV_OK : KDACONV_ELAUNCH;
+}
+
+extern "C" int kdaconv_gated_delta_rule_update(const kdaconv_rule_args* args,
+                                               kdaconv_stream_t stream) {
+  const int rc = validate_rule(args, true);
+  if (rc != KDACONV_OK || nothing(args)) return rc;
+  const RuleParams P = rule_params(args, true);
+  for_formats(args, Step{P, (int)args->head_dim, reinterpret_cast<hipStream_t>(stream)});
+  return hipGetLastError() == hipSuccess ? KDACONV_OK : KDACONV_ELAUNCH;
+}

@@ -1,0 +1,357 @@
+// The norms around the gated delta rule (include/kdaconv.h states both).
+//
+// Both are streams: every input is read once and every output written once, 16 bytes (8
+// elements of the 16-bit formats) per lane and access, with a row held in registers
+// between the sum of squares and the scaling. What bounds them is HBM.
+#include "delta_rule_device.h"
+
+#include <algorithm>
+
+namespace kdaconv {
+namespace {
+
+typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
+typedef u32x4v u32x4a2 __attribute__((aligned(2)));
+
+// 8 neighbouring elements as FP32.
+struct Eight {
+  float v[8];
+};
+
+template <int kF>
+__device__ __forceinline__ Eight load8(const char* p) {
+  Eight e;
+  if constexpr (kF == kRuleF32) {
+    const f32x4 a = *(const f32x4a4*)p, b = *(const f32x4a4*)(p + 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      e.v[i] = a[i];
+      e.v[4 + i] = b[i];
+    }
+  } else {
+    const u32x4v r = *(const u32x4a2*)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x2 a = Pair<kF>::value(r[i]);
+      e.v[2 * i] = a.x;
+      e.v[2 * i + 1] = a.y;
+    }
+  }
+  return e;
+}
+
+template <int kF>
+__device__ __forceinline__ void store8(char* p, const Eight& e) {
+  if constexpr (kF == kRuleF32) {
+    *(f32x4a4*)p = f32x4{e.v[0], e.v[1], e.v[2], e.v[3]};
+    *(f32x4a4*)(p + 16) = f32x4{e.v[4], e.v[5], e.v[6], e.v[7]};
+  } else {
+    u32x4v r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x2 a = {e.v[2 * i], e.v[2 * i + 1]};
+      if constexpr (kF == kRuleBF16)
+        r[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(a, bf16x2));
+      else
+        r[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(a, f16x2));
+    }
+    *(u32x4a2*)p = r;
+  }
+}
+
+// The last elements of a row whose length is no multiple of 8.
+template <int kF>
+__device__ __forceinline__ Eight load_tail(const char* p, int n) {
+  Eight e;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e.v[i] = i < n ? load_elem<kF>(p + i * elem_bytes<kF>()) : 0.0f;
+  return e;
+}
+
+template <int kF>
+__device__ __forceinline__ void store_tail(char* p, const Eight& e, int n) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < n) store_elem<kF>(p + i * elem_bytes<kF>(), e.v[i]);
+}
+
+__device__ __forceinline__ float rsqrt_f(float x) { return 1.0f / __builtin_sqrtf(x); }
+
+struct GatedNormParams {
+  const char* x;
+  const char* gate;
+  const float* weight;
+  char* out;
+  int64_t x_s0, x_s1, g_s0, g_s1;
+  int64_t rows;
+  uint32_t heads, heads_magic;  // n / heads = (umulhi(n, magic) + n) >> shift
+  int32_t heads_shift;
+  int32_t dim;
+  int32_t lanes_log;  // log2 of the lanes per row (a power of two >= dim / 8)
+  int32_t activation;
+  float inv_dim, eps;
+};
+
+// kU rows per lane group: their loads are all issued before the first sum.
+template <int kF, int kU>
+__global__ __launch_bounds__(256) void gated_rms_norm_kernel(const GatedNormParams P) {
+  constexpr int kEB = elem_bytes<kF>();
+  const int lanes = 1 << P.lanes_log;
+  const int c = 8 * (threadIdx.x & (lanes - 1));
+  const int64_t groups = 256 >> P.lanes_log;
+  const int64_t first = (int64_t)blockIdx.x * groups * kU + (threadIdx.x >> P.lanes_log);
+  const bool in = c < P.dim;
+  Eight x[kU], z[kU];
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    const int64_t row = first + u * groups;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[u].v[i] = z[u].v[i] = 0.0f;
+    if (in && row < P.rows) {
+      const uint32_t n = (uint32_t)row;
+      const uint32_t t = (__umulhi(n, P.heads_magic) + n) >> P.heads_shift, h = n - t * P.heads;
+      x[u] = load8<kF>(P.x + ((int64_t)t * P.x_s0 + (int64_t)h * P.x_s1 + c) * kEB);
+      if (P.activation != KDACONV_NORM_GATE_NONE)
+        z[u] = load8<kF>(P.gate + ((int64_t)t * P.g_s0 + (int64_t)h * P.g_s1 + c) * kEB);
+    }
+  }
+  Eight w;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w.v[i] = 1.0f;
+  if (in && P.weight != nullptr) w = load8<kRuleF32>((const char*)(P.weight + c));
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    const int64_t row = first + u * groups;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = __builtin_fmaf(x[u].v[i], x[u].v[i], s);
+    for (int m = lanes >> 1; m > 0; m >>= 1) s += __shfl_xor(s, m);
+    const float r = rsqrt_f(__builtin_fmaf(s, P.inv_dim, P.eps));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float y = x[u].v[i] * r * w.v[i];
+      if (P.activation != KDACONV_NORM_GATE_NONE) {
+        y *= sigmoid_f(z[u].v[i]);
+        if (P.activation == KDACONV_NORM_GATE_SILU) y *= z[u].v[i];
+      }
+      x[u].v[i] = y;
+    }
+    if (in && row < P.rows) store8<kF>(P.out + (row * P.dim + c) * kEB, x[u]);
+  }
+}
+
+struct ResidualNormParams {
+  const char* x;
+  char* residual;
+  const float* weight;
+  char* out;
+  int64_t x_stride, r_stride;
+  int32_t hidden;
+  float scale, inv_hidden, eps;
+};
+
+// One row per workgroup of kThreads, kV vectors of 8 per lane.
+template <int kF, int kThreads, int kV>
+__global__ __launch_bounds__(kThreads) void residual_rms_norm_kernel(const ResidualNormParams P) {
+  constexpr int kEB = elem_bytes<kF>();
+  const int64_t row = blockIdx.x;
+  const char* const x = P.x + row * P.x_stride * kEB;
+  char* const residual = P.residual == nullptr ? nullptr : P.residual + row * P.r_stride * kEB;
+  Eight a[kV], b[kV];
+#pragma unroll
+  for (int i = 0; i < kV; ++i) {
+    const int c = 8 * (threadIdx.x + i * kThreads), n = P.hidden - c;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[i].v[e] = b[i].v[e] = 0.0f;
+    if (n >= 8) {
+      a[i] = load8<kF>(x + c * kEB);
+      if (residual != nullptr) b[i] = load8<kF>(residual + c * kEB);
+    } else if (n > 0) {
+      a[i] = load_tail<kF>(x + c * kEB, n);
+      if (residual != nullptr) b[i] = load_tail<kF>(residual + c * kEB, n);
+    }
+  }
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kV; ++i) {
+    const int c = 8 * (threadIdx.x + i * kThreads), n = P.hidden - c;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      a[i].v[e] = __builtin_fmaf(P.scale, a[i].v[e], b[i].v[e]);
+      s = __builtin_fmaf(a[i].v[e], a[i].v[e], s);
+    }
+    if (residual != nullptr) {
+      if (n >= 8)
+        store8<kF>(residual + c * kEB, a[i]);
+      else if (n > 0)
+        store_tail<kF>(residual + c * kEB, a[i], n);
+    }
+  }
+  s = lane_sum<kRuleWave>(s);
+  if constexpr (kThreads > kRuleWave) {
+    __shared__ float part[kThreads / kRuleWave];
+    if (threadIdx.x % kRuleWave == 0) part[threadIdx.x / kRuleWave] = s;
+    __syncthreads();
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kThreads / kRuleWave; ++w) s += part[w];
+  }
+  const float r = rsqrt_f(__builtin_fmaf(s, P.inv_hidden, P.eps));
+  char* const out = P.out + row * P.hidden * kEB;
+#pragma unroll
+  for (int i = 0; i < kV; ++i) {
+    const int c = 8 * (threadIdx.x + i * kThreads), n = P.hidden - c;
+    if (n <= 0) continue;
+    if (P.weight != nullptr) {
+      const Eight w = n >= 8 ? load8<kRuleF32>((const char*)(P.weight + c))
+                             : load_tail<kRuleF32>((const char*)(P.weight + c), n);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a[i].v[e] *= r * w.v[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a[i].v[e] *= r;
+    }
+    if (n >= 8)
+      store8<kF>(out + c * kEB, a[i]);
+    else
+      store_tail<kF>(out + c * kEB, a[i], n);
+  }
+}
+
+bool element_aligned(const void* p, int dtype) {
+  return reinterpret_cast<uintptr_t>(p) % (dtype == KDACONV_F32 ? 4 : 2) == 0;
+}
+
+bool known(int dtype) { return dtype == KDACONV_BF16 || dtype == KDACONV_F16 || dtype == KDACONV_F32; }
+
+// Multiplier and shift of n / d for n < 2^31 (d >= 1): magic = ceil(2^(32 + L) / d) - 2^32
+// with 2^L >= d.
+void divider(uint32_t d, uint32_t* magic, int32_t* shift) {
+  int l = 0;
+  while (((uint64_t)1 << l) < d) ++l;
+  const unsigned __int128 num = (unsigned __int128)1 << (32 + l);
+  *magic = (uint32_t)((num + d - 1) / d - ((unsigned __int128)1 << 32));
+  *shift = l;
+}
+
+template <int kF>
+void launch_gated(const GatedNormParams& P, hipStream_t st) {
+  const int64_t groups = 256 >> P.lanes_log;
+  // Four rows per lane group where that still leaves every CU several workgroups; else one,
+  // for latency.
+  if (P.rows >= groups * 4 * 1024)
+    hipLaunchKernelGGL((gated_rms_norm_kernel<kF, 4>), dim3((unsigned)((P.rows + 4 * groups - 1) / (4 * groups))), dim3(256), 0, st, P);
+  else
+    hipLaunchKernelGGL((gated_rms_norm_kernel<kF, 1>), dim3((unsigned)((P.rows + groups - 1) / groups)), dim3(256), 0, st, P);
+}
+
+template <int kF>
+void launch_residual(const ResidualNormParams& P, int64_t rows, hipStream_t st) {
+  const dim3 grid((unsigned)rows);
+#define KDACONV_RESIDUAL(T, V) \
+  hipLaunchKernelGGL((residual_rms_norm_kernel<kF, T, V>), grid, dim3(T), 0, st, P)
+  if (P.hidden <= 512)
+    KDACONV_RESIDUAL(64, 1);
+  else if (P.hidden <= 1024)
+    KDACONV_RESIDUAL(64, 2);
+  else if (P.hidden <= 2048)
+    KDACONV_RESIDUAL(256, 1);
+  else if (P.hidden <= 4096)
+    KDACONV_RESIDUAL(256, 2);
+  else if (P.hidden <= 8192)
+    KDACONV_RESIDUAL(256, 4);
+  else
+    KDACONV_RESIDUAL(256, 8);
+#undef KDACONV_RESIDUAL
+}
+
+}  // namespace
+}  // namespace kdaconv
+
+using namespace kdaconv;
+
+extern "C" int kdaconv_gated_rms_norm(const void* x, int dtype, int64_t num_tokens,
+                                      int64_t num_heads, int64_t dim, int64_t x_stride0,
+                                      int64_t x_stride1, const void* gate, int64_t gate_stride0,
+                                      int64_t gate_stride1, int activation, const float* weight,
+                                      double eps, void* out, kdaconv_stream_t stream) {
+  if (num_tokens < 0 || num_heads < 0 || dim <= 0 || !known(dtype)) return KDACONV_EINVAL;
+  if (activation != KDACONV_NORM_GATE_NONE && activation != KDACONV_NORM_GATE_SIGMOID &&
+      activation != KDACONV_NORM_GATE_SILU)
+    return KDACONV_EINVAL;
+  if (!(eps >= 0.0)) return KDACONV_EINVAL;
+  if (dim % 8 != 0 || dim > 512) return KDACONV_EUNSUPPORTED;
+  if (x_stride0 < 0 || x_stride1 < 0 || gate_stride0 < 0 || gate_stride1 < 0)
+    return KDACONV_EUNSUPPORTED;
+  if (num_tokens > INT32_MAX || num_heads > INT32_MAX || num_tokens * num_heads > INT32_MAX)
+    return KDACONV_EUNSUPPORTED;
+  if (num_tokens == 0 || num_heads == 0) return KDACONV_OK;
+  const bool gated = activation != KDACONV_NORM_GATE_NONE;
+  if (!x || !out || (gated && !gate)) return KDACONV_EINVAL;
+  if (!element_aligned(x, dtype) || !element_aligned(out, dtype) ||
+      (gated && !element_aligned(gate, dtype)) || !element_aligned(weight, KDACONV_F32))
+    return KDACONV_EUNSUPPORTED;
+  GatedNormParams P;
+  P.x = static_cast<const char*>(x);
+  P.gate = static_cast<const char*>(gate);
+  P.weight = weight;
+  P.out = static_cast<char*>(out);
+  P.x_s0 = x_stride0;
+  P.x_s1 = x_stride1;
+  P.g_s0 = gate_stride0;
+  P.g_s1 = gate_stride1;
+  P.rows = num_tokens * num_heads;
+  P.heads = (uint32_t)num_heads;
+  divider(P.heads, &P.heads_magic, &P.heads_shift);
+  P.dim = (int32_t)dim;
+  P.lanes_log = 0;
+  while ((8 << P.lanes_log) < dim) ++P.lanes_log;
+  P.activation = activation;
+  P.inv_dim = (float)(1.0 / (double)dim);
+  P.eps = (float)eps;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (dtype == KDACONV_F32)
+    launch_gated<kRuleF32>(P, st);
+  else if (dtype == KDACONV_F16)
+    launch_gated<kRuleF16>(P, st);
+  else
+    launch_gated<kRuleBF16>(P, st);
+  return hipGetLastError() == hipSuccess ? KDACONV_OK : KDACONV_ELAUNCH;
+}
+
+extern "C" int kdaconv_residual_rms_norm(const void* x, int dtype, int64_t num_tokens,
+                                         int64_t hidden, int64_t x_stride, void* residual,
+                                         int64_t residual_stride, double residual_scale,
+                                         const float* weight, double eps, void* out,
+                                         kdaconv_stream_t stream) {
+  if (num_tokens < 0 || hidden <= 0 || !known(dtype)) return KDACONV_EINVAL;
+  if (!(eps >= 0.0)) return KDACONV_EINVAL;
+  if (hidden > 16384 || num_tokens > INT32_MAX) return KDACONV_EUNSUPPORTED;
+  if (x_stride < 0 || residual_stride < 0) return KDACONV_EUNSUPPORTED;
+  // Rows of the residual may not overlap: each is written.
+  if (residual != nullptr && num_tokens > 1 && residual_stride < hidden) return KDACONV_EINVAL;
+  if (num_tokens == 0) return KDACONV_OK;
+  if (!x || !out) return KDACONV_EINVAL;
+  if (!element_aligned(x, dtype) || !element_aligned(out, dtype) ||
+      !element_aligned(residual, dtype) || !element_aligned(weight, KDACONV_F32))
+    return KDACONV_EUNSUPPORTED;
+  ResidualNormParams P;
+  P.x = static_cast<const char*>(x);
+  P.residual = static_cast<char*>(residual);
+  P.weight = weight;
+  P.out = static_cast<char*>(out);
+  P.x_stride = x_stride;
+  P.r_stride = residual_stride;
+  P.hidden = (int32_t)hidden;
+  P.scale = (float)residual_scale;
+  P.inv_hidden = (float)(1.0 / (double)hidden);
+  P.eps = (float)eps;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (dtype == KDACONV_F32)
+    launch_residual<kRuleF32>(P, num_tokens, st);
+  else if (dtype == KDACONV_F16)
+    launch_residual<kRuleF16>(P, num_tokens, st);
+  else
+    launch_residual<kRuleBF16>(P, num_tokens, st);
+  return hipGetLastError() == hipSuccess ? KDACONV_OK : KDACONV_ELAUNCH;
+}
