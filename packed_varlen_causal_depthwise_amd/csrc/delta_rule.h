@@ -36,11 +36,37 @@ struct RuleParams {
   int32_t g_cs;  // 1, or 0: one gate per head
   int32_t gate, beta_logits, beta_f32, has_null_block;
   int32_t all_init;  // every sequence starts from its line (the update)
+  int32_t max_len;  // the step kernel leaves longer sequences alone
 };
+
+constexpr int kChunk = 32;  // tokens per chunk
+
+// What the chunked kernels need beside the call: where chunks and segments lie, and the
+// scratch memory.
+struct ChunkParams {
+  RuleParams R;
+  char* slots;  // kSlotBytes per (chunk program, head)
+  float* ends;  // head_dim^2 per (segment program, head): a segment's end, then a start
+  char* moves;  // kMoveBytes per (segment program, head): the segment's transition
+  int32_t chunk_programs, segment_programs;
+  int32_t segment_shift;  // log2 of the tokens per segment
+  int32_t search_top;  // 64^(levels - 1), 64^levels >= num_seqs
+  int32_t min_len;  // shorter sequences are left to the step kernel
+};
+
+// One chunk of one head as the scan reads it: T as three and A as two FP16 matrices in the
+// order of matrix operands, then six rows of kChunk floats (see prepare).
+constexpr int kSlotT = 0, kSlotA = 6144, kSlotRows = 10240, kSlotBytes = 11264;
+
+// The transition: pairs of FP16 matrices and a scale.
+inline __host__ __device__ int64_t move_bytes(int head_dim) { return (int64_t)head_dim * head_dim * 4 + 256; }
 
 // Launchers, one set per format (kF: x, kG: gate), defined where they are instantiated.
 template <int kF, int kG>
 void launch_rule_step(const RuleParams& P, int head_dim, hipStream_t st);
+
+template <int kF, int kG>
+void launch_rule_chunks(const ChunkParams& P, int head_dim, hipStream_t st);
 
 }  // namespace kdaconv
 

@@ -15,6 +15,59 @@ bool aligned_to(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_
 
 int64_t dtype_size(int d) { return d == KDACONV_F32 ? 4 : 2; }
 
+// How a prefill call is worked on. It depends on host sizes alone.
+struct Plan {
+  bool step;  // the step kernel takes sequences of up to max_len tokens
+  bool chunks;  // the chunked kernels take the others
+  bool segments;  // sequences of several segments are possible
+  int64_t max_len;
+  int segment_shift;  // log2 of the tokens per segment
+  int64_t chunk_programs, segment_programs;
+  int64_t slot_bytes, ends_bytes, moves_bytes;
+};
+
+// Sequences of up to this many tokens are faster token by token.
+constexpr int64_t kStepTokens = 8;
+// The step kernel is launched beside the chunked ones where sequences average under this.
+constexpr int64_t kStepAverage = 64;
+// Segments: as long as leaves about this many workgroups for a call of long sequences, from
+// 8 to 64 chunks.
+constexpr int64_t kSegmentCells = 512;
+constexpr int kSegmentShiftMin = 8, kSegmentShiftMax = 11;
+
+int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
+
+Plan make_plan(int64_t tokens, int64_t seqs, int64_t heads, int64_t head_dim) {
+  Plan p = {};
+  p.step = tokens <= kStepTokens || tokens < kStepAverage * seqs;
+  p.chunks = tokens > kStepTokens;
+  p.max_len = p.step ? kStepTokens : 0;
+  p.segment_shift = kSegmentShiftMin;
+  while (p.segment_shift < kSegmentShiftMax && (tokens >> p.segment_shift) * heads > kSegmentCells)
+    ++p.segment_shift;
+  p.segments = tokens > ((int64_t)1 << p.segment_shift);
+  p.chunk_programs = tokens / kChunk + seqs;
+  p.segment_programs = (tokens >> p.segment_shift) + seqs;
+  if (p.chunks) {
+    p.slot_bytes = round256(p.chunk_programs * heads * kSlotBytes);
+    if (p.segments) {
+      p.ends_bytes = round256(p.segment_programs * heads * head_dim * head_dim * 4);
+      p.moves_bytes = p.segment_programs * heads * move_bytes((int)head_dim);
+    }
+  }
+  return p;
+}
+
+// Workgroups of the largest launch; a launch may not reach 2^32 threads.
+constexpr int64_t kMaxGrid = (int64_t)1 << 24;
+
+int64_t largest_grid(const kdaconv_rule_args* a, bool update) {
+  const int64_t heads = std::max<int64_t>(1, a->num_heads);
+  if (update) return a->num_seqs * heads;
+  const Plan p = make_plan(a->num_tokens, a->num_seqs, heads, a->head_dim);
+  return std::max(p.chunk_programs, p.segment_programs * (a->head_dim / 16)) * heads;
+}
+
 int validate_rule(const kdaconv_rule_args* a, bool update) {
   if (a == nullptr) return KDACONV_EINVAL;
   if (a->num_tokens < 0 || a->num_seqs < 0 || a->num_heads < 0 || a->num_cache_lines < 0)
@@ -43,6 +96,7 @@ int validate_rule(const kdaconv_rule_args* a, bool update) {
     return KDACONV_EUNSUPPORTED;
   if ((a->num_tokens + a->num_seqs) * std::max<int64_t>(1, a->num_heads) > INT32_MAX / 4)
     return KDACONV_EUNSUPPORTED;
+  if (largest_grid(a, update) >= kMaxGrid) return KDACONV_EUNSUPPORTED;
   if (a->num_tokens == 0 || a->num_seqs == 0 || a->num_heads == 0) return KDACONV_OK;
   if (!a->q || !a->k || !a->v || !a->g || !a->beta || !a->states || !a->cache_indices || !a->out)
     return KDACONV_EINVAL;
@@ -99,6 +153,7 @@ RuleParams rule_params(const kdaconv_rule_args* a, bool update) {
   P.beta_f32 = a->beta_dtype == KDACONV_F32;
   P.has_null_block = a->has_null_block != 0;
   P.all_init = update;
+  P.max_len = INT32_MAX;
   return P;
 }
 
@@ -127,6 +182,16 @@ struct Step {
   }
 };
 
+struct Chunks {
+  const ChunkParams& P;
+  int head_dim;
+  hipStream_t st;
+  template <int kF, int kG>
+  void run() {
+    launch_rule_chunks<kF, kG>(P, head_dim, st);
+  }
+};
+
 bool nothing(const kdaconv_rule_args* a) {
   return a->num_tokens == 0 || a->num_seqs == 0 || a->num_heads == 0;
 }
@@ -138,11 +203,9 @@ using namespace kdaconv;
 
 extern "C" int64_t kdaconv_gated_delta_rule_workspace(int64_t num_tokens, int64_t num_seqs,
                                                       int64_t num_heads, int64_t head_dim) {
-  (void)num_tokens;
-  (void)num_seqs;
-  (void)num_heads;
-  (void)head_dim;
-  return 0;
+  if (num_tokens <= 0 || num_seqs <= 0 || num_heads <= 0 || head_dim <= 0) return 0;
+  const Plan p = make_plan(num_tokens, num_seqs, num_heads, head_dim);
+  return p.slot_bytes + p.ends_bytes + p.moves_bytes;
 }
 
 extern "C" int kdaconv_gated_delta_rule_validate(const kdaconv_rule_args* args, int update,
@@ -160,8 +223,27 @@ extern "C" int kdaconv_gated_delta_rule(const kdaconv_rule_args* args, void* wor
                                         int64_t workspace_bytes, kdaconv_stream_t stream) {
   const int rc = kdaconv_gated_delta_rule_validate(args, 0, workspace, workspace_bytes);
   if (rc != KDACONV_OK || nothing(args)) return rc;
-  const RuleParams P = rule_params(args, false);
-  for_formats(args, Step{P, (int)args->head_dim, reinterpret_cast<hipStream_t>(stream)});
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  const Plan plan = make_plan(args->num_tokens, args->num_seqs, args->num_heads, args->head_dim);
+  ChunkParams P;
+  P.R = rule_params(args, false);
+  if (plan.step) {
+    if (plan.chunks) P.R.max_len = (int32_t)plan.max_len;
+    for_formats(args, Step{P.R, (int)args->head_dim, st});
+  }
+  if (plan.chunks) {
+    P.slots = static_cast<char*>(workspace);
+    P.ends = reinterpret_cast<float*>(P.slots + plan.slot_bytes);
+    P.moves = plan.segments ? P.slots + plan.slot_bytes + plan.ends_bytes : nullptr;
+    P.chunk_programs = (int32_t)plan.chunk_programs;
+    P.segment_programs = (int32_t)plan.segment_programs;
+    P.segment_shift = plan.segment_shift;
+    int64_t reach = kRuleWave;
+    while (reach < args->num_seqs) reach *= kRuleWave;
+    P.search_top = (int32_t)(reach / kRuleWave);
+    P.min_len = (int32_t)plan.max_len + 1;
+    for_formats(args, Chunks{P, (int)args->head_dim, st});
+  }
   return hipGetLastError() == hipSuccess ? KDACONV_OK : KDACONV_ELAUNCH;
 }
 

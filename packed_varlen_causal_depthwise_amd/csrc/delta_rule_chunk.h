@@ -1,0 +1,1098 @@
+// The gated delta rule in chunks of 32 tokens: the prefill.
+//
+// Mathematics. Inside a chunk let G_t be the running sum of the log decays (per key
+// channel), k^ = k |k|^-1 (or the normalised key), n_t = |k_t| (or 1). With the state S at
+// the chunk's start,
+//     L_ti = b_t n_t n_i sum_c k^_tc k^_ic e^(G_tc - G_ic)   for i < t, else 0
+//     T = diag(n) (I + L)^-1 diag(b)
+//     U = T (V - diag(n) (K^ e^G) S)                         the updates, times n
+//     O = scale |q| ((Q^ e^G) S + A U),  A_ti = sum_c q^_tc k^_ic e^(G_tc - G_ic), i <= t
+//     S <- diag(e^G_end) S + (K^ e^(G_end - G))^T U
+// so a chunk costs matrix products and one 32 x 32 triangular inverse instead of 32 steps.
+// T and A do not depend on S.
+//
+// A long sequence is cut into segments. Over a segment S_end = M S_start + B: the scan of
+// a segment from zero gives B, the scan of the identity without values gives M, and the
+// starts follow by S_(j+1) = M_j S_j + B_j. Then all segments run side by side.
+//
+// Kernels, one workgroup of 4 waves each:
+//   prepare   (chunk, head)             T, A and row factors into a slot
+//   scan      (segment, head, B or M)   only for sequences of several segments
+//   join      (sequence, head, columns) the starts of the segments from the third on
+//   scan      (segment, head)           outputs and the final state
+//
+// Numbers. Matrix products run on the FP16 matrix instructions with every operand split
+// into a pair of FP16 values (22 bits) and three products: hi hi + hi lo + lo hi, summed
+// in FP32. (One FP32 instruction costs as much as 16 FP16 ones of the same size; pairs of
+// bfloat16 would keep 16 bits, which left the FP32 state 4e-6 off.) FP16's range holds
+// because vectors have unit length, decays are at most 1, and the columns of S, V and U
+// share a power-of-two factor per column that follows their size. T and A come from FP64
+// and FP32 matrix instructions: their decays e^(G_t - G_i) are products of factors far
+// outside FP16.
+#ifndef KDACONV_DELTA_RULE_CHUNK_H_
+#define KDACONV_DELTA_RULE_CHUNK_H_
+
+#include "delta_rule_device.h"
+
+namespace kdaconv {
+
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32q __attribute__((ext_vector_type(4)));
+
+constexpr float kVec = 16.0f;  // factor on stored unit vectors (their entries are small)
+
+__device__ __forceinline__ f32x4 mfma16(f16x8 a, f16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ f32x4 mfma32(float a, float b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ f64x4 mfma64(double a, double b, f64x4 c) {
+  return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0);
+}
+
+// x as an FP16 pair: hi rounded, lo the rounded rest.
+struct HalfPair {
+  f16x2 hi, lo;
+};
+
+__device__ __forceinline__ HalfPair split2(f32x2 x) {
+  HalfPair p;
+  p.hi = __builtin_convertvector(x, f16x2);
+  p.lo = __builtin_convertvector(f32x2{__builtin_fmaf(x.x, 1.0f, -(float)p.hi.x),
+                                      __builtin_fmaf(x.y, 1.0f, -(float)p.hi.y)}, f16x2);
+  return p;
+}
+
+// Eight values (two tiles' four rows of one column) as matrix operands.
+struct Operand {
+  f16x8 hi, lo;
+};
+
+__device__ __forceinline__ Operand split8(f32x4 a, f32x4 b) {
+  Operand o;
+  const HalfPair p0 = split2(f32x2{a[0], a[1]}), p1 = split2(f32x2{a[2], a[3]});
+  const HalfPair p2 = split2(f32x2{b[0], b[1]}), p3 = split2(f32x2{b[2], b[3]});
+  o.hi = f16x8{p0.hi.x, p0.hi.y, p1.hi.x, p1.hi.y, p2.hi.x, p2.hi.y, p3.hi.x, p3.hi.y};
+  o.lo = f16x8{p0.lo.x, p0.lo.y, p1.lo.x, p1.lo.y, p2.lo.x, p2.lo.y, p3.lo.x, p3.lo.y};
+  return o;
+}
+
+// Operand order. A product's result leaves lane l with rows 4 (l / 16) + r of each 16-row
+// tile, in column l % 16. As the next product's right operand those registers are used as
+// they are: position (l / 16, j) of a 32-deep step then stands for row 16 (j / 4) +
+// 4 (l / 16) + j % 4, and left operands are stored in that order: index x of 32 goes to
+// place 8 ((x % 16) / 4) + 4 (x / 16) + x % 4.
+__device__ __forceinline__ int place(int x) { return 8 * ((x & 15) >> 2) + 4 * (x >> 4) + (x & 3); }
+
+// The sequence and piece that program p owns when pieces of 2^shift tokens are counted by
+// v(s) = s + (start of s >> shift): the largest s with v(s) <= p, and p - v(s). A sequence
+// of n tokens has at most v(s + 1) - v(s) pieces, so every piece has a program and the
+// program count needs no lengths. A 64-way search, one ballot per level. Returns s = -1
+// when no sequence starts early enough.
+struct Piece {
+  int s, index;
+};
+
+__device__ __forceinline__ Piece find_piece(const ChunkParams& P, int p, int shift, int lane) {
+  const RuleParams& R = P.R;
+  int base = 0, v = 0;
+  for (int stride = P.search_top; stride > 0; stride >>= 6) {
+    const int s = base + lane * stride;
+    int at = 0;
+    bool ok = s < R.num_seqs;
+    if (ok) {
+      int a = R.qsl[s];
+      a = a < 0 ? 0 : (a > R.num_tokens ? R.num_tokens : a);
+      at = s + (a >> shift);
+      ok = at <= p;
+    }
+    const uint64_t mask = __ballot(ok);
+    const int n = __builtin_popcountll(mask);
+    if (n == 0) return Piece{-1, 0};
+    base += (n - 1) * stride;
+    v = __shfl(at, n - 1);
+  }
+  base = uniform(base);
+  return Piece{base, p - uniform(v)};
+}
+
+// How a workgroup of 4 waves holds a chunk's rows for elementwise work: groups of kRows
+// neighbouring rows, kLanes lanes per group, two channels per lane.
+template <int D>
+struct Rows {
+  static constexpr int kLanes = D / 2;
+  static constexpr int kGroups = 4 * 64 / kLanes;  // 4 or 8
+  static constexpr int kRows = kChunk / kGroups;  // 8 or 4
+};
+
+template <int kF>
+__device__ __forceinline__ typename Pair<kF>::raw load_row(const char* p, int row, int valid,
+                                                           int stride_bytes) {
+  // Rows past the last are read as the last and replaced by zeros where they are used.
+  return Pair<kF>::load(p + (row < valid ? row : valid - 1) * (int64_t)stride_bytes);
+}
+
+// Sums of N values over kWidth lanes, each lane receiving the sum of value (lane index /
+// (kWidth / N)); exchanges halves while values are left, so N + log2(kWidth / N) - 1
+// exchanges instead of N log2(kWidth).
+template <int N, int kWidth>
+__device__ __forceinline__ double scatter_sum(double (&x)[N], int lane) {
+  int m = kWidth / 2;
+#pragma unroll
+  for (int n = N / 2; n > 0; n >>= 1, m >>= 1) {
+    const bool upper = (lane & m) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const double keep = upper ? x[n + i] : x[i];
+      const double send = upper ? x[i] : x[n + i];
+      x[i] = keep + __shfl_xor(send, m);
+    }
+  }
+  double s = x[0];
+  for (; m > 0; m >>= 1) s += __shfl_xor(s, m);
+  return s;
+}
+
+// ---------------------------------------------------------------------------- prepare
+
+template <int kF, int kG, int D>
+__global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkParams P) {
+  typedef Rows<D> RW;
+  constexpr int kRows = RW::kRows, kLanes = RW::kLanes, kGroups = RW::kGroups;
+  constexpr int kEB = elem_bytes<kF>(), kGB = elem_bytes<kG>();
+  constexpr int kLd = D + 4;  // floats per operand row: 16 rows reach all banks
+  constexpr int kMat = kChunk * kLd;
+  constexpr int kSq = 34;  // doubles per row of a 32 x 32 matrix
+  // Operand rows q, k (times the decay from the block's middle) and columns k; later the
+  // 32 x 32 matrices.
+  __shared__ __attribute__((aligned(16))) float mats[3 * kMat];
+  __shared__ __attribute__((aligned(16))) float tot[kGroups][D];
+  __shared__ __attribute__((aligned(16))) float across[D];
+  __shared__ __attribute__((aligned(16))) float fac[6][kChunk];  // the slot's rows
+  __shared__ float beta[kChunk];
+  __shared__ int steep;
+  float* const mq = mats;
+  float* const mk = mats + kMat;
+  float* const mc = mats + 2 * kMat;
+
+  const RuleParams& R = P.R;
+  const int program = blockIdx.x / R.heads, h = blockIdx.x % R.heads;
+  const int wave = uniform(threadIdx.x / kRuleWave), lane = threadIdx.x % kRuleWave;
+  const Piece piece = find_piece(P, program, 5, lane);
+  if (piece.s < 0) return;
+  const Sequence seq(R, piece.s);
+  if (seq.len < P.min_len || piece.index * kChunk >= seq.len) return;
+  const int first = seq.start + piece.index * kChunk;
+  const int valid = seq.len - piece.index * kChunk < kChunk ? seq.len - piece.index * kChunk : kChunk;
+
+  const int group = threadIdx.x / kLanes, c = 2 * (threadIdx.x % kLanes), row0 = group * kRows;
+  const int64_t qk = h / R.share;
+  const char* const qp = R.q + (first * R.q_ts + qk * R.q_hs + c) * kEB;
+  const char* const kp = R.k + (first * R.k_ts + qk * R.k_hs + c) * kEB;
+  const char* const gp = R.g + (first * R.g_ts + h * R.g_hs + c * R.g_cs) * kGB;
+
+  f32x2 q[kRows], k[kRows], p[kRows];  // p: log2 decays, then their running sums
+  const Gate gate(R, h);
+  f32x2 bias = {0.0f, 0.0f};
+  if (R.dt_bias != nullptr) bias = *(const f32x2a4*)(R.dt_bias + h * D + c);
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const bool in = row0 + i < valid;
+    const f32x2 a = Pair<kF>::value(load_row<kF>(qp, row0 + i, valid, (int)R.q_ts * kEB));
+    const f32x2 b = Pair<kF>::value(load_row<kF>(kp, row0 + i, valid, (int)R.k_ts * kEB));
+    f32x2 g;
+    if (R.g_cs != 0) {
+      g = Pair<kG>::value(load_row<kG>(gp, row0 + i, valid, (int)R.g_ts * kGB));
+    } else {
+      const int r = row0 + i < valid ? row0 + i : valid - 1;
+      g.x = g.y = load_elem<kG>(gp + r * R.g_ts * kGB);
+    }
+    q[i] = in ? a : f32x2{0.0f, 0.0f};
+    k[i] = in ? b : f32x2{0.0f, 0.0f};
+    p[i] = in ? f32x2{gate(g.x, bias.x), gate(g.y, bias.y)} : f32x2{0.0f, 0.0f};
+  }
+  if (threadIdx.x < kChunk)
+    beta[threadIdx.x] = (int)threadIdx.x < valid ? beta_value(R, kF, first + threadIdx.x, h) : 0.0f;
+  if (threadIdx.x == 0) steep = 0;
+
+  // Lengths of the rows' queries and keys.
+  {
+    double ss[2 * kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const double qx = q[i].x, qy = q[i].y, kx = k[i].x, ky = k[i].y;
+      ss[i] = __builtin_fma(qx, qx, qy * qy);
+      ss[kRows + i] = __builtin_fma(kx, kx, ky * ky);
+    }
+    const double s = scatter_sum<2 * kRows, kLanes>(ss, lane);
+    constexpr int kShare = kLanes / (2 * kRows);  // lanes holding the same sum
+    const int l = lane % kLanes, which = l / kShare, r = row0 + which % kRows;
+    if (l % kShare == 0) {
+      const bool norm = R.l2_eps >= 0.0f;
+      const Factor f = inverse_root(norm ? s + (double)R.l2_eps : s);
+      const float n = norm ? 1.0f : (float)(s * ((double)f.hi + (double)f.lo));
+      if (which < kRows) {
+        fac[2][r] = f.hi;
+        fac[4][r] = n * R.scale;
+      } else {
+        fac[0][r] = f.hi;
+        fac[1][r] = f.lo;
+        fac[3][r] = n;
+      }
+    }
+  }
+  // Running sums inside the group.
+#pragma unroll
+  for (int i = 1; i < kRows; ++i) p[i] += p[i - 1];
+  *(f32x2*)&tot[group][c] = p[kRows - 1];
+  __syncthreads();
+
+  // Each block of 16 rows takes its decays from its middle (after 8 rows): rows carry
+  // 2^(p - mid), columns 2^(mid - p), whose product is exact to FP32 while both halves of
+  // the block stay within 2^101 (8 tokens of log decay -8.75 each; the bounded gate
+  // reaches -5). Steeper chunks take the direct sums below.
+  constexpr int kPer = kGroups / 2;  // groups per block
+  const int block = group / kPer;
+  f32x2 before = {0.0f, 0.0f}, mid = {0.0f, 0.0f}, all = {0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const f32x2 t = *(const f32x2*)&tot[block * kPer + i][c];
+    if (i < group % kPer) before += t;
+    if (i < kPer / 2) mid += t;
+    all += t;
+  }
+  if (mid.x < -101.0f || mid.y < -101.0f || all.x - mid.x < -101.0f || all.y - mid.y < -101.0f)
+    steep = 1;
+  if (group == 0) {
+    // From the middle of block 0 to the middle of block 1: what a column of block 0 needs
+    // to meet a row of block 1.
+    f32x2 mid1 = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kPer / 2; ++i) mid1 += *(const f32x2*)&tot[kPer + i][c];
+    const f32x2 d = all - mid + mid1;
+    *(f32x2*)&across[c] = f32x2{exp2_hw(d.x), exp2_hw(d.y)};
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int r = row0 + i;
+    const f32x2 d = p[i] + before - mid;
+    const f32x2 e = {exp2_hw(d.x), exp2_hw(d.y)}, m = {exp2_hw(-d.x), exp2_hw(-d.y)};
+    const Factor f = {fac[0][r], fac[1][r]};
+    const float fq = fac[2][r];
+    k[i] = f32x2{scaled(k[i].x, f), scaled(k[i].y, f)};
+    *(f32x2*)&mq[r * kLd + c] = q[i] * fq * e;
+    *(f32x2*)&mk[r * kLd + c] = k[i] * e;
+    *(f32x2*)&mc[r * kLd + c] = k[i] * m;
+  }
+  __syncthreads();
+
+  const int n16 = lane % 16, n4 = lane / 16;
+  f64x4 akk = {0.0, 0.0, 0.0, 0.0};  // waves 0 to 2: one 16 x 16 block each
+  f32x4 aqk[3] = {};  // wave 3: all three
+  float dkk[3], dqk[3];
+  const bool direct = steep != 0;
+  if (!direct) {
+    // Blocks (row, column): 0 (0, 0), 1 (1, 1), 2 (1, 0). The key products are summed in
+    // FP64: equal keys with steps near 2 (reflections) and no decay make an error common to
+    // L's entries grow with the tokens, by 32 per chunk. FP32 sums and an FP32 inverse left
+    // such a state 1e-4 off after 97 tokens. Both kinds take as long: the 96 FP32
+    // instructions of wave 3 run at twice the rate of the other waves' 32 in FP64.
+    if (wave < 3) {
+      const float* const rk = mk + ((wave == 0 ? 0 : 16) + n16) * kLd + 4 * n4;
+      const float* const rc = mc + ((wave == 1 ? 16 : 0) + n16) * kLd + 4 * n4;
+#pragma unroll
+      for (int b = 0; b < D; b += 16) {
+        const f32x4 x = *(const f32x4*)(rk + b);
+        f32x4 z = *(const f32x4*)(rc + b);
+        if (wave == 2) z *= *(const f32x4*)&across[b + 4 * n4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) akk = mfma64((double)x[e], (double)z[e], akk);
+      }
+    } else {
+      const float* const rq = mq + n16 * kLd + 4 * n4;
+      const float* const rc = mc + n16 * kLd + 4 * n4;
+#pragma unroll
+      for (int b = 0; b < D; b += 16) {
+        const f32x4 x0 = *(const f32x4*)(rq + b), x1 = *(const f32x4*)(rq + 16 * kLd + b);
+        const f32x4 z0 = *(const f32x4*)(rc + b), z1 = *(const f32x4*)(rc + 16 * kLd + b);
+        const f32x4 z2 = z0 * *(const f32x4*)&across[b + 4 * n4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          aqk[0] = mfma32(x0[e], z0[e], aqk[0]);
+          aqk[1] = mfma32(x1[e], z1[e], aqk[1]);
+          aqk[2] = mfma32(x1[e], z2[e], aqk[2]);
+        }
+      }
+    }
+  } else {
+    // Direct sums of k_t k_i 2^(G_t - G_i), with the running sums G in FP64 (a chunk may
+    // hold many resets, and FP32 sums of -150 each would lose the small decays between).
+    __syncthreads();
+    // The decays, from the sums: exact enough again, then summed in FP64 per channel.
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int r = row0 + i;
+      f32x2 g;
+      if (R.g_cs != 0) {
+        g = Pair<kG>::value(load_row<kG>(gp, r, valid, (int)R.g_ts * kGB));
+      } else {
+        g.x = g.y = load_elem<kG>(gp + (r < valid ? r : valid - 1) * R.g_ts * kGB);
+      }
+      *(f32x2*)&mk[r * kLd + c] =
+          r < valid ? f32x2{gate(g.x, bias.x), gate(g.y, bias.y)} : f32x2{0.0f, 0.0f};
+    }
+    __syncthreads();
+    double* const sums = (double*)mc;  // rows of D doubles over mc and mq's place
+    static_assert(sizeof(double) * kChunk * D <= sizeof(float) * 2 * kMat, "FP64 sums fit");
+    double* const lower = (double*)mq;
+    // Rows 0-15 in mc, rows 16-31 in mq (each 16 D doubles <= kMat floats).
+    if (threadIdx.x < D) {
+      double s = 0.0;
+      for (int r = 0; r < kChunk; ++r) {
+        s += (double)mk[r * kLd + threadIdx.x];
+        (r < 16 ? sums : lower)[(r & 15) * D + threadIdx.x] = s;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) *(f32x2*)&mk[(row0 + i) * kLd + c] = k[i];
+    __syncthreads();
+    for (int u = 0; u < 3; ++u) {
+      const int pair = threadIdx.x + 256 * u;  // (t, i) with i <= t, 528 in all
+      dkk[u] = dqk[u] = 0.0f;
+      if (pair >= 528) continue;
+      int t = 0;
+      while ((t + 1) * (t + 2) / 2 <= pair) ++t;
+      const int i = pair - t * (t + 1) / 2;
+      const double* const gt = (t < 16 ? sums : lower) + (t & 15) * D;
+      const double* const gi = (i < 16 ? sums : lower) + (i & 15) * D;
+      const char* const qrow =
+          R.q + ((first + (t < valid ? t : valid - 1)) * R.q_ts + qk * R.q_hs) * kEB;
+      const float fq = t < valid ? fac[2][t] : 0.0f;
+      float sk = 0.0f, sq = 0.0f;
+      for (int ch = 0; ch < D; ++ch) {
+        const float w = mk[i * kLd + ch] * exp2_hw((float)(gt[ch] - gi[ch]));
+        sk = __builtin_fmaf(mk[t * kLd + ch], w, sk);
+        sq = __builtin_fmaf(load_elem<kF>(qrow + ch * kEB) * fq, w, sq);
+      }
+      dkk[u] = sk;
+      dqk[u] = t < valid ? sq : 0.0f;
+    }
+  }
+  __syncthreads();
+
+  // The operands are done with; their place takes L, the inverse and the staged outputs.
+  double* const ml = (double*)mats;  // L [row][column]
+  double* const mt = ml + kChunk * kSq;  // (I + L)^-1
+  // T in three parts and A in two, as they go to the slot. L's place is free for T by then.
+  _Float16* const st = (_Float16*)mats;
+  _Float16* const sa = (_Float16*)(mt + kChunk * kSq);
+  static_assert(6144 <= kChunk * kSq * sizeof(double) &&
+                2 * kChunk * kSq * sizeof(double) + 4096 <= sizeof(float) * 3 * kMat, "they fit");
+  char* const slot = P.slots + ((int64_t)program * R.heads + h) * kSlotBytes;
+  const auto put_a = [&](int t, int i, float a) {
+    // A times 256 in operand order: row tile, lane, place.
+    const int at = (t / 16 * 64 + (place(i) / 8) * 16 + t % 16) * 8 + place(i) % 8;
+    const float x = 256.0f * a;
+    const _Float16 hi = (_Float16)x;
+    sa[at] = hi;
+    sa[1024 + at] = (_Float16)(x - (float)hi);
+  };
+  const auto put_l = [&](int t, int i, double a) {
+    ml[t * kSq + i] =
+        i < t ? (double)beta[t] * ((double)fac[3][t] * (double)fac[3][i]) * a : 0.0;
+  };
+  if (!direct) {
+    if (wave < 3) {
+      // FP64 results: register r of lane l is row 4 r + l / 16.
+      const int rows = wave == 0 ? 0 : 16, cols = wave == 1 ? 16 : 0;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) put_l(rows + 4 * r + n4, cols + n16, akk[r]);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = 4 * n4 + r;
+        put_a(t, n16, n16 <= t ? aqk[0][r] : 0.0f);
+        put_a(16 + t, 16 + n16, n16 <= t ? aqk[1][r] : 0.0f);
+        put_a(16 + t, n16, aqk[2][r]);
+        put_a(t, 16 + n16, 0.0f);
+      }
+    }
+  } else {
+    for (int u = 0; u < 3; ++u) {
+      const int pair = threadIdx.x + 256 * u;
+      if (pair >= 528) continue;
+      int t = 0;
+      while ((t + 1) * (t + 2) / 2 <= pair) ++t;
+      const int i = pair - t * (t + 1) / 2;
+      put_l(t, i, dkk[u]);
+      put_a(t, i, dqk[u]);
+      if (i < t) put_a(i, t, 0.0f);
+    }
+  }
+  __syncthreads();
+
+  if (wave == 0) {
+    // (I + L)^-1: the two diagonal blocks by forward substitution, a column per lane, then
+    // T10 = -T11 (L10 T00). FP64 (the vector unit runs it at FP32's rate).
+    if (lane < 32) {
+      const int b = lane & 16, col = lane & 15;
+      double x[16];
+#pragma unroll
+      for (int t = 0; t < 16; ++t) {
+        double s = t == col ? 1.0 : 0.0;
+#pragma unroll
+        for (int i = 0; i < t; ++i) s = __builtin_fma(-ml[(b + t) * kSq + b + i], x[i], s);
+        x[t] = s;
+        mt[(b + t) * kSq + b + col] = s;
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+    double z[4] = {}, y[4] = {};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const double x = mt[i * kSq + n16];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) z[r] = __builtin_fma(ml[(16 + 4 * n4 + r) * kSq + i], x, z[r]);
+    }
+    // L is done with: its first rows take L10 T00.
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int r = 0; r < 4; ++r) ml[(4 * n4 + r) * kSq + n16] = z[r];
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const double x = ml[i * kSq + n16];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        y[r] = __builtin_fma(mt[(16 + 4 * n4 + r) * kSq + 16 + i], x, y[r]);
+    }
+    // diag(n) T diag(b), scaled to a largest entry of 256 to 512, in three FP16 parts: with
+    // two (22 bits) the reflections above still lost 1e-5.
+    double t00[4], t11[4], t10[4];
+    float top = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 4 * n4 + r;
+      t00[r] = (double)fac[3][t] * mt[t * kSq + n16] * (double)beta[n16];
+      t11[r] = (double)fac[3][16 + t] * mt[(16 + t) * kSq + 16 + n16] * (double)beta[16 + n16];
+      t10[r] = -(double)fac[3][16 + t] * y[r] * (double)beta[n16];
+      top = __builtin_fmaxf(
+          top, __builtin_fmaxf(__builtin_fabsf((float)t10[r]),
+                               __builtin_fmaxf(__builtin_fabsf((float)t00[r]), __builtin_fabsf((float)t11[r]))));
+    }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, m));
+    int e = 0;
+    if (top > 0.0f && top < __builtin_huge_valf()) e = 9 - __builtin_amdgcn_frexp_expf(top);
+    e = e > 100 ? 100 : e;
+    const auto put_t = [&](int t, int i, double x) {
+      x = __builtin_amdgcn_ldexp(x, e);
+      const int at = (t / 16 * 64 + (place(i) / 8) * 16 + t % 16) * 8 + place(i) % 8;
+      const _Float16 hi = (_Float16)(float)x;
+      const float rest = (float)(x - (double)(float)hi);
+      const _Float16 lo = (_Float16)rest;
+      st[at] = hi;
+      st[1024 + at] = lo;
+      st[2048 + at] = (_Float16)(rest - (float)lo);
+    };
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 4 * n4 + r;
+      put_t(t, n16, t00[r]);
+      put_t(16 + t, 16 + n16, t11[r]);
+      put_t(16 + t, n16, t10[r]);
+      put_t(t, 16 + n16, 0.0f);
+    }
+    // U is kept times 1 / 16, so that (16 k^)^T (U / 16) adds to S as it is.
+    if (lane == 0) fac[5][0] = __builtin_amdgcn_ldexpf(1.0f / kVec, -e);
+  }
+  __syncthreads();
+  // The slot: 10 KB of operands and the rows of factors, 16 bytes per thread and store.
+  u32q* const dst = (u32q*)slot;
+  dst[threadIdx.x] = ((const u32q*)st)[threadIdx.x];
+  if (threadIdx.x < 128) dst[256 + threadIdx.x] = ((const u32q*)st)[256 + threadIdx.x];
+  dst[384 + threadIdx.x] = ((const u32q*)sa)[threadIdx.x];
+  if (threadIdx.x < 6 * kChunk / 4)
+    ((u32q*)(slot + kSlotRows))[threadIdx.x] = ((const u32q*)&fac[0][0])[threadIdx.x];
+}
+
+// ------------------------------------------------------------------------------- scan
+
+// The largest magnitude of a column over its 4 lanes.
+__device__ __forceinline__ float column_max(float x) {
+  x = __builtin_fmaxf(x, __shfl_xor(x, 16));
+  return __builtin_fmaxf(x, __shfl_xor(x, 32));
+}
+
+// What the scan is run for.
+constexpr int kScanOut = 0;  // outputs and final states
+constexpr int kScanMove = 1;  // a segment's B and M
+
+constexpr float kColLow = 1.0f, kColHigh = 8192.0f;  // columns' largest value stays between
+constexpr int kColExp = 8;  // and is brought to 2^7 .. 2^8 when it leaves
+
+// kN column tiles of 16 per wave; lane l owns columns kN (l % 16) + n.
+template <int kM, int kN>
+struct ScanState {
+  f32x4 s[kM][kN];  // times the column's scale
+  float scale[kN], inverse[kN];
+
+  __device__ __forceinline__ float largest(int n) const {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kM; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) m = __builtin_fmaxf(m, __builtin_fabsf(s[i][n][r]));
+    return m;
+  }
+
+  // Whether some column's largest value (over lanes holding m) left its range. Zero
+  // columns stay as they are; infinities and NaN count as in range.
+  static __device__ __forceinline__ bool left(float m) {
+    if (__ballot(m >= kColHigh) != 0) return true;
+    uint64_t big = __ballot(m >= kColLow), some = __ballot(m > 0.0f);
+    big |= big >> 32;
+    big |= big >> 16;
+    some |= some >> 32;
+    some |= some >> 16;
+    return ((some & ~big) & 0xFFFF) != 0;
+  }
+
+  // The factor that brings a column whose largest value is m back (m from all its lanes).
+  static __device__ __forceinline__ float factor(float m) {
+    if (!(m > 0.0f) || !(m < __builtin_huge_valf())) return 1.0f;
+    if (m >= kColLow && m < kColHigh) return 1.0f;
+    int e = kColExp - __builtin_amdgcn_frexp_expf(m);
+    e = e > 100 ? 100 : (e < -100 ? -100 : e);
+    return __builtin_amdgcn_ldexpf(1.0f, e);
+  }
+
+  __device__ __forceinline__ void apply(int n, float f) {
+#pragma unroll
+    for (int i = 0; i < kM; ++i) s[i][n] *= f;
+    scale[n] *= f;
+    inverse[n] *= 1.0f / f;
+  }
+};
+
+template <int kF, int kG, int D, int kMode>
+__global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkParams P) {
+  typedef Rows<D> RW;
+  constexpr int kRows = RW::kRows, kLanes = RW::kLanes, kGroups = RW::kGroups;
+  constexpr int kEB = elem_bytes<kF>(), kGB = elem_bytes<kG>();
+  constexpr int kM = D / 16, kN = D / 64, kK = D / 32;
+  constexpr bool kOut = kMode == kScanOut;
+  constexpr int kLd = D + 8, kLt = kChunk + 8;  // halves per row: 16 rows reach all banks
+  __shared__ __attribute__((aligned(16))) _Float16 kg[2][kChunk * kLd];
+  __shared__ __attribute__((aligned(16))) _Float16 qg[2][kOut ? kChunk * kLd : 8];
+  __shared__ __attribute__((aligned(16))) _Float16 kt[2][D * kLt];
+  __shared__ __attribute__((aligned(16))) float tot[kGroups][D];
+  __shared__ __attribute__((aligned(16))) float decay[D];
+  __shared__ float part[4];
+
+  const RuleParams& R = P.R;
+  int id = blockIdx.x;
+  const bool identity = !kOut && (id & 1) != 0;  // the segment's M
+  if (!kOut) id >>= 1;
+  const int program = id / R.heads, h = id % R.heads;
+  const int wave = uniform(threadIdx.x / kRuleWave), lane = threadIdx.x % kRuleWave;
+  const Piece piece = find_piece(P, program, P.segment_shift, lane);
+  if (piece.s < 0) return;
+  const Sequence seq(R, piece.s);
+  if (seq.len < P.min_len) return;
+  const int per = 1 << (P.segment_shift - 5);  // chunks per segment
+  const int chunks = (seq.len + kChunk - 1) / kChunk;
+  const int begin = piece.index * per, end = begin + per < chunks ? begin + per : chunks;
+  if (begin >= chunks) return;
+  if (!kOut && (end == chunks || (identity && begin == 0))) return;
+
+  const int n16 = lane % 16, n4 = lane / 16;
+  const int col = wave * (16 * kN) + kN * n16;
+  const int64_t cell = (int64_t)program * R.heads + h;
+
+  ScanState<kM, kN> S;
+  {
+    const float* from = nullptr;
+    if (begin == 0) {
+      if (seq.init) from = R.states + seq.line * R.st_line + h * R.st_head;
+    } else if (kOut) {
+      from = P.ends + (cell - R.heads) * (D * D);
+    }
+#pragma unroll
+    for (int m = 0; m < kM; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * m + 4 * n4 + r;
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          float x = 0.0f;
+          if (from != nullptr) x = from[row * D + col + n];
+          if (identity) x = row == col + n ? 1.0f : 0.0f;
+          S.s[m][n][r] = x;
+        }
+      }
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      S.scale[n] = S.inverse[n] = 1.0f;
+      S.apply(n, S.factor(column_max(S.largest(n))));
+    }
+  }
+
+  const int group = threadIdx.x / kLanes, c = 2 * (threadIdx.x % kLanes), row0 = group * kRows;
+  const int64_t qk = h / R.share;
+  const Gate gate(R, h);
+  f32x2 bias = {0.0f, 0.0f};
+  if (R.dt_bias != nullptr) bias = *(const f32x2a4*)(R.dt_bias + h * D + c);
+  const int slot0 = piece.s + (seq.start >> 5);  // the sequence's first chunk program
+  // Where this lane's two channels go in operand rows.
+  const int cpos = 32 * (c / 32) + place(c % 32);
+
+  for (int chunk = begin; chunk < end; ++chunk) {
+    const int first = seq.start + chunk * kChunk;
+    const int valid = seq.len - chunk * kChunk < kChunk ? seq.len - chunk * kChunk : kChunk;
+    const char* const slot = P.slots + ((int64_t)(slot0 + chunk) * R.heads + h) * kSlotBytes;
+    const float* const fac = (const float*)(slot + kSlotRows);
+
+    // ---- operands
+    f32x2 q[kRows], k[kRows], p[kRows];
+    {
+      const char* const kp = R.k + (first * R.k_ts + qk * R.k_hs + c) * kEB;
+      const char* const qp = R.q + (first * R.q_ts + qk * R.q_hs + c) * kEB;
+      const char* const gp = R.g + (first * R.g_ts + h * R.g_hs + c * R.g_cs) * kGB;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int r = row0 + i;
+        const bool in = r < valid;
+        const f32x2 b = Pair<kF>::value(load_row<kF>(kp, r, valid, (int)R.k_ts * kEB));
+        k[i] = in ? b : f32x2{0.0f, 0.0f};
+        if (kOut) {
+          const f32x2 a = Pair<kF>::value(load_row<kF>(qp, r, valid, (int)R.q_ts * kEB));
+          q[i] = in ? a : f32x2{0.0f, 0.0f};
+        }
+        f32x2 g;
+        if (R.g_cs != 0) {
+          g = Pair<kG>::value(load_row<kG>(gp, r, valid, (int)R.g_ts * kGB));
+        } else {
+          g.x = g.y = load_elem<kG>(gp + (in ? r : valid - 1) * R.g_ts * kGB);
+        }
+        p[i] = in ? f32x2{gate(g.x, bias.x), gate(g.y, bias.y)} : f32x2{0.0f, 0.0f};
+      }
+    }
+    f32x2 rest[kRows];  // log2 decay after each row, inside the group
+    rest[kRows - 1] = f32x2{0.0f, 0.0f};
+#pragma unroll
+    for (int i = kRows - 1; i > 0; --i) rest[i - 1] = rest[i] + p[i];
+#pragma unroll
+    for (int i = 1; i < kRows; ++i) p[i] += p[i - 1];
+    *(f32x2*)&tot[group][c] = p[kRows - 1];
+    // Also: every wave is done with the operands of the chunk before.
+    __syncthreads();
+    f32x2 before = {0.0f, 0.0f}, after = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      const f32x2 t = *(const f32x2*)&tot[i][c];
+      if (i < group) before += t;
+      if (i > group) after += t;
+    }
+    if (group == 0) {
+      const f32x2 d = p[kRows - 1] + after;
+      *(f32x2*)&decay[c] = f32x2{exp2_hw(d.x), exp2_hw(d.y)};
+    }
+    f16x2 th[kRows], tl[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int r = row0 + i;
+      const Factor f = {kVec * fac[r], kVec * fac[kChunk + r]};
+      const f32x2 unit = {scaled(k[i].x, f), scaled(k[i].y, f)};
+      const f32x2 up = p[i] + before, down = rest[i] + after;
+      const f32x2 e = {exp2_hw(up.x), exp2_hw(up.y)};
+      const HalfPair g = split2(unit * e);
+      *(f16x2*)&kg[0][r * kLd + cpos] = g.hi;
+      *(f16x2*)&kg[1][r * kLd + cpos] = g.lo;
+      const HalfPair t = split2(unit * f32x2{exp2_hw(down.x), exp2_hw(down.y)});
+      th[i] = t.hi;
+      tl[i] = t.lo;
+      if (kOut) {
+        const HalfPair w = split2(q[i] * (kVec * fac[2 * kChunk + r]) * e);
+        *(f16x2*)&qg[0][r * kLd + cpos] = w.hi;
+        *(f16x2*)&qg[1][r * kLd + cpos] = w.lo;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; i += 4) {
+      const int at = place(row0 + i);  // 4 rows in a row of the transposed operand
+      *(f16x4*)&kt[0][c * kLt + at] = f16x4{th[i].x, th[i + 1].x, th[i + 2].x, th[i + 3].x};
+      *(f16x4*)&kt[0][(c + 1) * kLt + at] = f16x4{th[i].y, th[i + 1].y, th[i + 2].y, th[i + 3].y};
+      *(f16x4*)&kt[1][c * kLt + at] = f16x4{tl[i].x, tl[i + 1].x, tl[i + 2].x, tl[i + 3].x};
+      *(f16x4*)&kt[1][(c + 1) * kLt + at] = f16x4{tl[i].y, tl[i + 1].y, tl[i + 2].y, tl[i + 3].y};
+    }
+    __syncthreads();
+
+    // ---- Y = (K e^G) S and O = (Q e^G) S
+    f32x4 Y[2][kN], O[2][kN];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int n = 0; n < kN; ++n) Y[t][n] = O[t][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int kk = 0; kk < kK; ++kk) {
+      Operand b[kN];
+#pragma unroll
+      for (int n = 0; n < kN; ++n) b[n] = split8(S.s[2 * kk][n], S.s[2 * kk + 1][n]);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int at = (16 * t + n16) * kLd + 32 * kk + 8 * n4;
+        const f16x8 ah = *(const f16x8*)&kg[0][at], al = *(const f16x8*)&kg[1][at];
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          Y[t][n] = mfma16(ah, b[n].hi, Y[t][n]);
+          Y[t][n] = mfma16(ah, b[n].lo, Y[t][n]);
+          Y[t][n] = mfma16(al, b[n].hi, Y[t][n]);
+        }
+        if (kOut) {
+          const f16x8 qh = *(const f16x8*)&qg[0][at], ql = *(const f16x8*)&qg[1][at];
+#pragma unroll
+          for (int n = 0; n < kN; ++n) {
+            O[t][n] = mfma16(qh, b[n].hi, O[t][n]);
+            O[t][n] = mfma16(qh, b[n].lo, O[t][n]);
+            O[t][n] = mfma16(ql, b[n].hi, O[t][n]);
+          }
+        }
+      }
+    }
+
+    // ---- X = V - n Y, in the columns' scales
+    const char* const vp = R.v + (first * R.v_ts + h * R.v_hs + col) * kEB;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * t + 4 * n4 + r;
+        const float n_t = fac[3 * kChunk + row] * (1.0f / kVec);
+        f32x2 v = {0.0f, 0.0f};
+        if (!identity && row < valid) {
+          if (kN == 2)
+            v = Pair<kF>::value(Pair<kF>::load(vp + row * R.v_ts * kEB));
+          else
+            v.x = load_elem<kF>(vp + row * R.v_ts * kEB);
+        }
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+          Y[t][n][r] = __builtin_fmaf(v[n], S.scale[n], -n_t * Y[t][n][r]);
+      }
+    // The columns' range over S and X.
+    float high[kN];
+    bool left = false;
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      float m = S.largest(n);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m = __builtin_fmaxf(m, __builtin_fabsf(Y[t][n][r]));
+      high[n] = m;
+      left |= S.left(m);
+    }
+    if (left) {
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        const float f = S.factor(column_max(high[n]));
+        S.apply(n, f);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          Y[t][n] *= f;
+          O[t][n] *= f;
+        }
+      }
+    }
+
+    // ---- U = T X
+    f32x4 U[2][kN];
+    {
+      const f16x8* const tp = (const f16x8*)(slot + kSlotT);
+      Operand b[kN];
+#pragma unroll
+      for (int n = 0; n < kN; ++n) b[n] = split8(Y[0][n], Y[1][n]);
+      const float us = fac[5 * kChunk];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const f16x8 ah = tp[64 * t + lane], al = tp[128 + 64 * t + lane], ar = tp[256 + 64 * t + lane];
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          f32x4 u = {0.0f, 0.0f, 0.0f, 0.0f};
+          u = mfma16(ar, b[n].hi, u);
+          u = mfma16(ah, b[n].hi, u);
+          u = mfma16(ah, b[n].lo, u);
+          u = mfma16(al, b[n].hi, u);
+          U[t][n] = u * us;
+        }
+      }
+    }
+    // U may outgrow X where keys are longer than 1 (S is safe at any smaller scale).
+    left = false;
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      float m = 0.0f;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m = __builtin_fmaxf(m, __builtin_fabsf(U[t][n][r]));
+      high[n] = m;
+      left |= __ballot(m >= kColHigh) != 0;
+    }
+    if (left) {
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        const float m = column_max(high[n]);
+        const float f = m >= kColHigh ? S.factor(m) : 1.0f;
+        S.apply(n, f);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          U[t][n] *= f;
+          O[t][n] *= f;
+        }
+      }
+    }
+
+    // ---- S <- e^G_end S + K^T U; O += A U
+    Operand u[kN];
+#pragma unroll
+    for (int n = 0; n < kN; ++n) u[n] = split8(U[0][n], U[1][n]);
+#pragma unroll
+    for (int m = 0; m < kM; ++m) {
+      const f32x4 d = *(const f32x4*)&decay[16 * m + 4 * n4];
+      const int at = (16 * m + n16) * kLt + 8 * n4;
+      const f16x8 ah = *(const f16x8*)&kt[0][at], al = *(const f16x8*)&kt[1][at];
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        f32x4 s = S.s[m][n] * d;
+        s = mfma16(ah, u[n].hi, s);
+        s = mfma16(ah, u[n].lo, s);
+        S.s[m][n] = mfma16(al, u[n].hi, s);
+      }
+    }
+    if (kOut) {
+      const f16x8* const ap = (const f16x8*)(slot + kSlotA);
+      char* const op = R.out + ((first * (int64_t)R.heads + h) * D + col) * kEB;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const f16x8 ah = ap[64 * t + lane], al = ap[128 + 64 * t + lane];
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          O[t][n] = mfma16(ah, u[n].hi, O[t][n]);
+          O[t][n] = mfma16(ah, u[n].lo, O[t][n]);
+          O[t][n] = mfma16(al, u[n].hi, O[t][n]);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = 16 * t + 4 * n4 + r;
+          if (row < valid) {
+            const float f = fac[4 * kChunk + row] * (1.0f / kVec);
+            char* const o = op + row * (int64_t)R.heads * (D * kEB);
+            if (kN == 2)
+              Pair<kF>::store(o, f32x2{O[t][0][r] * f * S.inverse[0],
+                                       O[t][kN - 1][r] * f * S.inverse[kN - 1]});
+            else
+              store_elem<kF>(o, O[t][0][r] * f * S.inverse[0]);
+          }
+        }
+      }
+    }
+    // The columns' range for the next chunk.
+    left = false;
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      high[n] = S.largest(n);
+      left |= S.left(high[n]);
+    }
+    if (left) {
+#pragma unroll
+      for (int n = 0; n < kN; ++n) S.apply(n, S.factor(column_max(high[n])));
+    }
+  }
+
+  // ---- the end
+  if (identity) {
+    // M as pairs in operand order, scaled by one power of two to a largest entry of 256 to
+    // 512.
+    float top = 0.0f;
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      S.apply(n, S.inverse[n]);
+      top = __builtin_fmaxf(top, S.largest(n));
+    }
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, m));
+    if (lane == 0) part[wave] = top;
+    __syncthreads();
+    top = __builtin_fmaxf(__builtin_fmaxf(part[0], part[1]), __builtin_fmaxf(part[2], part[3]));
+    int e = 0;
+    if (top > 0.0f && top < __builtin_huge_valf()) e = 9 - __builtin_amdgcn_frexp_expf(top);
+    e = e > 100 ? 100 : e;
+    char* const to = P.moves + cell * move_bytes(D);
+    _Float16* const hi = (_Float16*)to;
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      const int cc = col + n, pl = place(cc % 32);
+#pragma unroll
+      for (int m = 0; m < kM; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float x = __builtin_amdgcn_ldexpf(S.s[m][n][r], e);
+          const int at = ((m * kK + cc / 32) * 64 + (pl / 8) * 16 + 4 * n4 + r) * 8 + pl % 8;
+          hi[at] = (_Float16)x;
+          hi[D * D + at] = (_Float16)(x - (float)(_Float16)x);
+        }
+    }
+    if (threadIdx.x == 0) *(float*)(to + (int64_t)D * D * 4) = __builtin_amdgcn_ldexpf(1.0f, -e);
+  } else {
+    float* to = nullptr;
+    if (!kOut)
+      to = P.ends + cell * (D * D);
+    else if (end == chunks && seq.line >= 0)
+      to = R.states + seq.line * R.st_line + h * R.st_head;
+    if (to != nullptr) {
+#pragma unroll
+      for (int m = 0; m < kM; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float* const at = to + (16 * m + 4 * n4 + r) * D + col;
+          if (kN == 2)
+            *(f32x2a4*)at = f32x2{S.s[m][0][r] * S.inverse[0], S.s[m][kN - 1][r] * S.inverse[kN - 1]};
+          else
+            *at = S.s[m][0][r] * S.inverse[0];
+        }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------- join
+
+// The starts of a sequence's segments: ends[0] is segment 0's end and so segment 1's
+// start; ends[j] <- M_j ends[j - 1] + ends[j] makes it segment j + 1's start. One workgroup
+// per (sequence, head, 16 columns); wave w owns rows D / 4 w .. of the columns and hands
+// its operands to the others through LDS.
+template <int D>
+__global__ __launch_bounds__(256) void delta_rule_join_kernel(const ChunkParams P) {
+  constexpr int kK = D / 32, kT = D / 64, kSlices = D / 16;  // row tiles per wave
+  __shared__ __attribute__((aligned(16))) _Float16 hi[2][kK][64 * 8], lo[2][kK][64 * 8];
+  __shared__ float most[2][4][16];
+  const RuleParams& R = P.R;
+  const int slice = blockIdx.x % kSlices, id = blockIdx.x / kSlices;
+  const int program = id / R.heads, h = id % R.heads;
+  const int wave = uniform(threadIdx.x / kRuleWave), lane = threadIdx.x % kRuleWave;
+  const Piece piece = find_piece(P, program, P.segment_shift, lane);
+  if (piece.s < 0 || piece.index != 0) return;
+  const Sequence seq(R, piece.s);
+  if (seq.len < P.min_len) return;
+  const int segments = (seq.len + (1 << P.segment_shift) - 1) >> P.segment_shift;
+  const int n16 = lane % 16, n4 = lane / 16;
+  const int64_t cell = (int64_t)program * R.heads + h;
+  float* end = P.ends + cell * (D * D) + 16 * slice + n16;
+  const char* move = P.moves + cell * move_bytes(D);
+  const int row0 = 16 * kT * wave + 4 * n4;
+  f32x4 S[kT];
+  if (segments < 3) return;
+#pragma unroll
+  for (int t = 0; t < kT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) S[t][r] = end[(row0 + 16 * t + r) * D];
+  for (int j = 1; j < segments - 1; ++j) {
+    const int buf = j & 1;
+    end += (int64_t)R.heads * (D * D);
+    move += (int64_t)R.heads * move_bytes(D);
+    f16x8 ah[kT][kK], al[kT][kK];
+#pragma unroll
+    for (int t = 0; t < kT; ++t)
+#pragma unroll
+      for (int kk = 0; kk < kK; ++kk) {
+        const f16x8* const a = (const f16x8*)move + ((kT * wave + t) * kK + kk) * 64 + lane;
+        ah[t][kk] = a[0];
+        al[t][kk] = a[D * D / 8];
+      }
+    const float back = *(const float*)(move + (int64_t)D * D * 4);
+    f32x4 B[kT];
+    float m = 0.0f;
+#pragma unroll
+    for (int t = 0; t < kT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        B[t][r] = end[(row0 + 16 * t + r) * D];
+        m = __builtin_fmaxf(m, __builtin_fabsf(S[t][r]));
+      }
+    m = column_max(m);
+    if (n4 == 0) most[buf][wave][n16] = m;
+    __syncthreads();
+    m = __builtin_fmaxf(__builtin_fmaxf(most[buf][0][n16], most[buf][1][n16]),
+                        __builtin_fmaxf(most[buf][2][n16], most[buf][3][n16]));
+    int e = 0;
+    if (m > 0.0f && m < __builtin_huge_valf()) e = kColExp - __builtin_amdgcn_frexp_expf(m);
+    e = e > 100 ? 100 : e;
+#pragma unroll
+    for (int t = 0; t < kT; ++t) {
+      const int tile = kT * wave + t;
+      f32x4 x;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[r] = __builtin_amdgcn_ldexpf(S[t][r], e);
+      const HalfPair p0 = split2(f32x2{x[0], x[1]}), p1 = split2(f32x2{x[2], x[3]});
+      const int at = lane * 8 + 4 * (tile & 1);
+      *(f16x4*)&hi[buf][tile / 2][at] = f16x4{p0.hi.x, p0.hi.y, p1.hi.x, p1.hi.y};
+      *(f16x4*)&lo[buf][tile / 2][at] = f16x4{p0.lo.x, p0.lo.y, p1.lo.x, p1.lo.y};
+    }
+    __syncthreads();
+    const float f = __builtin_amdgcn_ldexpf(back, -e);
+#pragma unroll
+    for (int t = 0; t < kT; ++t) S[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int kk = 0; kk < kK; ++kk) {
+      const f16x8 bh = *(const f16x8*)&hi[buf][kk][lane * 8], bl = *(const f16x8*)&lo[buf][kk][lane * 8];
+#pragma unroll
+      for (int t = 0; t < kT; ++t) {
+        S[t] = mfma16(ah[t][kk], bh, S[t]);
+        S[t] = mfma16(ah[t][kk], bl, S[t]);
+        S[t] = mfma16(al[t][kk], bh, S[t]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        S[t][r] = __builtin_fmaf(S[t][r], f, B[t][r]);
+        end[(row0 + 16 * t + r) * D] = S[t][r];
+      }
+  }
+}
+
+// ----------------------------------------------------------------------------- launches
+
+template <int kF, int kG, int D>
+void launch_chunks(const ChunkParams& P, hipStream_t st) {
+  const unsigned heads = (unsigned)P.R.heads;
+  const unsigned chunks = (unsigned)P.chunk_programs * heads;
+  const unsigned segments = (unsigned)P.segment_programs * heads;
+  hipLaunchKernelGGL((delta_rule_prepare_kernel<kF, kG, D>), dim3(chunks), dim3(256), 0, st, P);
+  if (P.moves != nullptr) {
+    hipLaunchKernelGGL((delta_rule_scan_kernel<kF, kG, D, kScanMove>), dim3(2 * segments), dim3(256), 0, st, P);
+    hipLaunchKernelGGL((delta_rule_join_kernel<D>), dim3(segments * (D / 16)), dim3(256), 0, st, P);
+  }
+  hipLaunchKernelGGL((delta_rule_scan_kernel<kF, kG, D, kScanOut>), dim3(segments), dim3(256), 0, st, P);
+}
+
+template <int kF, int kG>
+void launch_rule_chunks(const ChunkParams& P, int head_dim, hipStream_t st) {
+  if (head_dim == 128)
+    launch_chunks<kF, kG, 128>(P, st);
+  else
+    launch_chunks<kF, kG, 64>(P, st);
+}
+
+}  // namespace kdaconv
+
+#endif  // KDACONV_DELTA_RULE_CHUNK_H_

@@ -171,7 +171,7 @@ __device__ __forceinline__ float beta_value(const RuleParams& P, int kF, int64_t
   return P.beta_logits ? sigmoid_f(b) : b;
 }
 
-// 1 / sqrt(x) as the sum of two FP32 values, from FP32's and one Newton step in FP64. Keys
+// 1 / sqrt(x) as the sum of two FP32 values (0 for 0), by Newton's steps in FP64. Keys
 // are scaled with both (k hi + k lo, rounded once): the rule applies I - beta k k^T once
 // per token, so an error of 2^-24 in the length of equal keys, with no decay and beta
 // near 2, would grow with every token (measured on 97 equal keys: 1.3e-5 of the largest
@@ -181,9 +181,11 @@ struct Factor {
 };
 
 __device__ __forceinline__ Factor inverse_root(double x) {
-  const double r = 1.0f / __builtin_sqrtf((float)x);
-  const double y = __builtin_fma(0.5 * r, __builtin_fma(-x * r, r, 1.0), r);
-  Factor f;
+  Factor f = {0.0f, 0.0f};
+  if (x == 0.0) return f;
+  double y = __builtin_amdgcn_rsq(x);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) y = __builtin_fma(0.5 * y, __builtin_fma(-x * y, y, 1.0), y);
   f.hi = (float)y;
   f.lo = (float)(y - (double)f.hi);
   return f;

@@ -283,7 +283,9 @@ extern "C" int kdaconv_gated_rms_norm(const void* x, int dtype, int64_t num_toke
   if (dim % 8 != 0 || dim > 512) return KDACONV_EUNSUPPORTED;
   if (x_stride0 < 0 || x_stride1 < 0 || gate_stride0 < 0 || gate_stride1 < 0)
     return KDACONV_EUNSUPPORTED;
-  if (num_tokens > INT32_MAX || num_heads > INT32_MAX || num_tokens * num_heads > INT32_MAX)
+  // A launch may not reach 2^32 threads.
+  constexpr int64_t kMaxRows = (int64_t)1 << 28;
+  if (num_tokens > kMaxRows || num_heads > kMaxRows || num_tokens * num_heads > kMaxRows)
     return KDACONV_EUNSUPPORTED;
   if (num_tokens == 0 || num_heads == 0) return KDACONV_OK;
   const bool gated = activation != KDACONV_NORM_GATE_NONE;
@@ -326,7 +328,7 @@ extern "C" int kdaconv_residual_rms_norm(const void* x, int dtype, int64_t num_t
                                          kdaconv_stream_t stream) {
   if (num_tokens < 0 || hidden <= 0 || !known(dtype)) return KDACONV_EINVAL;
   if (!(eps >= 0.0)) return KDACONV_EINVAL;
-  if (hidden > 16384 || num_tokens > INT32_MAX) return KDACONV_EUNSUPPORTED;
+  if (hidden > 16384 || num_tokens >= (int64_t)1 << 24) return KDACONV_EUNSUPPORTED;
   if (x_stride < 0 || residual_stride < 0) return KDACONV_EUNSUPPORTED;
   // Rows of the residual may not overlap: each is written.
   if (residual != nullptr && num_tokens > 1 && residual_stride < hidden) return KDACONV_EINVAL;
