@@ -37,6 +37,7 @@ struct RuleParams {
   int32_t gate, beta_logits, beta_f32, has_null_block;
   int32_t all_init;  // every sequence starts from its line (the update)
   int32_t max_len;  // the step kernel leaves longer sequences alone
+  float one;  // 1
 };
 
 constexpr int kChunk = 32;  // tokens per chunk
@@ -56,7 +57,8 @@ struct ChunkParams {
 
 // One chunk of one head as the scan reads it: T as three and A as two FP16 matrices in the
 // order of matrix operands, then six rows of kChunk floats (see prepare).
-constexpr int kSlotT = 0, kSlotA = 6144, kSlotRows = 10240, kSlotBytes = 11264;
+constexpr int kSlotT = 0, kSlotA = 6144, kSlotRows = 10240;
+constexpr int kSlotUsed = kSlotRows + 6 * kChunk * 4, kSlotBytes = 11264;
 
 // The transition: pairs of FP16 matrices and a scale.
 inline __host__ __device__ int64_t move_bytes(int head_dim) { return (int64_t)head_dim * head_dim * 4 + 256; }

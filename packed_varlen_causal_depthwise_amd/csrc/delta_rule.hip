@@ -7,7 +7,8 @@
 namespace kdaconv {
 namespace {
 
-constexpr int64_t kMaxStride = (int64_t)1 << 24;
+// 32 rows stay below 2^30 bytes.
+constexpr int64_t kMaxStride = (int64_t)1 << 23;
 
 bool known_rule_dtype(int d) { return d == KDACONV_BF16 || d == KDACONV_F16 || d == KDACONV_F32; }
 
@@ -154,6 +155,7 @@ RuleParams rule_params(const kdaconv_rule_args* a, bool update) {
   P.has_null_block = a->has_null_block != 0;
   P.all_init = update;
   P.max_len = INT32_MAX;
+  P.one = 1.0f;
   return P;
 }
 

@@ -55,16 +55,24 @@ __device__ __forceinline__ f64x4 mfma64(double a, double b, f64x4 c) {
   return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0);
 }
 
+// 16 bytes per lane from memory to LDS, at the wave's place + 16 times the lane's number.
+__device__ __forceinline__ void to_lds(const char* from, char* wave_to) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                   (__attribute__((address_space(3))) void*)wave_to, 16, 0, 0);
+}
+
 // x as an FP16 pair: hi rounded, lo the rounded rest.
 struct HalfPair {
   f16x2 hi, lo;
 };
 
-__device__ __forceinline__ HalfPair split2(f32x2 x) {
+// `one` is 1 in a register the compiler does not know: x one - hi then is one mixed-format
+// fused multiply-add on the packed hi, where x - hi takes a conversion and a subtraction.
+__device__ __forceinline__ HalfPair split2(f32x2 x, float one) {
   HalfPair p;
   p.hi = __builtin_convertvector(x, f16x2);
-  p.lo = __builtin_convertvector(f32x2{__builtin_fmaf(x.x, 1.0f, -(float)p.hi.x),
-                                      __builtin_fmaf(x.y, 1.0f, -(float)p.hi.y)}, f16x2);
+  p.lo = __builtin_convertvector(f32x2{__builtin_fmaf(x.x, one, -(float)p.hi.x),
+                                      __builtin_fmaf(x.y, one, -(float)p.hi.y)}, f16x2);
   return p;
 }
 
@@ -73,10 +81,10 @@ struct Operand {
   f16x8 hi, lo;
 };
 
-__device__ __forceinline__ Operand split8(f32x4 a, f32x4 b) {
+__device__ __forceinline__ Operand split8(f32x4 a, f32x4 b, float one) {
   Operand o;
-  const HalfPair p0 = split2(f32x2{a[0], a[1]}), p1 = split2(f32x2{a[2], a[3]});
-  const HalfPair p2 = split2(f32x2{b[0], b[1]}), p3 = split2(f32x2{b[2], b[3]});
+  const HalfPair p0 = split2(f32x2{a[0], a[1]}, one), p1 = split2(f32x2{a[2], a[3]}, one);
+  const HalfPair p2 = split2(f32x2{b[0], b[1]}, one), p3 = split2(f32x2{b[2], b[3]}, one);
   o.hi = f16x8{p0.hi.x, p0.hi.y, p1.hi.x, p1.hi.y, p2.hi.x, p2.hi.y, p3.hi.x, p3.hi.y};
   o.lo = f16x8{p0.lo.x, p0.lo.y, p1.lo.x, p1.lo.y, p2.lo.x, p2.lo.y, p3.lo.x, p3.lo.y};
   return o;
@@ -130,32 +138,96 @@ struct Rows {
   static constexpr int kRows = kChunk / kGroups;  // 8 or 4
 };
 
-template <int kF>
-__device__ __forceinline__ typename Pair<kF>::raw load_row(const char* p, int row, int valid,
-                                                           int stride_bytes) {
-  // Rows past the last are read as the last and replaced by zeros where they are used.
-  return Pair<kF>::load(p + (row < valid ? row : valid - 1) * (int64_t)stride_bytes);
+// Hides that x is the same in every iteration of a loop. Without it the compiler computes
+// each row's offset once, before the loop, and keeps all of them in registers (40 of 256,
+// which spilled) to save an addition each.
+__device__ __forceinline__ uint32_t fresh(uint32_t x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// A lane's pairs of N rows from row0 on, as loaded. base is the same for all lanes, so a
+// load takes it from scalar registers and a 32-bit offset: the stride of 32 rows stays
+// below 2^30 bytes. Rows past the last valid one are read as the last (and replaced by
+// zeros, see mask_rows). All loads of a chunk are issued together.
+template <int kF, int N>
+struct RawRows {
+  typename Pair<kF>::raw r[N];
+
+  // offset: of the lane's channels in a row; stride: of rows, in bytes. kSame: one element
+  // per row, for both of the lane's channels (gates per head).
+  template <bool kSame>
+  __device__ __forceinline__ void load(const char* base, uint32_t offset, int row0, int valid,
+                                       uint32_t stride) {
+    if (valid == kChunk) {
+      const uint32_t at = fresh(offset + row0 * stride);
+#pragma unroll
+      for (int i = 0; i < N; ++i) r[i] = one<kSame>(base, at + i * stride);
+    } else {
+      row0 = fresh(row0);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int row = row0 + i < valid ? row0 + i : valid - 1;
+        r[i] = one<kSame>(base, offset + row * stride);
+      }
+    }
+  }
+
+  template <bool kSame>
+  static __device__ __forceinline__ typename Pair<kF>::raw one(const char* base, uint32_t at) {
+    if constexpr (!kSame) {
+      return Pair<kF>::load(base + at);
+    } else if constexpr (elem_bytes<kF>() == 4) {
+      const float x = *(const float*)(base + at);
+      return typename Pair<kF>::raw{x, x};
+    } else {
+      const uint32_t x = *(const uint16_t*)(base + at);
+      return x | x << 16;
+    }
+  }
+
+  __device__ __forceinline__ void values(f32x2 (&x)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = Pair<kF>::value(r[i]);
+  }
+};
+
+// Zeros in the rows past the last.
+template <int N>
+__device__ __forceinline__ void mask_rows(f32x2 (&x)[N], int row0, int valid) {
+  if (valid == kChunk) return;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (row0 + i >= valid) x[i] = f32x2{0.0f, 0.0f};
 }
 
 // Sums of N values over kWidth lanes, each lane receiving the sum of value (lane index /
 // (kWidth / N)); exchanges halves while values are left, so N + log2(kWidth / N) - 1
-// exchanges instead of N log2(kWidth).
-template <int N, int kWidth>
-__device__ __forceinline__ double scatter_sum(double (&x)[N], int lane) {
-  int m = kWidth / 2;
+// exchanges instead of N log2(kWidth). The values travel as a vector: the compiler turns a
+// choice between two elements of an array into a choice of the index, which costs more than
+// all the rest.
+template <int N>
+struct Doubles {
+  typedef double type __attribute__((ext_vector_type(N)));
+};
+
+template <int N, int kMask>
+__device__ __forceinline__ double scatter_sum(typename Doubles<N>::type x, int lane) {
+  const bool upper = (lane & kMask) != 0;
+  if constexpr (N == 2) {
+    double s = (upper ? x[1] : x[0]) + __shfl_xor(upper ? x[0] : x[1], kMask);
 #pragma unroll
-  for (int n = N / 2; n > 0; n >>= 1, m >>= 1) {
-    const bool upper = (lane & m) != 0;
+    for (int m = kMask / 2; m > 0; m >>= 1) s += __shfl_xor(s, m);
+    return s;
+  } else {
+    typename Doubles<N / 2>::type y;
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const double keep = upper ? x[n + i] : x[i];
-      const double send = upper ? x[i] : x[n + i];
-      x[i] = keep + __shfl_xor(send, m);
+    for (int i = 0; i < N / 2; ++i) {
+      const double a = x[i], b = x[N / 2 + i];
+      y[i] = (upper ? b : a) + __shfl_xor(upper ? a : b, kMask);
     }
+    return scatter_sum<N / 2, kMask / 2>(y, lane);
   }
-  double s = x[0];
-  for (; m > 0; m >>= 1) s += __shfl_xor(s, m);
-  return s;
 }
 
 // ---------------------------------------------------------------------------- prepare
@@ -173,9 +245,16 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
   __shared__ __attribute__((aligned(16))) float mats[3 * kMat];
   __shared__ __attribute__((aligned(16))) float tot[kGroups][D];
   __shared__ __attribute__((aligned(16))) float across[D];
-  __shared__ __attribute__((aligned(16))) float fac[6][kChunk];  // the slot's rows
+  // The slot's rows: keys' factor times 16 (hi, lo), queries' times 16, n / 16, the outputs'
+  // factor / 16, and T's factor.
+  __shared__ __attribute__((aligned(16))) float fac[6][kChunk];
   __shared__ float beta[kChunk];
+  // Keys enter the products times a power of two (exact); the rest of their factor, and n,
+  // follow in FP64 (a key rounded to unit length would be off by 3e-8, see below).
+  __shared__ float krest[kChunk];
+  __shared__ double kfac[kChunk];
   __shared__ int steep;
+  float* const ktwo = fac[5];  // until the last step puts T's factor there
   float* const mq = mats;
   float* const mk = mats + kMat;
   float* const mc = mats + 2 * kMat;
@@ -192,29 +271,30 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
 
   const int group = threadIdx.x / kLanes, c = 2 * (threadIdx.x % kLanes), row0 = group * kRows;
   const int64_t qk = h / R.share;
-  const char* const qp = R.q + (first * R.q_ts + qk * R.q_hs + c) * kEB;
-  const char* const kp = R.k + (first * R.k_ts + qk * R.k_hs + c) * kEB;
-  const char* const gp = R.g + (first * R.g_ts + h * R.g_hs + c * R.g_cs) * kGB;
+  const char* const qp = R.q + (first * R.q_ts + qk * R.q_hs) * kEB;
+  const char* const kp = R.k + (first * R.k_ts + qk * R.k_hs) * kEB;
+  const char* const gp = R.g + (first * R.g_ts + h * R.g_hs) * kGB;
 
   f32x2 q[kRows], k[kRows], p[kRows];  // p: log2 decays, then their running sums
   const Gate gate(R, h);
   f32x2 bias = {0.0f, 0.0f};
   if (R.dt_bias != nullptr) bias = *(const f32x2a4*)(R.dt_bias + h * D + c);
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const bool in = row0 + i < valid;
-    const f32x2 a = Pair<kF>::value(load_row<kF>(qp, row0 + i, valid, (int)R.q_ts * kEB));
-    const f32x2 b = Pair<kF>::value(load_row<kF>(kp, row0 + i, valid, (int)R.k_ts * kEB));
-    f32x2 g;
-    if (R.g_cs != 0) {
-      g = Pair<kG>::value(load_row<kG>(gp, row0 + i, valid, (int)R.g_ts * kGB));
-    } else {
-      const int r = row0 + i < valid ? row0 + i : valid - 1;
-      g.x = g.y = load_elem<kG>(gp + r * R.g_ts * kGB);
-    }
-    q[i] = in ? a : f32x2{0.0f, 0.0f};
-    k[i] = in ? b : f32x2{0.0f, 0.0f};
-    p[i] = in ? f32x2{gate(g.x, bias.x), gate(g.y, bias.y)} : f32x2{0.0f, 0.0f};
+  {
+    RawRows<kF, kRows> rq, rk;
+    RawRows<kG, kRows> rg;
+    if (R.g_cs != 0)
+      rg.template load<false>(gp, c * kGB, row0, valid, (uint32_t)R.g_ts * kGB);
+    else
+      rg.template load<true>(gp, 0, row0, valid, (uint32_t)R.g_ts * kGB);
+    rk.template load<false>(kp, c * kEB, row0, valid, (uint32_t)R.k_ts * kEB);
+    rq.template load<false>(qp, c * kEB, row0, valid, (uint32_t)R.q_ts * kEB);
+    rg.values(p);
+    rk.values(k);
+    mask_rows(k, row0, valid);
+    rq.values(q);
+    mask_rows(q, row0, valid);
+    gate.eval(p, bias);
+    mask_rows(p, row0, valid);
   }
   if (threadIdx.x < kChunk)
     beta[threadIdx.x] = (int)threadIdx.x < valid ? beta_value(R, kF, first + threadIdx.x, h) : 0.0f;
@@ -222,14 +302,14 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
 
   // Lengths of the rows' queries and keys.
   {
-    double ss[2 * kRows];
+    typename Doubles<2 * kRows>::type ss;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const double qx = q[i].x, qy = q[i].y, kx = k[i].x, ky = k[i].y;
       ss[i] = __builtin_fma(qx, qx, qy * qy);
       ss[kRows + i] = __builtin_fma(kx, kx, ky * ky);
     }
-    const double s = scatter_sum<2 * kRows, kLanes>(ss, lane);
+    const double s = scatter_sum<2 * kRows, kLanes / 2>(ss, lane);
     constexpr int kShare = kLanes / (2 * kRows);  // lanes holding the same sum
     const int l = lane % kLanes, which = l / kShare, r = row0 + which % kRows;
     if (l % kShare == 0) {
@@ -237,12 +317,16 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
       const Factor f = inverse_root(norm ? s + (double)R.l2_eps : s);
       const float n = norm ? 1.0f : (float)(s * ((double)f.hi + (double)f.lo));
       if (which < kRows) {
-        fac[2][r] = f.hi;
-        fac[4][r] = n * R.scale;
+        fac[2][r] = kVec * f.hi;
+        fac[4][r] = n * R.scale * (1.0f / kVec);
       } else {
-        fac[0][r] = f.hi;
-        fac[1][r] = f.lo;
-        fac[3][r] = n;
+        fac[0][r] = kVec * f.hi;
+        fac[1][r] = kVec * f.lo;
+        fac[3][r] = n * (1.0f / kVec);
+        const int e = f.hi > 0.0f ? __builtin_amdgcn_frexp_expf(f.hi) : 0;
+        ktwo[r] = __builtin_amdgcn_ldexpf(1.0f, e);
+        krest[r] = __builtin_amdgcn_ldexpf(f.hi, -e);
+        kfac[r] = (double)n * __builtin_amdgcn_ldexp((double)f.hi + (double)f.lo, -e);
       }
     }
   }
@@ -282,9 +366,8 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
     const int r = row0 + i;
     const f32x2 d = p[i] + before - mid;
     const f32x2 e = {exp2_hw(d.x), exp2_hw(d.y)}, m = {exp2_hw(-d.x), exp2_hw(-d.y)};
-    const Factor f = {fac[0][r], fac[1][r]};
     const float fq = fac[2][r];
-    k[i] = f32x2{scaled(k[i].x, f), scaled(k[i].y, f)};
+    k[i] *= ktwo[r];
     *(f32x2*)&mq[r * kLd + c] = q[i] * fq * e;
     *(f32x2*)&mk[r * kLd + c] = k[i] * e;
     *(f32x2*)&mc[r * kLd + c] = k[i] * m;
@@ -334,17 +417,18 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
     // hold many resets, and FP32 sums of -150 each would lose the small decays between).
     __syncthreads();
     // The decays, from the sums: exact enough again, then summed in FP64 per channel.
+    {
+      RawRows<kG, kRows> rg;
+      if (R.g_cs != 0)
+        rg.template load<false>(gp, c * kGB, row0, valid, (uint32_t)R.g_ts * kGB);
+      else
+        rg.template load<true>(gp, 0, row0, valid, (uint32_t)R.g_ts * kGB);
+      f32x2 g[kRows];
+      rg.values(g);
+      gate.eval(g, bias);
+      mask_rows(g, row0, valid);
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int r = row0 + i;
-      f32x2 g;
-      if (R.g_cs != 0) {
-        g = Pair<kG>::value(load_row<kG>(gp, r, valid, (int)R.g_ts * kGB));
-      } else {
-        g.x = g.y = load_elem<kG>(gp + (r < valid ? r : valid - 1) * R.g_ts * kGB);
-      }
-      *(f32x2*)&mk[r * kLd + c] =
-          r < valid ? f32x2{gate(g.x, bias.x), gate(g.y, bias.y)} : f32x2{0.0f, 0.0f};
+      for (int i = 0; i < kRows; ++i) *(f32x2*)&mk[(row0 + i) * kLd + c] = g[i];
     }
     __syncthreads();
     double* const sums = (double*)mc;  // rows of D doubles over mc and mq's place
@@ -396,16 +480,16 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
                 2 * kChunk * kSq * sizeof(double) + 4096 <= sizeof(float) * 3 * kMat, "they fit");
   char* const slot = P.slots + ((int64_t)program * R.heads + h) * kSlotBytes;
   const auto put_a = [&](int t, int i, float a) {
-    // A times 256 in operand order: row tile, lane, place.
+    // A times 256 in operand order: row tile, lane, place. (a carries the query's 16.)
     const int at = (t / 16 * 64 + (place(i) / 8) * 16 + t % 16) * 8 + place(i) % 8;
-    const float x = 256.0f * a;
+    const float x = 16.0f * krest[i] * a;
     const _Float16 hi = (_Float16)x;
     sa[at] = hi;
     sa[1024 + at] = (_Float16)(x - (float)hi);
   };
   const auto put_l = [&](int t, int i, double a) {
     ml[t * kSq + i] =
-        i < t ? (double)beta[t] * ((double)fac[3][t] * (double)fac[3][i]) * a : 0.0;
+        i < t ? (double)beta[t] * (kfac[t] * kfac[i]) * a : 0.0;
   };
   if (!direct) {
     if (wave < 3) {
@@ -479,9 +563,9 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = 4 * n4 + r;
-      t00[r] = (double)fac[3][t] * mt[t * kSq + n16] * (double)beta[n16];
-      t11[r] = (double)fac[3][16 + t] * mt[(16 + t) * kSq + 16 + n16] * (double)beta[16 + n16];
-      t10[r] = -(double)fac[3][16 + t] * y[r] * (double)beta[n16];
+      t00[r] = (double)(kVec * fac[3][t]) * mt[t * kSq + n16] * (double)beta[n16];
+      t11[r] = (double)(kVec * fac[3][16 + t]) * mt[(16 + t) * kSq + 16 + n16] * (double)beta[16 + n16];
+      t10[r] = -(double)(kVec * fac[3][16 + t]) * y[r] * (double)beta[n16];
       top = __builtin_fmaxf(
           top, __builtin_fmaxf(__builtin_fabsf((float)t10[r]),
                                __builtin_fmaxf(__builtin_fabsf((float)t00[r]), __builtin_fabsf((float)t11[r]))));
@@ -578,7 +662,7 @@ struct ScanState {
 #pragma unroll
     for (int i = 0; i < kM; ++i) s[i][n] *= f;
     scale[n] *= f;
-    inverse[n] *= 1.0f / f;
+    inverse[n] *= rcp_hw(f);  // exact for powers of two
   }
 };
 
@@ -595,6 +679,8 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
   __shared__ __attribute__((aligned(16))) _Float16 kt[2][D * kLt];
   __shared__ __attribute__((aligned(16))) float tot[kGroups][D];
   __shared__ __attribute__((aligned(16))) float decay[D];
+  // The chunk's slot, and the next one's on its way.
+  __shared__ __attribute__((aligned(16))) char held[2][kSlotUsed];
   __shared__ float part[4];
 
   const RuleParams& R = P.R;
@@ -618,6 +704,7 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
   const int64_t cell = (int64_t)program * R.heads + h;
 
   ScanState<kM, kN> S;
+  float most[kN];  // the largest magnitude among the lane's values of each column
   {
     const float* from = nullptr;
     if (begin == 0) {
@@ -625,23 +712,34 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
     } else if (kOut) {
       from = P.ends + (cell - R.heads) * (D * D);
     }
+    if (from != nullptr) {
 #pragma unroll
-    for (int m = 0; m < kM; ++m)
+      for (int m = 0; m < kM; ++m)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * m + 4 * n4 + r;
-#pragma unroll
-        for (int n = 0; n < kN; ++n) {
-          float x = 0.0f;
-          if (from != nullptr) x = from[row * D + col + n];
-          if (identity) x = row == col + n ? 1.0f : 0.0f;
-          S.s[m][n][r] = x;
+        for (int r = 0; r < 4; ++r) {
+          const float* const at = from + (16 * m + 4 * n4 + r) * D + col;
+          if constexpr (kN == 2) {
+            const f32x2 x = *(const f32x2a4*)at;
+            S.s[m][0][r] = x.x;
+            S.s[m][kN - 1][r] = x.y;
+          } else {
+            S.s[m][0][r] = *at;
+          }
         }
-      }
+    } else {
+#pragma unroll
+      for (int m = 0; m < kM; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int n = 0; n < kN; ++n)
+            S.s[m][n][r] = identity && 16 * m + 4 * n4 + r == col + n ? 1.0f : 0.0f;
+    }
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
       S.scale[n] = S.inverse[n] = 1.0f;
       S.apply(n, S.factor(column_max(S.largest(n))));
+      most[n] = S.largest(n);
     }
   }
 
@@ -654,36 +752,50 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
   // Where this lane's two channels go in operand rows.
   const int cpos = 32 * (c / 32) + place(c % 32);
 
+  // A chunk's rows and slot, loaded one chunk ahead; values, when the chunk begins.
+  RawRows<kF, kRows> rk, rq;
+  RawRows<kG, kRows> rg;
+  const char* const kbase = R.k + qk * R.k_hs * kEB;
+  const char* const qbase = R.q + qk * R.q_hs * kEB;
+  const char* const gbase = R.g + h * R.g_hs * kGB;
+  const char* const vbase = R.v + h * R.v_hs * kEB;
+  const auto load_chunk = [&](int chunk) {
+    const int64_t first = seq.start + chunk * kChunk;
+    const int valid = seq.len - chunk * kChunk < kChunk ? seq.len - chunk * kChunk : kChunk;
+    const char* const gp = gbase + first * R.g_ts * kGB;
+    if (R.g_cs != 0)
+      rg.template load<false>(gp, c * kGB, row0, valid, (uint32_t)R.g_ts * kGB);
+    else
+      rg.template load<true>(gp, 0, row0, valid, (uint32_t)R.g_ts * kGB);
+    rk.template load<false>(kbase + first * R.k_ts * kEB, c * kEB, row0, valid, (uint32_t)R.k_ts * kEB);
+    if (kOut)
+      rq.template load<false>(qbase + first * R.q_ts * kEB, c * kEB, row0, valid, (uint32_t)R.q_ts * kEB);
+    // The slot goes straight to LDS: 688 pieces of 16 bytes, T (384), A (256) and the row
+    // factors (48), 64 per wave and load.
+    const char* const slot = P.slots + ((int64_t)(slot0 + chunk) * R.heads + h) * kSlotBytes;
+    char* const into = held[chunk & 1];
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (i < 2 || threadIdx.x < 176) to_lds(slot + 4096 * i + 16 * threadIdx.x, into + 4096 * i + 1024 * wave);
+  };
+  load_chunk(begin);
+
   for (int chunk = begin; chunk < end; ++chunk) {
     const int first = seq.start + chunk * kChunk;
     const int valid = seq.len - chunk * kChunk < kChunk ? seq.len - chunk * kChunk : kChunk;
-    const char* const slot = P.slots + ((int64_t)(slot0 + chunk) * R.heads + h) * kSlotBytes;
+    const char* const slot = held[chunk & 1];
     const float* const fac = (const float*)(slot + kSlotRows);
 
     // ---- operands
     f32x2 q[kRows], k[kRows], p[kRows];
-    {
-      const char* const kp = R.k + (first * R.k_ts + qk * R.k_hs + c) * kEB;
-      const char* const qp = R.q + (first * R.q_ts + qk * R.q_hs + c) * kEB;
-      const char* const gp = R.g + (first * R.g_ts + h * R.g_hs + c * R.g_cs) * kGB;
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int r = row0 + i;
-        const bool in = r < valid;
-        const f32x2 b = Pair<kF>::value(load_row<kF>(kp, r, valid, (int)R.k_ts * kEB));
-        k[i] = in ? b : f32x2{0.0f, 0.0f};
-        if (kOut) {
-          const f32x2 a = Pair<kF>::value(load_row<kF>(qp, r, valid, (int)R.q_ts * kEB));
-          q[i] = in ? a : f32x2{0.0f, 0.0f};
-        }
-        f32x2 g;
-        if (R.g_cs != 0) {
-          g = Pair<kG>::value(load_row<kG>(gp, r, valid, (int)R.g_ts * kGB));
-        } else {
-          g.x = g.y = load_elem<kG>(gp + (in ? r : valid - 1) * R.g_ts * kGB);
-        }
-        p[i] = in ? f32x2{gate(g.x, bias.x), gate(g.y, bias.y)} : f32x2{0.0f, 0.0f};
-      }
+    rg.values(p);
+    gate.eval(p, bias);
+    mask_rows(p, row0, valid);
+    rk.values(k);
+    mask_rows(k, row0, valid);
+    if (kOut) {
+      rq.values(q);
+      mask_rows(q, row0, valid);
     }
     f32x2 rest[kRows];  // log2 decay after each row, inside the group
     rest[kRows - 1] = f32x2{0.0f, 0.0f};
@@ -692,8 +804,41 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
 #pragma unroll
     for (int i = 1; i < kRows; ++i) p[i] += p[i - 1];
     *(f32x2*)&tot[group][c] = p[kRows - 1];
-    // Also: every wave is done with the operands of the chunk before.
+    // The slot's loads to LDS are counted per wave: each waits for its own before the barrier
+    // that lets the others read. Also: every wave is done with the operands of the chunk
+    // before.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
+    typename Pair<kF>::raw rv[8];  // rows 16 t + 4 (lane / 16) + r, this lane's columns
+    {
+      const char* const vp = vbase + first * R.v_ts * kEB;
+      const uint32_t stride = (uint32_t)R.v_ts * kEB;
+      const auto load_value = [&](uint32_t at) {
+        if constexpr (kN == 2)
+          return Pair<kF>::load(vp + at);
+        else if constexpr (kEB == 4)
+          return typename Pair<kF>::raw{*(const float*)(vp + at), 0.0f};
+        else
+          return (uint32_t) * (const uint16_t*)(vp + at);
+      };
+      if (valid == kChunk) {
+        const uint32_t at = fresh(4 * n4 * stride + col * kEB);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rv[i] = load_value(at + (16 * (i / 4) + i % 4) * stride);
+      } else {
+        const int r4 = fresh(4 * n4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = 16 * (i / 4) + r4 + i % 4;
+          rv[i] = load_value((row < valid ? row : valid - 1) * stride + col * kEB);
+        }
+      }
+    }
+    if (identity || valid != kChunk) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (identity || 16 * (i / 4) + 4 * n4 + i % 4 >= valid) rv[i] = Pair<kF>::zero();
+    }
     f32x2 before = {0.0f, 0.0f}, after = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < kGroups; ++i) {
@@ -709,18 +854,18 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const int r = row0 + i;
-      const Factor f = {kVec * fac[r], kVec * fac[kChunk + r]};
+      const Factor f = {fac[r], fac[kChunk + r]};
       const f32x2 unit = {scaled(k[i].x, f), scaled(k[i].y, f)};
       const f32x2 up = p[i] + before, down = rest[i] + after;
       const f32x2 e = {exp2_hw(up.x), exp2_hw(up.y)};
-      const HalfPair g = split2(unit * e);
+      const HalfPair g = split2(unit * e, R.one);
       *(f16x2*)&kg[0][r * kLd + cpos] = g.hi;
       *(f16x2*)&kg[1][r * kLd + cpos] = g.lo;
-      const HalfPair t = split2(unit * f32x2{exp2_hw(down.x), exp2_hw(down.y)});
+      const HalfPair t = split2(unit * f32x2{exp2_hw(down.x), exp2_hw(down.y)}, R.one);
       th[i] = t.hi;
       tl[i] = t.lo;
       if (kOut) {
-        const HalfPair w = split2(q[i] * (kVec * fac[2 * kChunk + r]) * e);
+        const HalfPair w = split2(q[i] * fac[2 * kChunk + r] * e, R.one);
         *(f16x2*)&qg[0][r * kLd + cpos] = w.hi;
         *(f16x2*)&qg[1][r * kLd + cpos] = w.lo;
       }
@@ -734,6 +879,7 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
       *(f16x4*)&kt[1][(c + 1) * kLt + at] = f16x4{tl[i].y, tl[i + 1].y, tl[i + 2].y, tl[i + 3].y};
     }
     __syncthreads();
+    if (chunk + 1 < end) load_chunk(chunk + 1);
 
     // ---- Y = (K e^G) S and O = (Q e^G) S
     f32x4 Y[2][kN], O[2][kN];
@@ -741,58 +887,67 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int n = 0; n < kN; ++n) Y[t][n] = O[t][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int kk = 0; kk < kK; ++kk) {
-      Operand b[kN];
-#pragma unroll
-      for (int n = 0; n < kN; ++n) b[n] = split8(S.s[2 * kk][n], S.s[2 * kk + 1][n]);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int at = (16 * t + n16) * kLd + 32 * kk + 8 * n4;
-        const f16x8 ah = *(const f16x8*)&kg[0][at], al = *(const f16x8*)&kg[1][at];
-#pragma unroll
-        for (int n = 0; n < kN; ++n) {
-          Y[t][n] = mfma16(ah, b[n].hi, Y[t][n]);
-          Y[t][n] = mfma16(ah, b[n].lo, Y[t][n]);
-          Y[t][n] = mfma16(al, b[n].hi, Y[t][n]);
-        }
-        if (kOut) {
-          const f16x8 qh = *(const f16x8*)&qg[0][at], ql = *(const f16x8*)&qg[1][at];
-#pragma unroll
-          for (int n = 0; n < kN; ++n) {
-            O[t][n] = mfma16(qh, b[n].hi, O[t][n]);
-            O[t][n] = mfma16(qh, b[n].lo, O[t][n]);
-            O[t][n] = mfma16(ql, b[n].hi, O[t][n]);
-          }
-        }
+    // Steps of (32 channels, 16 rows): each one's left operands are read while the step
+    // before runs. The scheduling barriers keep the compiler from reading all of them first,
+    // which spills.
+    f16x8 kh, kl, qh, ql;
+    const auto read_step = [&](int step) {
+      const int at = (16 * (step & 1) + n16) * kLd + 32 * (step >> 1) + 8 * n4;
+      kh = *(const f16x8*)&kg[0][at];
+      kl = *(const f16x8*)&kg[1][at];
+      if (kOut) {
+        qh = *(const f16x8*)&qg[0][at];
+        ql = *(const f16x8*)&qg[1][at];
       }
+    };
+    read_step(0);
+    Operand b[kN];
+#pragma unroll
+    for (int step = 0; step < 2 * kK; ++step) {
+      const int t = step & 1;
+      const f16x8 ch = kh, cl = kl, dh = qh, dl = ql;
+      if (step + 1 < 2 * kK) read_step(step + 1);
+      if (t == 0) {
+#pragma unroll
+        for (int n = 0; n < kN; ++n) b[n] = split8(S.s[step][n], S.s[step + 1][n], R.one);
+      }
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        Y[t][n] = mfma16(ch, b[n].hi, Y[t][n]);
+        if (kOut) O[t][n] = mfma16(dh, b[n].hi, O[t][n]);
+      }
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        Y[t][n] = mfma16(ch, b[n].lo, Y[t][n]);
+        if (kOut) O[t][n] = mfma16(dh, b[n].lo, O[t][n]);
+      }
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        Y[t][n] = mfma16(cl, b[n].hi, Y[t][n]);
+        if (kOut) O[t][n] = mfma16(dl, b[n].hi, O[t][n]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
 
     // ---- X = V - n Y, in the columns' scales
-    const char* const vp = R.v + (first * R.v_ts + h * R.v_hs + col) * kEB;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < 2; ++t) {
+      const f32x4 nt = *(const f32x4*)(fac + 3 * kChunk + 16 * t + 4 * n4);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int row = 16 * t + 4 * n4 + r;
-        const float n_t = fac[3 * kChunk + row] * (1.0f / kVec);
-        f32x2 v = {0.0f, 0.0f};
-        if (!identity && row < valid) {
-          if (kN == 2)
-            v = Pair<kF>::value(Pair<kF>::load(vp + row * R.v_ts * kEB));
-          else
-            v.x = load_elem<kF>(vp + row * R.v_ts * kEB);
-        }
+        const float n_t = nt[r];
+        const f32x2 v = Pair<kF>::value(rv[4 * t + r]);
 #pragma unroll
         for (int n = 0; n < kN; ++n)
           Y[t][n][r] = __builtin_fmaf(v[n], S.scale[n], -n_t * Y[t][n][r]);
       }
+    }
     // The columns' range over S and X.
     float high[kN];
     bool left = false;
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
-      float m = S.largest(n);
+      float m = most[n];
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -817,20 +972,19 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
     f32x4 U[2][kN];
     {
       const f16x8* const tp = (const f16x8*)(slot + kSlotT);
-      Operand b[kN];
 #pragma unroll
-      for (int n = 0; n < kN; ++n) b[n] = split8(Y[0][n], Y[1][n]);
+      for (int n = 0; n < kN; ++n) b[n] = split8(Y[0][n], Y[1][n], R.one);
       const float us = fac[5 * kChunk];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const f16x8 ah = tp[64 * t + lane], al = tp[128 + 64 * t + lane], ar = tp[256 + 64 * t + lane];
+        const f16x8 th = tp[64 * t + lane], tl = tp[128 + 64 * t + lane], tr = tp[256 + 64 * t + lane];
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
           f32x4 u = {0.0f, 0.0f, 0.0f, 0.0f};
-          u = mfma16(ar, b[n].hi, u);
-          u = mfma16(ah, b[n].hi, u);
-          u = mfma16(ah, b[n].lo, u);
-          u = mfma16(al, b[n].hi, u);
+          u = mfma16(tr, b[n].hi, u);
+          u = mfma16(tl, b[n].hi, u);
+          u = mfma16(th, b[n].lo, u);
+          u = mfma16(th, b[n].hi, u);
           U[t][n] = u * us;
         }
       }
@@ -864,26 +1018,37 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
     // ---- S <- e^G_end S + K^T U; O += A U
     Operand u[kN];
 #pragma unroll
-    for (int n = 0; n < kN; ++n) u[n] = split8(U[0][n], U[1][n]);
+    for (int n = 0; n < kN; ++n) u[n] = split8(U[0][n], U[1][n], R.one);
+    f16x8 ah, al;
+    f32x4 d;
+    const auto read_tile = [&](int m) {
+      d = *(const f32x4*)&decay[16 * m + 4 * n4];
+      const int at = (16 * m + n16) * kLt + 8 * n4;
+      ah = *(const f16x8*)&kt[0][at];
+      al = *(const f16x8*)&kt[1][at];
+    };
+    read_tile(0);
 #pragma unroll
     for (int m = 0; m < kM; ++m) {
-      const f32x4 d = *(const f32x4*)&decay[16 * m + 4 * n4];
-      const int at = (16 * m + n16) * kLt + 8 * n4;
-      const f16x8 ah = *(const f16x8*)&kt[0][at], al = *(const f16x8*)&kt[1][at];
+      const f16x8 ch = ah, cl = al;
+      const f32x4 e = d;
+      if (m + 1 < kM) read_tile(m + 1);
 #pragma unroll
-      for (int n = 0; n < kN; ++n) {
-        f32x4 s = S.s[m][n] * d;
-        s = mfma16(ah, u[n].hi, s);
-        s = mfma16(ah, u[n].lo, s);
-        S.s[m][n] = mfma16(al, u[n].hi, s);
-      }
+      for (int n = 0; n < kN; ++n) S.s[m][n] = mfma16(ch, u[n].hi, S.s[m][n] * e);
+#pragma unroll
+      for (int n = 0; n < kN; ++n) S.s[m][n] = mfma16(ch, u[n].lo, S.s[m][n]);
+#pragma unroll
+      for (int n = 0; n < kN; ++n) S.s[m][n] = mfma16(cl, u[n].hi, S.s[m][n]);
+      if (m & 1) __builtin_amdgcn_sched_barrier(0);
     }
     if (kOut) {
+      char* const op = R.out + (first * (int64_t)R.heads + h) * (D * kEB);
+      const uint32_t ostride = (uint32_t)R.heads * (D * kEB), at = fresh(4 * n4 * ostride + col * kEB);
       const f16x8* const ap = (const f16x8*)(slot + kSlotA);
-      char* const op = R.out + ((first * (int64_t)R.heads + h) * D + col) * kEB;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const f16x8 ah = ap[64 * t + lane], al = ap[128 + 64 * t + lane];
+        const f32x4 nq = *(const f32x4*)(fac + 4 * kChunk + 16 * t + 4 * n4);
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
           O[t][n] = mfma16(ah, u[n].hi, O[t][n]);
@@ -892,29 +1057,41 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int row = 16 * t + 4 * n4 + r;
-          if (row < valid) {
-            const float f = fac[4 * kChunk + row] * (1.0f / kVec);
-            char* const o = op + row * (int64_t)R.heads * (D * kEB);
-            if (kN == 2)
-              Pair<kF>::store(o, f32x2{O[t][0][r] * f * S.inverse[0],
-                                       O[t][kN - 1][r] * f * S.inverse[kN - 1]});
-            else
-              store_elem<kF>(o, O[t][0][r] * f * S.inverse[0]);
-          }
+          const float f = nq[r];
+#pragma unroll
+          for (int n = 0; n < kN; ++n) O[t][n][r] *= f * S.inverse[n];
         }
+      }
+      const auto store_row = [&](int t, int r) {
+        char* const o = op + (at + (16 * t + r) * ostride);
+        if constexpr (kN == 2)
+          Pair<kF>::store(o, f32x2{O[t][0][r], O[t][kN - 1][r]});
+        else
+          store_elem<kF>(o, O[t][0][r]);
+      };
+      if (valid == kChunk) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) store_row(i / 4, i % 4);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (16 * (i / 4) + 4 * n4 + i % 4 < valid) store_row(i / 4, i % 4);
       }
     }
     // The columns' range for the next chunk.
     left = false;
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
-      high[n] = S.largest(n);
-      left |= S.left(high[n]);
+      most[n] = S.largest(n);
+      left |= S.left(most[n]);
     }
     if (left) {
 #pragma unroll
-      for (int n = 0; n < kN; ++n) S.apply(n, S.factor(column_max(high[n])));
+      for (int n = 0; n < kN; ++n) {
+        const float f = S.factor(column_max(most[n]));
+        S.apply(n, f);
+        most[n] *= f;
+      }
     }
   }
 
@@ -1041,7 +1218,7 @@ __global__ __launch_bounds__(256) void delta_rule_join_kernel(const ChunkParams 
       f32x4 x;
 #pragma unroll
       for (int r = 0; r < 4; ++r) x[r] = __builtin_amdgcn_ldexpf(S[t][r], e);
-      const HalfPair p0 = split2(f32x2{x[0], x[1]}), p1 = split2(f32x2{x[2], x[3]});
+      const HalfPair p0 = split2(f32x2{x[0], x[1]}, R.one), p1 = split2(f32x2{x[2], x[3]}, R.one);
       const int at = lane * 8 + 4 * (tile & 1);
       *(f16x4*)&hi[buf][tile / 2][at] = f16x4{p0.hi.x, p0.hi.y, p1.hi.x, p1.hi.y};
       *(f16x4*)&lo[buf][tile / 2][at] = f16x4{p0.lo.x, p0.lo.y, p1.lo.x, p1.lo.y};

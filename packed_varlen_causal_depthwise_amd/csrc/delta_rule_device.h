@@ -110,24 +110,45 @@ __device__ __forceinline__ float softplus_f(float x) {
 // The gate of one head: log2 of the decay of a channel.
 struct Gate {
   int mode;
-  float a;  // log2e * exp(a_log), or exp(a_log) for the bounded gate
+  float a;  // -log2e * exp(a_log), or for the bounded gate log2e * exp(a_log)
   float lower;  // log2e * lower_bound
 
-  __device__ __forceinline__ Gate(const RuleParams& P, int h) : mode(P.gate), a(0.0f), lower(0.0f) {
-    if (mode != KDACONV_GATE_LOG) a = __builtin_expf(P.a_log[h]);
-    if (mode == KDACONV_GATE_SOFTPLUS) a *= -kLog2e;
+  __device__ __forceinline__ Gate(const RuleParams& P, int h) : mode(P.gate), a(0.0f) {
+    if (mode != KDACONV_GATE_LOG) a = kLog2e * __builtin_expf(P.a_log[h]);
+    if (mode == KDACONV_GATE_SOFTPLUS) a = -a;
     lower = kLog2e * P.lower_bound;
   }
 
-  __device__ __forceinline__ float operator()(float g, float bias) const {
+  template <int kGate>
+  __device__ __forceinline__ float eval(float g, float bias) const {
     float d;
-    if (mode == KDACONV_GATE_LOG)
+    if constexpr (kGate == KDACONV_GATE_LOG)
       d = kLog2e * g;
-    else if (mode == KDACONV_GATE_SOFTPLUS)
+    else if constexpr (kGate == KDACONV_GATE_SOFTPLUS)
       d = a * softplus_f(g + bias);
     else
-      d = lower * sigmoid_f(a * (g + bias));
+      d = lower * rcp_hw(1.0f + exp2_hw(-a * (g + bias)));
     return d < kLog2e * kMinLogDecay ? kLog2e * kMinLogDecay : d;  // a NaN stays one
+  }
+
+  // N pairs at once: one (uniform) branch on the kind of gate.
+  template <int N>
+  __device__ __forceinline__ void eval(f32x2 (&g)[N], f32x2 bias) const {
+    if (mode == KDACONV_GATE_LOG) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        g[i] = f32x2{eval<KDACONV_GATE_LOG>(g[i].x, 0.0f), eval<KDACONV_GATE_LOG>(g[i].y, 0.0f)};
+    } else if (mode == KDACONV_GATE_SOFTPLUS) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        g[i] = f32x2{eval<KDACONV_GATE_SOFTPLUS>(g[i].x, bias.x),
+                     eval<KDACONV_GATE_SOFTPLUS>(g[i].y, bias.y)};
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        g[i] = f32x2{eval<KDACONV_GATE_BOUNDED>(g[i].x, bias.x),
+                     eval<KDACONV_GATE_BOUNDED>(g[i].y, bias.y)};
+    }
   }
 };
 

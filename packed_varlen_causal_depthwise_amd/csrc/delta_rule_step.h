@@ -72,7 +72,9 @@ __global__ __launch_bounds__(2 * D) void delta_rule_step_kernel(const RuleParams
       if (lane < D / 2) {
         *(f32x2*)&sk[buf][wave][c] = f32x2{scaled(kk.x, rk), scaled(kk.y, rk)};
         *(f32x2*)&sq[buf][wave][c] = f32x2{qq.x * rq, qq.y * rq};
-        *(f32x2*)&sd[buf][wave][c] = f32x2{exp2_hw(gate(gg.x, bias.x)), exp2_hw(gate(gg.y, bias.y))};
+        f32x2 d[1] = {gg};
+        gate.eval(d, bias);
+        *(f32x2*)&sd[buf][wave][c] = f32x2{exp2_hw(d[0].x), exp2_hw(d[0].y)};
       }
       if (lane == 0) sb[buf][wave] = beta_value(P, kF, t, h);
     }
