@@ -129,66 +129,119 @@ __device__ __forceinline__ Piece find_piece(const ChunkParams& P, int p, int shi
   return Piece{base, p - uniform(v)};
 }
 
-// How a workgroup of 4 waves holds a chunk's rows for elementwise work: groups of kRows
-// neighbouring rows, kLanes lanes per group, two channels per lane.
-template <int D>
+// How a workgroup holds a chunk's rows for elementwise work: groups of kRows neighbouring
+// rows, kLanes lanes per group, two channels per lane.
+template <int D, int kWaves>
 struct Rows {
   static constexpr int kLanes = D / 2;
-  static constexpr int kGroups = 4 * 64 / kLanes;  // 4 or 8
-  static constexpr int kRows = kChunk / kGroups;  // 8 or 4
+  static constexpr int kGroups = kWaves * 64 / kLanes;
+  static constexpr int kRows = kChunk / kGroups;
+
+  // The lane's group; the same for the whole wave (and known to be) where a group is a wave.
+  static __device__ __forceinline__ int group(int wave, int lane) {
+    return kLanes == kRuleWave ? wave : wave * (kRuleWave / kLanes) + lane / kLanes;
+  }
+
+  // The wave's first row, and the lane's after it.
+  static __device__ __forceinline__ int wave_row(int wave) { return wave * (kRuleWave / kLanes) * kRows; }
+  static __device__ __forceinline__ int lane_row(int lane) {
+    return kLanes == kRuleWave ? 0 : lane / kLanes * kRows;
+  }
 };
 
 // Hides that x is the same in every iteration of a loop. Without it the compiler computes
-// each row's offset once, before the loop, and keeps all of them in registers (40 of 256,
-// which spilled) to save an addition each.
+// each row's offset once, before the loop, and keeps all of them in registers, which
+// spilled.
 __device__ __forceinline__ uint32_t fresh(uint32_t x) {
   asm volatile("" : "+v"(x));
   return x;
 }
 
-// A lane's pairs of N rows from row0 on, as loaded. base is the same for all lanes, so a
-// load takes it from scalar registers and a 32-bit offset: the stride of 32 rows stays
-// below 2^30 bytes. Rows past the last valid one are read as the last (and replaced by
-// zeros, see mask_rows). All loads of a chunk are issued together.
+// Rows of a chunk behind a buffer descriptor that ends with the last valid row: a load past
+// it brings zeros and a store past it does nothing, so rows need no branches, and lanes
+// need one 32-bit offset (32 rows stay below 2^30 bytes). Rows that share memory (a token
+// stride below a row) may still be read past the last: mask_rows.
+struct Window {
+  __amdgpu_buffer_rsrc_t r;
+  uint32_t stride;
+
+  __device__ __forceinline__ Window(const char* base, int valid, uint32_t stride, uint32_t row_bytes)
+      : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), (short)0,
+                                            (int)((valid - 1) * stride + row_bytes), 0x00020000)),
+        stride(stride) {}
+};
+
+template <int kF>
+struct Cell;  // loads and stores of one element or a pair
+
+template <>
+struct Cell<kRuleF32> {
+  static __device__ __forceinline__ f32x2 pair(const Window& w, uint32_t lane, uint32_t row) {
+    return __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(w.r, lane, row * w.stride, 0));
+  }
+  static __device__ __forceinline__ f32x2 one(const Window& w, uint32_t lane, uint32_t row) {
+    return f32x2{__builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(w.r, lane, row * w.stride, 0)), 0.0f};
+  }
+  static __device__ __forceinline__ void store_pair(const Window& w, uint32_t lane, uint32_t row, f32x2 v) {
+    typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2v, v), w.r, lane, row * w.stride, 0);
+  }
+  static __device__ __forceinline__ void store_one(const Window& w, uint32_t lane, uint32_t row, float v) {
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), w.r, lane, row * w.stride, 0);
+  }
+};
+
+template <int kF>
+struct Cell {
+  static __device__ __forceinline__ uint32_t pair(const Window& w, uint32_t lane, uint32_t row) {
+    return __builtin_amdgcn_raw_buffer_load_b32(w.r, lane, row * w.stride, 0);
+  }
+  static __device__ __forceinline__ uint32_t one(const Window& w, uint32_t lane, uint32_t row) {
+    return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(w.r, lane, row * w.stride, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack(f32x2 v) {
+    if constexpr (kF == kRuleBF16)
+      return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+    else
+      return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+  }
+  static __device__ __forceinline__ void store_pair(const Window& w, uint32_t lane, uint32_t row, f32x2 v) {
+    __builtin_amdgcn_raw_buffer_store_b32(pack(v), w.r, lane, row * w.stride, 0);
+  }
+  static __device__ __forceinline__ void store_one(const Window& w, uint32_t lane, uint32_t row, float v) {
+    __builtin_amdgcn_raw_buffer_store_b16((short)pack(f32x2{v, v}), w.r, lane, row * w.stride, 0);
+  }
+};
+
+// A lane's pairs of N rows, as loaded. row0 is the same for all lanes of the wave; `lane`
+// is the lane's offset: its channels, and its rows where a wave holds two groups of rows.
+// All loads of a chunk are issued together.
 template <int kF, int N>
 struct RawRows {
   typename Pair<kF>::raw r[N];
 
-  // offset: of the lane's channels in a row; stride: of rows, in bytes. kSame: one element
-  // per row, for both of the lane's channels (gates per head).
-  template <bool kSame>
-  __device__ __forceinline__ void load(const char* base, uint32_t offset, int row0, int valid,
-                                       uint32_t stride) {
-    if (valid == kChunk) {
-      const uint32_t at = fresh(offset + row0 * stride);
+  __device__ __forceinline__ void load(const Window& w, uint32_t lane, int row0) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) r[i] = one<kSame>(base, at + i * stride);
-    } else {
-      row0 = fresh(row0);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int row = row0 + i < valid ? row0 + i : valid - 1;
-        r[i] = one<kSame>(base, offset + row * stride);
-      }
-    }
+    for (int i = 0; i < N; ++i) r[i] = Cell<kF>::pair(w, lane, row0 + i);
   }
 
-  template <bool kSame>
-  static __device__ __forceinline__ typename Pair<kF>::raw one(const char* base, uint32_t at) {
-    if constexpr (!kSame) {
-      return Pair<kF>::load(base + at);
-    } else if constexpr (elem_bytes<kF>() == 4) {
-      const float x = *(const float*)(base + at);
-      return typename Pair<kF>::raw{x, x};
-    } else {
-      const uint32_t x = *(const uint16_t*)(base + at);
-      return x | x << 16;
-    }
+  // One element per row, for both of the lane's channels (gates per head).
+  __device__ __forceinline__ void load_same(const Window& w, uint32_t lane, int row0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = Cell<kF>::one(w, lane, row0 + i);
   }
 
   __device__ __forceinline__ void values(f32x2 (&x)[N]) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = Pair<kF>::value(r[i]);
+  }
+
+  __device__ __forceinline__ void values(f32x2 (&x)[N], bool same) const {
+    values(x);
+    if (same) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i].y = x[i].x;
+    }
   }
 };
 
@@ -234,7 +287,7 @@ __device__ __forceinline__ double scatter_sum(typename Doubles<N>::type x, int l
 
 template <int kF, int kG, int D>
 __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkParams P) {
-  typedef Rows<D> RW;
+  typedef Rows<D, 4> RW;
   constexpr int kRows = RW::kRows, kLanes = RW::kLanes, kGroups = RW::kGroups;
   constexpr int kEB = elem_bytes<kF>(), kGB = elem_bytes<kG>();
   constexpr int kLd = D + 4;  // floats per operand row: 16 rows reach all banks
@@ -269,11 +322,19 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
   const int first = seq.start + piece.index * kChunk;
   const int valid = seq.len - piece.index * kChunk < kChunk ? seq.len - piece.index * kChunk : kChunk;
 
-  const int group = threadIdx.x / kLanes, c = 2 * (threadIdx.x % kLanes), row0 = group * kRows;
+  const int group = RW::group(wave, lane), c = 2 * (lane % kLanes), row0 = group * kRows;
   const int64_t qk = h / R.share;
-  const char* const qp = R.q + (first * R.q_ts + qk * R.q_hs) * kEB;
-  const char* const kp = R.k + (first * R.k_ts + qk * R.k_hs) * kEB;
-  const char* const gp = R.g + (first * R.g_ts + h * R.g_hs) * kGB;
+  const Window wq(R.q + (first * R.q_ts + qk * R.q_hs) * kEB, valid, (uint32_t)R.q_ts * kEB, D * kEB);
+  const Window wk(R.k + (first * R.k_ts + qk * R.k_hs) * kEB, valid, (uint32_t)R.k_ts * kEB, D * kEB);
+  const Window wg(R.g + (first * R.g_ts + h * R.g_hs) * kGB, valid, (uint32_t)R.g_ts * kGB,
+                  (R.g_cs != 0 ? D : 1) * kGB);
+  const int wrow = RW::wave_row(wave), lrow = RW::lane_row(lane);
+  const auto load_gates = [&](RawRows<kG, kRows>& rg) {
+    if (R.g_cs != 0)
+      rg.load(wg, lrow * wg.stride + c * kGB, wrow);
+    else
+      rg.load_same(wg, lrow * wg.stride, wrow);
+  };
 
   f32x2 q[kRows], k[kRows], p[kRows];  // p: log2 decays, then their running sums
   const Gate gate(R, h);
@@ -282,13 +343,10 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
   {
     RawRows<kF, kRows> rq, rk;
     RawRows<kG, kRows> rg;
-    if (R.g_cs != 0)
-      rg.template load<false>(gp, c * kGB, row0, valid, (uint32_t)R.g_ts * kGB);
-    else
-      rg.template load<true>(gp, 0, row0, valid, (uint32_t)R.g_ts * kGB);
-    rk.template load<false>(kp, c * kEB, row0, valid, (uint32_t)R.k_ts * kEB);
-    rq.template load<false>(qp, c * kEB, row0, valid, (uint32_t)R.q_ts * kEB);
-    rg.values(p);
+    load_gates(rg);
+    rk.load(wk, lrow * wk.stride + c * kEB, wrow);
+    rq.load(wq, lrow * wq.stride + c * kEB, wrow);
+    rg.values(p, R.g_cs == 0);
     rk.values(k);
     mask_rows(k, row0, valid);
     rq.values(q);
@@ -419,12 +477,9 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
     // The decays, from the sums: exact enough again, then summed in FP64 per channel.
     {
       RawRows<kG, kRows> rg;
-      if (R.g_cs != 0)
-        rg.template load<false>(gp, c * kGB, row0, valid, (uint32_t)R.g_ts * kGB);
-      else
-        rg.template load<true>(gp, 0, row0, valid, (uint32_t)R.g_ts * kGB);
+      load_gates(rg);
       f32x2 g[kRows];
-      rg.values(g);
+      rg.values(g, R.g_cs == 0);
       gate.eval(g, bias);
       mask_rows(g, row0, valid);
 #pragma unroll
@@ -668,7 +723,8 @@ struct ScanState {
 
 template <int kF, int kG, int D, int kMode>
 __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkParams P) {
-  typedef Rows<D> RW;
+  constexpr int kWaves = 4, kThreads = 64 * kWaves;
+  typedef Rows<D, kWaves> RW;
   constexpr int kRows = RW::kRows, kLanes = RW::kLanes, kGroups = RW::kGroups;
   constexpr int kEB = elem_bytes<kF>(), kGB = elem_bytes<kG>();
   constexpr int kM = D / 16, kN = D / 64, kK = D / 32;
@@ -681,7 +737,7 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
   __shared__ __attribute__((aligned(16))) float decay[D];
   // The chunk's slot, and the next one's on its way.
   __shared__ __attribute__((aligned(16))) char held[2][kSlotUsed];
-  __shared__ float part[4];
+  __shared__ float part[kWaves];
 
   const RuleParams& R = P.R;
   int id = blockIdx.x;
@@ -743,7 +799,7 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
     }
   }
 
-  const int group = threadIdx.x / kLanes, c = 2 * (threadIdx.x % kLanes), row0 = group * kRows;
+  const int group = RW::group(wave, lane), c = 2 * (lane % kLanes), row0 = group * kRows;
   const int64_t qk = h / R.share;
   const Gate gate(R, h);
   f32x2 bias = {0.0f, 0.0f};
@@ -755,40 +811,42 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
   // A chunk's rows and slot, loaded one chunk ahead; values, when the chunk begins.
   RawRows<kF, kRows> rk, rq;
   RawRows<kG, kRows> rg;
-  const char* const kbase = R.k + qk * R.k_hs * kEB;
-  const char* const qbase = R.q + qk * R.q_hs * kEB;
-  const char* const gbase = R.g + h * R.g_hs * kGB;
-  const char* const vbase = R.v + h * R.v_hs * kEB;
+  const int wrow = RW::wave_row(wave), lrow = RW::lane_row(lane);
   const auto load_chunk = [&](int chunk) {
     const int64_t first = seq.start + chunk * kChunk;
     const int valid = seq.len - chunk * kChunk < kChunk ? seq.len - chunk * kChunk : kChunk;
-    const char* const gp = gbase + first * R.g_ts * kGB;
+    const Window wg(R.g + (first * R.g_ts + h * R.g_hs) * kGB, valid, (uint32_t)R.g_ts * kGB,
+                    (R.g_cs != 0 ? D : 1) * kGB);
     if (R.g_cs != 0)
-      rg.template load<false>(gp, c * kGB, row0, valid, (uint32_t)R.g_ts * kGB);
+      rg.load(wg, lrow * wg.stride + c * kGB, wrow);
     else
-      rg.template load<true>(gp, 0, row0, valid, (uint32_t)R.g_ts * kGB);
-    rk.template load<false>(kbase + first * R.k_ts * kEB, c * kEB, row0, valid, (uint32_t)R.k_ts * kEB);
-    if (kOut)
-      rq.template load<false>(qbase + first * R.q_ts * kEB, c * kEB, row0, valid, (uint32_t)R.q_ts * kEB);
+      rg.load_same(wg, lrow * wg.stride, wrow);
+    const Window wk(R.k + (first * R.k_ts + qk * R.k_hs) * kEB, valid, (uint32_t)R.k_ts * kEB, D * kEB);
+    rk.load(wk, lrow * wk.stride + c * kEB, wrow);
+    if (kOut) {
+      const Window wq(R.q + (first * R.q_ts + qk * R.q_hs) * kEB, valid, (uint32_t)R.q_ts * kEB, D * kEB);
+      rq.load(wq, lrow * wq.stride + c * kEB, wrow);
+    }
     // The slot goes straight to LDS: 688 pieces of 16 bytes, T (384), A (256) and the row
     // factors (48), 64 per wave and load.
     const char* const slot = P.slots + ((int64_t)(slot0 + chunk) * R.heads + h) * kSlotBytes;
     char* const into = held[chunk & 1];
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if (i < 2 || threadIdx.x < 176) to_lds(slot + 4096 * i + 16 * threadIdx.x, into + 4096 * i + 1024 * wave);
+    for (int i = 0; i < kSlotUsed / 16; i += kThreads)
+      if (i + kThreads <= kSlotUsed / 16 || threadIdx.x < kSlotUsed / 16 - i)
+        to_lds(slot + 16 * (i + threadIdx.x), into + 16 * (i + 64 * wave));
   };
   load_chunk(begin);
 
   for (int chunk = begin; chunk < end; ++chunk) {
-    const int first = seq.start + chunk * kChunk;
+    const int64_t first = seq.start + chunk * kChunk;
     const int valid = seq.len - chunk * kChunk < kChunk ? seq.len - chunk * kChunk : kChunk;
     const char* const slot = held[chunk & 1];
     const float* const fac = (const float*)(slot + kSlotRows);
 
     // ---- operands
     f32x2 q[kRows], k[kRows], p[kRows];
-    rg.values(p);
+    rg.values(p, R.g_cs == 0);
     gate.eval(p, bias);
     mask_rows(p, row0, valid);
     rk.values(k);
@@ -811,27 +869,12 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
     __syncthreads();
     typename Pair<kF>::raw rv[8];  // rows 16 t + 4 (lane / 16) + r, this lane's columns
     {
-      const char* const vp = vbase + first * R.v_ts * kEB;
-      const uint32_t stride = (uint32_t)R.v_ts * kEB;
-      const auto load_value = [&](uint32_t at) {
-        if constexpr (kN == 2)
-          return Pair<kF>::load(vp + at);
-        else if constexpr (kEB == 4)
-          return typename Pair<kF>::raw{*(const float*)(vp + at), 0.0f};
-        else
-          return (uint32_t) * (const uint16_t*)(vp + at);
-      };
-      if (valid == kChunk) {
-        const uint32_t at = fresh(4 * n4 * stride + col * kEB);
+      const Window wv(R.v + (first * R.v_ts + h * R.v_hs) * kEB, valid, (uint32_t)R.v_ts * kEB, D * kEB);
+      const uint32_t at = fresh(n4) * (4 * wv.stride) + col * kEB;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) rv[i] = load_value(at + (16 * (i / 4) + i % 4) * stride);
-      } else {
-        const int r4 = fresh(4 * n4);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int row = 16 * (i / 4) + r4 + i % 4;
-          rv[i] = load_value((row < valid ? row : valid - 1) * stride + col * kEB);
-        }
+      for (int i = 0; i < 8; ++i) {
+        const int row = 16 * (i / 4) + i % 4;
+        rv[i] = kN == 2 ? Cell<kF>::pair(wv, at, row) : Cell<kF>::one(wv, at, row);
       }
     }
     if (identity || valid != kChunk) {
@@ -851,32 +894,32 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
       *(f32x2*)&decay[c] = f32x2{exp2_hw(d.x), exp2_hw(d.y)};
     }
     f16x2 th[kRows], tl[kRows];
+    const int cw = fresh(cpos), tw = fresh(c * kLt);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const int r = row0 + i;
-      const Factor f = {fac[r], fac[kChunk + r]};
-      const f32x2 unit = {scaled(k[i].x, f), scaled(k[i].y, f)};
+      const f32x2 unit = k[i] * fac[r];
       const f32x2 up = p[i] + before, down = rest[i] + after;
       const f32x2 e = {exp2_hw(up.x), exp2_hw(up.y)};
       const HalfPair g = split2(unit * e, R.one);
-      *(f16x2*)&kg[0][r * kLd + cpos] = g.hi;
-      *(f16x2*)&kg[1][r * kLd + cpos] = g.lo;
+      *(f16x2*)&kg[0][r * kLd + cw] = g.hi;
+      *(f16x2*)&kg[1][r * kLd + cw] = g.lo;
       const HalfPair t = split2(unit * f32x2{exp2_hw(down.x), exp2_hw(down.y)}, R.one);
       th[i] = t.hi;
       tl[i] = t.lo;
       if (kOut) {
         const HalfPair w = split2(q[i] * fac[2 * kChunk + r] * e, R.one);
-        *(f16x2*)&qg[0][r * kLd + cpos] = w.hi;
-        *(f16x2*)&qg[1][r * kLd + cpos] = w.lo;
+        *(f16x2*)&qg[0][r * kLd + cw] = w.hi;
+        *(f16x2*)&qg[1][r * kLd + cw] = w.lo;
       }
     }
 #pragma unroll
     for (int i = 0; i < kRows; i += 4) {
       const int at = place(row0 + i);  // 4 rows in a row of the transposed operand
-      *(f16x4*)&kt[0][c * kLt + at] = f16x4{th[i].x, th[i + 1].x, th[i + 2].x, th[i + 3].x};
-      *(f16x4*)&kt[0][(c + 1) * kLt + at] = f16x4{th[i].y, th[i + 1].y, th[i + 2].y, th[i + 3].y};
-      *(f16x4*)&kt[1][c * kLt + at] = f16x4{tl[i].x, tl[i + 1].x, tl[i + 2].x, tl[i + 3].x};
-      *(f16x4*)&kt[1][(c + 1) * kLt + at] = f16x4{tl[i].y, tl[i + 1].y, tl[i + 2].y, tl[i + 3].y};
+      *(f16x4*)&kt[0][tw + at] = f16x4{th[i].x, th[i + 1].x, th[i + 2].x, th[i + 3].x};
+      *(f16x4*)&kt[0][tw + kLt + at] = f16x4{th[i].y, th[i + 1].y, th[i + 2].y, th[i + 3].y};
+      *(f16x4*)&kt[1][tw + at] = f16x4{tl[i].x, tl[i + 1].x, tl[i + 2].x, tl[i + 3].x};
+      *(f16x4*)&kt[1][tw + kLt + at] = f16x4{tl[i].y, tl[i + 1].y, tl[i + 2].y, tl[i + 3].y};
     }
     __syncthreads();
     if (chunk + 1 < end) load_chunk(chunk + 1);
@@ -887,44 +930,36 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int n = 0; n < kN; ++n) Y[t][n] = O[t][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    // Steps of (32 channels, 16 rows): each one's left operands are read while the step
-    // before runs. The scheduling barriers keep the compiler from reading all of them first,
-    // which spills.
-    f16x8 kh, kl, qh, ql;
-    const auto read_step = [&](int step) {
-      const int at = (16 * (step & 1) + n16) * kLd + 32 * (step >> 1) + 8 * n4;
-      kh = *(const f16x8*)&kg[0][at];
-      kl = *(const f16x8*)&kg[1][at];
+    // The scheduling barriers keep the compiler from reading the left operands of all steps
+    // first, which spills; four waves per SIMD cover the reads.
+    Operand b[kN];
+#pragma unroll
+    for (int step = 0; step < 2 * kK; ++step) {
+      const int t = step & 1, at = (16 * t + n16) * kLd + 32 * (step >> 1) + 8 * n4;
+      const f16x8 kh = *(const f16x8*)&kg[0][at], kl = *(const f16x8*)&kg[1][at];
+      f16x8 qh, ql;
       if (kOut) {
         qh = *(const f16x8*)&qg[0][at];
         ql = *(const f16x8*)&qg[1][at];
       }
-    };
-    read_step(0);
-    Operand b[kN];
-#pragma unroll
-    for (int step = 0; step < 2 * kK; ++step) {
-      const int t = step & 1;
-      const f16x8 ch = kh, cl = kl, dh = qh, dl = ql;
-      if (step + 1 < 2 * kK) read_step(step + 1);
       if (t == 0) {
 #pragma unroll
         for (int n = 0; n < kN; ++n) b[n] = split8(S.s[step][n], S.s[step + 1][n], R.one);
       }
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
-        Y[t][n] = mfma16(ch, b[n].hi, Y[t][n]);
-        if (kOut) O[t][n] = mfma16(dh, b[n].hi, O[t][n]);
+        Y[t][n] = mfma16(kh, b[n].hi, Y[t][n]);
+        if (kOut) O[t][n] = mfma16(qh, b[n].hi, O[t][n]);
       }
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
-        Y[t][n] = mfma16(ch, b[n].lo, Y[t][n]);
-        if (kOut) O[t][n] = mfma16(dh, b[n].lo, O[t][n]);
+        Y[t][n] = mfma16(kh, b[n].lo, Y[t][n]);
+        if (kOut) O[t][n] = mfma16(qh, b[n].lo, O[t][n]);
       }
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
-        Y[t][n] = mfma16(cl, b[n].hi, Y[t][n]);
-        if (kOut) O[t][n] = mfma16(dl, b[n].hi, O[t][n]);
+        Y[t][n] = mfma16(kl, b[n].hi, Y[t][n]);
+        if (kOut) O[t][n] = mfma16(ql, b[n].hi, O[t][n]);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -1019,31 +1054,22 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
     Operand u[kN];
 #pragma unroll
     for (int n = 0; n < kN; ++n) u[n] = split8(U[0][n], U[1][n], R.one);
-    f16x8 ah, al;
-    f32x4 d;
-    const auto read_tile = [&](int m) {
-      d = *(const f32x4*)&decay[16 * m + 4 * n4];
-      const int at = (16 * m + n16) * kLt + 8 * n4;
-      ah = *(const f16x8*)&kt[0][at];
-      al = *(const f16x8*)&kt[1][at];
-    };
-    read_tile(0);
 #pragma unroll
     for (int m = 0; m < kM; ++m) {
-      const f16x8 ch = ah, cl = al;
-      const f32x4 e = d;
-      if (m + 1 < kM) read_tile(m + 1);
+      const f32x4 d = *(const f32x4*)&decay[16 * m + 4 * n4];
+      const int at = (16 * m + n16) * kLt + 8 * n4;
+      const f16x8 ah = *(const f16x8*)&kt[0][at], al = *(const f16x8*)&kt[1][at];
 #pragma unroll
-      for (int n = 0; n < kN; ++n) S.s[m][n] = mfma16(ch, u[n].hi, S.s[m][n] * e);
+      for (int n = 0; n < kN; ++n) S.s[m][n] = mfma16(ah, u[n].hi, S.s[m][n] * d);
 #pragma unroll
-      for (int n = 0; n < kN; ++n) S.s[m][n] = mfma16(ch, u[n].lo, S.s[m][n]);
+      for (int n = 0; n < kN; ++n) S.s[m][n] = mfma16(ah, u[n].lo, S.s[m][n]);
 #pragma unroll
-      for (int n = 0; n < kN; ++n) S.s[m][n] = mfma16(cl, u[n].hi, S.s[m][n]);
+      for (int n = 0; n < kN; ++n) S.s[m][n] = mfma16(al, u[n].hi, S.s[m][n]);
       if (m & 1) __builtin_amdgcn_sched_barrier(0);
     }
     if (kOut) {
-      char* const op = R.out + (first * (int64_t)R.heads + h) * (D * kEB);
-      const uint32_t ostride = (uint32_t)R.heads * (D * kEB), at = fresh(4 * n4 * ostride + col * kEB);
+      const Window wo(R.out + (first * R.heads + h) * (D * kEB), valid, (uint32_t)R.heads * (D * kEB), D * kEB);
+      const uint32_t at = fresh(n4) * (4 * wo.stride) + col * kEB;
       const f16x8* const ap = (const f16x8*)(slot + kSlotA);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -1062,20 +1088,13 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
           for (int n = 0; n < kN; ++n) O[t][n][r] *= f * S.inverse[n];
         }
       }
-      const auto store_row = [&](int t, int r) {
-        char* const o = op + (at + (16 * t + r) * ostride);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int t = i / 4, r = i % 4, row = 16 * t + r;
         if constexpr (kN == 2)
-          Pair<kF>::store(o, f32x2{O[t][0][r], O[t][kN - 1][r]});
+          Cell<kF>::store_pair(wo, at, row, f32x2{O[t][0][r], O[t][kN - 1][r]});
         else
-          store_elem<kF>(o, O[t][0][r]);
-      };
-      if (valid == kChunk) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) store_row(i / 4, i % 4);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (16 * (i / 4) + 4 * n4 + i % 4 < valid) store_row(i / 4, i % 4);
+          Cell<kF>::store_one(wo, at, row, O[t][0][r]);
       }
     }
     // The columns' range for the next chunk.
@@ -1109,7 +1128,8 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
     for (int m = 32; m > 0; m >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, m));
     if (lane == 0) part[wave] = top;
     __syncthreads();
-    top = __builtin_fmaxf(__builtin_fmaxf(part[0], part[1]), __builtin_fmaxf(part[2], part[3]));
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = __builtin_fmaxf(top, part[w]);
     int e = 0;
     if (top > 0.0f && top < __builtin_huge_valf()) e = 9 - __builtin_amdgcn_frexp_expf(top);
     e = e > 100 ? 100 : e;

@@ -112,23 +112,26 @@ struct Gate {
   int mode;
   float a;  // -log2e * exp(a_log), or for the bounded gate log2e * exp(a_log)
   float lower;  // log2e * lower_bound
+  bool deep;  // the bounded gate may reach kMinLogDecay
 
   __device__ __forceinline__ Gate(const RuleParams& P, int h) : mode(P.gate), a(0.0f) {
     if (mode != KDACONV_GATE_LOG) a = kLog2e * __builtin_expf(P.a_log[h]);
     if (mode == KDACONV_GATE_SOFTPLUS) a = -a;
     lower = kLog2e * P.lower_bound;
+    deep = P.lower_bound < kMinLogDecay;
   }
 
-  template <int kGate>
-  __device__ __forceinline__ float eval(float g, float bias) const {
-    float d;
-    if constexpr (kGate == KDACONV_GATE_LOG)
-      d = kLog2e * g;
-    else if constexpr (kGate == KDACONV_GATE_SOFTPLUS)
-      d = a * softplus_f(g + bias);
-    else
-      d = lower * rcp_hw(1.0f + exp2_hw(-a * (g + bias)));
+  static __device__ __forceinline__ float clamp(float d) {
     return d < kLog2e * kMinLogDecay ? kLog2e * kMinLogDecay : d;  // a NaN stays one
+  }
+
+  __device__ __forceinline__ float soft(float g, float bias) const {
+    return clamp(a * softplus_f(g + bias));
+  }
+
+  // shift: -a * bias
+  __device__ __forceinline__ float bounded(float g, float shift) const {
+    return lower * rcp_hw(1.0f + exp2_hw(__builtin_fmaf(-a, g, shift)));
   }
 
   // N pairs at once: one (uniform) branch on the kind of gate.
@@ -136,18 +139,18 @@ struct Gate {
   __device__ __forceinline__ void eval(f32x2 (&g)[N], f32x2 bias) const {
     if (mode == KDACONV_GATE_LOG) {
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        g[i] = f32x2{eval<KDACONV_GATE_LOG>(g[i].x, 0.0f), eval<KDACONV_GATE_LOG>(g[i].y, 0.0f)};
+      for (int i = 0; i < N; ++i) g[i] = f32x2{clamp(kLog2e * g[i].x), clamp(kLog2e * g[i].y)};
     } else if (mode == KDACONV_GATE_SOFTPLUS) {
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        g[i] = f32x2{eval<KDACONV_GATE_SOFTPLUS>(g[i].x, bias.x),
-                     eval<KDACONV_GATE_SOFTPLUS>(g[i].y, bias.y)};
+      for (int i = 0; i < N; ++i) g[i] = f32x2{soft(g[i].x, bias.x), soft(g[i].y, bias.y)};
     } else {
+      const f32x2 shift = {-a * bias.x, -a * bias.y};
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        g[i] = f32x2{eval<KDACONV_GATE_BOUNDED>(g[i].x, bias.x),
-                     eval<KDACONV_GATE_BOUNDED>(g[i].y, bias.y)};
+      for (int i = 0; i < N; ++i) g[i] = f32x2{bounded(g[i].x, shift.x), bounded(g[i].y, shift.y)};
+      if (deep) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) g[i] = f32x2{clamp(g[i].x), clamp(g[i].y)};
+      }
     }
   }
 };
