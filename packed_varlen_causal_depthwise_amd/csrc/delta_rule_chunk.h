@@ -812,23 +812,18 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
   RawRows<kF, kRows> rk, rq;
   RawRows<kG, kRows> rg;
   const int wrow = RW::wave_row(wave), lrow = RW::lane_row(lane);
-  const auto load_chunk = [&](int chunk) {
+  const bool same = R.g_cs == 0;
+  const auto window = [&](const char* base, int64_t ts, int64_t head, int eb, int row, int chunk) {
     const int64_t first = seq.start + chunk * kChunk;
     const int valid = seq.len - chunk * kChunk < kChunk ? seq.len - chunk * kChunk : kChunk;
-    const Window wg(R.g + (first * R.g_ts + h * R.g_hs) * kGB, valid, (uint32_t)R.g_ts * kGB,
-                    (R.g_cs != 0 ? D : 1) * kGB);
-    if (R.g_cs != 0)
-      rg.load(wg, lrow * wg.stride + c * kGB, wrow);
-    else
-      rg.load_same(wg, lrow * wg.stride, wrow);
-    const Window wk(R.k + (first * R.k_ts + qk * R.k_hs) * kEB, valid, (uint32_t)R.k_ts * kEB, D * kEB);
-    rk.load(wk, lrow * wk.stride + c * kEB, wrow);
-    if (kOut) {
-      const Window wq(R.q + (first * R.q_ts + qk * R.q_hs) * kEB, valid, (uint32_t)R.q_ts * kEB, D * kEB);
-      rq.load(wq, lrow * wq.stride + c * kEB, wrow);
-    }
-    // The slot goes straight to LDS: 688 pieces of 16 bytes, T (384), A (256) and the row
-    // factors (48), 64 per wave and load.
+    return Window(base + (first * ts + head) * eb, valid, (uint32_t)ts * eb, row * eb);
+  };
+  const auto gates = [&](int chunk) { return window(R.g, R.g_ts, h * R.g_hs, kGB, same ? 1 : D, chunk); };
+  const auto keys = [&](int chunk) { return window(R.k, R.k_ts, qk * R.k_hs, kEB, D, chunk); };
+  const auto queries = [&](int chunk) { return window(R.q, R.q_ts, qk * R.q_hs, kEB, D, chunk); };
+  // The slot goes straight to LDS: 688 pieces of 16 bytes, T (384), A (256) and the row
+  // factors (48), 64 per wave and load.
+  const auto load_slot = [&](int chunk) {
     const char* const slot = P.slots + ((int64_t)(slot0 + chunk) * R.heads + h) * kSlotBytes;
     char* const into = held[chunk & 1];
 #pragma unroll
@@ -836,7 +831,19 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
       if (i + kThreads <= kSlotUsed / 16 || threadIdx.x < kSlotUsed / 16 - i)
         to_lds(slot + 16 * (i + threadIdx.x), into + 16 * (i + 64 * wave));
   };
-  load_chunk(begin);
+  {
+    const Window wg = gates(begin), wk = keys(begin);
+    if (same)
+      rg.load_same(wg, lrow * wg.stride, wrow);
+    else
+      rg.load(wg, lrow * wg.stride + c * kGB, wrow);
+    rk.load(wk, lrow * wk.stride + c * kEB, wrow);
+    if (kOut) {
+      const Window wq = queries(begin);
+      rq.load(wq, lrow * wq.stride + c * kEB, wrow);
+    }
+    load_slot(begin);
+  }
 
   for (int chunk = begin; chunk < end; ++chunk) {
     const int64_t first = seq.start + chunk * kChunk;
@@ -846,7 +853,7 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
 
     // ---- operands
     f32x2 q[kRows], k[kRows], p[kRows];
-    rg.values(p, R.g_cs == 0);
+    rg.values(p, same);
     gate.eval(p, bias);
     mask_rows(p, row0, valid);
     rk.values(k);
@@ -893,12 +900,25 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
       const f32x2 d = p[kRows - 1] + after;
       *(f32x2*)&decay[c] = f32x2{exp2_hw(d.x), exp2_hw(d.y)};
     }
+    // The rows' factors before any of the stores below: LDS serves a wave in order.
+    float kf[kRows], qf[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; i += 4) {
+      const f32x4 a = *(const f32x4*)(fac + row0 + i);
+      f32x4 b = a;
+      if (kOut) b = *(const f32x4*)(fac + 2 * kChunk + row0 + i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        kf[i + e] = a[e];
+        qf[i + e] = b[e];
+      }
+    }
     f16x2 th[kRows], tl[kRows];
     const int cw = fresh(cpos), tw = fresh(c * kLt);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const int r = row0 + i;
-      const f32x2 unit = k[i] * fac[r];
+      const f32x2 unit = k[i] * kf[i];
       const f32x2 up = p[i] + before, down = rest[i] + after;
       const f32x2 e = {exp2_hw(up.x), exp2_hw(up.y)};
       const HalfPair g = split2(unit * e, R.one);
@@ -908,7 +928,7 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
       th[i] = t.hi;
       tl[i] = t.lo;
       if (kOut) {
-        const HalfPair w = split2(q[i] * fac[2 * kChunk + r] * e, R.one);
+        const HalfPair w = split2(q[i] * qf[i] * e, R.one);
         *(f16x2*)&qg[0][r * kLd + cw] = w.hi;
         *(f16x2*)&qg[1][r * kLd + cw] = w.lo;
       }
@@ -922,44 +942,61 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
       *(f16x4*)&kt[1][tw + kLt + at] = f16x4{tl[i].y, tl[i + 1].y, tl[i + 2].y, tl[i + 3].y};
     }
     __syncthreads();
-    if (chunk + 1 < end) load_chunk(chunk + 1);
-
     // ---- Y = (K e^G) S and O = (Q e^G) S
     f32x4 Y[2][kN], O[2][kN];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int n = 0; n < kN; ++n) Y[t][n] = O[t][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    // The scheduling barriers keep the compiler from reading the left operands of all steps
-    // first, which spills; four waves per SIMD cover the reads.
-    Operand b[kN];
-#pragma unroll
-    for (int step = 0; step < 2 * kK; ++step) {
-      const int t = step & 1, at = (16 * t + n16) * kLd + 32 * (step >> 1) + 8 * n4;
-      const f16x8 kh = *(const f16x8*)&kg[0][at], kl = *(const f16x8*)&kg[1][at];
-      f16x8 qh, ql;
+    // Steps of (32 channels, 16 rows). A step's left operands are read while the step before
+    // runs, and one row of the next chunk's inputs is loaded (after the last chunk: that
+    // chunk's own again), so that neither waits on the other. The scheduling barriers keep
+    // the steps apart.
+    const int next = chunk + 1 < end ? chunk + 1 : chunk;
+    if (chunk + 1 < end) load_slot(next);
+    const Window wg = gates(next), wk = keys(next), wq = queries(next);
+    const uint32_t g_at = fresh(lrow) * wg.stride + (same ? 0 : c * kGB);
+    const uint32_t k_at = fresh(lrow) * wk.stride + c * kEB, q_at = fresh(lrow) * wq.stride + c * kEB;
+    if (same) rg.load_same(wg, g_at, wrow);
+    f16x8 kh, kl, qh, ql;
+    const auto read_step = [&](int step) {
+      const int at = (16 * (step & 1) + n16) * kLd + 32 * (step >> 1) + 8 * n4;
+      kh = *(const f16x8*)&kg[0][at];
+      kl = *(const f16x8*)&kg[1][at];
       if (kOut) {
         qh = *(const f16x8*)&qg[0][at];
         ql = *(const f16x8*)&qg[1][at];
       }
+    };
+    static_assert(2 * kK == kRows, "a row per step");
+    read_step(0);
+    Operand b[kN];
+#pragma unroll
+    for (int step = 0; step < 2 * kK; ++step) {
+      const int t = step & 1;
+      const f16x8 ch = kh, cl = kl, dh = qh, dl = ql;
+      if (step + 1 < 2 * kK) read_step(step + 1);
+      if (!same) rg.r[step] = Cell<kG>::pair(wg, g_at, wrow + step);
+      rk.r[step] = Cell<kF>::pair(wk, k_at, wrow + step);
+      if (kOut) rq.r[step] = Cell<kF>::pair(wq, q_at, wrow + step);
       if (t == 0) {
 #pragma unroll
         for (int n = 0; n < kN; ++n) b[n] = split8(S.s[step][n], S.s[step + 1][n], R.one);
       }
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
-        Y[t][n] = mfma16(kh, b[n].hi, Y[t][n]);
-        if (kOut) O[t][n] = mfma16(qh, b[n].hi, O[t][n]);
+        Y[t][n] = mfma16(ch, b[n].hi, Y[t][n]);
+        if (kOut) O[t][n] = mfma16(dh, b[n].hi, O[t][n]);
       }
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
-        Y[t][n] = mfma16(kh, b[n].lo, Y[t][n]);
-        if (kOut) O[t][n] = mfma16(qh, b[n].lo, O[t][n]);
+        Y[t][n] = mfma16(ch, b[n].lo, Y[t][n]);
+        if (kOut) O[t][n] = mfma16(dh, b[n].lo, O[t][n]);
       }
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
-        Y[t][n] = mfma16(kl, b[n].hi, Y[t][n]);
-        if (kOut) O[t][n] = mfma16(ql, b[n].hi, O[t][n]);
+        Y[t][n] = mfma16(cl, b[n].hi, Y[t][n]);
+        if (kOut) O[t][n] = mfma16(dl, b[n].hi, O[t][n]);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -1054,17 +1091,26 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
     Operand u[kN];
 #pragma unroll
     for (int n = 0; n < kN; ++n) u[n] = split8(U[0][n], U[1][n], R.one);
+    f16x8 ah, al;
+    f32x4 d;
+    const auto read_tile = [&](int m) {
+      d = *(const f32x4*)&decay[16 * m + 4 * n4];
+      const int at = (16 * m + n16) * kLt + 8 * n4;
+      ah = *(const f16x8*)&kt[0][at];
+      al = *(const f16x8*)&kt[1][at];
+    };
+    read_tile(0);
 #pragma unroll
     for (int m = 0; m < kM; ++m) {
-      const f32x4 d = *(const f32x4*)&decay[16 * m + 4 * n4];
-      const int at = (16 * m + n16) * kLt + 8 * n4;
-      const f16x8 ah = *(const f16x8*)&kt[0][at], al = *(const f16x8*)&kt[1][at];
+      const f16x8 ch = ah, cl = al;
+      const f32x4 e = d;
+      if (m + 1 < kM) read_tile(m + 1);
 #pragma unroll
-      for (int n = 0; n < kN; ++n) S.s[m][n] = mfma16(ah, u[n].hi, S.s[m][n] * d);
+      for (int n = 0; n < kN; ++n) S.s[m][n] = mfma16(ch, u[n].hi, S.s[m][n] * e);
 #pragma unroll
-      for (int n = 0; n < kN; ++n) S.s[m][n] = mfma16(ah, u[n].lo, S.s[m][n]);
+      for (int n = 0; n < kN; ++n) S.s[m][n] = mfma16(ch, u[n].lo, S.s[m][n]);
 #pragma unroll
-      for (int n = 0; n < kN; ++n) S.s[m][n] = mfma16(al, u[n].hi, S.s[m][n]);
+      for (int n = 0; n < kN; ++n) S.s[m][n] = mfma16(cl, u[n].hi, S.s[m][n]);
       if (m & 1) __builtin_amdgcn_sched_barrier(0);
     }
     if (kOut) {
