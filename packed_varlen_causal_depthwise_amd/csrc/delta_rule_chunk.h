@@ -17,7 +17,7 @@
 //
 // Kernels, one workgroup of 4 waves each:
 //   prepare   (chunk, head)             T, A and row factors into a slot
-//   scan      (segment, head, B or M)   only for sequences of several segments
+//   scan      (segment, head)           B and M, only for sequences of several segments
 //   join      (sequence, head, columns) the starts of the segments from the third on
 //   scan      (segment, head)           outputs and the final state
 //
@@ -722,13 +722,16 @@ struct ScanState {
 };
 
 template <int kF, int kG, int D, int kMode>
-__global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkParams P) {
-  constexpr int kWaves = 4, kThreads = 64 * kWaves;
+__global__ __launch_bounds__(kMode == kScanOut ? 256 : 4 * D, 2) void delta_rule_scan_kernel(const ChunkParams P) {
+  // For a segment's transition, half of the waves for B and half for M.
+  constexpr int kWaves = kMode == kScanOut ? 4 : D / 16, kThreads = 64 * kWaves;
+  constexpr int kColWaves = kMode == kScanOut ? 4 : D / 32;
   typedef Rows<D, kWaves> RW;
   constexpr int kRows = RW::kRows, kLanes = RW::kLanes, kGroups = RW::kGroups;
+  static_assert(kRows % 4 == 0, "rows are written to the transposed operand four at a time");
   constexpr int kEB = elem_bytes<kF>(), kGB = elem_bytes<kG>();
-  constexpr int kM = D / 16, kN = D / 64, kK = D / 32;
   constexpr bool kOut = kMode == kScanOut;
+  constexpr int kM = D / 16, kN = D / (16 * kColWaves), kK = D / 32;
   constexpr int kLd = D + 8, kLt = kChunk + 8;  // halves per row: 16 rows reach all banks
   __shared__ __attribute__((aligned(16))) _Float16 kg[2][kChunk * kLd];
   __shared__ __attribute__((aligned(16))) _Float16 qg[2][kOut ? kChunk * kLd : 8];
@@ -737,13 +740,10 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
   __shared__ __attribute__((aligned(16))) float decay[D];
   // The chunk's slot, and the next one's on its way.
   __shared__ __attribute__((aligned(16))) char held[2][kSlotUsed];
-  __shared__ float part[kWaves];
+  __shared__ float part[4];
 
   const RuleParams& R = P.R;
-  int id = blockIdx.x;
-  const bool identity = !kOut && (id & 1) != 0;  // the segment's M
-  if (!kOut) id >>= 1;
-  const int program = id / R.heads, h = id % R.heads;
+  const int program = blockIdx.x / R.heads, h = blockIdx.x % R.heads;
   const int wave = uniform(threadIdx.x / kRuleWave), lane = threadIdx.x % kRuleWave;
   const Piece piece = find_piece(P, program, P.segment_shift, lane);
   if (piece.s < 0) return;
@@ -753,10 +753,11 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
   const int chunks = (seq.len + kChunk - 1) / kChunk;
   const int begin = piece.index * per, end = begin + per < chunks ? begin + per : chunks;
   if (begin >= chunks) return;
-  if (!kOut && (end == chunks || (identity && begin == 0))) return;
+  if (!kOut && end == chunks) return;
 
   const int n16 = lane % 16, n4 = lane / 16;
-  const int col = wave * (16 * kN) + kN * n16;
+  const bool identity = !kOut && wave >= kColWaves;  // this wave's columns are M's
+  const int col = wave % kColWaves * (16 * kN) + kN * n16;
   const int64_t cell = (int64_t)program * R.heads + h;
 
   ScanState<kM, kN> S;
@@ -768,7 +769,7 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
     } else if (kOut) {
       from = P.ends + (cell - R.heads) * (D * D);
     }
-    if (from != nullptr) {
+    if (from != nullptr && !identity) {
 #pragma unroll
       for (int m = 0; m < kM; ++m)
 #pragma unroll
@@ -777,7 +778,7 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
           if constexpr (kN == 2) {
             const f32x2 x = *(const f32x2a4*)at;
             S.s[m][0][r] = x.x;
-            S.s[m][kN - 1][r] = x.y;
+            S.s[m][1][r] = x.y;
           } else {
             S.s[m][0][r] = *at;
           }
@@ -968,7 +969,7 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
         ql = *(const f16x8*)&qg[1][at];
       }
     };
-    static_assert(2 * kK == kRows, "a row per step");
+    static_assert(2 * kK >= kRows, "a row per step");
     read_step(0);
     Operand b[kN];
 #pragma unroll
@@ -976,9 +977,11 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
       const int t = step & 1;
       const f16x8 ch = kh, cl = kl, dh = qh, dl = ql;
       if (step + 1 < 2 * kK) read_step(step + 1);
-      if (!same) rg.r[step] = Cell<kG>::pair(wg, g_at, wrow + step);
-      rk.r[step] = Cell<kF>::pair(wk, k_at, wrow + step);
-      if (kOut) rq.r[step] = Cell<kF>::pair(wq, q_at, wrow + step);
+      if (step < kRows) {
+        if (!same) rg.r[step] = Cell<kG>::pair(wg, g_at, wrow + step);
+        rk.r[step] = Cell<kF>::pair(wk, k_at, wrow + step);
+        if (kOut) rq.r[step] = Cell<kF>::pair(wq, q_at, wrow + step);
+      }
       if (t == 0) {
 #pragma unroll
         for (int n = 0; n < kN; ++n) b[n] = split8(S.s[step][n], S.s[step + 1][n], R.one);
@@ -1161,41 +1164,7 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
   }
 
   // ---- the end
-  if (identity) {
-    // M as pairs in operand order, scaled by one power of two to a largest entry of 256 to
-    // 512.
-    float top = 0.0f;
-#pragma unroll
-    for (int n = 0; n < kN; ++n) {
-      S.apply(n, S.inverse[n]);
-      top = __builtin_fmaxf(top, S.largest(n));
-    }
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, m));
-    if (lane == 0) part[wave] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = __builtin_fmaxf(top, part[w]);
-    int e = 0;
-    if (top > 0.0f && top < __builtin_huge_valf()) e = 9 - __builtin_amdgcn_frexp_expf(top);
-    e = e > 100 ? 100 : e;
-    char* const to = P.moves + cell * move_bytes(D);
-    _Float16* const hi = (_Float16*)to;
-#pragma unroll
-    for (int n = 0; n < kN; ++n) {
-      const int cc = col + n, pl = place(cc % 32);
-#pragma unroll
-      for (int m = 0; m < kM; ++m)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float x = __builtin_amdgcn_ldexpf(S.s[m][n][r], e);
-          const int at = ((m * kK + cc / 32) * 64 + (pl / 8) * 16 + 4 * n4 + r) * 8 + pl % 8;
-          hi[at] = (_Float16)x;
-          hi[D * D + at] = (_Float16)(x - (float)(_Float16)x);
-        }
-    }
-    if (threadIdx.x == 0) *(float*)(to + (int64_t)D * D * 4) = __builtin_amdgcn_ldexpf(1.0f, -e);
-  } else {
+  if (!identity) {
     float* to = nullptr;
     if (!kOut)
       to = P.ends + cell * (D * D);
@@ -1207,11 +1176,50 @@ __global__ __launch_bounds__(256, 2) void delta_rule_scan_kernel(const ChunkPara
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           float* const at = to + (16 * m + 4 * n4 + r) * D + col;
-          if (kN == 2)
-            *(f32x2a4*)at = f32x2{S.s[m][0][r] * S.inverse[0], S.s[m][kN - 1][r] * S.inverse[kN - 1]};
+          if constexpr (kN == 2)
+            *(f32x2a4*)at = f32x2{S.s[m][0][r] * S.inverse[0], S.s[m][1][r] * S.inverse[1]};
           else
             *at = S.s[m][0][r] * S.inverse[0];
         }
+    }
+  }
+  if (!kOut && begin > 0) {
+    // M as pairs in operand order, scaled by one power of two to a largest entry of 256 to
+    // 512.
+    float top = 0.0f;
+    if (identity) {
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        S.apply(n, S.inverse[n]);
+        top = __builtin_fmaxf(top, S.largest(n));
+      }
+#pragma unroll
+      for (int m = 32; m > 0; m >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, m));
+      if (lane == 0) part[wave - kColWaves] = top;
+    }
+    __syncthreads();
+    if (identity) {
+#pragma unroll
+      for (int w = 0; w < kColWaves; ++w) top = __builtin_fmaxf(top, part[w]);
+      int e = 0;
+      if (top > 0.0f && top < __builtin_huge_valf()) e = 9 - __builtin_amdgcn_frexp_expf(top);
+      e = e > 100 ? 100 : e;
+      char* const to = P.moves + cell * move_bytes(D);
+      _Float16* const hi = (_Float16*)to;
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        const int cc = col + n, pl = place(cc % 32);
+#pragma unroll
+        for (int m = 0; m < kM; ++m)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float x = __builtin_amdgcn_ldexpf(S.s[m][n][r], e);
+            const int at = ((m * kK + cc / 32) * 64 + (pl / 8) * 16 + 4 * n4 + r) * 8 + pl % 8;
+            hi[at] = (_Float16)x;
+            hi[D * D + at] = (_Float16)(x - (float)(_Float16)x);
+          }
+      }
+      if (wave == kColWaves && lane == 0) *(float*)(to + (int64_t)D * D * 4) = __builtin_amdgcn_ldexpf(1.0f, -e);
     }
   }
 }
@@ -1322,7 +1330,7 @@ void launch_chunks(const ChunkParams& P, hipStream_t st) {
   const unsigned segments = (unsigned)P.segment_programs * heads;
   hipLaunchKernelGGL((delta_rule_prepare_kernel<kF, kG, D>), dim3(chunks), dim3(256), 0, st, P);
   if (P.moves != nullptr) {
-    hipLaunchKernelGGL((delta_rule_scan_kernel<kF, kG, D, kScanMove>), dim3(2 * segments), dim3(256), 0, st, P);
+    hipLaunchKernelGGL((delta_rule_scan_kernel<kF, kG, D, kScanMove>), dim3(segments), dim3(4 * D), 0, st, P);
     hipLaunchKernelGGL((delta_rule_join_kernel<D>), dim3(segments * (D / 16)), dim3(256), 0, st, P);
   }
   hipLaunchKernelGGL((delta_rule_scan_kernel<kF, kG, D, kScanOut>), dim3(segments), dim3(256), 0, st, P);
