@@ -46,19 +46,33 @@ constexpr int kChunk = 32;  // tokens per chunk
 // scratch memory.
 struct ChunkParams {
   RuleParams R;
-  char* slots;  // kSlotBytes per (chunk program, head)
+  char* slots;  // a Slot per (chunk program, head)
   float* ends;  // head_dim^2 per (segment program, head): a segment's end, then a start
-  char* moves;  // kMoveBytes per (segment program, head): the segment's transition
+  char* moves;  // move_bytes per (segment program, head): the segment's transition
   int32_t chunk_programs, segment_programs;
   int32_t segment_shift;  // log2 of the tokens per segment
   int32_t search_top;  // 64^(levels - 1), 64^levels >= num_seqs
   int32_t min_len;  // shorter sequences are left to the step kernel
 };
 
-// One chunk of one head as the scan reads it: T as three and A as two FP16 matrices in the
-// order of matrix operands, then six rows of kChunk floats (see prepare).
-constexpr int kSlotT = 0, kSlotA = 6144, kSlotRows = 10240;
-constexpr int kSlotUsed = kSlotRows + 6 * kChunk * 4, kSlotBytes = 11264;
+// One chunk of one head as the scans read it, in pieces of 1 KB that are one matrix operand
+// each (64 lanes x 8 FP16): K e^G, Q e^G and K e^(G_end - G) as pairs, decays and row
+// factors, T as three parts, A as a pair.
+struct Slot {
+  int64_t head_dim;
+  __host__ __device__ constexpr int64_t matrix() const { return 128 * head_dim; }  // a pair of 32 x head_dim
+  __host__ __device__ constexpr int64_t kg() const { return 0; }
+  __host__ __device__ constexpr int64_t qg() const { return matrix(); }
+  __host__ __device__ constexpr int64_t kt() const { return 2 * matrix(); }
+  __host__ __device__ constexpr int64_t factors() const { return 3 * matrix(); }  // 1 KB
+  __host__ __device__ constexpr int64_t t() const { return 3 * matrix() + 1024; }
+  __host__ __device__ constexpr int64_t a() const { return t() + 6144; }
+  __host__ __device__ constexpr int64_t bytes() const { return a() + 4096; }
+};
+
+// In a slot's factors: decays over the chunk (head_dim), then |k| / 16 and the outputs'
+// factors / 16 (kChunk each) and T's factor.
+constexpr int kFactorRows = 128;
 
 // The transition: pairs of FP16 matrices and a scale.
 inline __host__ __device__ int64_t move_bytes(int head_dim) { return (int64_t)head_dim * head_dim * 4 + 256; }

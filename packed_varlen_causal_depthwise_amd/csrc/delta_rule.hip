@@ -50,7 +50,7 @@ Plan make_plan(int64_t tokens, int64_t seqs, int64_t heads, int64_t head_dim) {
   p.chunk_programs = tokens / kChunk + seqs;
   p.segment_programs = (tokens >> p.segment_shift) + seqs;
   if (p.chunks) {
-    p.slot_bytes = round256(p.chunk_programs * heads * kSlotBytes);
+    p.slot_bytes = round256(p.chunk_programs * heads * Slot{head_dim}.bytes());
     if (p.segments) {
       p.ends_bytes = round256(p.segment_programs * heads * head_dim * head_dim * 4);
       p.moves_bytes = p.segment_programs * heads * move_bytes((int)head_dim);

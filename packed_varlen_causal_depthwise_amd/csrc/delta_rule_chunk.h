@@ -15,11 +15,14 @@
 // a segment from zero gives B, the scan of the identity without values gives M, and the
 // starts follow by S_(j+1) = M_j S_j + B_j. Then all segments run side by side.
 //
-// Kernels, one workgroup of 4 waves each:
-//   prepare   (chunk, head)             T, A and row factors into a slot
+// Kernels:
+//   prepare   (chunk, head)             all that does not depend on S, into a slot
 //   scan      (segment, head)           B and M, only for sequences of several segments
 //   join      (sequence, head, columns) the starts of the segments from the third on
 //   scan      (segment, head)           outputs and the final state
+// A chunk's gates, norms and exponentials are worked out once, by prepare, and handed over
+// as matrix operands (60 KB per chunk and head of 128): the scans were bound by that vector
+// work when they repeated it (5 us per chunk, 0.5 TB/s).
 //
 // Numbers. Matrix products run on the FP16 matrix instructions with every operand split
 // into a pair of FP16 values (22 bits) and three products: hi hi + hi lo + lo hi, summed
@@ -129,24 +132,19 @@ __device__ __forceinline__ Piece find_piece(const ChunkParams& P, int p, int shi
   return Piece{base, p - uniform(v)};
 }
 
-// How a workgroup holds a chunk's rows for elementwise work: groups of kRows neighbouring
-// rows, kLanes lanes per group, two channels per lane.
-template <int D, int kWaves>
+// How the prepare kernel's 4 waves hold a chunk's rows. Wave w has rows 4 w .. + 3 and
+// 16 + 4 w .. + 3 (one place of 8 in the order above), two channels per lane: with 128
+// channels each lane has all 8 rows, with 64 the lanes' halves have 4 each. Running sums go
+// over groups of 4 rows, numbered 4 (row / 16) + w.
+template <int D>
 struct Rows {
-  static constexpr int kLanes = D / 2;
-  static constexpr int kGroups = kWaves * 64 / kLanes;
-  static constexpr int kRows = kChunk / kGroups;
+  static constexpr int kLanes = D / 2;  // lanes per row
+  static constexpr int kParts = kLanes / 32;  // groups of 4 rows per lane
+  static constexpr int kRows = 4 * kParts;
 
-  // The lane's group; the same for the whole wave (and known to be) where a group is a wave.
-  static __device__ __forceinline__ int group(int wave, int lane) {
-    return kLanes == kRuleWave ? wave : wave * (kRuleWave / kLanes) + lane / kLanes;
-  }
-
-  // The wave's first row, and the lane's after it.
-  static __device__ __forceinline__ int wave_row(int wave) { return wave * (kRuleWave / kLanes) * kRows; }
-  static __device__ __forceinline__ int lane_row(int lane) {
-    return kLanes == kRuleWave ? 0 : lane / kLanes * kRows;
-  }
+  // Row i of a lane: the same for all lanes of a wave, plus the lane's part.
+  static __device__ __forceinline__ int wave_row(int wave, int i) { return 4 * wave + i % 4 + 16 * (i / 4); }
+  static __device__ __forceinline__ int lane_row(int lane) { return kParts == 2 ? 0 : lane / 32 * 16; }
 };
 
 // Hides that x is the same in every iteration of a loop. Without it the compiler computes
@@ -213,31 +211,27 @@ struct Cell {
   }
 };
 
-// A lane's pairs of N rows, as loaded. row0 is the same for all lanes of the wave; `lane`
-// is the lane's offset: its channels, and its rows where a wave holds two groups of rows.
-// All loads of a chunk are issued together.
-template <int kF, int N>
+// A lane's pairs of its rows, as loaded; `lane` is the lane's offset (its channels, and its
+// part of the rows).
+template <int kF, int D>
 struct RawRows {
+  static constexpr int N = Rows<D>::kRows;
   typename Pair<kF>::raw r[N];
 
-  __device__ __forceinline__ void load(const Window& w, uint32_t lane, int row0) {
+  __device__ __forceinline__ void load(const Window& w, uint32_t lane, int wave) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = Cell<kF>::pair(w, lane, row0 + i);
+    for (int i = 0; i < N; ++i) r[i] = Cell<kF>::pair(w, lane, Rows<D>::wave_row(wave, i));
   }
 
   // One element per row, for both of the lane's channels (gates per head).
-  __device__ __forceinline__ void load_same(const Window& w, uint32_t lane, int row0) {
+  __device__ __forceinline__ void load_same(const Window& w, uint32_t lane, int wave) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = Cell<kF>::one(w, lane, row0 + i);
-  }
-
-  __device__ __forceinline__ void values(f32x2 (&x)[N]) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = Pair<kF>::value(r[i]);
+    for (int i = 0; i < N; ++i) r[i] = Cell<kF>::one(w, lane, Rows<D>::wave_row(wave, i));
   }
 
   __device__ __forceinline__ void values(f32x2 (&x)[N], bool same) const {
-    values(x);
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = Pair<kF>::value(r[i]);
     if (same) {
 #pragma unroll
       for (int i = 0; i < N; ++i) x[i].y = x[i].x;
@@ -246,12 +240,12 @@ struct RawRows {
 };
 
 // Zeros in the rows past the last.
-template <int N>
-__device__ __forceinline__ void mask_rows(f32x2 (&x)[N], int row0, int valid) {
+template <int D>
+__device__ __forceinline__ void mask_rows(f32x2 (&x)[Rows<D>::kRows], int wave, int lane, int valid) {
   if (valid == kChunk) return;
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (row0 + i >= valid) x[i] = f32x2{0.0f, 0.0f};
+  for (int i = 0; i < Rows<D>::kRows; ++i)
+    if (Rows<D>::wave_row(wave, i) + Rows<D>::lane_row(lane) >= valid) x[i] = f32x2{0.0f, 0.0f};
 }
 
 // Sums of N values over kWidth lanes, each lane receiving the sum of value (lane index /
@@ -287,30 +281,34 @@ __device__ __forceinline__ double scatter_sum(typename Doubles<N>::type x, int l
 
 template <int kF, int kG, int D>
 __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkParams P) {
-  typedef Rows<D, 4> RW;
-  constexpr int kRows = RW::kRows, kLanes = RW::kLanes, kGroups = RW::kGroups;
+  typedef Rows<D> RW;
+  constexpr int kRows = RW::kRows, kLanes = RW::kLanes, kParts = RW::kParts;
   constexpr int kEB = elem_bytes<kF>(), kGB = elem_bytes<kG>();
   constexpr int kLd = D + 4;  // floats per operand row: 16 rows reach all banks
   constexpr int kMat = kChunk * kLd;
   constexpr int kSq = 34;  // doubles per row of a 32 x 32 matrix
-  // Operand rows q, k (times the decay from the block's middle) and columns k; later the
-  // 32 x 32 matrices.
-  __shared__ __attribute__((aligned(16))) float mats[3 * kMat];
-  __shared__ __attribute__((aligned(16))) float tot[kGroups][D];
+  // After the products: L and its inverse, T's and A's parts, and 32 D bytes per wave to
+  // turn rows into operands.
+  constexpr int kSquares = 2 * kChunk * kSq * (int)sizeof(double), kStage = kSquares + 4096;
+  constexpr int kBytes = 3 * kMat * 4 > kStage + 128 * D ? 3 * kMat * 4 : kStage + 128 * D;
+  // Operand rows q, k (times the decay from the block's middle) and columns k.
+  __shared__ __attribute__((aligned(16))) char shared[kBytes];
+  __shared__ __attribute__((aligned(16))) float tot[8][D];
   __shared__ __attribute__((aligned(16))) float across[D];
-  // The slot's rows: keys' factor times 16 (hi, lo), queries' times 16, n / 16, the outputs'
-  // factor / 16, and T's factor.
-  __shared__ __attribute__((aligned(16))) float fac[6][kChunk];
+  // Per row: the key's factor times 16, the query's times 16, the key's power of two; and
+  // as they go to the slot |k| / 16, the outputs' factor / 16 and T's factor.
+  __shared__ float kf16[kChunk], qf16[kChunk], ktwo[kChunk];
+  __shared__ __attribute__((aligned(16))) float rows[2][kChunk];
+  __shared__ float tfac;
   __shared__ float beta[kChunk];
   // Keys enter the products times a power of two (exact); the rest of their factor, and n,
   // follow in FP64 (a key rounded to unit length would be off by 3e-8, see below).
   __shared__ float krest[kChunk];
   __shared__ double kfac[kChunk];
   __shared__ int steep;
-  float* const ktwo = fac[5];  // until the last step puts T's factor there
-  float* const mq = mats;
-  float* const mk = mats + kMat;
-  float* const mc = mats + 2 * kMat;
+  float* const mq = (float*)shared;
+  float* const mk = mq + kMat;
+  float* const mc = mq + 2 * kMat;
 
   const RuleParams& R = P.R;
   const int program = blockIdx.x / R.heads, h = blockIdx.x % R.heads;
@@ -319,40 +317,40 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
   if (piece.s < 0) return;
   const Sequence seq(R, piece.s);
   if (seq.len < P.min_len || piece.index * kChunk >= seq.len) return;
-  const int first = seq.start + piece.index * kChunk;
+  const int64_t first = seq.start + piece.index * kChunk;
   const int valid = seq.len - piece.index * kChunk < kChunk ? seq.len - piece.index * kChunk : kChunk;
 
-  const int group = RW::group(wave, lane), c = 2 * (lane % kLanes), row0 = group * kRows;
+  const int c = 2 * (lane % kLanes), lrow = RW::lane_row(lane);
   const int64_t qk = h / R.share;
   const Window wq(R.q + (first * R.q_ts + qk * R.q_hs) * kEB, valid, (uint32_t)R.q_ts * kEB, D * kEB);
   const Window wk(R.k + (first * R.k_ts + qk * R.k_hs) * kEB, valid, (uint32_t)R.k_ts * kEB, D * kEB);
   const Window wg(R.g + (first * R.g_ts + h * R.g_hs) * kGB, valid, (uint32_t)R.g_ts * kGB,
                   (R.g_cs != 0 ? D : 1) * kGB);
-  const int wrow = RW::wave_row(wave), lrow = RW::lane_row(lane);
-  const auto load_gates = [&](RawRows<kG, kRows>& rg) {
+  const auto load_gates = [&](RawRows<kG, D>& rg) {
     if (R.g_cs != 0)
-      rg.load(wg, lrow * wg.stride + c * kGB, wrow);
+      rg.load(wg, lrow * wg.stride + c * kGB, wave);
     else
-      rg.load_same(wg, lrow * wg.stride, wrow);
+      rg.load_same(wg, lrow * wg.stride, wave);
   };
 
   f32x2 q[kRows], k[kRows], p[kRows];  // p: log2 decays, then their running sums
+  f32x2 rest[kRows];  // log2 decay after each row, inside its group of 4
   const Gate gate(R, h);
   f32x2 bias = {0.0f, 0.0f};
   if (R.dt_bias != nullptr) bias = *(const f32x2a4*)(R.dt_bias + h * D + c);
   {
-    RawRows<kF, kRows> rq, rk;
-    RawRows<kG, kRows> rg;
+    RawRows<kF, D> rq, rk;
+    RawRows<kG, D> rg;
     load_gates(rg);
-    rk.load(wk, lrow * wk.stride + c * kEB, wrow);
-    rq.load(wq, lrow * wq.stride + c * kEB, wrow);
+    rk.load(wk, lrow * wk.stride + c * kEB, wave);
+    rq.load(wq, lrow * wq.stride + c * kEB, wave);
     rg.values(p, R.g_cs == 0);
-    rk.values(k);
-    mask_rows(k, row0, valid);
-    rq.values(q);
-    mask_rows(q, row0, valid);
+    rk.values(k, false);
+    mask_rows<D>(k, wave, lane, valid);
+    rq.values(q, false);
+    mask_rows<D>(q, wave, lane, valid);
     gate.eval(p, bias);
-    mask_rows(p, row0, valid);
+    mask_rows<D>(p, wave, lane, valid);
   }
   if (threadIdx.x < kChunk)
     beta[threadIdx.x] = (int)threadIdx.x < valid ? beta_value(R, kF, first + threadIdx.x, h) : 0.0f;
@@ -369,18 +367,17 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
     }
     const double s = scatter_sum<2 * kRows, kLanes / 2>(ss, lane);
     constexpr int kShare = kLanes / (2 * kRows);  // lanes holding the same sum
-    const int l = lane % kLanes, which = l / kShare, r = row0 + which % kRows;
+    const int l = lane % kLanes, which = l / kShare, r = RW::wave_row(wave, which % kRows) + lrow;
     if (l % kShare == 0) {
       const bool norm = R.l2_eps >= 0.0f;
       const Factor f = inverse_root(norm ? s + (double)R.l2_eps : s);
       const float n = norm ? 1.0f : (float)(s * ((double)f.hi + (double)f.lo));
       if (which < kRows) {
-        fac[2][r] = kVec * f.hi;
-        fac[4][r] = n * R.scale * (1.0f / kVec);
+        qf16[r] = kVec * f.hi;
+        rows[1][r] = n * R.scale * (1.0f / kVec);
       } else {
-        fac[0][r] = kVec * f.hi;
-        fac[1][r] = kVec * f.lo;
-        fac[3][r] = n * (1.0f / kVec);
+        kf16[r] = kVec * f.hi;
+        rows[0][r] = n * (1.0f / kVec);
         const int e = f.hi > 0.0f ? __builtin_amdgcn_frexp_expf(f.hi) : 0;
         ktwo[r] = __builtin_amdgcn_ldexpf(1.0f, e);
         krest[r] = __builtin_amdgcn_ldexpf(f.hi, -e);
@@ -388,47 +385,60 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
       }
     }
   }
-  // Running sums inside the group.
+  // Running sums inside the groups.
 #pragma unroll
-  for (int i = 1; i < kRows; ++i) p[i] += p[i - 1];
-  *(f32x2*)&tot[group][c] = p[kRows - 1];
+  for (int j = 0; j < kParts; ++j) {
+    rest[4 * j + 3] = f32x2{0.0f, 0.0f};
+#pragma unroll
+    for (int i = 3; i > 0; --i) rest[4 * j + i - 1] = rest[4 * j + i] + p[4 * j + i];
+#pragma unroll
+    for (int i = 1; i < 4; ++i) p[4 * j + i] += p[4 * j + i - 1];
+    *(f32x2*)&tot[4 * (j + lrow / 16) + wave][c] = p[4 * j + 3];
+  }
   __syncthreads();
 
   // Each block of 16 rows takes its decays from its middle (after 8 rows): rows carry
   // 2^(p - mid), columns 2^(mid - p), whose product is exact to FP32 while both halves of
   // the block stay within 2^101 (8 tokens of log decay -8.75 each; the bounded gate
   // reaches -5). Steeper chunks take the direct sums below.
-  constexpr int kPer = kGroups / 2;  // groups per block
-  const int block = group / kPer;
-  f32x2 before = {0.0f, 0.0f}, mid = {0.0f, 0.0f}, all = {0.0f, 0.0f};
+  f32x2 all[2], mid[2];  // of both blocks
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const f32x2 t = *(const f32x2*)&tot[block * kPer + i][c];
-    if (i < group % kPer) before += t;
-    if (i < kPer / 2) mid += t;
-    all += t;
+  for (int b = 0; b < 2; ++b) {
+    const f32x2 t0 = *(const f32x2*)&tot[4 * b][c], t1 = *(const f32x2*)&tot[4 * b + 1][c];
+    const f32x2 t2 = *(const f32x2*)&tot[4 * b + 2][c], t3 = *(const f32x2*)&tot[4 * b + 3][c];
+    mid[b] = t0 + t1;
+    all[b] = mid[b] + (t2 + t3);
+    const f32x2 late = t2 + t3;
+    if (mid[b].x < -101.0f || mid[b].y < -101.0f || late.x < -101.0f || late.y < -101.0f) steep = 1;
   }
-  if (mid.x < -101.0f || mid.y < -101.0f || all.x - mid.x < -101.0f || all.y - mid.y < -101.0f)
-    steep = 1;
-  if (group == 0) {
+  f32x2 before[kParts], after[kParts];  // log2 decays of the block before and after the group
+#pragma unroll
+  for (int j = 0; j < kParts; ++j) {
+    before[j] = after[j] = f32x2{0.0f, 0.0f};
+    const int b = j + lrow / 16;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x2 t = *(const f32x2*)&tot[4 * b + i][c];
+      if (i < wave) before[j] += t;
+      if (i > wave) after[j] += t;
+    }
+  }
+  if (wave == 0 && lane < kLanes) {
     // From the middle of block 0 to the middle of block 1: what a column of block 0 needs
     // to meet a row of block 1.
-    f32x2 mid1 = {0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < kPer / 2; ++i) mid1 += *(const f32x2*)&tot[kPer + i][c];
-    const f32x2 d = all - mid + mid1;
+    const f32x2 d = all[0] - mid[0] + mid[1];
     *(f32x2*)&across[c] = f32x2{exp2_hw(d.x), exp2_hw(d.y)};
   }
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    const int r = row0 + i;
-    const f32x2 d = p[i] + before - mid;
+    const int r = RW::wave_row(wave, i) + lrow, j = i / 4;
+    const f32x2 m0 = kParts == 2 ? mid[j] : (lrow != 0 ? mid[1] : mid[0]);
+    const f32x2 d = p[i] + before[j] - m0;
     const f32x2 e = {exp2_hw(d.x), exp2_hw(d.y)}, m = {exp2_hw(-d.x), exp2_hw(-d.y)};
-    const float fq = fac[2][r];
-    k[i] *= ktwo[r];
-    *(f32x2*)&mq[r * kLd + c] = q[i] * fq * e;
-    *(f32x2*)&mk[r * kLd + c] = k[i] * e;
-    *(f32x2*)&mc[r * kLd + c] = k[i] * m;
+    const f32x2 kk = k[i] * ktwo[r];
+    *(f32x2*)&mq[r * kLd + c] = q[i] * qf16[r] * e;
+    *(f32x2*)&mk[r * kLd + c] = kk * e;
+    *(f32x2*)&mc[r * kLd + c] = kk * m;
   }
   __syncthreads();
 
@@ -476,14 +486,14 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
     __syncthreads();
     // The decays, from the sums: exact enough again, then summed in FP64 per channel.
     {
-      RawRows<kG, kRows> rg;
+      RawRows<kG, D> rg;
       load_gates(rg);
       f32x2 g[kRows];
       rg.values(g, R.g_cs == 0);
       gate.eval(g, bias);
-      mask_rows(g, row0, valid);
+      mask_rows<D>(g, wave, lane, valid);
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) *(f32x2*)&mk[(row0 + i) * kLd + c] = g[i];
+      for (int i = 0; i < kRows; ++i) *(f32x2*)&mk[(RW::wave_row(wave, i) + lrow) * kLd + c] = g[i];
     }
     __syncthreads();
     double* const sums = (double*)mc;  // rows of D doubles over mc and mq's place
@@ -499,7 +509,10 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) *(f32x2*)&mk[(row0 + i) * kLd + c] = k[i];
+    for (int i = 0; i < kRows; ++i) {
+      const int r = RW::wave_row(wave, i) + lrow;
+      *(f32x2*)&mk[r * kLd + c] = k[i] * ktwo[r];
+    }
     __syncthreads();
     for (int u = 0; u < 3; ++u) {
       const int pair = threadIdx.x + 256 * u;  // (t, i) with i <= t, 528 in all
@@ -512,7 +525,7 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
       const double* const gi = (i < 16 ? sums : lower) + (i & 15) * D;
       const char* const qrow =
           R.q + ((first + (t < valid ? t : valid - 1)) * R.q_ts + qk * R.q_hs) * kEB;
-      const float fq = t < valid ? fac[2][t] : 0.0f;
+      const float fq = t < valid ? qf16[t] : 0.0f;
       float sk = 0.0f, sq = 0.0f;
       for (int ch = 0; ch < D; ++ch) {
         const float w = mk[i * kLd + ch] * exp2_hw((float)(gt[ch] - gi[ch]));
@@ -526,14 +539,14 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
   __syncthreads();
 
   // The operands are done with; their place takes L, the inverse and the staged outputs.
-  double* const ml = (double*)mats;  // L [row][column]
+  double* const ml = (double*)shared;  // L [row][column]
   double* const mt = ml + kChunk * kSq;  // (I + L)^-1
   // T in three parts and A in two, as they go to the slot. L's place is free for T by then.
-  _Float16* const st = (_Float16*)mats;
-  _Float16* const sa = (_Float16*)(mt + kChunk * kSq);
-  static_assert(6144 <= kChunk * kSq * sizeof(double) &&
-                2 * kChunk * kSq * sizeof(double) + 4096 <= sizeof(float) * 3 * kMat, "they fit");
-  char* const slot = P.slots + ((int64_t)program * R.heads + h) * kSlotBytes;
+  _Float16* const st = (_Float16*)shared;
+  _Float16* const sa = (_Float16*)(shared + kSquares);
+  static_assert(6144 <= kChunk * kSq * sizeof(double), "T fits L's place");
+  constexpr Slot kSlot{D};
+  char* const slot = P.slots + ((int64_t)program * R.heads + h) * kSlot.bytes();
   const auto put_a = [&](int t, int i, float a) {
     // A times 256 in operand order: row tile, lane, place. (a carries the query's 16.)
     const int at = (t / 16 * 64 + (place(i) / 8) * 16 + t % 16) * 8 + place(i) % 8;
@@ -575,6 +588,78 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
     }
   }
   __syncthreads();
+
+  // The scans' operands.
+  {
+    constexpr int kFrags = D / 32 * 4;  // of a row matrix: (32 channels, 16 rows, hi or lo)
+    _Float16* const own = (_Float16*)(shared + kStage + 32 * D * wave);
+    const int x = c % 32, kk = c / 32, place16 = place(x);
+    f16x2 th[kRows], tl[kRows];
+    HalfPair qs[kRows];
+    // The wave's 4 rows of a row tile and 4 channels of 8 make 4 x 4 blocks of 16 bytes per
+    // operand piece; block (channels n, row r) sits at 4 n + (r ^ n), xor the piece's number
+    // of 32 channels, so that a row's 64 lanes reach all banks.
+    const auto own_at = [&](int i, int part) {
+      const int tt = i / 4 + lrow / 16, n = place16 / 8, r = i % 4;
+      return ((kk * 2 + tt) * 2 + part) * 128 + (((4 * n + (r ^ n)) ^ kk) * 8) + place16 % 8;
+    };
+    const auto copy_out = [&](char* to) {
+#pragma unroll
+      for (int f0 = 0; f0 < kFrags; f0 += 4) {
+        const int f = f0 + lane / 16, b = lane % 16, fk = f / 4;
+        const u32q v = *(const u32q*)(own + f * 128 + ((b ^ fk) * 8));
+        // In the slot block (channels n, row r of 16) of a piece is 16 n + (r ^ (n + 4 kk)).
+        *(u32q*)(to + f * 1024 + (16 * (b / 4) + 4 * (wave ^ fk) + b % 4) * 16) = v;
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int r = RW::wave_row(wave, i) + lrow, j = i / 4;
+      const bool second = kParts == 2 ? j == 1 : lrow != 0;
+      const f32x2 up = p[i] + before[j] + (second ? all[0] : f32x2{0.0f, 0.0f});
+      const f32x2 down = rest[i] + after[j] + (second ? f32x2{0.0f, 0.0f} : all[1]);
+      const f32x2 e = {exp2_hw(up.x), exp2_hw(up.y)};
+      const f32x2 unit = k[i] * kf16[r];
+      const HalfPair g = split2(unit * e, R.one);
+      *(f16x2*)&own[own_at(i, 0)] = g.hi;
+      *(f16x2*)&own[own_at(i, 1)] = g.lo;
+      qs[i] = split2(q[i] * qf16[r] * e, R.one);
+      const HalfPair t = split2(unit * f32x2{exp2_hw(down.x), exp2_hw(down.y)}, R.one);
+      th[i] = t.hi;
+      tl[i] = t.lo;
+    }
+    __builtin_amdgcn_wave_barrier();
+    copy_out(slot + kSlot.kg());
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      *(f16x2*)&own[own_at(i, 0)] = qs[i].hi;
+      *(f16x2*)&own[own_at(i, 1)] = qs[i].lo;
+    }
+    __builtin_amdgcn_wave_barrier();
+    copy_out(slot + kSlot.qg());
+    // Columns: the wave's 8 rows are one block of 16 bytes per channel.
+    _Float16* const kt = (_Float16*)(slot + kSlot.kt());
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int ch = c + y, at = (ch / 16) * 1024 + (16 * wave + ch % 16) * 8 + lrow / 4;
+#pragma unroll
+      for (int j = 0; j < kParts; ++j) {
+        f16x4 hi, lo;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          hi[i] = th[4 * j + i][y];
+          lo[i] = tl[4 * j + i][y];
+        }
+        *(f16x4*)&kt[at + 4 * j] = hi;
+        *(f16x4*)&kt[at + 512 + 4 * j] = lo;
+      }
+    }
+    if (wave == 0 && lane < kLanes) {
+      const f32x2 d = all[0] + all[1];
+      *(f32x2*)(slot + kSlot.factors() + 4 * c) = f32x2{exp2_hw(d.x), exp2_hw(d.y)};
+    }
+  }
 
   if (wave == 0) {
     // (I + L)^-1: the two diagonal blocks by forward substitution, a column per lane, then
@@ -618,9 +703,9 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = 4 * n4 + r;
-      t00[r] = (double)(kVec * fac[3][t]) * mt[t * kSq + n16] * (double)beta[n16];
-      t11[r] = (double)(kVec * fac[3][16 + t]) * mt[(16 + t) * kSq + 16 + n16] * (double)beta[16 + n16];
-      t10[r] = -(double)(kVec * fac[3][16 + t]) * y[r] * (double)beta[n16];
+      t00[r] = (double)(kVec * rows[0][t]) * mt[t * kSq + n16] * (double)beta[n16];
+      t11[r] = (double)(kVec * rows[0][16 + t]) * mt[(16 + t) * kSq + 16 + n16] * (double)beta[16 + n16];
+      t10[r] = -(double)(kVec * rows[0][16 + t]) * y[r] * (double)beta[n16];
       top = __builtin_fmaxf(
           top, __builtin_fmaxf(__builtin_fabsf((float)t10[r]),
                                __builtin_fmaxf(__builtin_fabsf((float)t00[r]), __builtin_fabsf((float)t11[r]))));
@@ -650,16 +735,16 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
       put_t(t, 16 + n16, 0.0f);
     }
     // U is kept times 1 / 16, so that (16 k^)^T (U / 16) adds to S as it is.
-    if (lane == 0) fac[5][0] = __builtin_amdgcn_ldexpf(1.0f / kVec, -e);
+    if (lane == 0) tfac = __builtin_amdgcn_ldexpf(1.0f / kVec, -e);
   }
   __syncthreads();
-  // The slot: 10 KB of operands and the rows of factors, 16 bytes per thread and store.
-  u32q* const dst = (u32q*)slot;
-  dst[threadIdx.x] = ((const u32q*)st)[threadIdx.x];
-  if (threadIdx.x < 128) dst[256 + threadIdx.x] = ((const u32q*)st)[256 + threadIdx.x];
-  dst[384 + threadIdx.x] = ((const u32q*)sa)[threadIdx.x];
-  if (threadIdx.x < 6 * kChunk / 4)
-    ((u32q*)(slot + kSlotRows))[threadIdx.x] = ((const u32q*)&fac[0][0])[threadIdx.x];
+  u32q* const dt = (u32q*)(slot + kSlot.t());
+  dt[threadIdx.x] = ((const u32q*)st)[threadIdx.x];
+  if (threadIdx.x < 128) dt[256 + threadIdx.x] = ((const u32q*)st)[256 + threadIdx.x];
+  ((u32q*)(slot + kSlot.a()))[threadIdx.x] = ((const u32q*)sa)[threadIdx.x];
+  float* const df = (float*)(slot + kSlot.factors());
+  if (threadIdx.x < 2 * kChunk) df[kFactorRows + threadIdx.x] = (&rows[0][0])[threadIdx.x];
+  if (threadIdx.x == 0) df[kFactorRows + 2 * kChunk] = tfac;
 }
 
 // ------------------------------------------------------------------------------- scan
@@ -721,25 +806,23 @@ struct ScanState {
   }
 };
 
-template <int kF, int kG, int D, int kMode>
+// Chunk by chunk with S in registers. Operands come from the slot to LDS by direct loads: the
+// row matrices for the next chunk while this chunk's updates run, the rest while the next
+// chunk's products with S run; two barriers per chunk. Waves share the operands and own
+// columns: 4 waves for outputs; for a segment's transition half of the waves for B and half
+// for M.
+template <int kF, int D, int kMode>
 __global__ __launch_bounds__(kMode == kScanOut ? 256 : 4 * D, 2) void delta_rule_scan_kernel(const ChunkParams P) {
-  // For a segment's transition, half of the waves for B and half for M.
-  constexpr int kWaves = kMode == kScanOut ? 4 : D / 16, kThreads = 64 * kWaves;
-  constexpr int kColWaves = kMode == kScanOut ? 4 : D / 32;
-  typedef Rows<D, kWaves> RW;
-  constexpr int kRows = RW::kRows, kLanes = RW::kLanes, kGroups = RW::kGroups;
-  static_assert(kRows % 4 == 0, "rows are written to the transposed operand four at a time");
-  constexpr int kEB = elem_bytes<kF>(), kGB = elem_bytes<kG>();
   constexpr bool kOut = kMode == kScanOut;
+  constexpr int kWaves = kOut ? 4 : D / 16, kColWaves = kOut ? 4 : D / 32;
+  constexpr int kEB = elem_bytes<kF>();
   constexpr int kM = D / 16, kN = D / (16 * kColWaves), kK = D / 32;
-  constexpr int kLd = D + 8, kLt = kChunk + 8;  // halves per row: 16 rows reach all banks
-  __shared__ __attribute__((aligned(16))) _Float16 kg[2][kChunk * kLd];
-  __shared__ __attribute__((aligned(16))) _Float16 qg[2][kOut ? kChunk * kLd : 8];
-  __shared__ __attribute__((aligned(16))) _Float16 kt[2][D * kLt];
-  __shared__ __attribute__((aligned(16))) float tot[kGroups][D];
-  __shared__ __attribute__((aligned(16))) float decay[D];
-  // The chunk's slot, and the next one's on its way.
-  __shared__ __attribute__((aligned(16))) char held[2][kSlotUsed];
+  constexpr Slot kSlot{D};
+  constexpr int kMatrix = (int)kSlot.matrix();
+  __shared__ __attribute__((aligned(16))) char krows[kMatrix];
+  __shared__ __attribute__((aligned(16))) char qrows[kOut ? kMatrix : 16];
+  // K^T, factors, T and, for outputs, A, as in the slot.
+  __shared__ __attribute__((aligned(16))) char rest[kMatrix + 1024 + 6144 + (kOut ? 4096 : 0)];
   __shared__ float part[4];
 
   const RuleParams& R = P.R;
@@ -759,6 +842,22 @@ __global__ __launch_bounds__(kMode == kScanOut ? 256 : 4 * D, 2) void delta_rule
   const bool identity = !kOut && wave >= kColWaves;  // this wave's columns are M's
   const int col = wave % kColWaves * (16 * kN) + kN * n16;
   const int64_t cell = (int64_t)program * R.heads + h;
+
+  // The sequence's first chunk program is its number + its start / 32.
+  const char* slot = P.slots + ((int64_t)(piece.s + (seq.start >> 5) + begin) * R.heads + h) * kSlot.bytes();
+  const int64_t slot_step = R.heads * kSlot.bytes();
+  const auto copy = [&](const char* from, char* to, int pieces) {
+    for (int i = wave; i < pieces; i += kWaves) to_lds(from + 1024 * i + 16 * lane, to + 1024 * i);
+  };
+  const auto load_rows = [&](const char* from) {
+    copy(from + kSlot.kg(), krows, kMatrix / 1024);
+    if (kOut) copy(from + kSlot.qg(), qrows, kMatrix / 1024);
+  };
+  const auto load_rest = [&](const char* from) {
+    copy(from + kSlot.kt(), rest, kMatrix / 1024 + 7 + (kOut ? 4 : 0));
+  };
+  load_rows(slot);
+  load_rest(slot);
 
   ScanState<kM, kN> S;
   float most[kN];  // the largest magnitude among the lane's values of each column
@@ -800,83 +899,23 @@ __global__ __launch_bounds__(kMode == kScanOut ? 256 : 4 * D, 2) void delta_rule
     }
   }
 
-  const int group = RW::group(wave, lane), c = 2 * (lane % kLanes), row0 = group * kRows;
-  const int64_t qk = h / R.share;
-  const Gate gate(R, h);
-  f32x2 bias = {0.0f, 0.0f};
-  if (R.dt_bias != nullptr) bias = *(const f32x2a4*)(R.dt_bias + h * D + c);
-  const int slot0 = piece.s + (seq.start >> 5);  // the sequence's first chunk program
-  // Where this lane's two channels go in operand rows.
-  const int cpos = 32 * (c / 32) + place(c % 32);
+  const f16x8* const kq = (const f16x8*)krows;
+  const f16x8* const qq = (const f16x8*)qrows;
+  const f16x8* const kt = (const f16x8*)rest;
+  const float* const factors = (const float*)(rest + kMatrix);
+  const f16x8* const tp = (const f16x8*)(rest + kMatrix + 1024);
+  const f16x8* const ap = (const f16x8*)(rest + kMatrix + 1024 + 6144);
 
-  // A chunk's rows and slot, loaded one chunk ahead; values, when the chunk begins.
-  RawRows<kF, kRows> rk, rq;
-  RawRows<kG, kRows> rg;
-  const int wrow = RW::wave_row(wave), lrow = RW::lane_row(lane);
-  const bool same = R.g_cs == 0;
-  const auto window = [&](const char* base, int64_t ts, int64_t head, int eb, int row, int chunk) {
-    const int64_t first = seq.start + chunk * kChunk;
-    const int valid = seq.len - chunk * kChunk < kChunk ? seq.len - chunk * kChunk : kChunk;
-    return Window(base + (first * ts + head) * eb, valid, (uint32_t)ts * eb, row * eb);
-  };
-  const auto gates = [&](int chunk) { return window(R.g, R.g_ts, h * R.g_hs, kGB, same ? 1 : D, chunk); };
-  const auto keys = [&](int chunk) { return window(R.k, R.k_ts, qk * R.k_hs, kEB, D, chunk); };
-  const auto queries = [&](int chunk) { return window(R.q, R.q_ts, qk * R.q_hs, kEB, D, chunk); };
-  // The slot goes straight to LDS: 688 pieces of 16 bytes, T (384), A (256) and the row
-  // factors (48), 64 per wave and load.
-  const auto load_slot = [&](int chunk) {
-    const char* const slot = P.slots + ((int64_t)(slot0 + chunk) * R.heads + h) * kSlotBytes;
-    char* const into = held[chunk & 1];
-#pragma unroll
-    for (int i = 0; i < kSlotUsed / 16; i += kThreads)
-      if (i + kThreads <= kSlotUsed / 16 || threadIdx.x < kSlotUsed / 16 - i)
-        to_lds(slot + 16 * (i + threadIdx.x), into + 16 * (i + 64 * wave));
-  };
-  {
-    const Window wg = gates(begin), wk = keys(begin);
-    if (same)
-      rg.load_same(wg, lrow * wg.stride, wrow);
-    else
-      rg.load(wg, lrow * wg.stride + c * kGB, wrow);
-    rk.load(wk, lrow * wk.stride + c * kEB, wrow);
-    if (kOut) {
-      const Window wq = queries(begin);
-      rq.load(wq, lrow * wq.stride + c * kEB, wrow);
-    }
-    load_slot(begin);
-  }
+  // Loads to LDS are counted per wave: each waits for its own before a barrier that lets the
+  // others read.
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
 
   for (int chunk = begin; chunk < end; ++chunk) {
     const int64_t first = seq.start + chunk * kChunk;
     const int valid = seq.len - chunk * kChunk < kChunk ? seq.len - chunk * kChunk : kChunk;
-    const char* const slot = held[chunk & 1];
-    const float* const fac = (const float*)(slot + kSlotRows);
-
-    // ---- operands
-    f32x2 q[kRows], k[kRows], p[kRows];
-    rg.values(p, same);
-    gate.eval(p, bias);
-    mask_rows(p, row0, valid);
-    rk.values(k);
-    mask_rows(k, row0, valid);
-    if (kOut) {
-      rq.values(q);
-      mask_rows(q, row0, valid);
-    }
-    f32x2 rest[kRows];  // log2 decay after each row, inside the group
-    rest[kRows - 1] = f32x2{0.0f, 0.0f};
-#pragma unroll
-    for (int i = kRows - 1; i > 0; --i) rest[i - 1] = rest[i] + p[i];
-#pragma unroll
-    for (int i = 1; i < kRows; ++i) p[i] += p[i - 1];
-    *(f32x2*)&tot[group][c] = p[kRows - 1];
-    // The slot's loads to LDS are counted per wave: each waits for its own before the barrier
-    // that lets the others read. Also: every wave is done with the operands of the chunk
-    // before.
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    typename Pair<kF>::raw rv[8];  // rows 16 t + 4 (lane / 16) + r, this lane's columns
-    {
+    typename Pair<kF>::raw rv[8];  // values: rows 16 t + 4 (lane / 16) + r, this lane's columns
+    if (!identity) {
       const Window wv(R.v + (first * R.v_ts + h * R.v_hs) * kEB, valid, (uint32_t)R.v_ts * kEB, D * kEB);
       const uint32_t at = fresh(n4) * (4 * wv.stride) + col * kEB;
 #pragma unroll
@@ -885,64 +924,7 @@ __global__ __launch_bounds__(kMode == kScanOut ? 256 : 4 * D, 2) void delta_rule
         rv[i] = kN == 2 ? Cell<kF>::pair(wv, at, row) : Cell<kF>::one(wv, at, row);
       }
     }
-    if (identity || valid != kChunk) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (identity || 16 * (i / 4) + 4 * n4 + i % 4 >= valid) rv[i] = Pair<kF>::zero();
-    }
-    f32x2 before = {0.0f, 0.0f}, after = {0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      const f32x2 t = *(const f32x2*)&tot[i][c];
-      if (i < group) before += t;
-      if (i > group) after += t;
-    }
-    if (group == 0) {
-      const f32x2 d = p[kRows - 1] + after;
-      *(f32x2*)&decay[c] = f32x2{exp2_hw(d.x), exp2_hw(d.y)};
-    }
-    // The rows' factors before any of the stores below: LDS serves a wave in order.
-    float kf[kRows], qf[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; i += 4) {
-      const f32x4 a = *(const f32x4*)(fac + row0 + i);
-      f32x4 b = a;
-      if (kOut) b = *(const f32x4*)(fac + 2 * kChunk + row0 + i);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        kf[i + e] = a[e];
-        qf[i + e] = b[e];
-      }
-    }
-    f16x2 th[kRows], tl[kRows];
-    const int cw = fresh(cpos), tw = fresh(c * kLt);
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int r = row0 + i;
-      const f32x2 unit = k[i] * kf[i];
-      const f32x2 up = p[i] + before, down = rest[i] + after;
-      const f32x2 e = {exp2_hw(up.x), exp2_hw(up.y)};
-      const HalfPair g = split2(unit * e, R.one);
-      *(f16x2*)&kg[0][r * kLd + cw] = g.hi;
-      *(f16x2*)&kg[1][r * kLd + cw] = g.lo;
-      const HalfPair t = split2(unit * f32x2{exp2_hw(down.x), exp2_hw(down.y)}, R.one);
-      th[i] = t.hi;
-      tl[i] = t.lo;
-      if (kOut) {
-        const HalfPair w = split2(q[i] * qf[i] * e, R.one);
-        *(f16x2*)&qg[0][r * kLd + cw] = w.hi;
-        *(f16x2*)&qg[1][r * kLd + cw] = w.lo;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kRows; i += 4) {
-      const int at = place(row0 + i);  // 4 rows in a row of the transposed operand
-      *(f16x4*)&kt[0][tw + at] = f16x4{th[i].x, th[i + 1].x, th[i + 2].x, th[i + 3].x};
-      *(f16x4*)&kt[0][tw + kLt + at] = f16x4{th[i].y, th[i + 1].y, th[i + 2].y, th[i + 3].y};
-      *(f16x4*)&kt[1][tw + at] = f16x4{tl[i].x, tl[i + 1].x, tl[i + 2].x, tl[i + 3].x};
-      *(f16x4*)&kt[1][tw + kLt + at] = f16x4{tl[i].y, tl[i + 1].y, tl[i + 2].y, tl[i + 3].y};
-    }
-    __syncthreads();
+
     // ---- Y = (K e^G) S and O = (Q e^G) S
     f32x4 Y[2][kN], O[2][kN];
 #pragma unroll
@@ -950,26 +932,17 @@ __global__ __launch_bounds__(kMode == kScanOut ? 256 : 4 * D, 2) void delta_rule
 #pragma unroll
       for (int n = 0; n < kN; ++n) Y[t][n] = O[t][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     // Steps of (32 channels, 16 rows). A step's left operands are read while the step before
-    // runs, and one row of the next chunk's inputs is loaded (after the last chunk: that
-    // chunk's own again), so that neither waits on the other. The scheduling barriers keep
-    // the steps apart.
-    const int next = chunk + 1 < end ? chunk + 1 : chunk;
-    if (chunk + 1 < end) load_slot(next);
-    const Window wg = gates(next), wk = keys(next), wq = queries(next);
-    const uint32_t g_at = fresh(lrow) * wg.stride + (same ? 0 : c * kGB);
-    const uint32_t k_at = fresh(lrow) * wk.stride + c * kEB, q_at = fresh(lrow) * wq.stride + c * kEB;
-    if (same) rg.load_same(wg, g_at, wrow);
+    // runs; the scheduling barriers keep the steps apart.
     f16x8 kh, kl, qh, ql;
     const auto read_step = [&](int step) {
-      const int at = (16 * (step & 1) + n16) * kLd + 32 * (step >> 1) + 8 * n4;
-      kh = *(const f16x8*)&kg[0][at];
-      kl = *(const f16x8*)&kg[1][at];
+      const int kk = step >> 1, at = step * 128 + 16 * n4 + (n16 ^ (n4 + 4 * kk));
+      kh = kq[at];
+      kl = kq[at + 64];
       if (kOut) {
-        qh = *(const f16x8*)&qg[0][at];
-        ql = *(const f16x8*)&qg[1][at];
+        qh = qq[at];
+        ql = qq[at + 64];
       }
     };
-    static_assert(2 * kK >= kRows, "a row per step");
     read_step(0);
     Operand b[kN];
 #pragma unroll
@@ -977,11 +950,6 @@ __global__ __launch_bounds__(kMode == kScanOut ? 256 : 4 * D, 2) void delta_rule
       const int t = step & 1;
       const f16x8 ch = kh, cl = kl, dh = qh, dl = ql;
       if (step + 1 < 2 * kK) read_step(step + 1);
-      if (step < kRows) {
-        if (!same) rg.r[step] = Cell<kG>::pair(wg, g_at, wrow + step);
-        rk.r[step] = Cell<kF>::pair(wk, k_at, wrow + step);
-        if (kOut) rq.r[step] = Cell<kF>::pair(wq, q_at, wrow + step);
-      }
       if (t == 0) {
 #pragma unroll
         for (int n = 0; n < kN; ++n) b[n] = split8(S.s[step][n], S.s[step + 1][n], R.one);
@@ -1003,18 +971,27 @@ __global__ __launch_bounds__(kMode == kScanOut ? 256 : 4 * D, 2) void delta_rule
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    // This chunk's other operands have arrived, and all waves are done with its rows.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    slot += slot_step;
+    if (chunk + 1 < end) load_rows(slot);
 
     // ---- X = V - n Y, in the columns' scales
+    if (identity || valid != kChunk) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (identity || 16 * (i / 4) + 4 * n4 + i % 4 >= valid) rv[i] = Pair<kF>::zero();
+    }
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const f32x4 nt = *(const f32x4*)(fac + 3 * kChunk + 16 * t + 4 * n4);
+      const f32x4 nt = *(const f32x4*)(factors + kFactorRows + 16 * t + 4 * n4);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float n_t = nt[r];
         const f32x2 v = Pair<kF>::value(rv[4 * t + r]);
 #pragma unroll
         for (int n = 0; n < kN; ++n)
-          Y[t][n][r] = __builtin_fmaf(v[n], S.scale[n], -n_t * Y[t][n][r]);
+          Y[t][n][r] = __builtin_fmaf(v[n], S.scale[n], -nt[r] * Y[t][n][r]);
       }
     }
     // The columns' range over S and X.
@@ -1046,10 +1023,9 @@ __global__ __launch_bounds__(kMode == kScanOut ? 256 : 4 * D, 2) void delta_rule
     // ---- U = T X
     f32x4 U[2][kN];
     {
-      const f16x8* const tp = (const f16x8*)(slot + kSlotT);
 #pragma unroll
       for (int n = 0; n < kN; ++n) b[n] = split8(Y[0][n], Y[1][n], R.one);
-      const float us = fac[5 * kChunk];
+      const float us = factors[kFactorRows + 2 * kChunk];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const f16x8 th = tp[64 * t + lane], tl = tp[128 + 64 * t + lane], tr = tp[256 + 64 * t + lane];
@@ -1097,10 +1073,9 @@ __global__ __launch_bounds__(kMode == kScanOut ? 256 : 4 * D, 2) void delta_rule
     f16x8 ah, al;
     f32x4 d;
     const auto read_tile = [&](int m) {
-      d = *(const f32x4*)&decay[16 * m + 4 * n4];
-      const int at = (16 * m + n16) * kLt + 8 * n4;
-      ah = *(const f16x8*)&kt[0][at];
-      al = *(const f16x8*)&kt[1][at];
+      d = *(const f32x4*)(factors + 16 * m + 4 * n4);
+      ah = kt[128 * m + lane];
+      al = kt[128 * m + 64 + lane];
     };
     read_tile(0);
 #pragma unroll
@@ -1119,11 +1094,10 @@ __global__ __launch_bounds__(kMode == kScanOut ? 256 : 4 * D, 2) void delta_rule
     if (kOut) {
       const Window wo(R.out + (first * R.heads + h) * (D * kEB), valid, (uint32_t)R.heads * (D * kEB), D * kEB);
       const uint32_t at = fresh(n4) * (4 * wo.stride) + col * kEB;
-      const f16x8* const ap = (const f16x8*)(slot + kSlotA);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const f16x8 ah = ap[64 * t + lane], al = ap[128 + 64 * t + lane];
-        const f32x4 nq = *(const f32x4*)(fac + 4 * kChunk + 16 * t + 4 * n4);
+        const f32x4 nq = *(const f32x4*)(factors + kFactorRows + kChunk + 16 * t + 4 * n4);
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
           O[t][n] = mfma16(ah, u[n].hi, O[t][n]);
@@ -1161,6 +1135,10 @@ __global__ __launch_bounds__(kMode == kScanOut ? 256 : 4 * D, 2) void delta_rule
         most[n] *= f;
       }
     }
+    // The next chunk's rows have arrived, and all waves are done with this chunk.
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (chunk + 1 < end) load_rest(slot);
   }
 
   // ---- the end
@@ -1330,10 +1308,10 @@ void launch_chunks(const ChunkParams& P, hipStream_t st) {
   const unsigned segments = (unsigned)P.segment_programs * heads;
   hipLaunchKernelGGL((delta_rule_prepare_kernel<kF, kG, D>), dim3(chunks), dim3(256), 0, st, P);
   if (P.moves != nullptr) {
-    hipLaunchKernelGGL((delta_rule_scan_kernel<kF, kG, D, kScanMove>), dim3(segments), dim3(4 * D), 0, st, P);
+    hipLaunchKernelGGL((delta_rule_scan_kernel<kF, D, kScanMove>), dim3(segments), dim3(4 * D), 0, st, P);
     hipLaunchKernelGGL((delta_rule_join_kernel<D>), dim3(segments * (D / 16)), dim3(256), 0, st, P);
   }
-  hipLaunchKernelGGL((delta_rule_scan_kernel<kF, kG, D, kScanOut>), dim3(segments), dim3(256), 0, st, P);
+  hipLaunchKernelGGL((delta_rule_scan_kernel<kF, D, kScanOut>), dim3(segments), dim3(256), 0, st, P);
 }
 
 template <int kF, int kG>
