@@ -42,6 +42,18 @@ struct RuleParams {
 
 constexpr int kChunk = 32;  // tokens per chunk
 
+// How pieces of sequences are numbered: sequence s owns programs v(s) up to v(s + 1), where
+// v(s) = s * extra + floor(start of s / tokens). With `extra` 1 that is at least
+// ceil(n / tokens) programs for any n tokens. With `extra` 0 it is at least one program for
+// every `tokens` full tokens, and none for many of the sequences that are shorter. Either
+// way the number of programs needs no lengths.
+struct Pieces {
+  int32_t tokens, extra;
+  __host__ __device__ int32_t first(int32_t s, int64_t start) const {
+    return s * extra + (int32_t)((uint32_t)start / (uint32_t)tokens);
+  }
+};
+
 // What the chunked kernels need beside the call: where chunks and segments lie, and the
 // scratch memory.
 struct ChunkParams {
@@ -50,7 +62,8 @@ struct ChunkParams {
   float* ends;  // head_dim^2 per (segment program, head): a segment's end, then a start
   char* moves;  // move_bytes per (segment program, head): the segment's transition
   int32_t chunk_programs, segment_programs;
-  int32_t segment_shift;  // log2 of the tokens per segment
+  Pieces chunk_pieces, segment_pieces;
+  int32_t segment_chunks;  // chunks per segment
   int32_t search_top;  // 64^(levels - 1), 64^levels >= num_seqs
   int32_t min_len;  // shorter sequences are left to the step kernel
 };

@@ -22,7 +22,8 @@ struct Plan {
   bool chunks;  // the chunked kernels take the others
   bool segments;  // sequences of several segments are possible
   int64_t max_len;
-  int segment_shift;  // log2 of the tokens per segment
+  int segment_chunks;
+  Pieces chunk_pieces, segment_pieces;
   int64_t chunk_programs, segment_programs;
   int64_t slot_bytes, ends_bytes, moves_bytes;
 };
@@ -31,10 +32,9 @@ struct Plan {
 constexpr int64_t kStepTokens = 8;
 // The step kernel is launched beside the chunked ones where sequences average under this.
 constexpr int64_t kStepAverage = 64;
-// Segments: as long as leaves about this many workgroups for a call of long sequences, from
-// 8 to 64 chunks.
-constexpr int64_t kSegmentCells = 512;
-constexpr int kSegmentShiftMin = 8, kSegmentShiftMax = 11;
+// Segments: as long as fills the card with about this many workgroups, and no shorter than
+// kSegmentMin chunks.
+constexpr int64_t kSegmentCells = 512, kSegmentMin = 4;
 
 int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 
@@ -43,12 +43,20 @@ Plan make_plan(int64_t tokens, int64_t seqs, int64_t heads, int64_t head_dim) {
   p.step = tokens <= kStepTokens || tokens < kStepAverage * seqs;
   p.chunks = tokens > kStepTokens;
   p.max_len = p.step ? kStepTokens : 0;
-  p.segment_shift = kSegmentShiftMin;
-  while (p.segment_shift < kSegmentShiftMax && (tokens >> p.segment_shift) * heads > kSegmentCells)
-    ++p.segment_shift;
-  p.segments = tokens > ((int64_t)1 << p.segment_shift);
-  p.chunk_programs = tokens / kChunk + seqs;
-  p.segment_programs = (tokens >> p.segment_shift) + seqs;
+  const int64_t cells = std::max(kSegmentCells - seqs * heads, kSegmentCells / 2);
+  const int64_t units = (tokens + kChunk - 1) / kChunk * heads;
+  p.segment_chunks = (int)std::max(kSegmentMin, (units + cells - 1) / cells);
+  p.segments = tokens > p.segment_chunks * kChunk;
+  const auto pieces = [&](int64_t piece_tokens, Pieces& how) {
+    const int64_t all = tokens / piece_tokens + seqs;
+    // Sequences of more than max_len tokens alone: max_len tokens and more per program are
+    // enough for a piece of 32 or more.
+    const int64_t longer = p.max_len > 0 ? tokens / p.max_len + 1 : all;
+    how = longer < all ? Pieces{(int32_t)p.max_len, 0} : Pieces{(int32_t)piece_tokens, 1};
+    return std::min(all, longer);
+  };
+  p.chunk_programs = pieces(kChunk, p.chunk_pieces);
+  p.segment_programs = pieces(p.segment_chunks * kChunk, p.segment_pieces);
   if (p.chunks) {
     p.slot_bytes = round256(p.chunk_programs * heads * Slot{head_dim}.bytes());
     if (p.segments) {
@@ -239,7 +247,9 @@ extern "C" int kdaconv_gated_delta_rule(const kdaconv_rule_args* args, void* wor
     P.moves = plan.segments ? P.slots + plan.slot_bytes + plan.ends_bytes : nullptr;
     P.chunk_programs = (int32_t)plan.chunk_programs;
     P.segment_programs = (int32_t)plan.segment_programs;
-    P.segment_shift = plan.segment_shift;
+    P.chunk_pieces = plan.chunk_pieces;
+    P.segment_pieces = plan.segment_pieces;
+    P.segment_chunks = plan.segment_chunks;
     int64_t reach = kRuleWave;
     while (reach < args->num_seqs) reach *= kRuleWave;
     P.search_top = (int32_t)(reach / kRuleWave);

@@ -100,16 +100,14 @@ __device__ __forceinline__ Operand split8(f32x4 a, f32x4 b, float one) {
 // place 8 ((x % 16) / 4) + 4 (x / 16) + x % 4.
 __device__ __forceinline__ int place(int x) { return 8 * ((x & 15) >> 2) + 4 * (x >> 4) + (x & 3); }
 
-// The sequence and piece that program p owns when pieces of 2^shift tokens are counted by
-// v(s) = s + (start of s >> shift): the largest s with v(s) <= p, and p - v(s). A sequence
-// of n tokens has at most v(s + 1) - v(s) pieces, so every piece has a program and the
-// program count needs no lengths. A 64-way search, one ballot per level. Returns s = -1
-// when no sequence starts early enough.
+// The sequence and piece that program p owns: the largest s with v(s) <= p, and p - v(s),
+// where v(s) numbers the sequence's first program (see Pieces). A 64-way search, one ballot
+// per level. Returns s = -1 when no sequence starts early enough.
 struct Piece {
   int s, index;
 };
 
-__device__ __forceinline__ Piece find_piece(const ChunkParams& P, int p, int shift, int lane) {
+__device__ __forceinline__ Piece find_piece(const ChunkParams& P, const Pieces& pieces, int p, int lane) {
   const RuleParams& R = P.R;
   int base = 0, v = 0;
   for (int stride = P.search_top; stride > 0; stride >>= 6) {
@@ -119,7 +117,7 @@ __device__ __forceinline__ Piece find_piece(const ChunkParams& P, int p, int shi
     if (ok) {
       int a = R.qsl[s];
       a = a < 0 ? 0 : (a > R.num_tokens ? R.num_tokens : a);
-      at = s + (a >> shift);
+      at = pieces.first(s, a);
       ok = at <= p;
     }
     const uint64_t mask = __ballot(ok);
@@ -293,7 +291,8 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
   constexpr int kBytes = 3 * kMat * 4 > kStage + 128 * D ? 3 * kMat * 4 : kStage + 128 * D;
   // Operand rows q, k (times the decay from the block's middle) and columns k.
   __shared__ __attribute__((aligned(16))) char shared[kBytes];
-  __shared__ __attribute__((aligned(16))) float tot[8][D];
+  // The groups' decays, read before the operands take their place.
+  float (*const tot)[D] = (float (*)[D])shared;
   __shared__ __attribute__((aligned(16))) float across[D];
   // Per row: the key's factor times 16, the query's times 16, the key's power of two; and
   // as they go to the slot |k| / 16, the outputs' factor / 16 and T's factor.
@@ -313,7 +312,7 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
   const RuleParams& R = P.R;
   const int program = blockIdx.x / R.heads, h = blockIdx.x % R.heads;
   const int wave = uniform(threadIdx.x / kRuleWave), lane = threadIdx.x % kRuleWave;
-  const Piece piece = find_piece(P, program, 5, lane);
+  const Piece piece = find_piece(P, P.chunk_pieces, program, lane);
   if (piece.s < 0) return;
   const Sequence seq(R, piece.s);
   if (seq.len < P.min_len || piece.index * kChunk >= seq.len) return;
@@ -429,6 +428,7 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
     const f32x2 d = all[0] - mid[0] + mid[1];
     *(f32x2*)&across[c] = f32x2{exp2_hw(d.x), exp2_hw(d.y)};
   }
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int r = RW::wave_row(wave, i) + lrow, j = i / 4;
@@ -828,11 +828,11 @@ __global__ __launch_bounds__(kMode == kScanOut ? 256 : 4 * D, 2) void delta_rule
   const RuleParams& R = P.R;
   const int program = blockIdx.x / R.heads, h = blockIdx.x % R.heads;
   const int wave = uniform(threadIdx.x / kRuleWave), lane = threadIdx.x % kRuleWave;
-  const Piece piece = find_piece(P, program, P.segment_shift, lane);
+  const Piece piece = find_piece(P, P.segment_pieces, program, lane);
   if (piece.s < 0) return;
   const Sequence seq(R, piece.s);
   if (seq.len < P.min_len) return;
-  const int per = 1 << (P.segment_shift - 5);  // chunks per segment
+  const int per = P.segment_chunks;
   const int chunks = (seq.len + kChunk - 1) / kChunk;
   const int begin = piece.index * per, end = begin + per < chunks ? begin + per : chunks;
   if (begin >= chunks) return;
@@ -843,8 +843,7 @@ __global__ __launch_bounds__(kMode == kScanOut ? 256 : 4 * D, 2) void delta_rule
   const int col = wave % kColWaves * (16 * kN) + kN * n16;
   const int64_t cell = (int64_t)program * R.heads + h;
 
-  // The sequence's first chunk program is its number + its start / 32.
-  const char* slot = P.slots + ((int64_t)(piece.s + (seq.start >> 5) + begin) * R.heads + h) * kSlot.bytes();
+  const char* slot = P.slots + ((int64_t)(P.chunk_pieces.first(piece.s, seq.start) + begin) * R.heads + h) * kSlot.bytes();
   const int64_t slot_step = R.heads * kSlot.bytes();
   const auto copy = [&](const char* from, char* to, int pieces) {
     for (int i = wave; i < pieces; i += kWaves) to_lds(from + 1024 * i + 16 * lane, to + 1024 * i);
@@ -1206,96 +1205,105 @@ __global__ __launch_bounds__(kMode == kScanOut ? 256 : 4 * D, 2) void delta_rule
 
 // The starts of a sequence's segments: ends[0] is segment 0's end and so segment 1's
 // start; ends[j] <- M_j ends[j - 1] + ends[j] makes it segment j + 1's start. One workgroup
-// per (sequence, head, 16 columns); wave w owns rows D / 4 w .. of the columns and hands
-// its operands to the others through LDS.
+// per (sequence, head, 16 columns); wave w owns rows 16 w .. of the columns and hands its
+// operands to the others through LDS. A step is short, so M and B are loaded kAhead steps
+// ahead. Workgroups of one (sequence, head) read the same M: the grid's rows are whole
+// multiples of 8, which puts them on one of the card's 8 dies and in one L2.
 template <int D>
-__global__ __launch_bounds__(256) void delta_rule_join_kernel(const ChunkParams P) {
-  constexpr int kK = D / 32, kT = D / 64, kSlices = D / 16;  // row tiles per wave
+__global__ __launch_bounds__(4 * D, 2) void delta_rule_join_kernel(const ChunkParams P) {
+  constexpr int kK = D / 32, kWaves = D / 16, kAhead = 2;
   __shared__ __attribute__((aligned(16))) _Float16 hi[2][kK][64 * 8], lo[2][kK][64 * 8];
-  __shared__ float most[2][4][16];
+  __shared__ float most[2][kWaves][16];
   const RuleParams& R = P.R;
-  const int slice = blockIdx.x % kSlices, id = blockIdx.x / kSlices;
-  const int program = id / R.heads, h = id % R.heads;
+  const int program = blockIdx.x / R.heads, h = blockIdx.x % R.heads, slice = blockIdx.y;
   const int wave = uniform(threadIdx.x / kRuleWave), lane = threadIdx.x % kRuleWave;
-  const Piece piece = find_piece(P, program, P.segment_shift, lane);
+  if (program >= P.segment_programs) return;
+  const Piece piece = find_piece(P, P.segment_pieces, program, lane);
   if (piece.s < 0 || piece.index != 0) return;
   const Sequence seq(R, piece.s);
   if (seq.len < P.min_len) return;
-  const int segments = (seq.len + (1 << P.segment_shift) - 1) >> P.segment_shift;
+  const int chunks = (seq.len + kChunk - 1) / kChunk;
+  const int segments = (chunks + P.segment_chunks - 1) / P.segment_chunks;
+  if (segments < 3) return;
   const int n16 = lane % 16, n4 = lane / 16;
   const int64_t cell = (int64_t)program * R.heads + h;
-  float* end = P.ends + cell * (D * D) + 16 * slice + n16;
-  const char* move = P.moves + cell * move_bytes(D);
-  const int row0 = 16 * kT * wave + 4 * n4;
-  f32x4 S[kT];
-  if (segments < 3) return;
+  float* const ends = P.ends + cell * (D * D) + (16 * wave + 4 * n4) * D + 16 * slice + n16;
+  const char* const moves = P.moves + cell * move_bytes(D);
+
+  // A step's M rows and B.
+  struct Step {
+    f16x8 ah[kK], al[kK];
+    float back;
+    f32x4 B;
+  };
+  const auto load = [&](int j, Step& x) {
+    j = j < segments - 1 ? j : segments - 2;
+    const char* const move = moves + (int64_t)j * R.heads * move_bytes(D);
+    const f16x8* const a = (const f16x8*)move + wave * kK * 64 + lane;
 #pragma unroll
-  for (int t = 0; t < kT; ++t)
+    for (int kk = 0; kk < kK; ++kk) {
+      x.ah[kk] = a[64 * kk];
+      x.al[kk] = a[64 * kk + D * D / 8];
+    }
+    x.back = *(const float*)(move + (int64_t)D * D * 4);
+    const float* const end = ends + (int64_t)j * R.heads * (D * D);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) S[t][r] = end[(row0 + 16 * t + r) * D];
-  for (int j = 1; j < segments - 1; ++j) {
+    for (int r = 0; r < 4; ++r) x.B[r] = end[r * D];
+  };
+  f32x4 S;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) S[r] = ends[r * D];
+  const auto step = [&](int j, const Step& x) {
     const int buf = j & 1;
-    end += (int64_t)R.heads * (D * D);
-    move += (int64_t)R.heads * move_bytes(D);
-    f16x8 ah[kT][kK], al[kT][kK];
-#pragma unroll
-    for (int t = 0; t < kT; ++t)
-#pragma unroll
-      for (int kk = 0; kk < kK; ++kk) {
-        const f16x8* const a = (const f16x8*)move + ((kT * wave + t) * kK + kk) * 64 + lane;
-        ah[t][kk] = a[0];
-        al[t][kk] = a[D * D / 8];
-      }
-    const float back = *(const float*)(move + (int64_t)D * D * 4);
-    f32x4 B[kT];
-    float m = 0.0f;
-#pragma unroll
-    for (int t = 0; t < kT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        B[t][r] = end[(row0 + 16 * t + r) * D];
-        m = __builtin_fmaxf(m, __builtin_fabsf(S[t][r]));
-      }
+    float m = __builtin_fmaxf(__builtin_fmaxf(__builtin_fabsf(S[0]), __builtin_fabsf(S[1])),
+                              __builtin_fmaxf(__builtin_fabsf(S[2]), __builtin_fabsf(S[3])));
     m = column_max(m);
     if (n4 == 0) most[buf][wave][n16] = m;
     __syncthreads();
-    m = __builtin_fmaxf(__builtin_fmaxf(most[buf][0][n16], most[buf][1][n16]),
-                        __builtin_fmaxf(most[buf][2][n16], most[buf][3][n16]));
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) m = __builtin_fmaxf(m, most[buf][w][n16]);
     int e = 0;
     if (m > 0.0f && m < __builtin_huge_valf()) e = kColExp - __builtin_amdgcn_frexp_expf(m);
     e = e > 100 ? 100 : e;
+    {
+      f32x4 s;
 #pragma unroll
-    for (int t = 0; t < kT; ++t) {
-      const int tile = kT * wave + t;
-      f32x4 x;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) x[r] = __builtin_amdgcn_ldexpf(S[t][r], e);
-      const HalfPair p0 = split2(f32x2{x[0], x[1]}, R.one), p1 = split2(f32x2{x[2], x[3]}, R.one);
-      const int at = lane * 8 + 4 * (tile & 1);
-      *(f16x4*)&hi[buf][tile / 2][at] = f16x4{p0.hi.x, p0.hi.y, p1.hi.x, p1.hi.y};
-      *(f16x4*)&lo[buf][tile / 2][at] = f16x4{p0.lo.x, p0.lo.y, p1.lo.x, p1.lo.y};
+      for (int r = 0; r < 4; ++r) s[r] = __builtin_amdgcn_ldexpf(S[r], e);
+      const HalfPair p0 = split2(f32x2{s[0], s[1]}, R.one), p1 = split2(f32x2{s[2], s[3]}, R.one);
+      const int at = lane * 8 + 4 * (wave & 1);
+      *(f16x4*)&hi[buf][wave / 2][at] = f16x4{p0.hi.x, p0.hi.y, p1.hi.x, p1.hi.y};
+      *(f16x4*)&lo[buf][wave / 2][at] = f16x4{p0.lo.x, p0.lo.y, p1.lo.x, p1.lo.y};
     }
     __syncthreads();
-    const float f = __builtin_amdgcn_ldexpf(back, -e);
-#pragma unroll
-    for (int t = 0; t < kT; ++t) S[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const float f = __builtin_amdgcn_ldexpf(x.back, -e);
+    f32x4 hh = {0.0f, 0.0f, 0.0f, 0.0f}, hl = hh, lh = hh;
 #pragma unroll
     for (int kk = 0; kk < kK; ++kk) {
       const f16x8 bh = *(const f16x8*)&hi[buf][kk][lane * 8], bl = *(const f16x8*)&lo[buf][kk][lane * 8];
-#pragma unroll
-      for (int t = 0; t < kT; ++t) {
-        S[t] = mfma16(ah[t][kk], bh, S[t]);
-        S[t] = mfma16(ah[t][kk], bl, S[t]);
-        S[t] = mfma16(al[t][kk], bh, S[t]);
-      }
+      hh = mfma16(x.ah[kk], bh, hh);
+      hl = mfma16(x.ah[kk], bl, hl);
+      lh = mfma16(x.al[kk], bh, lh);
     }
+    hh += hl + lh;
+    float* const end = ends + (int64_t)j * R.heads * (D * D);
 #pragma unroll
-    for (int t = 0; t < kT; ++t)
+    for (int r = 0; r < 4; ++r) {
+      S[r] = __builtin_fmaf(hh[r], f, x.B[r]);
+      end[r * D] = S[r];
+    }
+  };
+  // Left from the middle: a condition around each step made the compiler move the loaded
+  // registers at its end, and so wait for them.
+  Step x[kAhead + 1];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        S[t][r] = __builtin_fmaf(S[t][r], f, B[t][r]);
-        end[(row0 + 16 * t + r) * D] = S[t][r];
-      }
+  for (int i = 0; i < kAhead; ++i) load(1 + i, x[i]);
+  for (int j = 1;;) {
+#pragma unroll
+    for (int i = 0; i <= kAhead; ++i) {
+      load(j + kAhead, x[(i + kAhead) % (kAhead + 1)]);
+      step(j, x[i]);
+      if (++j == segments - 1) return;
+    }
   }
 }
 
@@ -1309,7 +1317,7 @@ void launch_chunks(const ChunkParams& P, hipStream_t st) {
   hipLaunchKernelGGL((delta_rule_prepare_kernel<kF, kG, D>), dim3(chunks), dim3(256), 0, st, P);
   if (P.moves != nullptr) {
     hipLaunchKernelGGL((delta_rule_scan_kernel<kF, D, kScanMove>), dim3(segments), dim3(4 * D), 0, st, P);
-    hipLaunchKernelGGL((delta_rule_join_kernel<D>), dim3(segments * (D / 16)), dim3(256), 0, st, P);
+    hipLaunchKernelGGL((delta_rule_join_kernel<D>), dim3((segments + 7) / 8 * 8, D / 16), dim3(4 * D), 0, st, P);
   }
   hipLaunchKernelGGL((delta_rule_scan_kernel<kF, D, kScanOut>), dim3(segments), dim3(256), 0, st, P);
 }
