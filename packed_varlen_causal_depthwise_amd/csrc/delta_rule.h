@@ -44,9 +44,8 @@ constexpr int kChunk = 32;  // tokens per chunk
 
 // How pieces of sequences are numbered: sequence s owns programs v(s) up to v(s + 1), where
 // v(s) = s * extra + floor(start of s / tokens). With `extra` 1 that is at least
-// ceil(n / tokens) programs for any n tokens. With `extra` 0 it is at least one program for
-// every `tokens` full tokens, and none for many of the sequences that are shorter. Either
-// way the number of programs needs no lengths.
+// ceil(n / tokens) programs for any n tokens, with `extra` 0 at least floor(n / tokens), and
+// then none for most shorter sequences. Either way the number of programs needs no lengths.
 struct Pieces {
   int32_t tokens, extra;
   __host__ __device__ int32_t first(int32_t s, int64_t start) const {
@@ -59,10 +58,11 @@ struct Pieces {
 struct ChunkParams {
   RuleParams R;
   char* slots;  // a Slot per (chunk program, head)
-  float* ends;  // head_dim^2 per (segment program, head): a segment's end, then a start
-  char* moves;  // move_bytes per (segment program, head): the segment's transition
-  int32_t chunk_programs, segment_programs;
-  Pieces chunk_pieces, segment_pieces;
+  float* ends;  // head_dim^2 per (move program, head): a segment's end, then the next's start
+  char* moves;  // move_bytes per (move program, head): the segment's transition
+  // Chunks; segments; segments but a sequence's last; sequences of 3 segments and more.
+  int32_t chunk_programs, segment_programs, move_programs, join_programs;
+  Pieces chunk_pieces, segment_pieces, move_pieces, join_pieces;
   int32_t segment_chunks;  // chunks per segment
   int32_t search_top;  // 64^(levels - 1), 64^levels >= num_seqs
   int32_t min_len;  // shorter sequences are left to the step kernel

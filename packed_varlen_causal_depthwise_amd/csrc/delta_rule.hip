@@ -23,8 +23,8 @@ struct Plan {
   bool segments;  // sequences of several segments are possible
   int64_t max_len;
   int segment_chunks;
-  Pieces chunk_pieces, segment_pieces;
-  int64_t chunk_programs, segment_programs;
+  Pieces chunk_pieces, segment_pieces, move_pieces, join_pieces;
+  int64_t chunk_programs, segment_programs, move_programs, join_programs;
   int64_t slot_bytes, ends_bytes, moves_bytes;
 };
 
@@ -32,9 +32,9 @@ struct Plan {
 constexpr int64_t kStepTokens = 8;
 // The step kernel is launched beside the chunked ones where sequences average under this.
 constexpr int64_t kStepAverage = 64;
-// Segments: as long as fills the card with about this many workgroups, and no shorter than
-// kSegmentMin chunks.
-constexpr int64_t kSegmentCells = 512, kSegmentMin = 4;
+// Segments: as long as leaves a workgroup for each of this many CUs, twice that where the
+// sequences alone fill them, and no shorter than kSegmentMin chunks.
+constexpr int64_t kSegmentCells = 256, kSegmentMin = 4;
 
 int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 
@@ -43,10 +43,11 @@ Plan make_plan(int64_t tokens, int64_t seqs, int64_t heads, int64_t head_dim) {
   p.step = tokens <= kStepTokens || tokens < kStepAverage * seqs;
   p.chunks = tokens > kStepTokens;
   p.max_len = p.step ? kStepTokens : 0;
-  const int64_t cells = std::max(kSegmentCells - seqs * heads, kSegmentCells / 2);
+  const int64_t cells = seqs * heads > kSegmentCells ? kSegmentCells / 2 : kSegmentCells;
   const int64_t units = (tokens + kChunk - 1) / kChunk * heads;
   p.segment_chunks = (int)std::max(kSegmentMin, (units + cells - 1) / cells);
-  p.segments = tokens > p.segment_chunks * kChunk;
+  const int64_t segment = (int64_t)p.segment_chunks * kChunk;
+  p.segments = tokens > segment;
   const auto pieces = [&](int64_t piece_tokens, Pieces& how) {
     const int64_t all = tokens / piece_tokens + seqs;
     // Sequences of more than max_len tokens alone: max_len tokens and more per program are
@@ -56,12 +57,17 @@ Plan make_plan(int64_t tokens, int64_t seqs, int64_t heads, int64_t head_dim) {
     return std::min(all, longer);
   };
   p.chunk_programs = pieces(kChunk, p.chunk_pieces);
-  p.segment_programs = pieces(p.segment_chunks * kChunk, p.segment_pieces);
+  p.segment_programs = pieces(segment, p.segment_pieces);
+  // Of n tokens ceil(n / segment) - 1 <= floor(n / segment) segments are not the last.
+  p.move_pieces = Pieces{(int32_t)segment, 0};
+  p.move_programs = tokens / segment + 1;
+  p.join_pieces = Pieces{(int32_t)(2 * segment), 0};
+  p.join_programs = tokens / (2 * segment) + 1;
   if (p.chunks) {
     p.slot_bytes = round256(p.chunk_programs * heads * Slot{head_dim}.bytes());
     if (p.segments) {
-      p.ends_bytes = round256(p.segment_programs * heads * head_dim * head_dim * 4);
-      p.moves_bytes = p.segment_programs * heads * move_bytes((int)head_dim);
+      p.ends_bytes = round256(p.move_programs * heads * head_dim * head_dim * 4);
+      p.moves_bytes = p.move_programs * heads * move_bytes((int)head_dim);
     }
   }
   return p;
@@ -74,7 +80,8 @@ int64_t largest_grid(const kdaconv_rule_args* a, bool update) {
   const int64_t heads = std::max<int64_t>(1, a->num_heads);
   if (update) return a->num_seqs * heads;
   const Plan p = make_plan(a->num_tokens, a->num_seqs, heads, a->head_dim);
-  return std::max(p.chunk_programs, p.segment_programs * (a->head_dim / 16)) * heads;
+  // (Moves and joins are at most kSegmentCells + heads.)
+  return std::max(p.chunk_programs, p.segment_programs) * heads;
 }
 
 int validate_rule(const kdaconv_rule_args* a, bool update) {
@@ -247,8 +254,12 @@ extern "C" int kdaconv_gated_delta_rule(const kdaconv_rule_args* args, void* wor
     P.moves = plan.segments ? P.slots + plan.slot_bytes + plan.ends_bytes : nullptr;
     P.chunk_programs = (int32_t)plan.chunk_programs;
     P.segment_programs = (int32_t)plan.segment_programs;
+    P.move_programs = (int32_t)plan.move_programs;
+    P.join_programs = (int32_t)plan.join_programs;
     P.chunk_pieces = plan.chunk_pieces;
     P.segment_pieces = plan.segment_pieces;
+    P.move_pieces = plan.move_pieces;
+    P.join_pieces = plan.join_pieces;
     P.segment_chunks = plan.segment_chunks;
     int64_t reach = kRuleWave;
     while (reach < args->num_seqs) reach *= kRuleWave;

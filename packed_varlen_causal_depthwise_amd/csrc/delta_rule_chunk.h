@@ -828,7 +828,7 @@ __global__ __launch_bounds__(kMode == kScanOut ? 256 : 4 * D, 2) void delta_rule
   const RuleParams& R = P.R;
   const int program = blockIdx.x / R.heads, h = blockIdx.x % R.heads;
   const int wave = uniform(threadIdx.x / kRuleWave), lane = threadIdx.x % kRuleWave;
-  const Piece piece = find_piece(P, P.segment_pieces, program, lane);
+  const Piece piece = find_piece(P, kOut ? P.segment_pieces : P.move_pieces, program, lane);
   if (piece.s < 0) return;
   const Sequence seq(R, piece.s);
   if (seq.len < P.min_len) return;
@@ -841,12 +841,16 @@ __global__ __launch_bounds__(kMode == kScanOut ? 256 : 4 * D, 2) void delta_rule
   const int n16 = lane % 16, n4 = lane / 16;
   const bool identity = !kOut && wave >= kColWaves;  // this wave's columns are M's
   const int col = wave % kColWaves * (16 * kN) + kN * n16;
-  const int64_t cell = (int64_t)program * R.heads + h;
+  // The segment's end; for outputs the end of the segment before.
+  const int move = kOut ? P.move_pieces.first(piece.s, seq.start) + piece.index - 1 : program;
+  const int64_t cell = (int64_t)move * R.heads + h;
 
   const char* slot = P.slots + ((int64_t)(P.chunk_pieces.first(piece.s, seq.start) + begin) * R.heads + h) * kSlot.bytes();
   const int64_t slot_step = R.heads * kSlot.bytes();
   const auto copy = [&](const char* from, char* to, int pieces) {
-    for (int i = wave; i < pieces; i += kWaves) to_lds(from + 1024 * i + 16 * lane, to + 1024 * i);
+#pragma unroll
+    for (int i = 0; i < pieces; i += kWaves)
+      if (i + wave < pieces) to_lds(from + 1024 * (i + wave) + 16 * lane, to + 1024 * (i + wave));
   };
   const auto load_rows = [&](const char* from) {
     copy(from + kSlot.kg(), krows, kMatrix / 1024);
@@ -865,7 +869,7 @@ __global__ __launch_bounds__(kMode == kScanOut ? 256 : 4 * D, 2) void delta_rule
     if (begin == 0) {
       if (seq.init) from = R.states + seq.line * R.st_line + h * R.st_head;
     } else if (kOut) {
-      from = P.ends + (cell - R.heads) * (D * D);
+      from = P.ends + cell * (D * D);
     }
     if (from != nullptr && !identity) {
 #pragma unroll
@@ -970,8 +974,14 @@ __global__ __launch_bounds__(kMode == kScanOut ? 256 : 4 * D, 2) void delta_rule
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    // This chunk's other operands have arrived, and all waves are done with its rows.
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // This chunk's other operands and values have arrived, and all waves are done with its
+    // rows. (Said of the values too: the compiler would wait for them at their use, and so
+    // for the loads issued until then.)
+    asm volatile("s_waitcnt vmcnt(0)"
+                 : "+v"(rv[0]), "+v"(rv[1]), "+v"(rv[2]), "+v"(rv[3]), "+v"(rv[4]), "+v"(rv[5]),
+                   "+v"(rv[6]), "+v"(rv[7])
+                 :
+                 : "memory");
     __syncthreads();
     slot += slot_step;
     if (chunk + 1 < end) load_rows(slot);
@@ -1217,8 +1227,8 @@ __global__ __launch_bounds__(4 * D, 2) void delta_rule_join_kernel(const ChunkPa
   const RuleParams& R = P.R;
   const int program = blockIdx.x / R.heads, h = blockIdx.x % R.heads, slice = blockIdx.y;
   const int wave = uniform(threadIdx.x / kRuleWave), lane = threadIdx.x % kRuleWave;
-  if (program >= P.segment_programs) return;
-  const Piece piece = find_piece(P, P.segment_pieces, program, lane);
+  if (program >= P.join_programs) return;
+  const Piece piece = find_piece(P, P.join_pieces, program, lane);
   if (piece.s < 0 || piece.index != 0) return;
   const Sequence seq(R, piece.s);
   if (seq.len < P.min_len) return;
@@ -1226,7 +1236,7 @@ __global__ __launch_bounds__(4 * D, 2) void delta_rule_join_kernel(const ChunkPa
   const int segments = (chunks + P.segment_chunks - 1) / P.segment_chunks;
   if (segments < 3) return;
   const int n16 = lane % 16, n4 = lane / 16;
-  const int64_t cell = (int64_t)program * R.heads + h;
+  const int64_t cell = (int64_t)P.move_pieces.first(piece.s, seq.start) * R.heads + h;
   float* const ends = P.ends + cell * (D * D) + (16 * wave + 4 * n4) * D + 16 * slice + n16;
   const char* const moves = P.moves + cell * move_bytes(D);
 
@@ -1314,10 +1324,11 @@ void launch_chunks(const ChunkParams& P, hipStream_t st) {
   const unsigned heads = (unsigned)P.R.heads;
   const unsigned chunks = (unsigned)P.chunk_programs * heads;
   const unsigned segments = (unsigned)P.segment_programs * heads;
+  const unsigned moves = (unsigned)P.move_programs * heads, joins = (unsigned)P.join_programs * heads;
   hipLaunchKernelGGL((delta_rule_prepare_kernel<kF, kG, D>), dim3(chunks), dim3(256), 0, st, P);
   if (P.moves != nullptr) {
-    hipLaunchKernelGGL((delta_rule_scan_kernel<kF, D, kScanMove>), dim3(segments), dim3(4 * D), 0, st, P);
-    hipLaunchKernelGGL((delta_rule_join_kernel<D>), dim3((segments + 7) / 8 * 8, D / 16), dim3(4 * D), 0, st, P);
+    hipLaunchKernelGGL((delta_rule_scan_kernel<kF, D, kScanMove>), dim3(moves), dim3(4 * D), 0, st, P);
+    hipLaunchKernelGGL((delta_rule_join_kernel<D>), dim3((joins + 7) / 8 * 8, D / 16), dim3(4 * D), 0, st, P);
   }
   hipLaunchKernelGGL((delta_rule_scan_kernel<kF, D, kScanOut>), dim3(segments), dim3(256), 0, st, P);
 }
