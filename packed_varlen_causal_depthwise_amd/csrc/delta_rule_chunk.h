@@ -808,13 +808,15 @@ struct ScanState {
 
 // Chunk by chunk with S in registers. Operands come from the slot to LDS by direct loads: the
 // row matrices for the next chunk while this chunk's updates run, the rest while the next
-// chunk's products with S run; two barriers per chunk. Waves share the operands and own
-// columns: 4 waves for outputs; for a segment's transition half of the waves for B and half
-// for M.
+// chunk's products with S run; two barriers per chunk. Waves share the operands and own 16
+// columns each; for a segment's transition half of the waves for B and half for M. (With 32
+// columns per wave the operands are read from LDS half as often, but the 172 matrix
+// instructions per chunk of a lone wave took 24 cycles each instead of 14: 20% longer with one
+// sequence of 64 tokens, 5% with many.)
 template <int kF, int D, int kMode>
-__global__ __launch_bounds__(kMode == kScanOut ? 256 : 4 * D, 2) void delta_rule_scan_kernel(const ChunkParams P) {
+__global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_rule_scan_kernel(const ChunkParams P) {
   constexpr bool kOut = kMode == kScanOut;
-  constexpr int kWaves = kOut ? 4 : D / 16, kColWaves = kOut ? 4 : D / 32;
+  constexpr int kColWaves = D / 16, kWaves = kOut ? kColWaves : 2 * kColWaves;
   constexpr int kEB = elem_bytes<kF>();
   constexpr int kM = D / 16, kN = D / (16 * kColWaves), kK = D / 32;
   constexpr Slot kSlot{D};
@@ -823,7 +825,7 @@ __global__ __launch_bounds__(kMode == kScanOut ? 256 : 4 * D, 2) void delta_rule
   __shared__ __attribute__((aligned(16))) char qrows[kOut ? kMatrix : 16];
   // K^T, factors, T and, for outputs, A, as in the slot.
   __shared__ __attribute__((aligned(16))) char rest[kMatrix + 1024 + 6144 + (kOut ? 4096 : 0)];
-  __shared__ float part[4];
+  __shared__ float part[8];
 
   const RuleParams& R = P.R;
   const int program = blockIdx.x / R.heads, h = blockIdx.x % R.heads;
@@ -1327,10 +1329,10 @@ void launch_chunks(const ChunkParams& P, hipStream_t st) {
   const unsigned moves = (unsigned)P.move_programs * heads, joins = (unsigned)P.join_programs * heads;
   hipLaunchKernelGGL((delta_rule_prepare_kernel<kF, kG, D>), dim3(chunks), dim3(256), 0, st, P);
   if (P.moves != nullptr) {
-    hipLaunchKernelGGL((delta_rule_scan_kernel<kF, D, kScanMove>), dim3(moves), dim3(4 * D), 0, st, P);
+    hipLaunchKernelGGL((delta_rule_scan_kernel<kF, D, kScanMove>), dim3(moves), dim3(8 * D), 0, st, P);
     hipLaunchKernelGGL((delta_rule_join_kernel<D>), dim3((joins + 7) / 8 * 8, D / 16), dim3(4 * D), 0, st, P);
   }
-  hipLaunchKernelGGL((delta_rule_scan_kernel<kF, D, kScanOut>), dim3(segments), dim3(256), 0, st, P);
+  hipLaunchKernelGGL((delta_rule_scan_kernel<kF, D, kScanOut>), dim3(segments), dim3(4 * D), 0, st, P);
 }
 
 template <int kF, int kG>
