@@ -59,7 +59,9 @@ struct ChunkParams {
   RuleParams R;
   char* slots;  // a Slot per (chunk program, head)
   float* ends;  // head_dim^2 per (move program, head): a segment's end, then the next's start
-  char* moves;  // move_bytes per (move program, head): the segment's transition
+  // move_bytes per (move program, head): the segment's transition; of a sequence's first
+  // segment a copy of the state that it starts from.
+  char* moves;
   // Chunks; segments; segments but a sequence's last; sequences of 3 segments and more.
   int32_t chunk_programs, segment_programs, move_programs, join_programs;
   Pieces chunk_pieces, segment_pieces, move_pieces, join_pieces;

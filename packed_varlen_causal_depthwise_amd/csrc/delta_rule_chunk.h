@@ -761,6 +761,7 @@ constexpr int kScanMove = 1;  // a segment's B and M
 
 constexpr float kColLow = 1.0f, kColHigh = 8192.0f;  // columns' largest value stays between
 constexpr int kColExp = 8;  // and is brought to 2^7 .. 2^8 when it leaves
+constexpr int kMostScale = 118;
 
 // kN column tiles of 16 per wave; lane l owns columns kN (l % 16) + n.
 template <int kM, int kN>
@@ -790,12 +791,14 @@ struct ScanState {
   }
 
   // The factor that brings a column whose largest value is m back (m from all its lanes).
-  static __device__ __forceinline__ float factor(float m) {
+  __device__ __forceinline__ float factor(int n, float m) const {
     if (!(m > 0.0f) || !(m < __builtin_huge_valf())) return 1.0f;
     if (m >= kColLow && m < kColHigh) return 1.0f;
-    int e = kColExp - __builtin_amdgcn_frexp_expf(m);
-    e = e > 100 ? 100 : (e < -100 ? -100 : e);
-    return __builtin_amdgcn_ldexpf(1.0f, e);
+    // The scale stays at most 2^kMostScale: a column that fades for long would take it to
+    // infinity (its values then go to zero as they are).
+    const int most = kMostScale + 1 - __builtin_amdgcn_frexp_expf(scale[n]);
+    const int e = kColExp - __builtin_amdgcn_frexp_expf(m);
+    return __builtin_amdgcn_ldexpf(1.0f, e < most ? e : most);
   }
 
   __device__ __forceinline__ void apply(int n, float f) {
@@ -869,7 +872,12 @@ __global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_ru
   {
     const float* from = nullptr;
     if (begin == 0) {
-      if (seq.init) from = R.states + seq.line * R.st_line + h * R.st_head;
+      // Of several segments the last one's outputs may end first, and with them the state:
+      // the first then starts from a copy, which the scan of its end leaves in M's place.
+      if (seq.init && kOut && chunks > per)
+        from = (const float*)(P.moves + (cell + R.heads) * move_bytes(D));
+      else if (seq.init)
+        from = R.states + seq.line * R.st_line + h * R.st_head;
     } else if (kOut) {
       from = P.ends + cell * (D * D);
     }
@@ -887,6 +895,15 @@ __global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_ru
             S.s[m][0][r] = *at;
           }
         }
+      if (!kOut) {
+        float* const copy_to = (float*)(P.moves + cell * move_bytes(D));
+#pragma unroll
+        for (int m = 0; m < kM; ++m)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int n = 0; n < kN; ++n) copy_to[(16 * m + 4 * n4 + r) * D + col + n] = S.s[m][n][r];
+      }
     } else {
 #pragma unroll
       for (int m = 0; m < kM; ++m)
@@ -899,7 +916,7 @@ __global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_ru
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
       S.scale[n] = S.inverse[n] = 1.0f;
-      S.apply(n, S.factor(column_max(S.largest(n))));
+      S.apply(n, S.factor(n, column_max(S.largest(n))));
       most[n] = S.largest(n);
     }
   }
@@ -994,38 +1011,56 @@ __global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_ru
       for (int i = 0; i < 8; ++i)
         if (identity || 16 * (i / 4) + 4 * n4 + i % 4 >= valid) rv[i] = Pair<kF>::zero();
     }
+    f32x4 X[2][kN];
+    const auto difference = [&](int n) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const f32x4 nt = *(const f32x4*)(factors + kFactorRows + 16 * t + 4 * n4);
+      for (int t = 0; t < 2; ++t) {
+        const f32x4 nt = *(const f32x4*)(factors + kFactorRows + 16 * t + 4 * n4);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const f32x2 v = Pair<kF>::value(rv[4 * t + r]);
-#pragma unroll
-        for (int n = 0; n < kN; ++n)
-          Y[t][n][r] = __builtin_fmaf(v[n], S.scale[n], -nt[r] * Y[t][n][r]);
+        for (int r = 0; r < 4; ++r) {
+          const f32x2 v = Pair<kF>::value(rv[4 * t + r]);
+          X[t][n][r] = __builtin_fmaf(v[n], S.scale[n], -nt[r] * Y[t][n][r]);
+        }
       }
-    }
+    };
     // The columns' range over S and X.
     float high[kN];
-    bool left = false;
-#pragma unroll
-    for (int n = 0; n < kN; ++n) {
+    const auto range = [&](int n) {
       float m = most[n];
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) m = __builtin_fmaxf(m, __builtin_fabsf(Y[t][n][r]));
+        for (int r = 0; r < 4; ++r) m = __builtin_fmaxf(m, __builtin_fabsf(X[t][n][r]));
       high[n] = m;
-      left |= S.left(m);
+    };
+    bool left = false;
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      difference(n);
+      range(n);
+      left |= S.left(high[n]);
     }
     if (left) {
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
-        const float f = S.factor(column_max(high[n]));
+        // Values beyond a faded column's scale: that goes back to 1 first.
+        if (column_max(high[n]) == __builtin_huge_valf() && S.scale[n] > 1.0f) {
+          const float f = S.inverse[n];
+          S.apply(n, f);
+          most[n] *= f;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            Y[t][n] *= f;
+            O[t][n] *= f;
+          }
+          difference(n);
+          range(n);
+        }
+        const float f = S.factor(n, column_max(high[n]));
         S.apply(n, f);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          Y[t][n] *= f;
+          X[t][n] *= f;
           O[t][n] *= f;
         }
       }
@@ -1035,7 +1070,7 @@ __global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_ru
     f32x4 U[2][kN];
     {
 #pragma unroll
-      for (int n = 0; n < kN; ++n) b[n] = split8(Y[0][n], Y[1][n], R.one);
+      for (int n = 0; n < kN; ++n) b[n] = split8(X[0][n], X[1][n], R.one);
       const float us = factors[kFactorRows + 2 * kChunk];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -1067,7 +1102,7 @@ __global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_ru
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
         const float m = column_max(high[n]);
-        const float f = m >= kColHigh ? S.factor(m) : 1.0f;
+        const float f = m >= kColHigh ? S.factor(n, m) : 1.0f;
         S.apply(n, f);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -1141,7 +1176,7 @@ __global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_ru
     if (left) {
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
-        const float f = S.factor(column_max(most[n]));
+        const float f = S.factor(n, column_max(most[n]));
         S.apply(n, f);
         most[n] *= f;
       }

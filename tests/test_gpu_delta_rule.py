@@ -198,6 +198,24 @@ def test_split_calls_equal_one_call():
     assert (g[5] - st).norm() <= 2 * ref.ARITHMETIC * st.norm()
 
 
+@pytest.mark.parametrize("rate", [0.3, 0.7, 1.3, 3.0])
+@pytest.mark.parametrize("lengths", [[900], [400, 1100, 9]], ids=str)
+def test_fading_states(lengths, rate):
+    """Decays that take a state, and what a stretch of tokens makes of the state before it,
+    below FP32's range in some chunks; then values return, small or very large."""
+    for dim in (64, 128):
+        args, kw = ref.rule_inputs(lengths, heads=3, dim=dim, dtype=F32, gate="log", seed=31,
+                                   initial=torch.ones(len(lengths), dtype=torch.bool))
+        g = args[3]
+        g[:, 0] = -rate
+        g[:, 1] = -rate * torch.linspace(0.5, 1.5, dim)
+        args[2][20:350, 2] = 0.0
+        g[20:350, 2] = -rate
+        compare(args, kw, f"rate {rate}")
+        args[2][350:] *= 1e20
+        compare(args, kw, f"rate {rate}, then large values")
+
+
 @pytest.mark.parametrize("lengths", [[700], [1024, 5, 333], [2100]], ids=str)
 def test_long_sequences(lengths):
     """Sequences long enough to be worked on in parts that run side by side."""
