@@ -37,7 +37,7 @@ __global__ __launch_bounds__(2 * D) void delta_rule_step_kernel(const RuleParams
                        row * D + col;
   if (seq.init) {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) S[i] = *(const f32x4a4*)(state + i * D);
+    for (int i = 0; i < kRows; ++i) S[i] = __builtin_nontemporal_load((const f32x4a4*)(state + i * D));
   } else {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) S[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -135,7 +135,7 @@ __global__ __launch_bounds__(2 * D) void delta_rule_step_kernel(const RuleParams
   }
   if (seq.line >= 0) {
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) *(f32x4a4*)(state + i * D) = S[i];
+    for (int i = 0; i < kRows; ++i) __builtin_nontemporal_store(S[i], (f32x4a4*)(state + i * D));
   }
 }
 
