@@ -28,22 +28,35 @@ struct Plan {
   int64_t slot_bytes, ends_bytes, moves_bytes;
 };
 
-// Sequences of up to this many tokens are faster token by token.
-constexpr int64_t kStepTokens = 8;
-// The step kernel is launched beside the chunked ones where sequences average under this.
-constexpr int64_t kStepAverage = 64;
-// Segments: as long as leaves a workgroup for each of this many CUs, twice that where the
-// sequences alone fill them, and no shorter than kSegmentMin chunks.
+// Sequences of up to this many tokens are faster token by token. (12 heads of 128: one
+// sequence of 12 tokens takes 24 us against 29 in a chunk, one of 24 41 against 30; 256
+// sequences of 12 tokens 161 against 236, of 24 261 against 246.)
+constexpr int64_t kStepTokens = 16;
+// The step kernel is launched beside the chunked ones, which then leave those sequences out,
+// where sequences average up to kStepAverage tokens, or under kStepAverageMany and make
+// kStepMany workgroups. (Every sequence of 4 tokens: 32 of 12 heads take 24 us against 42 by
+// chunks alone, 256 take 105 against 224. Lengths uniform about 24 tokens: 64 sequences 107
+// against 91, 256 266 against 276. About 20, 30 sequences of 4 heads: 61 against 36.)
+constexpr int64_t kStepAverage = 8, kStepAverageMany = 32, kStepMany = 2048;
+// Segments: as long as leaves one for each of this many CUs, twice that where the sequences
+// alone make more than two workgroups per CU, and no shorter than kSegmentMin chunks. (A
+// segment that is not a sequence's last is worked on twice, at twice the columns. 16384
+// tokens of 12 heads in all, lengths log-normal: 24 prompts take 400 us, with the segments
+// twice as long 518; 64 prompts 447 and 405. One sequence: 456 us, with half as long
+// segments, two per CU, 499. Segments of at least 4 chunks: 3 sequences of 2999 tokens in
+// all, 8 heads, 106 us, at least 3 chunks 121; 8 prompts of 1204 tokens, 12 heads, 77, at
+// least 6 chunks 81.)
 constexpr int64_t kSegmentCells = 256, kSegmentMin = 4;
 
 int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 
 Plan make_plan(int64_t tokens, int64_t seqs, int64_t heads, int64_t head_dim) {
   Plan p = {};
-  p.step = tokens <= kStepTokens || tokens < kStepAverage * seqs;
+  p.step = tokens <= kStepTokens || tokens <= kStepAverage * seqs ||
+           (tokens < kStepAverageMany * seqs && seqs * heads >= kStepMany);
   p.chunks = tokens > kStepTokens;
   p.max_len = p.step ? kStepTokens : 0;
-  const int64_t cells = seqs * heads > kSegmentCells ? kSegmentCells / 2 : kSegmentCells;
+  const int64_t cells = seqs * heads > 2 * kSegmentCells ? kSegmentCells / 2 : kSegmentCells;
   const int64_t units = (tokens + kChunk - 1) / kChunk * heads;
   p.segment_chunks = (int)std::max(kSegmentMin, (units + cells - 1) / cells);
   const int64_t segment = (int64_t)p.segment_chunks * kChunk;
