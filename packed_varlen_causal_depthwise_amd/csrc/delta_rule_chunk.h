@@ -59,9 +59,11 @@ __device__ __forceinline__ f64x4 mfma64(double a, double b, f64x4 c) {
 }
 
 // 16 bytes per lane from memory to LDS, at the wave's place + 16 times the lane's number.
+// kLast: the memory is not read again.
+template <bool kLast>
 __device__ __forceinline__ void to_lds(const char* from, char* wave_to) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
-                                   (__attribute__((address_space(3))) void*)wave_to, 16, 0, 0);
+                                   (__attribute__((address_space(3))) void*)wave_to, 16, 0, kLast ? 2 : 0);
 }
 
 // x as an FP16 pair: hi rounded, lo the rounded rest.
@@ -855,7 +857,7 @@ __global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_ru
   const auto copy = [&](const char* from, char* to, int pieces) {
 #pragma unroll
     for (int i = 0; i < pieces; i += kWaves)
-      if (i + wave < pieces) to_lds(from + 1024 * (i + wave) + 16 * lane, to + 1024 * (i + wave));
+      if (i + wave < pieces) to_lds<kOut>(from + 1024 * (i + wave) + 16 * lane, to + 1024 * (i + wave));
   };
   const auto load_rows = [&](const char* from) {
     copy(from + kSlot.kg(), krows, kMatrix / 1024);
