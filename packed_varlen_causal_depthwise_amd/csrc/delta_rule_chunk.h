@@ -128,8 +128,9 @@ __device__ __forceinline__ Piece find_piece(const ChunkParams& P, const Pieces& 
     base += (n - 1) * stride;
     v = __shfl(at, n - 1);
   }
-  base = uniform(base);
-  return Piece{base, p - uniform(v)};
+  // Offsets out of order may take the search to a sequence whose first program is later.
+  const int index = p - uniform(v);
+  return index < 0 ? Piece{-1, 0} : Piece{uniform(base), index};
 }
 
 // How the prepare kernel's 4 waves hold a chunk's rows. Wave w has rows 4 w .. + 3 and

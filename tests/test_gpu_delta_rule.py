@@ -233,6 +233,31 @@ def test_many_short_sequences():
         compare(args, kw)
 
 
+def mixed_lengths(short, most, long, seed):
+    """`short` lengths of 0 to `most` tokens with the long ones spread among them."""
+    gen = torch.Generator().manual_seed(seed)
+    lengths = torch.randint(0, most + 1, (short,), generator=gen).tolist()
+    for n in long:
+        lengths.insert(int(torch.randint(0, len(lengths) + 1, (1,), generator=gen)), n)
+    return lengths
+
+
+@pytest.mark.parametrize("short,most,long,heads", [
+    (70, 8, [500], 1),  # mostly short, few
+    (150, 6, [300, 17, 16], 2),  # short on average
+    (260, 30, [200, 33, 129], 8),  # not as short, many
+    (4200, 2, [150], 1),  # more sequences than 64^2
+], ids=str)
+def test_short_and_long_together(short, most, long, heads):
+    """Token-by-token and chunked sequences in one call, and the numbering of their pieces."""
+    for at_end in (False, True):
+        lengths = mixed_lengths(short, most, long, short)
+        if at_end:
+            lengths = sorted(lengths)
+        args, kw = ref.rule_inputs(lengths, heads=heads, dim=64, seed=short, pad=2)
+        compare(args, kw, f"sorted {at_end}")
+
+
 def test_far_lines():
     """Lines whose offset passes 2^31 elements."""
     args, kw = ref.rule_inputs([40, 3], heads=1, dim=128, seed=17, lines=4,
