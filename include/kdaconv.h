@@ -269,8 +269,10 @@ int kdaconv_activation_map(uint32_t first, int64_t count, int activation, int dt
  * kdaconv_packed_causal_conv1d: sequence s owns rows [qsl[s], qsl[s+1]), starts from
  * states[cache_indices[s]] when has_initial_state[s] is set (else zeros) and leaves its
  * last S there; a sequence on the null block, or on a line outside the state array, runs
- * from zeros and leaves the states alone; a sequence without tokens does nothing. The
- * arithmetic is FP32 or better than FP16 pairs (22 bits) throughout; only out is rounded.
+ * from zeros and leaves the states alone. A sequence without tokens leaves what it starts
+ * from: its line as it is, or zeros there without an initial state. States, sums and norms
+ * are held in FP32 or more; matrix products take FP32 values as pairs of FP16 values (22
+ * bits) and sum in FP32; only out is rounded to its format.
  * A log decay below -104 acts as -104 (its exp is zero in FP32, as is -infinity's).
  *
  * All strides count elements.
@@ -325,7 +327,7 @@ int64_t kdaconv_gated_delta_rule_workspace(int64_t num_tokens, int64_t num_seqs,
  * multiple of num_qk_heads (else EUNSUPPORTED and EINVAL). Sizes come from the host
  * arguments alone, so a call can be captured in a graph. Preconditions on device data as
  * for kdaconv_packed_causal_conv1d. num_tokens, num_seqs or num_heads of 0: KDACONV_OK
- * with no launch.
+ * with no launch (a call without any token leaves all states alone).
  */
 int kdaconv_gated_delta_rule(const kdaconv_rule_args* args, void* workspace,
                              int64_t workspace_bytes, kdaconv_stream_t stream);

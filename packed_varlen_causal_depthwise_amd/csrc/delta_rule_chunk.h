@@ -839,6 +839,11 @@ __global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_ru
   const Piece piece = find_piece(P, kOut ? P.segment_pieces : P.move_pieces, program, lane);
   if (piece.s < 0) return;
   const Sequence seq(R, piece.s);
+  if (kOut && seq.len == 0 && P.min_len == 1 && seq.line >= 0 && !seq.init && piece.index == 0) {
+    // Without tokens a sequence that starts from zeros leaves them.
+    float* const to = R.states + seq.line * R.st_line + h * R.st_head;
+    for (int i = threadIdx.x; i < D * D; i += 4 * D) to[i] = 0.0f;
+  }
   if (seq.len < P.min_len) return;
   const int per = P.segment_chunks;
   const int chunks = (seq.len + kChunk - 1) / kChunk;

@@ -28,7 +28,8 @@ __global__ __launch_bounds__(2 * D) void delta_rule_step_kernel(const RuleParams
 
   const int s = blockIdx.x / P.heads, h = blockIdx.x % P.heads;
   const Sequence seq(P, s);
-  if (seq.len == 0 || seq.len > P.max_len) return;
+  // (Without tokens a sequence that starts from zeros leaves them.)
+  if (seq.len > P.max_len || (seq.len == 0 && (seq.init || seq.line < 0))) return;
   const int wave = uniform(threadIdx.x / kRuleWave), lane = threadIdx.x % kRuleWave;
   const int col = 32 * wave + 4 * (lane % 8), row = kRows * (lane / 8);
 

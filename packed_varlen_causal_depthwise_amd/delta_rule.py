@@ -149,7 +149,8 @@ def gated_delta_rule_fn(
 
     states (cache lines, heads, head_dim, head_dim) float32 is read and written in place.
     query_start_loc, cache_indices, has_initial_state and null_block_id mean what they mean
-    for ``packed_causal_conv1d_fn``; rows no sequence owns are left unwritten. Returns (tokens,
+    for ``packed_causal_conv1d_fn``; rows no sequence owns are left unwritten, and a sequence
+    without tokens leaves what it starts from (zeros in its line without an initial state). Returns (tokens,
     heads, head_dim) in v's dtype (``out``, when given). The state and every intermediate hold
     FP32 or 22-bit pairs; only the output is rounded to its dtype. Queued on the current
     stream; no synchronisation.

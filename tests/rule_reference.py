@@ -61,7 +61,7 @@ def delta_rule(q, k, v, g, beta, states, query_start_loc, cache_indices, has_ini
             u = b[t][:, None] * (v[t] - torch.einsum("hk,hkv->hv", k[t], S))
             S = S + k[t][..., None] * u[:, None]
             out[t] = torch.einsum("hk,hkv->hv", q[t], S)
-        if stored and loc[s + 1] > loc[s]:
+        if stored:
             states[line] = S
     return out, states
 

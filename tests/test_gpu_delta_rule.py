@@ -39,7 +39,8 @@ def compare(args, kw, what="", **more):
     assert (out.cpu()[~owned] == -7.0).all(), "rows no sequence owns were written"
     ref.check(st, want_st, F32, what + " states")
     before = args[5]
-    touched = {int(args[7][s]) for s in range(len(args[6]) - 1) if args[6][s + 1] > args[6][s]}
+    touched = {int(args[7][s]) for s in range(len(args[6]) - 1)
+               if args[6][s + 1] > args[6][s] or not args[8][s]}
     for line in range(len(before)):
         if line not in touched or line == more.get("null_block_id"):
             assert torch.equal(st[line].cpu(), before[line]), f"line {line} was written"
@@ -223,6 +224,21 @@ def test_long_sequences(lengths):
         args, kw = ref.rule_inputs(lengths, heads=2, dim=dim, seed=7, gate=gate, gate_dtype=gd,
                                    initial=torch.ones(len(lengths), dtype=torch.bool))
         compare(args, kw)
+
+
+def test_sequences_without_tokens():
+    """They leave what they start from, whichever kernels a call takes."""
+    for lengths in ([0, 40, 0, 0], [0, 3, 0, 0], [0] * 40 + [90], [2] * 30 + [0, 0]):
+        initial = torch.arange(len(lengths)) % 2 == 0
+        for dim in (64, 128):
+            args, kw = ref.rule_inputs(lengths, heads=2, dim=dim, seed=9, initial=initial)
+            before = args[5].clone()
+            compare(args, kw, str(lengths))
+            _, st, _, _ = run(args, kw)
+            for s, n in enumerate(lengths):
+                line = int(args[7][s])
+                if n == 0:
+                    assert torch.equal(st[line].cpu(), before[line] * float(initial[s]))
 
 
 def test_many_short_sequences():
