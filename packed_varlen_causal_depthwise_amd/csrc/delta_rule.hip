@@ -38,14 +38,15 @@ constexpr int64_t kStepTokens = 16;
 // chunks alone, 256 take 105 against 224. Lengths uniform about 24 tokens: 64 sequences 107
 // against 91, 256 266 against 276. About 20, 30 sequences of 4 heads: 61 against 36.)
 constexpr int64_t kStepAverage = 8, kStepAverageMany = 32, kStepMany = 2048;
-// Segments: as long as leaves one for each of this many CUs, twice that where the sequences
-// alone make more than two workgroups per CU, and no shorter than kSegmentMin chunks. (A
-// segment that is not a sequence's last is worked on twice, at twice the columns. 16384
-// tokens of 12 heads in all, lengths log-normal: 24 prompts take 400 us, with the segments
-// twice as long 518; 64 prompts 447 and 405. One sequence: 456 us, with half as long
-// segments, two per CU, 499. Segments of at least 4 chunks: 3 sequences of 2999 tokens in
-// all, 8 heads, 106 us, at least 3 chunks 121; 8 prompts of 1204 tokens, 12 heads, 77, at
-// least 6 chunks 81.)
+// Segments: as long as leaves one for each of this many CUs, and no shorter than kSegmentMin
+// chunks. A segment that is not a sequence's last is worked on twice, at twice the columns;
+// but where the sequences alone make more than two workgroups per CU the longest of them are
+// what a call waits for, and segments are shorter by a third. (16384 tokens of 12 heads: one
+// sequence 449 us, with half as long segments 499; 64 prompts of log-normal lengths, over 12
+// draws, 376 us on average and 401 at most, with segments three times as long 420 and 526,
+// though prompts of uniform lengths take 326 and 306. 24 log-normal prompts: 400, with twice
+// as long segments 518. 3 sequences of 2999 tokens in all, 8 heads, 106 us, segments of 3
+// chunks 121; 8 prompts of 1204 tokens, 12 heads, 77, segments of 6 chunks 81.)
 constexpr int64_t kSegmentCells = 256, kSegmentMin = 4;
 
 int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
@@ -56,7 +57,7 @@ Plan make_plan(int64_t tokens, int64_t seqs, int64_t heads, int64_t head_dim) {
            (tokens < kStepAverageMany * seqs && seqs * heads >= kStepMany);
   p.chunks = tokens > kStepTokens;
   p.max_len = p.step ? kStepTokens : 0;
-  const int64_t cells = seqs * heads > 2 * kSegmentCells ? kSegmentCells / 2 : kSegmentCells;
+  const int64_t cells = seqs * heads > 2 * kSegmentCells ? kSegmentCells * 3 / 2 : kSegmentCells;
   const int64_t units = (tokens + kChunk - 1) / kChunk * heads;
   p.segment_chunks = (int)std::max(kSegmentMin, (units + cells - 1) / cells);
   const int64_t segment = (int64_t)p.segment_chunks * kChunk;
