@@ -249,31 +249,62 @@ __device__ __forceinline__ void mask_rows(f32x2 (&x)[Rows<D>::kRows], int wave, 
     if (Rows<D>::wave_row(wave, i) + Rows<D>::lane_row(lane) >= valid) x[i] = f32x2{0.0f, 0.0f};
 }
 
-// Sums of N values over kWidth lanes, each lane receiving the sum of value (lane index /
-// (kWidth / N)); exchanges halves while values are left, so N + log2(kWidth / N) - 1
-// exchanges instead of N log2(kWidth). The values travel as a vector: the compiler turns a
-// choice between two elements of an array into a choice of the index, which costs more than
-// all the rest.
+// Sums of N values over 2 kMask lanes, each lane receiving the sum of value (lane index /
+// (2 kMask / N)): exchanges halves while values are left, so N + log2(2 kMask / N) - 1
+// exchanges instead of N log2(2 kMask). All are moves inside the vector unit. The values
+// travel as a vector: the compiler turns a choice between two elements of an array into a
+// choice of the index, which costs more than all the rest.
 template <int N>
 struct Doubles {
   typedef double type __attribute__((ext_vector_type(N)));
 };
 
+typedef uint32_t u32two __attribute__((ext_vector_type(2)));
+
+// x of the lane whose number differs in bit kMask; for 4 the lower bits differ too (which
+// lane of its half a value comes from does not matter to a sum over all of them).
+template <int kMask>
+__device__ __forceinline__ double from_other(double x) {
+  constexpr int kMove = kMask == 8 ? 0x128 : kMask == 4 ? 0x141 : kMask == 2 ? 0x4E : 0xB1;
+  static_assert(kMask <= 8, "one move inside rows of 16 lanes");
+  u32two w = __builtin_bit_cast(u32two, x);
+  w.x = (uint32_t)__builtin_amdgcn_mov_dpp((int)w.x, kMove, 0xF, 0xF, true);
+  w.y = (uint32_t)__builtin_amdgcn_mov_dpp((int)w.y, kMove, 0xF, 0xF, true);
+  return __builtin_bit_cast(double, w);
+}
+
+// a + a of the other half of the lanes in the half without bit kMask, the same of b in the
+// half with it.
+template <int kMask>
+__device__ __forceinline__ double halves_sum(double a, double b, int lane) {
+  if constexpr (kMask >= 16) {
+    const u32two x = __builtin_bit_cast(u32two, a), y = __builtin_bit_cast(u32two, b);
+    u32two lo, hi;  // of both words
+    if constexpr (kMask == 32) {
+      lo = __builtin_amdgcn_permlane32_swap(x.x, y.x, false, false);
+      hi = __builtin_amdgcn_permlane32_swap(x.y, y.y, false, false);
+    } else {
+      lo = __builtin_amdgcn_permlane16_swap(x.x, y.x, false, false);
+      hi = __builtin_amdgcn_permlane16_swap(x.y, y.y, false, false);
+    }
+    return __builtin_bit_cast(double, u32two{lo.x, hi.x}) + __builtin_bit_cast(double, u32two{lo.y, hi.y});
+  } else {
+    const bool upper = (lane & kMask) != 0;
+    return (upper ? b : a) + from_other<kMask>(upper ? a : b);
+  }
+}
+
 template <int N, int kMask>
 __device__ __forceinline__ double scatter_sum(typename Doubles<N>::type x, int lane) {
-  const bool upper = (lane & kMask) != 0;
   if constexpr (N == 2) {
-    double s = (upper ? x[1] : x[0]) + __shfl_xor(upper ? x[0] : x[1], kMask);
-#pragma unroll
-    for (int m = kMask / 2; m > 0; m >>= 1) s += __shfl_xor(s, m);
-    return s;
+    double s = halves_sum<kMask>(x[0], x[1], lane);
+    if constexpr (kMask > 4) s += from_other<4>(s);
+    if constexpr (kMask > 2) s += from_other<2>(s);
+    return s + from_other<1>(s);
   } else {
     typename Doubles<N / 2>::type y;
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      const double a = x[i], b = x[N / 2 + i];
-      y[i] = (upper ? b : a) + __shfl_xor(upper ? a : b, kMask);
-    }
+    for (int i = 0; i < N / 2; ++i) y[i] = halves_sum<kMask>(x[i], x[N / 2 + i], lane);
     return scatter_sum<N / 2, kMask / 2>(y, lane);
   }
 }
@@ -288,8 +319,8 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
   constexpr int kLd = D + 4;  // floats per operand row: 16 rows reach all banks
   constexpr int kMat = kChunk * kLd;
   constexpr int kSq = 34;  // doubles per row of a 32 x 32 matrix
-  // After the products: L and its inverse, T's and A's parts, and 32 D bytes per wave to
-  // turn rows into operands.
+  // After the products: L and its inverse, A's parts, and 32 D bytes per wave to turn rows
+  // into operands.
   constexpr int kSquares = 2 * kChunk * kSq * (int)sizeof(double), kStage = kSquares + 4096;
   constexpr int kBytes = 3 * kMat * 4 > kStage + 128 * D ? 3 * kMat * 4 : kStage + 128 * D;
   // Operand rows q, k (times the decay from the block's middle) and columns k.
@@ -298,10 +329,10 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
   float (*const tot)[D] = (float (*)[D])shared;
   __shared__ __attribute__((aligned(16))) float across[D];
   // Per row: the key's factor times 16, the query's times 16, the key's power of two; and
-  // as they go to the slot |k| / 16, the outputs' factor / 16 and T's factor.
+  // as they go to the slot |k| / 16 and the outputs' factor / 16.
   __shared__ float kf16[kChunk], qf16[kChunk], ktwo[kChunk];
   __shared__ __attribute__((aligned(16))) float rows[2][kChunk];
-  __shared__ float tfac;
+  __shared__ int texp;  // T's scale is 2 to this
   __shared__ float beta[kChunk];
   // Keys enter the products times a power of two (exact); the rest of their factor, and n,
   // follow in FP64 (a key rounded to unit length would be off by 3e-8, see below).
@@ -454,8 +485,8 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
     // Blocks (row, column): 0 (0, 0), 1 (1, 1), 2 (1, 0). The key products are summed in
     // FP64: equal keys with steps near 2 (reflections) and no decay make an error common to
     // L's entries grow with the tokens, by 32 per chunk. FP32 sums and an FP32 inverse left
-    // such a state 1e-4 off after 97 tokens. Both kinds take as long: the 96 FP32
-    // instructions of wave 3 run at twice the rate of the other waves' 32 in FP64.
+    // such a state 1e-4 off after 97 tokens. Both kinds take as long: 4000 cycles for 32
+    // FP64 instructions in each of three waves, 4400 for the 96 FP32 ones of the fourth.
     if (wave < 3) {
       const float* const rk = mk + ((wave == 0 ? 0 : 16) + n16) * kLd + 4 * n4;
       const float* const rc = mc + ((wave == 1 ? 16 : 0) + n16) * kLd + 4 * n4;
@@ -544,10 +575,7 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
   // The operands are done with; their place takes L, the inverse and the staged outputs.
   double* const ml = (double*)shared;  // L [row][column]
   double* const mt = ml + kChunk * kSq;  // (I + L)^-1
-  // T in three parts and A in two, as they go to the slot. L's place is free for T by then.
-  _Float16* const st = (_Float16*)shared;
-  _Float16* const sa = (_Float16*)(shared + kSquares);
-  static_assert(6144 <= kChunk * kSq * sizeof(double), "T fits L's place");
+  _Float16* const sa = (_Float16*)(shared + kSquares);  // A in two parts, as it goes to the slot
   constexpr Slot kSlot{D};
   char* const slot = P.slots + ((int64_t)program * R.heads + h) * kSlot.bytes();
   const auto put_a = [&](int t, int i, float a) {
@@ -665,13 +693,15 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
   }
 
   if (wave == 0) {
-    // (I + L)^-1: the two diagonal blocks by forward substitution, a column per lane, then
-    // T10 = -T11 (L10 T00). FP64 (the vector unit runs it at FP32's rate).
+    // (I + L)^-1 in FP64. Four 8 x 8 diagonal blocks by forward substitution, a column per
+    // lane; then twice from blocks A, B on the diagonal and C below to the inverse of
+    // [A 0; C B], whose lower left is -B^-1 (C A^-1). A result's registers (row 4 r +
+    // lane / 16) are the next product's right operand as they are.
     if (lane < 32) {
-      const int b = lane & 16, col = lane & 15;
-      double x[16];
+      const int b = lane & 24, col = lane & 7;
+      double x[8];
 #pragma unroll
-      for (int t = 0; t < 16; ++t) {
+      for (int t = 0; t < 8; ++t) {
         double s = t == col ? 1.0 : 0.0;
 #pragma unroll
         for (int i = 0; i < t; ++i) s = __builtin_fma(-ml[(b + t) * kSq + b + i], x[i], s);
@@ -680,74 +710,95 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
       }
     }
     __builtin_amdgcn_wave_barrier();
-    double z[4] = {}, y[4] = {};
+    f64x4 t00, t11, t10 = {0.0, 0.0, 0.0, 0.0};
+    {
+      const bool diagonal = (n16 & 8) == 0;  // this lane's column is in the first 8
+      f64x4 w[2], y[2];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const double x = mt[i * kSq + n16];
+      for (int b = 0; b < 2; ++b) {
+        w[b] = y[b] = f64x4{0.0, 0.0, 0.0, 0.0};
 #pragma unroll
-      for (int r = 0; r < 4; ++r) z[r] = __builtin_fma(ml[(16 + 4 * n4 + r) * kSq + i], x, z[r]);
+        for (int k = 0; k < 2; ++k) {
+          const int row = 16 * b + n16, at = 16 * b + 4 * k + n4;
+          const double c = n16 >= 8 ? ml[row * kSq + at] : 0.0;
+          w[b] = mfma64(c, diagonal ? mt[at * kSq + row] : 0.0, w[b]);
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int k = 2; k < 4; ++k) {
+          const double x = n16 >= 8 ? mt[(16 * b + n16) * kSq + 16 * b + 4 * k + n4] : 0.0;
+          y[b] = mfma64(x, w[b][k], y[b]);
+        }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        // Registers 0 and 1 are rows 0 to 7.
+        const bool own = (r < 2) == diagonal;
+        const int at = (4 * r + n4) * kSq + n16;
+        t00[r] = own ? mt[at] : -y[0][r];
+        t11[r] = own ? mt[at + 16 * kSq + 16] : -y[1][r];
+      }
     }
-    // L is done with: its first rows take L10 T00.
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int r = 0; r < 4; ++r) ml[(4 * n4 + r) * kSq + n16] = z[r];
+    for (int r = 0; r < 4; ++r) mt[(16 + 4 * r + n4) * kSq + 16 + n16] = t11[r];
     __builtin_amdgcn_wave_barrier();
+    {
+      f64x4 w = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const double x = ml[i * kSq + n16];
+      for (int k = 0; k < 4; ++k) w = mfma64(ml[(16 + n16) * kSq + 4 * k + n4], t00[k], w);
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        y[r] = __builtin_fma(mt[(16 + 4 * n4 + r) * kSq + 16 + i], x, y[r]);
+      for (int k = 0; k < 4; ++k) t10 = mfma64(mt[(16 + n16) * kSq + 16 + 4 * k + n4], w[k], t10);
     }
-    // diag(n) T diag(b), scaled to a largest entry of 256 to 512, in three FP16 parts: with
-    // two (22 bits) the reflections above still lost 1e-5.
-    double t00[4], t11[4], t10[4];
+    __builtin_amdgcn_wave_barrier();
+    // diag(n) T diag(b), and its largest entry.
     float top = 0.0f;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int t = 4 * n4 + r;
-      t00[r] = (double)(kVec * rows[0][t]) * mt[t * kSq + n16] * (double)beta[n16];
-      t11[r] = (double)(kVec * rows[0][16 + t]) * mt[(16 + t) * kSq + 16 + n16] * (double)beta[16 + n16];
-      t10[r] = -(double)(kVec * rows[0][16 + t]) * y[r] * (double)beta[n16];
-      top = __builtin_fmaxf(
-          top, __builtin_fmaxf(__builtin_fabsf((float)t10[r]),
-                               __builtin_fmaxf(__builtin_fabsf((float)t00[r]), __builtin_fabsf((float)t11[r]))));
+      const int t = 4 * r + n4;
+      const double n0 = (double)(kVec * rows[0][t]), n1 = (double)(kVec * rows[0][16 + t]);
+      const double b0 = (double)beta[n16], b1 = (double)beta[16 + n16];
+      const double x0 = n0 * t00[r] * b0, x1 = n1 * t11[r] * b1, x2 = -n1 * t10[r] * b0;
+      mt[t * kSq + n16] = x0;
+      mt[(16 + t) * kSq + 16 + n16] = x1;
+      mt[(16 + t) * kSq + n16] = x2;
+      top = __builtin_fmaxf(top, __builtin_fmaxf(__builtin_fabsf((float)x2),
+                                                 __builtin_fmaxf(__builtin_fabsf((float)x0), __builtin_fabsf((float)x1))));
     }
-    __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int m = 32; m > 0; m >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, m));
     int e = 0;
     if (top > 0.0f && top < __builtin_huge_valf()) e = 9 - __builtin_amdgcn_frexp_expf(top);
     e = e > 100 ? 100 : e;
-    const auto put_t = [&](int t, int i, double x) {
-      x = __builtin_amdgcn_ldexp(x, e);
-      const int at = (t / 16 * 64 + (place(i) / 8) * 16 + t % 16) * 8 + place(i) % 8;
-      const _Float16 hi = (_Float16)(float)x;
-      const float rest = (float)(x - (double)(float)hi);
-      const _Float16 lo = (_Float16)rest;
-      st[at] = hi;
-      st[1024 + at] = lo;
-      st[2048 + at] = (_Float16)(rest - (float)lo);
-    };
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = 4 * n4 + r;
-      put_t(t, n16, t00[r]);
-      put_t(16 + t, 16 + n16, t11[r]);
-      put_t(16 + t, n16, t10[r]);
-      put_t(t, 16 + n16, 0.0f);
-    }
-    // U is kept times 1 / 16, so that (16 k^)^T (U / 16) adds to S as it is.
-    if (lane == 0) tfac = __builtin_amdgcn_ldexpf(1.0f / kVec, -e);
+    if (lane == 0) texp = e;
   }
   __syncthreads();
-  u32q* const dt = (u32q*)(slot + kSlot.t());
-  dt[threadIdx.x] = ((const u32q*)st)[threadIdx.x];
-  if (threadIdx.x < 128) dt[256 + threadIdx.x] = ((const u32q*)st)[256 + threadIdx.x];
-  ((u32q*)(slot + kSlot.a()))[threadIdx.x] = ((const u32q*)sa)[threadIdx.x];
   float* const df = (float*)(slot + kSlot.factors());
+  {
+    // T scaled to a largest entry of 256 to 512, in three FP16 parts: with two (22 bits) the
+    // reflections above still lost 1e-5. Thread u holds places 4 u .. + 3 of the operand
+    // order: four neighbouring columns of one row.
+    const int u = threadIdx.x, t = (u >> 7) * 16 + ((u >> 1) & 15), i0 = 16 * (u & 1) + 4 * ((u >> 5) & 3);
+    const int e = texp;
+    f16x4 hi, lo, last;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const double x = t < 16 && i0 >= 16 ? 0.0 : __builtin_amdgcn_ldexp(mt[t * kSq + i0 + j], e);
+      hi[j] = (_Float16)(float)x;
+      const float rest = (float)(x - (double)(float)hi[j]);
+      lo[j] = (_Float16)rest;
+      last[j] = (_Float16)(rest - (float)lo[j]);
+    }
+    f16x4* const to = (f16x4*)(slot + kSlot.t()) + u;
+    to[0] = hi;
+    to[256] = lo;
+    to[512] = last;
+    // U is kept times 1 / 16, so that (16 k^)^T (U / 16) adds to S as it is.
+    if (u == 0) df[kFactorRows + 2 * kChunk] = __builtin_amdgcn_ldexpf(1.0f / kVec, -e);
+  }
+  ((u32q*)(slot + kSlot.a()))[threadIdx.x] = ((const u32q*)sa)[threadIdx.x];
   if (threadIdx.x < 2 * kChunk) df[kFactorRows + threadIdx.x] = (&rows[0][0])[threadIdx.x];
-  if (threadIdx.x == 0) df[kFactorRows + 2 * kChunk] = tfac;
 }
 
 // ------------------------------------------------------------------------------- scan
