@@ -13,16 +13,20 @@
 //
 // A long sequence is cut into segments. Over a segment S_end = M S_start + B: the scan of
 // a segment from zero gives B, the scan of the identity without values gives M, and the
-// starts follow by S_(j+1) = M_j S_j + B_j. Then all segments run side by side.
+// starts follow by S_(j+1) = M_j S_j + B_j. Then all segments run side by side. (In one
+// piece a sequence of 16384 tokens, 12 heads, would keep 12 CUs busy for 512 chunks of 4 us.)
 //
 // Kernels:
 //   prepare   (chunk, head)             all that does not depend on S, into a slot
-//   scan      (segment, head)           B and M, only for sequences of several segments
+//   scan      (segment, head)           B and M, only for segments that others follow
 //   join      (sequence, head, columns) the starts of the segments from the third on
 //   scan      (segment, head)           outputs and the final state
 // A chunk's gates, norms and exponentials are worked out once, by prepare, and handed over
 // as matrix operands (60 KB per chunk and head of 128): the scans were bound by that vector
-// work when they repeated it (5 us per chunk, 0.5 TB/s).
+// work when they repeated it (5 us per chunk, 0.5 TB/s). One sequence of 16384 tokens, 12
+// heads of 128, bf16 now takes 145 us in prepare, 114 for the transitions, 32 for the join
+// and 100 for the outputs. Its tensors alone, 252 MB, are 50 us; the operands' way through
+// memory, 1.1 GB of reads and writes more, and the chain from chunk to chunk are the rest.
 //
 // Numbers. Matrix products run on the FP16 matrix instructions with every operand split
 // into a pair of FP16 values (22 bits) and three products: hi hi + hi lo + lo hi, summed
@@ -311,6 +315,13 @@ __device__ __forceinline__ double scatter_sum(typename Doubles<N>::type x, int l
 
 // ---------------------------------------------------------------------------- prepare
 
+// Three workgroups per CU (52 KB of LDS, 156 registers). A workgroup alone takes 24500 cycles:
+// finding its chunk 1600, loads and gates 3900, lengths and sums 1400, operands of the
+// products 2400, products 4400, L and A 1300, operands for the scans 3400, T 4600, the rest
+// its stores. 6144 of them (16384 tokens, 12 heads of 128) take 145 us for 550 MB, 3.8 TB/s,
+// and no single part bounds that: without its stores it takes 130 us, without the products
+// 114, without T 128, without the scans' operands 121. The way through all of them at three
+// workgroups per CU does; a fourth would need 40 KB of LDS and 128 registers.
 template <int kF, int kG, int D>
 __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkParams P) {
   typedef Rows<D> RW;
@@ -870,6 +881,11 @@ struct ScanState {
 // columns per wave the operands are read from LDS half as often, but the 172 matrix
 // instructions per chunk of a lone wave took 24 cycles each instead of 14: 20% longer with one
 // sequence of 64 tokens, 5% with many.)
+//
+// 264 output scans of 24 chunks take 100 us: 490 MB, 4.6 TB/s, close to what a copy reaches;
+// the matrix units are busy for 37% of it. The 252 transitions take 114 us for half the bytes:
+// 16 waves read 640 KB of operands from LDS per chunk, which is 5000 of its 10000 cycles, and
+// the matrix units are busy for 40%.
 template <int kF, int D, int kMode>
 __global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_rule_scan_kernel(const ChunkParams P) {
   constexpr bool kOut = kMode == kScanOut;
@@ -1315,6 +1331,10 @@ __global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_ru
 // operands to the others through LDS. A step is short, so M and B are loaded kAhead steps
 // ahead. Workgroups of one (sequence, head) read the same M: the grid's rows are whole
 // multiples of 8, which puts them on one of the card's 8 dies and in one L2.
+//
+// A step takes 1.6 us: the 64 KB of M alone are 0.5 at a CU's 64 bytes per cycle, the rest is
+// the chain largest value - split - exchange - product. Fewer, longer segments make it
+// shorter, not more workgroups.
 template <int D>
 __global__ __launch_bounds__(4 * D, 2) void delta_rule_join_kernel(const ChunkParams P) {
   constexpr int kK = D / 32, kWaves = D / 16, kAhead = 2;

@@ -10,7 +10,12 @@
 // state's loads are in flight.
 //
 // A token costs four FP32 operations per state element against 8 bytes read and written
-// for a single-token call, so the state's traffic bounds the decode step.
+// for a single-token call, so the state's traffic bounds the decode step. The state passes the
+// caches by: between two tokens every other layer's state passes too. 256 sequences of 12
+// heads of 128 (403 MB) take 77 us, 5.2 TB/s, after other data went through the caches, and
+// 89 with ordinary accesses; only where the state stays in the last-level cache are those
+// faster (64 us against 76). A call of 4096 sequences of 1 to 4 tokens, 3 heads of 64: 101 us
+// against 115.
 #ifndef KDACONV_DELTA_RULE_STEP_H_
 #define KDACONV_DELTA_RULE_STEP_H_
 
