@@ -54,5 +54,23 @@ def _on(device: torch.device):
     return torch.cuda.device(device)
 
 
+def _stream_of(index: int) -> int:
+    """The raw current stream of device `index`."""
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _call(index: int, function, *args) -> int:
+    """function(*args, current stream of device `index`) with that device current."""
+    if index == _current_device():
+        return function(*args, _stream_of(index))
+    with torch.cuda.device(index):
+        return function(*args, _stream_of(index))
+
+
+def _fresh_like(t: torch.Tensor) -> torch.Tensor:
+    """A contiguous tensor of t's shape, dtype and device (half the host time of torch.empty)."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()

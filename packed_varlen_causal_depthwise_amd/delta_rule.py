@@ -7,7 +7,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._host import DTYPE_CODES, NULL_BLOCK_ID, _on, _stream_handle
+from ._host import DTYPE_CODES, NULL_BLOCK_ID, _call, _fresh_like
 
 #: Added to the squared length of a query or key before its root (qk_l2norm).
 L2_EPS = 1e-6
@@ -68,13 +68,17 @@ def _pack(q, k, v, g, beta, states, cache_indices, query_start_loc, has_initial_
     if (cache_indices.dtype != torch.int32 or cache_indices.dim() != 1
             or cache_indices.shape[0] < num_seqs):
         raise ValueError("cache_indices must be a 1-D int32 tensor with one entry per sequence")
-    if not v.is_cuda:
-        raise ValueError("v must be a GPU tensor")
     device = v.get_device()
-    for t in (q, k, g, beta, states, cache_indices, query_start_loc, has_initial_state, a_log,
-              dt_bias):
-        if t is not None and t.get_device() != device:
-            raise ValueError("all tensors must be on the device of v")
+    if device < 0:
+        raise ValueError("v must be a GPU tensor")
+    if (q.get_device() != device or k.get_device() != device or g.get_device() != device
+            or beta.get_device() != device or states.get_device() != device
+            or cache_indices.get_device() != device
+            or query_start_loc is not None and query_start_loc.get_device() != device
+            or has_initial_state is not None and has_initial_state.get_device() != device
+            or a_log is not None and a_log.get_device() != device
+            or dt_bias is not None and dt_bias.get_device() != device):
+        raise ValueError("all tensors must be on the device of v")
     code = DTYPE_CODES[v.dtype]
     return _lib.RULE_ARGS.pack(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
@@ -95,7 +99,7 @@ def _pack(q, k, v, g, beta, states, cache_indices, query_start_loc, has_initial_
 
 def _output(v, out):
     if out is None:
-        return torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        return _fresh_like(v)
     if (out.shape != v.shape or out.dtype != v.dtype or not out.is_contiguous()
             or out.get_device() != v.get_device()):
         raise ValueError(f"out must be a contiguous {v.dtype} tensor of shape {tuple(v.shape)} on {v.device}")
@@ -171,14 +175,12 @@ def gated_delta_rule_fn(
                  num_seqs, sizes, a_log, dt_bias, lower_bound, beta_logits, qk_l2norm, scale,
                  null_block_id, out)
     lib = _lib.load()
-    device = v.device
-    with _on(device):
-        need = lib.kdaconv_gated_delta_rule_workspace(sizes[0], num_seqs, sizes[1], sizes[3])
-        # Memory of the current stream: the allocator hands it out again only to work that
-        # is queued behind this call.
-        scratch = torch.empty(need, dtype=torch.uint8, device=device) if need > 0 else None
-        rc = lib.kdaconv_gated_delta_rule(args, None if scratch is None else scratch.data_ptr(),
-                                          need, _stream_handle(device))
+    need = lib.kdaconv_gated_delta_rule_workspace(sizes[0], num_seqs, sizes[1], sizes[3])
+    # Memory of the current stream: the allocator hands it out again only to work that is
+    # queued behind this call.
+    scratch = torch.empty(need, dtype=torch.uint8, device=v.device) if need > 0 else None
+    rc = _call(v.get_device(), lib.kdaconv_gated_delta_rule, args,
+               None if scratch is None else scratch.data_ptr(), need)
     _lib.check(rc, "gated_delta_rule_fn")
     return out
 
@@ -210,10 +212,7 @@ def gated_delta_rule_update(
         return out
     args = _pack(q, k, v, g, beta, states, cache_indices, None, None, sizes[0], sizes, a_log,
                  dt_bias, lower_bound, beta_logits, qk_l2norm, scale, null_block_id, out)
-    lib = _lib.load()
-    device = v.device
-    with _on(device):
-        rc = lib.kdaconv_gated_delta_rule_update(args, _stream_handle(device))
+    rc = _call(v.get_device(), _lib.load().kdaconv_gated_delta_rule_update, args)
     _lib.check(rc, "gated_delta_rule_update")
     return out
 

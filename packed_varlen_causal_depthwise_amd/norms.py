@@ -7,7 +7,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._host import DTYPE_CODES, _on, _ptr, _stream_handle
+from ._host import DTYPE_CODES, _call, _fresh_like, _ptr
 
 _ACTIVATIONS = {"sigmoid": _lib.NORM_GATE_SIGMOID, "silu": _lib.NORM_GATE_SILU,
                 "swish": _lib.NORM_GATE_SILU}
@@ -21,7 +21,7 @@ def _check_weight(weight, dim, device):
 
 def _output(x, out):
     if out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        return _fresh_like(x)
     if (out.shape != x.shape or out.dtype != x.dtype or not out.is_contiguous()
             or out.get_device() != x.get_device()):
         raise ValueError(f"out must be a contiguous {x.dtype} tensor of shape {tuple(x.shape)} on {x.device}")
@@ -70,11 +70,9 @@ def gated_rms_norm(
         return out
     if not x.is_cuda:
         raise ValueError("x must be a GPU tensor")
-    lib = _lib.load()
-    with _on(x.device):
-        rc = lib.kdaconv_gated_rms_norm(
-            x.data_ptr(), DTYPE_CODES[x.dtype], tokens, heads, dim, xs[0], xs[1], _ptr(gate),
-            gs[0], gs[1], code, _ptr(weight), eps, out.data_ptr(), _stream_handle(x.device))
+    rc = _call(device, _lib.load().kdaconv_gated_rms_norm,
+               x.data_ptr(), DTYPE_CODES[x.dtype], tokens, heads, dim, xs[0], xs[1], _ptr(gate),
+               gs[0], gs[1], code, _ptr(weight), eps, out.data_ptr())
     _lib.check(rc, "gated_rms_norm")
     return out
 
@@ -121,10 +119,8 @@ def residual_rms_norm(
         return out
     if not x.is_cuda:
         raise ValueError("x must be a GPU tensor")
-    lib = _lib.load()
-    with _on(x.device):
-        rc = lib.kdaconv_residual_rms_norm(
-            x.data_ptr(), DTYPE_CODES[x.dtype], tokens, hidden, xs[0], _ptr(residual), rs[0],
-            residual_scale, _ptr(weight), eps, out.data_ptr(), _stream_handle(x.device))
+    rc = _call(device, _lib.load().kdaconv_residual_rms_norm,
+               x.data_ptr(), DTYPE_CODES[x.dtype], tokens, hidden, xs[0], _ptr(residual), rs[0],
+               residual_scale, _ptr(weight), eps, out.data_ptr())
     _lib.check(rc, "residual_rms_norm")
     return out
