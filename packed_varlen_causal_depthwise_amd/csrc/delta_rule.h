@@ -68,6 +68,7 @@ struct ChunkParams {
   int32_t segment_chunks;  // chunks per segment
   int32_t search_top;  // 64^(levels - 1), 64^levels >= num_seqs
   int32_t min_len;  // shorter sequences are left to the step kernel
+  bool wide;  // 8 waves per chunk of 128 channels, not 4
 };
 
 // One chunk of one head as the scans read it, in pieces of 1 KB that are one matrix operand

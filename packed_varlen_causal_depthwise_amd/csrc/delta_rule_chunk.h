@@ -137,19 +137,24 @@ __device__ __forceinline__ Piece find_piece(const ChunkParams& P, const Pieces& 
   return index < 0 ? Piece{-1, 0} : Piece{uniform(base), index};
 }
 
-// How the prepare kernel's 4 waves hold a chunk's rows. Wave w has rows 4 w .. + 3 and
-// 16 + 4 w .. + 3 (one place of 8 in the order above), two channels per lane: with 128
-// channels each lane has all 8 rows, with 64 the lanes' halves have 4 each. Running sums go
-// over groups of 4 rows, numbered 4 (row / 16) + w.
-template <int D>
+// How the prepare kernel's kWaves waves hold a chunk's rows: two channels per lane, in
+// groups of 4 neighbouring rows. Of 4 waves wave w has rows 4 w .. and 16 + 4 w .. (one place
+// of 8 in the order above): with 128 channels each lane has both groups, with 64 the lanes'
+// halves have one each. Of 8 waves (128 channels) wave w has rows 4 w .. . Running sums go
+// over these groups.
+template <int D, int kWaves>
 struct Rows {
   static constexpr int kLanes = D / 2;  // lanes per row
-  static constexpr int kParts = kLanes / 32;  // groups of 4 rows per lane
+  static constexpr int kParts = kLanes / (8 * kWaves);  // groups of 4 rows per lane
   static constexpr int kRows = 4 * kParts;
 
   // Row i of a lane: the same for all lanes of a wave, plus the lane's part.
   static __device__ __forceinline__ int wave_row(int wave, int i) { return 4 * wave + i % 4 + 16 * (i / 4); }
-  static __device__ __forceinline__ int lane_row(int lane) { return kParts == 2 ? 0 : lane / 32 * 16; }
+  static __device__ __forceinline__ int lane_row(int lane) { return D == 128 ? 0 : lane / 32 * 16; }
+  // Whether the lane's group j is in the chunk's second half.
+  static __device__ __forceinline__ bool second(int wave, int lane, int j) {
+    return kParts == 2 ? j == 1 : (D == 128 ? wave >= 4 : lane >= 32);
+  }
 };
 
 // Hides that x is the same in every iteration of a loop. Without it the compiler computes
@@ -218,20 +223,20 @@ struct Cell {
 
 // A lane's pairs of its rows, as loaded; `lane` is the lane's offset (its channels, and its
 // part of the rows).
-template <int kF, int D>
+template <int kF, class RW>
 struct RawRows {
-  static constexpr int N = Rows<D>::kRows;
+  static constexpr int N = RW::kRows;
   typename Pair<kF>::raw r[N];
 
   __device__ __forceinline__ void load(const Window& w, uint32_t lane, int wave) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = Cell<kF>::pair(w, lane, Rows<D>::wave_row(wave, i));
+    for (int i = 0; i < N; ++i) r[i] = Cell<kF>::pair(w, lane, RW::wave_row(wave, i));
   }
 
   // One element per row, for both of the lane's channels (gates per head).
   __device__ __forceinline__ void load_same(const Window& w, uint32_t lane, int wave) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) r[i] = Cell<kF>::one(w, lane, Rows<D>::wave_row(wave, i));
+    for (int i = 0; i < N; ++i) r[i] = Cell<kF>::one(w, lane, RW::wave_row(wave, i));
   }
 
   __device__ __forceinline__ void values(f32x2 (&x)[N], bool same) const {
@@ -245,12 +250,12 @@ struct RawRows {
 };
 
 // Zeros in the rows past the last.
-template <int D>
-__device__ __forceinline__ void mask_rows(f32x2 (&x)[Rows<D>::kRows], int wave, int lane, int valid) {
+template <class RW>
+__device__ __forceinline__ void mask_rows(f32x2 (&x)[RW::kRows], int wave, int lane, int valid) {
   if (valid == kChunk) return;
 #pragma unroll
-  for (int i = 0; i < Rows<D>::kRows; ++i)
-    if (Rows<D>::wave_row(wave, i) + Rows<D>::lane_row(lane) >= valid) x[i] = f32x2{0.0f, 0.0f};
+  for (int i = 0; i < RW::kRows; ++i)
+    if (RW::wave_row(wave, i) + RW::lane_row(lane) >= valid) x[i] = f32x2{0.0f, 0.0f};
 }
 
 // Sums of N values over 2 kMask lanes, each lane receiving the sum of value (lane index /
@@ -315,22 +320,24 @@ __device__ __forceinline__ double scatter_sum(typename Doubles<N>::type x, int l
 
 // ---------------------------------------------------------------------------- prepare
 
-// Three workgroups per CU (52 KB of LDS, 156 registers). A workgroup alone takes 24500 cycles:
+// With 128 channels 4 or 8 waves: of 8 only two workgroups fit a CU (52 KB of LDS, 112
+// registers), but each is faster; of 4 three do (148 registers). Of 4 one alone takes 24500 cycles:
 // finding its chunk 1600, loads and gates 3900, lengths and sums 1400, operands of the
 // products 2400, products 4400, L and A 1300, operands for the scans 3400, T 4600, the rest
 // its stores. 6144 of them (16384 tokens, 12 heads of 128) take 145 us for 550 MB, 3.8 TB/s,
 // and no single part bounds that: without its stores it takes 130 us, without the products
 // 114, without T 128, without the scans' operands 121. The way through all of them at three
 // workgroups per CU does; a fourth would need 40 KB of LDS and 128 registers.
-template <int kF, int kG, int D>
-__global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkParams P) {
-  typedef Rows<D> RW;
+template <int kF, int kG, int D, int kWaves>
+__global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_prepare_kernel(const ChunkParams P) {
+  typedef Rows<D, kWaves> RW;
+  constexpr int kThreads = 64 * kWaves;
   constexpr int kRows = RW::kRows, kLanes = RW::kLanes, kParts = RW::kParts;
   constexpr int kEB = elem_bytes<kF>(), kGB = elem_bytes<kG>();
   constexpr int kLd = D + 4;  // floats per operand row: 16 rows reach all banks
   constexpr int kMat = kChunk * kLd;
   constexpr int kSq = 34;  // doubles per row of a 32 x 32 matrix
-  // After the products: L and its inverse, A's parts, and 32 D bytes per wave to turn rows
+  // After the products: L and its inverse, A's parts, and 128 D bytes to turn rows
   // into operands.
   constexpr int kSquares = 2 * kChunk * kSq * (int)sizeof(double), kStage = kSquares + 4096;
   constexpr int kBytes = 3 * kMat * 4 > kStage + 128 * D ? 3 * kMat * 4 : kStage + 128 * D;
@@ -365,12 +372,13 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
   const int valid = seq.len - piece.index * kChunk < kChunk ? seq.len - piece.index * kChunk : kChunk;
 
   const int c = 2 * (lane % kLanes), lrow = RW::lane_row(lane);
+  const int quad = wave % 4;  // the lane's rows are 4 quad .. of their blocks of 16
   const int64_t qk = h / R.share;
   const Window wq(R.q + (first * R.q_ts + qk * R.q_hs) * kEB, valid, (uint32_t)R.q_ts * kEB, D * kEB);
   const Window wk(R.k + (first * R.k_ts + qk * R.k_hs) * kEB, valid, (uint32_t)R.k_ts * kEB, D * kEB);
   const Window wg(R.g + (first * R.g_ts + h * R.g_hs) * kGB, valid, (uint32_t)R.g_ts * kGB,
                   (R.g_cs != 0 ? D : 1) * kGB);
-  const auto load_gates = [&](RawRows<kG, D>& rg) {
+  const auto load_gates = [&](RawRows<kG, RW>& rg) {
     if (R.g_cs != 0)
       rg.load(wg, lrow * wg.stride + c * kGB, wave);
     else
@@ -383,18 +391,18 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
   f32x2 bias = {0.0f, 0.0f};
   if (R.dt_bias != nullptr) bias = *(const f32x2a4*)(R.dt_bias + h * D + c);
   {
-    RawRows<kF, D> rq, rk;
-    RawRows<kG, D> rg;
+    RawRows<kF, RW> rq, rk;
+    RawRows<kG, RW> rg;
     load_gates(rg);
     rk.load(wk, lrow * wk.stride + c * kEB, wave);
     rq.load(wq, lrow * wq.stride + c * kEB, wave);
     rg.values(p, R.g_cs == 0);
     rk.values(k, false);
-    mask_rows<D>(k, wave, lane, valid);
+    mask_rows<RW>(k, wave, lane, valid);
     rq.values(q, false);
-    mask_rows<D>(q, wave, lane, valid);
+    mask_rows<RW>(q, wave, lane, valid);
     gate.eval(p, bias);
-    mask_rows<D>(p, wave, lane, valid);
+    mask_rows<RW>(p, wave, lane, valid);
   }
   if (threadIdx.x < kChunk)
     beta[threadIdx.x] = (int)threadIdx.x < valid ? beta_value(R, kF, first + threadIdx.x, h) : 0.0f;
@@ -437,7 +445,7 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
     for (int i = 3; i > 0; --i) rest[4 * j + i - 1] = rest[4 * j + i] + p[4 * j + i];
 #pragma unroll
     for (int i = 1; i < 4; ++i) p[4 * j + i] += p[4 * j + i - 1];
-    *(f32x2*)&tot[4 * (j + lrow / 16) + wave][c] = p[4 * j + 3];
+    *(f32x2*)&tot[4 * RW::second(wave, lane, j) + quad][c] = p[4 * j + 3];
   }
   __syncthreads();
 
@@ -459,12 +467,12 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
 #pragma unroll
   for (int j = 0; j < kParts; ++j) {
     before[j] = after[j] = f32x2{0.0f, 0.0f};
-    const int b = j + lrow / 16;
+    const int b = RW::second(wave, lane, j);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const f32x2 t = *(const f32x2*)&tot[4 * b + i][c];
-      if (i < wave) before[j] += t;
-      if (i > wave) after[j] += t;
+      if (i < quad) before[j] += t;
+      if (i > quad) after[j] += t;
     }
   }
   if (wave == 0 && lane < kLanes) {
@@ -477,7 +485,7 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int r = RW::wave_row(wave, i) + lrow, j = i / 4;
-    const f32x2 m0 = kParts == 2 ? mid[j] : (lrow != 0 ? mid[1] : mid[0]);
+    const f32x2 m0 = RW::second(wave, lane, j) ? mid[1] : mid[0];
     const f32x2 d = p[i] + before[j] - m0;
     const f32x2 e = {exp2_hw(d.x), exp2_hw(d.y)}, m = {exp2_hw(-d.x), exp2_hw(-d.y)};
     const f32x2 kk = k[i] * ktwo[r];
@@ -488,35 +496,40 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
   __syncthreads();
 
   const int n16 = lane % 16, n4 = lane / 16;
-  f64x4 akk = {0.0, 0.0, 0.0, 0.0};  // waves 0 to 2: one 16 x 16 block each
-  f32x4 aqk[3] = {};  // wave 3: all three
+  f64x4 akk = {0.0, 0.0, 0.0, 0.0};  // kinds 0 to 2: one 16 x 16 block of key products each
+  f32x4 aqk[3] = {};  // kind 3: all three of queries and keys
+  // Of 8 waves two share a kind, half of the channels each.
+  const int kind = kWaves == 8 ? (wave < 6 ? wave % 3 : 3) : wave;
+  const int part = kWaves == 8 ? (wave < 6 ? wave / 3 : wave - 6) : 0;
+  constexpr int kShared = kWaves == 8 ? D / 2 : D;
   float dkk[3], dqk[3];
   const bool direct = steep != 0;
   if (!direct) {
     // Blocks (row, column): 0 (0, 0), 1 (1, 1), 2 (1, 0). The key products are summed in
     // FP64: equal keys with steps near 2 (reflections) and no decay make an error common to
     // L's entries grow with the tokens, by 32 per chunk. FP32 sums and an FP32 inverse left
-    // such a state 1e-4 off after 97 tokens. Both kinds take as long: 4000 cycles for 32
-    // FP64 instructions in each of three waves, 4400 for the 96 FP32 ones of the fourth.
-    if (wave < 3) {
-      const float* const rk = mk + ((wave == 0 ? 0 : 16) + n16) * kLd + 4 * n4;
-      const float* const rc = mc + ((wave == 1 ? 16 : 0) + n16) * kLd + 4 * n4;
+    // such a state 1e-4 off after 97 tokens. Both kinds take as long: 125 cycles for an FP64
+    // instruction, 46 for one of the three times as many FP32 ones of kind 3.
+    const int from = kShared * part + 4 * n4;
+    if (kind < 3) {
+      const float* const rk = mk + ((kind == 0 ? 0 : 16) + n16) * kLd + from;
+      const float* const rc = mc + ((kind == 1 ? 16 : 0) + n16) * kLd + from;
 #pragma unroll
-      for (int b = 0; b < D; b += 16) {
+      for (int b = 0; b < kShared; b += 16) {
         const f32x4 x = *(const f32x4*)(rk + b);
         f32x4 z = *(const f32x4*)(rc + b);
-        if (wave == 2) z *= *(const f32x4*)&across[b + 4 * n4];
+        if (kind == 2) z *= *(const f32x4*)&across[b + from];
 #pragma unroll
         for (int e = 0; e < 4; ++e) akk = mfma64((double)x[e], (double)z[e], akk);
       }
     } else {
-      const float* const rq = mq + n16 * kLd + 4 * n4;
-      const float* const rc = mc + n16 * kLd + 4 * n4;
+      const float* const rq = mq + n16 * kLd + from;
+      const float* const rc = mc + n16 * kLd + from;
 #pragma unroll
-      for (int b = 0; b < D; b += 16) {
+      for (int b = 0; b < kShared; b += 16) {
         const f32x4 x0 = *(const f32x4*)(rq + b), x1 = *(const f32x4*)(rq + 16 * kLd + b);
         const f32x4 z0 = *(const f32x4*)(rc + b), z1 = *(const f32x4*)(rc + 16 * kLd + b);
-        const f32x4 z2 = z0 * *(const f32x4*)&across[b + 4 * n4];
+        const f32x4 z2 = z0 * *(const f32x4*)&across[b + from];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           aqk[0] = mfma32(x0[e], z0[e], aqk[0]);
@@ -531,12 +544,12 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
     __syncthreads();
     // The decays, from the sums: exact enough again, then summed in FP64 per channel.
     {
-      RawRows<kG, D> rg;
+      RawRows<kG, RW> rg;
       load_gates(rg);
       f32x2 g[kRows];
       rg.values(g, R.g_cs == 0);
       gate.eval(g, bias);
-      mask_rows<D>(g, wave, lane, valid);
+      mask_rows<RW>(g, wave, lane, valid);
 #pragma unroll
       for (int i = 0; i < kRows; ++i) *(f32x2*)&mk[(RW::wave_row(wave, i) + lrow) * kLd + c] = g[i];
     }
@@ -560,7 +573,7 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
     }
     __syncthreads();
     for (int u = 0; u < 3; ++u) {
-      const int pair = threadIdx.x + 256 * u;  // (t, i) with i <= t, 528 in all
+      const int pair = threadIdx.x + kThreads * u;  // (t, i) with i <= t, 528 in all
       dkk[u] = dqk[u] = 0.0f;
       if (pair >= 528) continue;
       int t = 0;
@@ -602,24 +615,51 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
         i < t ? (double)beta[t] * (kfac[t] * kfac[i]) * a : 0.0;
   };
   if (!direct) {
-    if (wave < 3) {
-      // FP64 results: register r of lane l is row 4 r + l / 16.
-      const int rows = wave == 0 ? 0 : 16, cols = wave == 1 ? 16 : 0;
+    // FP64 results: register r of lane l is row 4 r + l / 16.
+    const int rows = kind == 0 ? 0 : 16, cols = kind == 1 ? 16 : 0;
+    if (kWaves == 8) {
+      // The second parts come through the inverse's place and the staging area.
+      float* const aside = (float*)(shared + kStage) + lane;
+      if (part == 1) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) put_l(rows + 4 * r + n4, cols + n16, akk[r]);
-    } else {
+        for (int r = 0; r < 4; ++r) {
+          if (kind < 3)
+            mt[(rows + 4 * r + n4) * kSq + cols + n16] = akk[r];
+          else
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = 4 * n4 + r;
-        put_a(t, n16, n16 <= t ? aqk[0][r] : 0.0f);
-        put_a(16 + t, 16 + n16, n16 <= t ? aqk[1][r] : 0.0f);
-        put_a(16 + t, n16, aqk[2][r]);
-        put_a(t, 16 + n16, 0.0f);
+            for (int b = 0; b < 3; ++b) aside[64 * (4 * b + r)] = aqk[b][r];
+        }
+      }
+      __syncthreads();
+      if (part == 0) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if (kind < 3)
+            akk[r] += mt[(rows + 4 * r + n4) * kSq + cols + n16];
+          else
+#pragma unroll
+            for (int b = 0; b < 3; ++b) aqk[b][r] += aside[64 * (4 * b + r)];
+        }
+      }
+    }
+    if (part == 0) {
+      if (kind < 3) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) put_l(rows + 4 * r + n4, cols + n16, akk[r]);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = 4 * n4 + r;
+          put_a(t, n16, n16 <= t ? aqk[0][r] : 0.0f);
+          put_a(16 + t, 16 + n16, n16 <= t ? aqk[1][r] : 0.0f);
+          put_a(16 + t, n16, aqk[2][r]);
+          put_a(t, 16 + n16, 0.0f);
+        }
       }
     }
   } else {
     for (int u = 0; u < 3; ++u) {
-      const int pair = threadIdx.x + 256 * u;
+      const int pair = threadIdx.x + kThreads * u;
       if (pair >= 528) continue;
       int t = 0;
       while ((t + 1) * (t + 2) / 2 <= pair) ++t;
@@ -633,8 +673,10 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
 
   // The scans' operands.
   {
-    constexpr int kFrags = D / 32 * 4;  // of a row matrix: (32 channels, 16 rows, hi or lo)
-    _Float16* const own = (_Float16*)(shared + kStage + 32 * D * wave);
+    // The wave's pieces of a row matrix: (32 channels, 16 rows, hi or lo), of both row tiles or
+    // of 8 waves of one.
+    constexpr int kTiles = kWaves == 8 ? 1 : 2, kFrags = D / 32 * kTiles * 2;
+    _Float16* const own = (_Float16*)(shared + kStage + kFrags * 256 * wave);
     const int x = c % 32, kk = c / 32, place16 = place(x);
     f16x2 th[kRows], tl[kRows];
     HalfPair qs[kRows];
@@ -642,22 +684,23 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
     // operand piece; block (channels n, row r) sits at 4 n + (r ^ n), xor the piece's number
     // of 32 channels, so that a row's 64 lanes reach all banks.
     const auto own_at = [&](int i, int part) {
-      const int tt = i / 4 + lrow / 16, n = place16 / 8, r = i % 4;
-      return ((kk * 2 + tt) * 2 + part) * 128 + (((4 * n + (r ^ n)) ^ kk) * 8) + place16 % 8;
+      const int tt = kTiles == 2 ? RW::second(wave, lane, i / 4) : 0, n = place16 / 8, r = i % 4;
+      return ((kk * kTiles + tt) * 2 + part) * 128 + (((4 * n + (r ^ n)) ^ kk) * 8) + place16 % 8;
     };
     const auto copy_out = [&](char* to) {
 #pragma unroll
       for (int f0 = 0; f0 < kFrags; f0 += 4) {
-        const int f = f0 + lane / 16, b = lane % 16, fk = f / 4;
+        const int f = f0 + lane / 16, b = lane % 16, fk = f / (2 * kTiles);
+        const int tt = kTiles == 2 ? f / 2 % 2 : wave / 4;
         const u32q v = *(const u32q*)(own + f * 128 + ((b ^ fk) * 8));
         // In the slot block (channels n, row r of 16) of a piece is 16 n + (r ^ (n + 4 kk)).
-        *(u32q*)(to + f * 1024 + (16 * (b / 4) + 4 * (wave ^ fk) + b % 4) * 16) = v;
+        *(u32q*)(to + ((2 * fk + tt) * 2 + f % 2) * 1024 + (16 * (b / 4) + 4 * (quad ^ fk) + b % 4) * 16) = v;
       }
     };
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const int r = RW::wave_row(wave, i) + lrow, j = i / 4;
-      const bool second = kParts == 2 ? j == 1 : lrow != 0;
+      const bool second = RW::second(wave, lane, j);
       const f32x2 up = p[i] + before[j] + (second ? all[0] : f32x2{0.0f, 0.0f});
       const f32x2 down = rest[i] + after[j] + (second ? f32x2{0.0f, 0.0f} : all[1]);
       const f32x2 e = {exp2_hw(up.x), exp2_hw(up.y)};
@@ -680,21 +723,22 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
     }
     __builtin_amdgcn_wave_barrier();
     copy_out(slot + kSlot.qg());
-    // Columns: the wave's 8 rows are one block of 16 bytes per channel.
+    // Columns: a channel's rows 4 quad .. of both blocks of 16 are one block of 16 bytes.
     _Float16* const kt = (_Float16*)(slot + kSlot.kt());
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
-      const int ch = c + y, at = (ch / 16) * 1024 + (16 * wave + ch % 16) * 8 + lrow / 4;
+      const int ch = c + y, row = (ch / 16) * 1024 + (16 * quad + ch % 16) * 8;
 #pragma unroll
       for (int j = 0; j < kParts; ++j) {
+        const int at = row + 4 * RW::second(wave, lane, j);
         f16x4 hi, lo;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           hi[i] = th[4 * j + i][y];
           lo[i] = tl[4 * j + i][y];
         }
-        *(f16x4*)&kt[at + 4 * j] = hi;
-        *(f16x4*)&kt[at + 512 + 4 * j] = lo;
+        *(f16x4*)&kt[at] = hi;
+        *(f16x4*)&kt[at + 512] = lo;
       }
     }
     if (wave == 0 && lane < kLanes) {
@@ -786,7 +830,7 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
   }
   __syncthreads();
   float* const df = (float*)(slot + kSlot.factors());
-  {
+  if (threadIdx.x < 256) {
     // T scaled to a largest entry of 256 to 512, in three FP16 parts: with two (22 bits) the
     // reflections above still lost 1e-5. Thread u holds places 4 u .. + 3 of the operand
     // order: four neighbouring columns of one row.
@@ -807,8 +851,8 @@ __global__ __launch_bounds__(256) void delta_rule_prepare_kernel(const ChunkPara
     to[512] = last;
     // U is kept times 1 / 16, so that (16 k^)^T (U / 16) adds to S as it is.
     if (u == 0) df[kFactorRows + 2 * kChunk] = __builtin_amdgcn_ldexpf(1.0f / kVec, -e);
+    ((u32q*)(slot + kSlot.a()))[u] = ((const u32q*)sa)[u];
   }
-  ((u32q*)(slot + kSlot.a()))[threadIdx.x] = ((const u32q*)sa)[threadIdx.x];
   if (threadIdx.x < 2 * kChunk) df[kFactorRows + threadIdx.x] = (&rows[0][0])[threadIdx.x];
 }
 
@@ -1441,7 +1485,10 @@ void launch_chunks(const ChunkParams& P, hipStream_t st) {
   const unsigned chunks = (unsigned)P.chunk_programs * heads;
   const unsigned segments = (unsigned)P.segment_programs * heads;
   const unsigned moves = (unsigned)P.move_programs * heads, joins = (unsigned)P.join_programs * heads;
-  hipLaunchKernelGGL((delta_rule_prepare_kernel<kF, kG, D>), dim3(chunks), dim3(256), 0, st, P);
+  if (D == 128 && P.wide)
+    hipLaunchKernelGGL((delta_rule_prepare_kernel<kF, kG, D, D / 16>), dim3(chunks), dim3(4 * D), 0, st, P);
+  else
+    hipLaunchKernelGGL((delta_rule_prepare_kernel<kF, kG, D, 4>), dim3(chunks), dim3(256), 0, st, P);
   if (P.moves != nullptr) {
     hipLaunchKernelGGL((delta_rule_scan_kernel<kF, D, kScanMove>), dim3(moves), dim3(8 * D), 0, st, P);
     hipLaunchKernelGGL((delta_rule_join_kernel<D>), dim3((joins + 7) / 8 * 8, D / 16), dim3(4 * D), 0, st, P);

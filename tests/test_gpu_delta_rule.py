@@ -126,6 +126,18 @@ def test_resets_and_strong_decays(lengths):
         compare(args, kw, "no decay")
 
 
+def test_strong_decays_in_many_chunks():
+    """Chunks whose decays leave the range of products, with the smaller workgroups."""
+    args, kw = ref.rule_inputs([1200], heads=16, dim=128, gate="log", gate_dtype=F32, seed=22)
+    g = args[3]
+    g[5::64, :, :] = -float("inf")
+    g[12::64, ::2, 1::4] = -40.0
+    g[20::64, 1, 2::5] = -12.0
+    for t in range(12, 30):
+        g[t::64, ::3, ::7] = -15.0
+    compare(args, kw)
+
+
 def test_equal_keys_with_full_steps():
     """All keys equal and beta one: the triangular system at its worst."""
     for dim in (64, 128):
@@ -272,6 +284,15 @@ def test_short_and_long_together(short, most, long, heads):
             lengths = sorted(lengths)
         args, kw = ref.rule_inputs(lengths, heads=heads, dim=64, seed=short, pad=2)
         compare(args, kw, f"sorted {at_end}")
+
+
+@pytest.mark.parametrize("dtype,gate", [(BF16, "bounded"), (F16, "log"), (F32, "softplus")], ids=str)
+def test_many_chunks(dtype, gate):
+    """More chunks than get the larger workgroups."""
+    lengths = [97, 33, 64, 129] * 8
+    args, kw = ref.rule_inputs(lengths, heads=8, qk_heads=4, dim=128, dtype=dtype, gate=gate,
+                               gate_dtype=F32 if gate == "log" else None, seed=12)
+    compare(args, kw)
 
 
 def test_far_lines():
