@@ -1376,9 +1376,9 @@ __global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_ru
 // ahead. Workgroups of one (sequence, head) read the same M: the grid's rows are whole
 // multiples of 8, which puts them on one of the card's 8 dies and in one L2.
 //
-// A step takes 1.6 us: the 64 KB of M alone are 0.5 at a CU's 64 bytes per cycle, the rest is
-// the chain largest value - split - exchange - product. Fewer, longer segments make it
-// shorter, not more workgroups.
+// A step takes 1.3 us (1.6 with its loads issued at once): the 64 KB of M alone are 0.5 at a
+// CU's 64 bytes per cycle, the rest is the chain largest value - split - exchange - product.
+// Fewer, longer segments make it shorter, not more workgroups.
 template <int D>
 __global__ __launch_bounds__(4 * D, 2) void delta_rule_join_kernel(const ChunkParams P) {
   constexpr int kK = D / 32, kWaves = D / 16, kAhead = 2;
@@ -1406,29 +1406,36 @@ __global__ __launch_bounds__(4 * D, 2) void delta_rule_join_kernel(const ChunkPa
     float back;
     f32x4 B;
   };
-  const auto load = [&](int j, Step& x) {
+  // In three parts: half of M's rows each, and B. A workgroup's loads of a step keep the CU's
+  // address unit busy for 1300 cycles, so they are issued where the waves wait for each other.
+  const auto load = [&](int j, Step& x, int part) {
     j = j < segments - 1 ? j : segments - 2;
     const char* const move = moves + (int64_t)j * R.heads * move_bytes(D);
-    const f16x8* const a = (const f16x8*)move + wave * kK * 64 + lane;
+    if (part < 2) {
+      const f16x8* const a = (const f16x8*)move + wave * kK * 64 + lane;
 #pragma unroll
-    for (int kk = 0; kk < kK; ++kk) {
-      x.ah[kk] = a[64 * kk];
-      x.al[kk] = a[64 * kk + D * D / 8];
+      for (int kk = 0; kk < kK / 2; ++kk) {
+        const int k = part * (kK / 2) + kk;
+        x.ah[k] = a[64 * k];
+        x.al[k] = a[64 * k + D * D / 8];
+      }
+    } else {
+      x.back = *(const float*)(move + (int64_t)D * D * 4);
+      const float* const end = ends + (int64_t)j * R.heads * (D * D);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x.B[r] = end[r * D];
     }
-    x.back = *(const float*)(move + (int64_t)D * D * 4);
-    const float* const end = ends + (int64_t)j * R.heads * (D * D);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) x.B[r] = end[r * D];
   };
   f32x4 S;
 #pragma unroll
   for (int r = 0; r < 4; ++r) S[r] = ends[r * D];
-  const auto step = [&](int j, const Step& x) {
+  const auto step = [&](int j, const Step& x, Step& ahead) {
     const int buf = j & 1;
     float m = __builtin_fmaxf(__builtin_fmaxf(__builtin_fabsf(S[0]), __builtin_fabsf(S[1])),
                               __builtin_fmaxf(__builtin_fabsf(S[2]), __builtin_fabsf(S[3])));
     m = column_max(m);
     if (n4 == 0) most[buf][wave][n16] = m;
+    load(j + kAhead, ahead, 0);
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) m = __builtin_fmaxf(m, most[buf][w][n16]);
@@ -1444,6 +1451,7 @@ __global__ __launch_bounds__(4 * D, 2) void delta_rule_join_kernel(const ChunkPa
       *(f16x4*)&hi[buf][wave / 2][at] = f16x4{p0.hi.x, p0.hi.y, p1.hi.x, p1.hi.y};
       *(f16x4*)&lo[buf][wave / 2][at] = f16x4{p0.lo.x, p0.lo.y, p1.lo.x, p1.lo.y};
     }
+    load(j + kAhead, ahead, 1);
     __syncthreads();
     const float f = __builtin_amdgcn_ldexpf(x.back, -e);
     f32x4 hh = {0.0f, 0.0f, 0.0f, 0.0f}, hl = hh, lh = hh;
@@ -1454,6 +1462,7 @@ __global__ __launch_bounds__(4 * D, 2) void delta_rule_join_kernel(const ChunkPa
       hl = mfma16(x.ah[kk], bl, hl);
       lh = mfma16(x.al[kk], bh, lh);
     }
+    load(j + kAhead, ahead, 2);
     hh += hl + lh;
     float* const end = ends + (int64_t)j * R.heads * (D * D);
 #pragma unroll
@@ -1466,12 +1475,13 @@ __global__ __launch_bounds__(4 * D, 2) void delta_rule_join_kernel(const ChunkPa
   // registers at its end, and so wait for them.
   Step x[kAhead + 1];
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) load(1 + i, x[i]);
+  for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+    for (int part = 0; part < 3; ++part) load(1 + i, x[i], part);
   for (int j = 1;;) {
 #pragma unroll
     for (int i = 0; i <= kAhead; ++i) {
-      load(j + kAhead, x[(i + kAhead) % (kAhead + 1)]);
-      step(j, x[i]);
+      step(j, x[i], x[(i + kAhead) % (kAhead + 1)]);
       if (++j == segments - 1) return;
     }
   }
