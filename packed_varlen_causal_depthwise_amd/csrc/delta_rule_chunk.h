@@ -24,8 +24,8 @@
 // A chunk's gates, norms and exponentials are worked out once, by prepare, and handed over
 // as matrix operands (60 KB per chunk and head of 128): the scans were bound by that vector
 // work when they repeated it (5 us per chunk, 0.5 TB/s). One sequence of 16384 tokens, 12
-// heads of 128, bf16 now takes 145 us in prepare, 114 for the transitions, 32 for the join
-// and 100 for the outputs. Its tensors alone, 252 MB, are 50 us; the operands' way through
+// heads of 128, bf16 now takes 143 us in prepare, 113 for the transitions, 27 for the join
+// and 96 for the outputs. Its tensors alone, 252 MB, are 50 us; the operands' way through
 // memory, 1.1 GB of reads and writes more, and the chain from chunk to chunk are the rest.
 //
 // Numbers. Matrix products run on the FP16 matrix instructions with every operand split
@@ -919,15 +919,15 @@ struct ScanState {
 };
 
 // Chunk by chunk with S in registers. Operands come from the slot to LDS by direct loads: the
-// row matrices for the next chunk while this chunk's updates run, the rest while the next
+// row matrices for the next chunk while this chunk's S is updated, the rest while the next
 // chunk's products with S run; two barriers per chunk. Waves share the operands and own 16
 // columns each; for a segment's transition half of the waves for B and half for M. (With 32
 // columns per wave the operands are read from LDS half as often, but the 172 matrix
 // instructions per chunk of a lone wave took 24 cycles each instead of 14: 20% longer with one
 // sequence of 64 tokens, 5% with many.)
 //
-// 264 output scans of 24 chunks take 100 us: 490 MB, 4.6 TB/s, close to what a copy reaches;
-// the matrix units are busy for 37% of it. The 252 transitions take 114 us for half the bytes:
+// 264 output scans of 24 chunks take 96 us: 490 MB, 5 TB/s, what a copy reaches; the matrix
+// units are busy for 37% of it. The 252 transitions take 113 us for half the bytes:
 // 16 waves read 640 KB of operands from LDS per chunk, which is 5000 of its 10000 cycles, and
 // the matrix units are busy for 40%.
 template <int kF, int D, int kMode>
@@ -1122,7 +1122,6 @@ __global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_ru
                  : "memory");
     __syncthreads();
     slot += slot_step;
-    if (chunk + 1 < end) load_rows(slot);
 
     // ---- X = V - n Y, in the columns' scales
     if (identity || valid != kChunk) {
@@ -1205,6 +1204,9 @@ __global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_ru
         }
       }
     }
+    // (Issued here and not right after the barrier: the products with T then start 300 cycles
+    // earlier, and the loads still have the rest of the chunk to arrive.)
+    if (chunk + 1 < end) load_rows(slot);
     // U may outgrow X where keys are longer than 1 (S is safe at any smaller scale).
     left = false;
 #pragma unroll
