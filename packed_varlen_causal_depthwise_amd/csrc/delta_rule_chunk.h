@@ -1052,6 +1052,20 @@ __global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_ru
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
 
+  if (identity && begin == 0) {
+    // Nobody needs the first segment's M: these waves only load.
+    for (int left = end; left > 0; --left) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+      slot += slot_step;
+      if (left > 1) load_rows(slot);
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+      if (left > 1) load_rest(slot);
+    }
+    return;
+  }
+
   for (int chunk = begin; chunk < end; ++chunk) {
     const int64_t first = seq.start + chunk * kChunk;
     const int valid = seq.len - chunk * kChunk < kChunk ? seq.len - chunk * kChunk : kChunk;
