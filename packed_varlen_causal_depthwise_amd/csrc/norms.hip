@@ -8,8 +8,10 @@
 // call of some size reads its inputs once, and what it writes to the residual is read again
 // only after the block between. That leaves the caches to the outputs, which the next
 // product reads at once. With all accesses ordinary 16384 x 4096 bf16 residual rows took
-// 98 us and 16384 tokens of 12 gated heads 32.9 us, against 82 (6.5 TB/s) and 30.2 (5.0
-// TB/s); with non-temporal outputs too 91 and 28.8.
+// 98 us and 16384 tokens of 12 gated heads 32.9 us, against 82 (6.5 TB/s) and 30.2; with
+// non-temporal outputs too 91 and 28.8. The gate's kind is a template argument: a branch per
+// element on it kept the vector units busy for 73% of those 30.2 us, without it 26.2 (5.8
+// TB/s).
 #include "delta_rule_device.h"
 
 #include <algorithm>
@@ -109,12 +111,12 @@ struct GatedNormParams {
   int32_t heads_shift;
   int32_t dim;
   int32_t lanes_log;  // log2 of the lanes per row (a power of two >= dim / 8)
-  int32_t activation;
   float inv_dim, eps;
 };
 
-// kU rows per lane group: their loads are all issued before the first sum.
-template <int kF, int kU>
+// kU rows per lane group: their loads are all issued before the first sum. Rows past the last
+// load the last one and lanes past dim the row's start, so that no load waits for a branch.
+template <int kF, int kU, int kGate>
 __global__ __launch_bounds__(256) void gated_rms_norm_kernel(const GatedNormParams P) {
   constexpr int kEB = elem_bytes<kF>();
   const int lanes = 1 << P.lanes_log;
@@ -122,39 +124,35 @@ __global__ __launch_bounds__(256) void gated_rms_norm_kernel(const GatedNormPara
   const int64_t groups = 256 >> P.lanes_log;
   const int64_t first = (int64_t)blockIdx.x * groups * kU + (threadIdx.x >> P.lanes_log);
   const bool in = c < P.dim;
+  const int at = in ? c : 0;
   Eight x[kU], z[kU];
 #pragma unroll
   for (int u = 0; u < kU; ++u) {
     const int64_t row = first + u * groups;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[u].v[i] = z[u].v[i] = 0.0f;
-    if (in && row < P.rows) {
-      const uint32_t n = (uint32_t)row;
-      const uint32_t t = (__umulhi(n, P.heads_magic) + n) >> P.heads_shift, h = n - t * P.heads;
-      x[u] = load8<kF, true>(P.x + ((int64_t)t * P.x_s0 + (int64_t)h * P.x_s1 + c) * kEB);
-      if (P.activation != KDACONV_NORM_GATE_NONE)
-        z[u] = load8<kF, true>(P.gate + ((int64_t)t * P.g_s0 + (int64_t)h * P.g_s1 + c) * kEB);
-    }
+    const uint32_t n = (uint32_t)(row < P.rows ? row : P.rows - 1);
+    const uint32_t t = (__umulhi(n, P.heads_magic) + n) >> P.heads_shift, h = n - t * P.heads;
+    x[u] = load8<kF, true>(P.x + ((int64_t)t * P.x_s0 + (int64_t)h * P.x_s1 + at) * kEB);
+    if constexpr (kGate != KDACONV_NORM_GATE_NONE)
+      z[u] = load8<kF, true>(P.gate + ((int64_t)t * P.g_s0 + (int64_t)h * P.g_s1 + at) * kEB);
   }
   Eight w;
 #pragma unroll
   for (int i = 0; i < 8; ++i) w.v[i] = 1.0f;
-  if (in && P.weight != nullptr) w = load8<kRuleF32>((const char*)(P.weight + c));
+  if (P.weight != nullptr) w = load8<kRuleF32>((const char*)(P.weight + at));
 #pragma unroll
   for (int u = 0; u < kU; ++u) {
     const int64_t row = first + u * groups;
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s = __builtin_fmaf(x[u].v[i], x[u].v[i], s);
+    s = in ? s : 0.0f;
     for (int m = lanes >> 1; m > 0; m >>= 1) s += __shfl_xor(s, m);
     const float r = rsqrt_f(__builtin_fmaf(s, P.inv_dim, P.eps));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float y = x[u].v[i] * r * w.v[i];
-      if (P.activation != KDACONV_NORM_GATE_NONE) {
-        y *= sigmoid_f(z[u].v[i]);
-        if (P.activation == KDACONV_NORM_GATE_SILU) y *= z[u].v[i];
-      }
+      if constexpr (kGate != KDACONV_NORM_GATE_NONE) y *= sigmoid_f(z[u].v[i]);
+      if constexpr (kGate == KDACONV_NORM_GATE_SILU) y *= z[u].v[i];
       x[u].v[i] = y;
     }
     if (in && row < P.rows) store8<kF>(P.out + (row * P.dim + c) * kEB, x[u]);
@@ -255,15 +253,27 @@ void divider(uint32_t d, uint32_t* magic, int32_t* shift) {
   *shift = l;
 }
 
-template <int kF>
-void launch_gated(const GatedNormParams& P, hipStream_t st) {
+template <int kF, int kGate>
+void launch_gated_as(const GatedNormParams& P, hipStream_t st) {
   const int64_t groups = 256 >> P.lanes_log;
   // Four rows per lane group where that still leaves every CU several workgroups; else one,
   // for latency.
-  if (P.rows >= groups * 4 * 1024)
-    hipLaunchKernelGGL((gated_rms_norm_kernel<kF, 4>), dim3((unsigned)((P.rows + 4 * groups - 1) / (4 * groups))), dim3(256), 0, st, P);
+  const int rows = P.rows >= groups * 4 * 1024 ? 4 : 1;
+  const dim3 grid((unsigned)((P.rows + rows * groups - 1) / (rows * groups)));
+  if (rows == 4)
+    hipLaunchKernelGGL((gated_rms_norm_kernel<kF, 4, kGate>), grid, dim3(256), 0, st, P);
   else
-    hipLaunchKernelGGL((gated_rms_norm_kernel<kF, 1>), dim3((unsigned)((P.rows + groups - 1) / groups)), dim3(256), 0, st, P);
+    hipLaunchKernelGGL((gated_rms_norm_kernel<kF, 1, kGate>), grid, dim3(256), 0, st, P);
+}
+
+template <int kF>
+void launch_gated(const GatedNormParams& P, int gate, hipStream_t st) {
+  if (gate == KDACONV_NORM_GATE_SIGMOID)
+    launch_gated_as<kF, KDACONV_NORM_GATE_SIGMOID>(P, st);
+  else if (gate == KDACONV_NORM_GATE_SILU)
+    launch_gated_as<kF, KDACONV_NORM_GATE_SILU>(P, st);
+  else
+    launch_gated_as<kF, KDACONV_NORM_GATE_NONE>(P, st);
 }
 
 template <int kF>
@@ -329,16 +339,15 @@ extern "C" int kdaconv_gated_rms_norm(const void* x, int dtype, int64_t num_toke
   P.dim = (int32_t)dim;
   P.lanes_log = 0;
   while ((8 << P.lanes_log) < dim) ++P.lanes_log;
-  P.activation = activation;
   P.inv_dim = (float)(1.0 / (double)dim);
   P.eps = (float)eps;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   if (dtype == KDACONV_F32)
-    launch_gated<kRuleF32>(P, st);
+    launch_gated<kRuleF32>(P, activation, st);
   else if (dtype == KDACONV_F16)
-    launch_gated<kRuleF16>(P, st);
+    launch_gated<kRuleF16>(P, activation, st);
   else
-    launch_gated<kRuleBF16>(P, st);
+    launch_gated<kRuleBF16>(P, activation, st);
   return hipGetLastError() == hipSuccess ? KDACONV_OK : KDACONV_ELAUNCH;
 }
 
