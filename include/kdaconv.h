@@ -273,7 +273,9 @@ int kdaconv_activation_map(uint32_t first, int64_t count, int activation, int dt
  * from: its line as it is, or zeros there without an initial state. States, sums and norms
  * are held in FP32 or more; matrix products take FP32 values as pairs of FP16 values (22
  * bits) and sum in FP32; only out is rounded to its format.
- * A log decay below -104 acts as -104 (its exp is zero in FP32, as is -infinity's).
+ * A log decay below -104 acts as -104 (its exp is zero in FP32, as is -infinity's). Log
+ * decays given as they are (KDACONV_GATE_LOG) are at most 0; positive ones are not looked for
+ * and may leave the range of the prefill's FP16 pairs.
  *
  * All strides count elements.
  */
@@ -316,7 +318,7 @@ typedef struct kdaconv_rule_args {
 
 /*
  * Bytes of device scratch memory that kdaconv_gated_delta_rule needs for these sizes (0
- * for none). The scratch holds no state between calls; calls that may run at the same
+ * for none; about 60 KB per 32 tokens and head of 128, 35 KB per head of 64). The scratch holds no state between calls; calls that may run at the same
  * time need scratch memories of their own. Aligned to 256 bytes.
  */
 int64_t kdaconv_gated_delta_rule_workspace(int64_t num_tokens, int64_t num_seqs,

@@ -143,7 +143,7 @@ def gated_delta_rule_fn(
     head_dim ** -0.5.
 
     g (tokens, heads, head_dim), or (tokens, heads) for one gate per head, is in v's dtype or
-    float32. It is the log decay itself, or with ``a_log`` (heads,) the gate's input::
+    float32. It is the log decay itself (at most 0), or with ``a_log`` (heads,) the gate's input::
 
         -exp(a_log) * softplus(g + dt_bias)                      # lower_bound None
         lower_bound * sigmoid(exp(a_log) * (g + dt_bias))        # otherwise
@@ -156,8 +156,9 @@ def gated_delta_rule_fn(
     for ``packed_causal_conv1d_fn``; rows no sequence owns are left unwritten, and a sequence
     without tokens leaves what it starts from (zeros in its line without an initial state). Returns (tokens,
     heads, head_dim) in v's dtype (``out``, when given). The state and every intermediate hold
-    FP32 or 22-bit pairs; only the output is rounded to its dtype. Queued on the current
-    stream; no synchronisation.
+    FP32 or 22-bit pairs; only the output is rounded to its dtype. Takes about 60 KB of scratch
+    memory per 32 tokens and head of 128 from torch's allocator. Queued on the current stream;
+    no synchronisation.
     """
     sizes = _heads(q, k, v, g, beta, states)
     out = _output(v, out)

@@ -295,6 +295,39 @@ def test_many_chunks(dtype, gate):
     compare(args, kw)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_a_very_long_sequence(dim):
+    """Nine thousand tokens through segment after segment."""
+    args, kw = ref.rule_inputs([9001], heads=1, dim=dim, dtype=F32, gate="log", seed=41,
+                               initial=torch.tensor([True]))
+    compare(args, kw)
+
+
+def test_far_rows():
+    """Rows whose offset passes 2^31 elements: the widest token stride there is."""
+    args, kw = ref.rule_inputs([290, 9], heads=1, dim=128, seed=42)
+    stride, tokens = (1 << 23) - 8, 299
+    big = torch.empty((tokens - 1) * stride + 4 * 128, dtype=BF16, device="cuda")
+    g = [to_gpu(a) for a in args]
+    for i in range(4):
+        g[i] = big.as_strided((tokens, 1, 128), (stride, 128, 1), 128 * i)
+        g[i].copy_(args[i])
+    out = kd.gated_delta_rule_fn(*g, **{k: to_gpu(v) for k, v in kw.items()}, null_block_id=None)
+    want, want_st = ref.delta_rule(*args, **kw)
+    ref.check(out, want, BF16, "out")
+    ref.check(g[5], want_st, F32, "states")
+    one = [a[250:251] for a in g[:5]]
+    before = g[5].clone()
+    stepped = kd.gated_delta_rule_update(*one, g[5], g[7][:1], **{k: to_gpu(v) for k, v in kw.items()},
+                                         null_block_id=None)
+    args[5] = before.cpu()
+    loc = torch.tensor([0, 1], dtype=torch.int32)
+    want, want_st = ref.delta_rule(*[a[250:251] for a in args[:5]], args[5], loc, args[7][:1],
+                                   torch.tensor([True]), **kw)
+    ref.check(stepped, want, BF16, "step out")
+    ref.check(g[5], want_st, F32, "step states")
+
+
 def test_far_lines():
     """Lines whose offset passes 2^31 elements."""
     args, kw = ref.rule_inputs([40, 3], heads=1, dim=128, seed=17, lines=4,
