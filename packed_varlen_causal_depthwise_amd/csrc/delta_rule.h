@@ -65,7 +65,7 @@ struct ChunkParams {
   // Chunks; segments; segments but a sequence's last; sequences of 3 segments and more.
   int32_t chunk_programs, segment_programs, move_programs, join_programs;
   Pieces chunk_pieces, segment_pieces, move_pieces, join_pieces;
-  int32_t segment_chunks;  // chunks per segment
+  int32_t segment_chunks, whole_chunks;  // chunks per segment; sequences of up to so many stay whole
   int32_t search_top;  // 64^(levels - 1), 64^levels >= num_seqs
   int32_t min_len;  // shorter sequences are left to the step kernel
   bool wide;  // 8 waves per chunk of 128 channels, not 4

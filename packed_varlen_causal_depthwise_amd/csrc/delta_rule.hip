@@ -24,6 +24,7 @@ struct Plan {
   bool wide;  // prepare takes 8 waves per chunk of 128 channels
   int64_t max_len;
   int segment_chunks;
+  int whole_chunks;  // sequences of up to so many are not cut
   Pieces chunk_pieces, segment_pieces, move_pieces, join_pieces;
   int64_t chunk_programs, segment_programs, move_programs, join_programs;
   int64_t slot_bytes, ends_bytes, moves_bytes;
@@ -49,10 +50,16 @@ constexpr int64_t kStepAverage = 8, kStepAverageMany = 32, kStepMany = 2048;
 // as long segments 518. 3 sequences of 2999 tokens in all, 8 heads, 106 us, segments of 3
 // chunks 121; 8 prompts of 1204 tokens, 12 heads, 77, segments of 6 chunks 81.)
 constexpr int64_t kSegmentCells = 256, kSegmentMin = 4;
+// Sequences of up to kWhole chunks stay whole where they are likely all that short: one that is,
+// or several of half that on average. (8 prompts of 1204 tokens, 12 heads: 69 us against 78;
+// one of 320 tokens 49 against 59, the launches that only cut ones need left out. But a
+// call waits for its longest whole sequence and for its cut ones: 8 prompts of 2400 tokens
+// would take 116 us, not 108, 3 sequences of 2999 tokens 104, not 101.)
+constexpr int64_t kWhole = 12;
 // Chunks get 8 waves in prepare where about this many workgroups, two per CU, are all there
 // are, else 4. A sequence's last chunk is counted half: some have none. (2 chunks 10.7 us
 // against 11.6, 500 19 against 22; 650 26 against 23, 6144 170 against 142.)
-constexpr int64_t kWide = 512;
+constexpr int64_t kWideCells = 512;
 
 int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 
@@ -66,8 +73,9 @@ Plan make_plan(int64_t tokens, int64_t seqs, int64_t heads, int64_t head_dim) {
   const int64_t units = (tokens + kChunk - 1) / kChunk * heads;
   p.segment_chunks = (int)std::max(kSegmentMin, (units + cells - 1) / cells);
   const int64_t segment = (int64_t)p.segment_chunks * kChunk;
-  p.wide = (tokens / kChunk + (seqs + 1) / 2) * heads <= kWide;
-  p.segments = tokens > segment;
+  p.wide = (tokens / kChunk + (seqs + 1) / 2) * heads <= kWideCells;
+  p.whole_chunks = tokens * (seqs > 1 ? 2 : 1) <= kWhole * kChunk * seqs ? (int)kWhole : 0;
+  p.segments = tokens > std::max(segment, (int64_t)p.whole_chunks * kChunk);
   const auto pieces = [&](int64_t piece_tokens, Pieces& how) {
     const int64_t all = tokens / piece_tokens + seqs;
     // Sequences of more than max_len tokens alone: max_len tokens and more per program are
@@ -281,6 +289,7 @@ extern "C" int kdaconv_gated_delta_rule(const kdaconv_rule_args* args, void* wor
     P.move_pieces = plan.move_pieces;
     P.join_pieces = plan.join_pieces;
     P.segment_chunks = plan.segment_chunks;
+    P.whole_chunks = plan.whole_chunks;
     int64_t reach = kRuleWave;
     while (reach < args->num_seqs) reach *= kRuleWave;
     P.search_top = (int32_t)(reach / kRuleWave);

@@ -137,6 +137,11 @@ __device__ __forceinline__ Piece find_piece(const ChunkParams& P, const Pieces& 
   return index < 0 ? Piece{-1, 0} : Piece{uniform(base), index};
 }
 
+// Sequences of up to P.whole_chunks are not cut.
+__device__ __forceinline__ int chunks_per_segment(const ChunkParams& P, int chunks) {
+  return chunks <= P.whole_chunks ? chunks : P.segment_chunks;
+}
+
 // How the prepare kernel's kWaves waves hold a chunk's rows: two channels per lane, in
 // groups of 4 neighbouring rows. Of 4 waves wave w has rows 4 w .. and 16 + 4 w .. (one place
 // of 8 in the order above): with 128 channels each lane has both groups, with 64 the lanes'
@@ -956,8 +961,8 @@ __global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_ru
     for (int i = threadIdx.x; i < D * D; i += 4 * D) to[i] = 0.0f;
   }
   if (seq.len < P.min_len) return;
-  const int per = P.segment_chunks;
   const int chunks = (seq.len + kChunk - 1) / kChunk;
+  const int per = chunks_per_segment(P, chunks);
   const int begin = piece.index * per, end = begin + per < chunks ? begin + per : chunks;
   if (begin >= chunks) return;
   if (!kOut && end == chunks) return;
@@ -1409,7 +1414,8 @@ __global__ __launch_bounds__(4 * D, 2) void delta_rule_join_kernel(const ChunkPa
   const Sequence seq(R, piece.s);
   if (seq.len < P.min_len) return;
   const int chunks = (seq.len + kChunk - 1) / kChunk;
-  const int segments = (chunks + P.segment_chunks - 1) / P.segment_chunks;
+  const int per = chunks_per_segment(P, chunks);
+  const int segments = (chunks + per - 1) / per;
   if (segments < 3) return;
   const int n16 = lane % 16, n4 = lane / 16;
   const int64_t cell = (int64_t)P.move_pieces.first(piece.s, seq.start) * R.heads + h;
