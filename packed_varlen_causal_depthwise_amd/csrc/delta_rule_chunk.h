@@ -926,19 +926,20 @@ struct ScanState {
 // Chunk by chunk with S in registers. Operands come from the slot to LDS by direct loads: the
 // row matrices for the next chunk while this chunk's S is updated, the rest while the next
 // chunk's products with S run; two barriers per chunk. Waves share the operands and own 16
-// columns each; for a segment's transition half of the waves for B and half for M. (With 32
-// columns per wave the operands are read from LDS half as often, but the 172 matrix
-// instructions per chunk of a lone wave took 24 cycles each instead of 14: 20% longer with one
-// sequence of 64 tokens, 5% with many.)
+// columns each; for a segment's transition half of the waves for B and half for M, or (kParts 2)
+// one of two workgroups each. (With 32 columns per wave the operands are read from LDS half as
+// often, but the 172 matrix instructions per chunk of a lone wave took 24 cycles each instead of
+// 14: 20% longer with one sequence of 64 tokens, 5% with many. Two workgroups for the outputs of
+// a segment, half of the columns each, took 37 us against 32 for 96 chains of up to 10 chunks.)
 //
 // 264 output scans of 24 chunks take 96 us: 490 MB, 5 TB/s, what a copy reaches; the matrix
 // units are busy for 37% of it. The 252 transitions take 113 us for half the bytes:
 // 16 waves read 640 KB of operands from LDS per chunk, which is 5000 of its 10000 cycles, and
 // the matrix units are busy for 40%.
-template <int kF, int D, int kMode>
-__global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_rule_scan_kernel(const ChunkParams P) {
+template <int kF, int D, int kMode, int kParts>
+__global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void delta_rule_scan_kernel(const ChunkParams P) {
   constexpr bool kOut = kMode == kScanOut;
-  constexpr int kColWaves = D / 16, kWaves = kOut ? kColWaves : 2 * kColWaves;
+  constexpr int kColWaves = D / 16, kWaves = (kOut ? 1 : 2) * kColWaves / kParts;
   constexpr int kEB = elem_bytes<kF>();
   constexpr int kM = D / 16, kN = D / (16 * kColWaves), kK = D / 32;
   constexpr Slot kSlot{D};
@@ -958,7 +959,7 @@ __global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_ru
   if (kOut && seq.len == 0 && P.min_len == 1 && seq.line >= 0 && !seq.init && piece.index == 0) {
     // Without tokens a sequence that starts from zeros leaves them.
     float* const to = R.states + seq.line * R.st_line + h * R.st_head;
-    for (int i = threadIdx.x; i < D * D; i += 4 * D) to[i] = 0.0f;
+    for (int i = threadIdx.x; i < D * D; i += kRuleWave * kWaves) to[i] = 0.0f;
   }
   if (seq.len < P.min_len) return;
   const int chunks = (seq.len + kChunk - 1) / kChunk;
@@ -968,8 +969,11 @@ __global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_ru
   if (!kOut && end == chunks) return;
 
   const int n16 = lane % 16, n4 = lane / 16;
-  const bool identity = !kOut && wave >= kColWaves;  // this wave's columns are M's
-  const int col = wave % kColWaves * (16 * kN) + kN * n16;
+  // This wave's columns are M's; and which.
+  const bool identity = !kOut && (kParts == 2 ? blockIdx.y == 1 : wave >= kColWaves);
+  const int cw = wave % kColWaves;
+  const int col = cw * (16 * kN) + kN * n16;
+  if (kParts == 2 && identity && begin == 0) return;  // nobody needs the first segment's M
   // The segment's end; for outputs the end of the segment before.
   const int move = kOut ? P.move_pieces.first(piece.s, seq.start) + piece.index - 1 : program;
   const int64_t cell = (int64_t)move * R.heads + h;
@@ -1057,7 +1061,7 @@ __global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_ru
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
 
-  if (identity && begin == 0) {
+  if (kParts == 1 && identity && begin == 0) {
     // Nobody needs the first segment's M: these waves only load.
     for (int left = end; left > 0; --left) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -1359,7 +1363,7 @@ __global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_ru
       }
 #pragma unroll
       for (int m = 32; m > 0; m >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, m));
-      if (lane == 0) part[wave - kColWaves] = top;
+      if (lane == 0) part[cw] = top;
     }
     __syncthreads();
     if (identity) {
@@ -1383,7 +1387,7 @@ __global__ __launch_bounds__(kMode == kScanOut ? 4 * D : 8 * D, 4) void delta_ru
             hi[D * D + at] = (_Float16)(x - (float)(_Float16)x);
           }
       }
-      if (wave == kColWaves && lane == 0) *(float*)(to + (int64_t)D * D * 4) = __builtin_amdgcn_ldexpf(1.0f, -e);
+      if (cw == 0 && lane == 0) *(float*)(to + (int64_t)D * D * 4) = __builtin_amdgcn_ldexpf(1.0f, -e);
     }
   }
 }
@@ -1522,10 +1526,16 @@ void launch_chunks(const ChunkParams& P, hipStream_t st) {
   else
     hipLaunchKernelGGL((delta_rule_prepare_kernel<kF, kG, D, 4>), dim3(chunks), dim3(256), 0, st, P);
   if (P.moves != nullptr) {
-    hipLaunchKernelGGL((delta_rule_scan_kernel<kF, D, kScanMove>), dim3(moves), dim3(8 * D), 0, st, P);
+    // Two workgroups per segment and head, one for B and one for M, where that makes at most two
+    // per CU: each CU then reads half as many operands from LDS (60 segments of 4 chunks 22.4 us
+    // against 17.3, 192 28.9 against 28.0; the operands are loaded twice).
+    if (moves <= 256)
+      hipLaunchKernelGGL((delta_rule_scan_kernel<kF, D, kScanMove, 2>), dim3(moves, 2), dim3(4 * D), 0, st, P);
+    else
+      hipLaunchKernelGGL((delta_rule_scan_kernel<kF, D, kScanMove, 1>), dim3(moves), dim3(8 * D), 0, st, P);
     hipLaunchKernelGGL((delta_rule_join_kernel<D>), dim3((joins + 7) / 8 * 8, D / 16), dim3(4 * D), 0, st, P);
   }
-  hipLaunchKernelGGL((delta_rule_scan_kernel<kF, D, kScanOut>), dim3(segments), dim3(4 * D), 0, st, P);
+  hipLaunchKernelGGL((delta_rule_scan_kernel<kF, D, kScanOut, 1>), dim3(segments), dim3(4 * D), 0, st, P);
 }
 
 template <int kF, int kG>

@@ -303,6 +303,14 @@ def test_a_very_long_sequence(dim):
     compare(args, kw)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+def test_many_segments(dim):
+    """More segments than CUs."""
+    args, kw = ref.rule_inputs([4096], heads=16, qk_heads=8, dim=dim, seed=43,
+                               initial=torch.tensor([True]))
+    compare(args, kw)
+
+
 def test_far_rows():
     """Rows whose offset passes 2^31 elements: the widest token stride there is."""
     args, kw = ref.rule_inputs([290, 9], heads=1, dim=128, seed=42)
