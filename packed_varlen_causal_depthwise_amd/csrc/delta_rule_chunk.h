@@ -325,7 +325,7 @@ __device__ __forceinline__ double scatter_sum(typename Doubles<N>::type x, int l
 
 // ---------------------------------------------------------------------------- prepare
 
-// With 128 channels 4 or 8 waves: of 8 only two workgroups fit a CU (52 KB of LDS, 112
+// With 128 channels 4 or 8 waves: of 8 only two workgroups fit a CU (53 KB of LDS, 112
 // registers), but each is faster; of 4 three do (148 registers). Of 4 one alone takes 24500 cycles:
 // finding its chunk 1600, loads and gates 3900, lengths and sums 1400, operands of the
 // products 2400, products 4400, L and A 1300, operands for the scans 3400, T 4600, the rest
@@ -350,7 +350,8 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
   __shared__ __attribute__((aligned(16))) char shared[kBytes];
   // The groups' decays, read before the operands take their place.
   float (*const tot)[D] = (float (*)[D])shared;
-  __shared__ __attribute__((aligned(16))) float across[D];
+  // Decays of a chunk's second 8 tokens and of its third.
+  __shared__ __attribute__((aligned(16))) float across[2][D];
   // Per row: the key's factor times 16, the query's times 16, the key's power of two; and
   // as they go to the slot |k| / 16 and the outputs' factor / 16.
   __shared__ float kf16[kChunk], qf16[kChunk], ktwo[kChunk];
@@ -457,16 +458,19 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
   // Each block of 16 rows takes its decays from its middle (after 8 rows): rows carry
   // 2^(p - mid), columns 2^(mid - p), whose product is exact to FP32 while both halves of
   // the block stay within 2^101 (8 tokens of log decay -8.75 each; the bounded gate
-  // reaches -5). Steeper chunks take the direct sums below.
-  f32x2 all[2], mid[2];  // of both blocks
+  // reaches -5). Steeper chunks take the direct sums below. Between the blocks lie the decays
+  // of block 0's second half and of block 1's first. Their product may leave FP32's range where
+  // neither does, so columns of block 0 carry one and rows of block 1 the other: each scaled
+  // operand is at most its vector.
+  f32x2 all[2], mid[2], late[2];  // of both blocks; late: of their second halves
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     const f32x2 t0 = *(const f32x2*)&tot[4 * b][c], t1 = *(const f32x2*)&tot[4 * b + 1][c];
     const f32x2 t2 = *(const f32x2*)&tot[4 * b + 2][c], t3 = *(const f32x2*)&tot[4 * b + 3][c];
     mid[b] = t0 + t1;
-    all[b] = mid[b] + (t2 + t3);
-    const f32x2 late = t2 + t3;
-    if (mid[b].x < -101.0f || mid[b].y < -101.0f || late.x < -101.0f || late.y < -101.0f) steep = 1;
+    late[b] = t2 + t3;
+    all[b] = mid[b] + late[b];
+    if (mid[b].x < -101.0f || mid[b].y < -101.0f || late[b].x < -101.0f || late[b].y < -101.0f) steep = 1;
   }
   f32x2 before[kParts], after[kParts];  // log2 decays of the block before and after the group
 #pragma unroll
@@ -481,10 +485,8 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
     }
   }
   if (wave == 0 && lane < kLanes) {
-    // From the middle of block 0 to the middle of block 1: what a column of block 0 needs
-    // to meet a row of block 1.
-    const f32x2 d = all[0] - mid[0] + mid[1];
-    *(f32x2*)&across[c] = f32x2{exp2_hw(d.x), exp2_hw(d.y)};
+    *(f32x2*)&across[0][c] = f32x2{exp2_hw(late[0].x), exp2_hw(late[0].y)};
+    *(f32x2*)&across[1][c] = f32x2{exp2_hw(mid[1].x), exp2_hw(mid[1].y)};
   }
   __syncthreads();
 #pragma unroll
@@ -521,9 +523,11 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
       const float* const rc = mc + ((kind == 1 ? 16 : 0) + n16) * kLd + from;
 #pragma unroll
       for (int b = 0; b < kShared; b += 16) {
-        const f32x4 x = *(const f32x4*)(rk + b);
-        f32x4 z = *(const f32x4*)(rc + b);
-        if (kind == 2) z *= *(const f32x4*)&across[b + from];
+        f32x4 x = *(const f32x4*)(rk + b), z = *(const f32x4*)(rc + b);
+        if (kind == 2) {
+          x *= *(const f32x4*)&across[1][b + from];
+          z *= *(const f32x4*)&across[0][b + from];
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) akk = mfma64((double)x[e], (double)z[e], akk);
       }
@@ -534,12 +538,13 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
       for (int b = 0; b < kShared; b += 16) {
         const f32x4 x0 = *(const f32x4*)(rq + b), x1 = *(const f32x4*)(rq + 16 * kLd + b);
         const f32x4 z0 = *(const f32x4*)(rc + b), z1 = *(const f32x4*)(rc + 16 * kLd + b);
-        const f32x4 z2 = z0 * *(const f32x4*)&across[b + from];
+        const f32x4 x2 = x1 * *(const f32x4*)&across[1][b + from];
+        const f32x4 z2 = z0 * *(const f32x4*)&across[0][b + from];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           aqk[0] = mfma32(x0[e], z0[e], aqk[0]);
           aqk[1] = mfma32(x1[e], z1[e], aqk[1]);
-          aqk[2] = mfma32(x1[e], z2[e], aqk[2]);
+          aqk[2] = mfma32(x2[e], z2[e], aqk[2]);
         }
       }
     }

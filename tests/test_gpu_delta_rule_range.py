@@ -1,0 +1,55 @@
+"""The gated delta rule over the whole range of its arguments."""
+
+import pytest
+import torch
+
+import rule_reference as ref
+from test_gpu_delta_rule import compare
+
+pytestmark = pytest.mark.gpu
+
+F32 = torch.float32
+
+# Lengths, heads and head_dim: heads of 64; of 128 with 8 waves per chunk; with 4.
+FORMS = [([100, 40], 3, 64), ([100, 40], 3, 128), ([1100], 16, 128)]
+forms = pytest.mark.parametrize("lengths,heads,dim", FORMS, ids=str)
+
+
+def log_inputs(lengths, heads, dim, seed=0, **kw):
+    return ref.rule_inputs(lengths, heads=heads, dim=dim, dtype=F32, gate="log", seed=seed, **kw)
+
+
+@forms
+@pytest.mark.parametrize("rate", [5.0, 5.5, 6.0, 7.0, 8.5])
+def test_uniform_strong_decays(rate, lengths, heads, dim):
+    """Decays that 8 tokens of a chunk can hold in one factor and 16 cannot: in every
+    channel, then in two of three of one head."""
+    args, kw = log_inputs(lengths, heads, dim, seed=60)
+    args[3] = torch.full_like(args[3], -rate)
+    compare(args, kw)
+    args[3][:, 1:] = -0.01
+    args[3][:, 0, 1::3] = -0.01
+    compare(args, kw)
+
+
+@forms
+@pytest.mark.parametrize("step", [1, 4, 1000])
+def test_two_strong_decays_in_a_chunk(step, lengths, heads, dim):
+    """Tokens between them meet without either: in every channel, every fourth, one."""
+    args, kw = log_inputs(lengths, heads, dim, seed=61)
+    args[3] = torch.zeros_like(args[3])
+    for at in (10, 20):
+        args[3][at::32, :, 2::step] = -60.0
+    compare(args, kw)
+
+
+@forms
+@pytest.mark.parametrize("lower_bound", [-6.0, -7.0, -8.0, None])
+def test_strong_gates(lower_bound, lengths, heads, dim):
+    """The gates at a_log = log 16, their inputs of standard deviation 2."""
+    args, kw = ref.rule_inputs(lengths, heads=heads, dim=dim, dtype=F32, seed=62,
+                               gate="softplus" if lower_bound is None else "bounded")
+    kw["a_log"] = torch.full_like(kw["a_log"], 2.772588722239781)
+    kw["lower_bound"] = lower_bound
+    args[3] = 2 * args[3]
+    compare(args, kw)
