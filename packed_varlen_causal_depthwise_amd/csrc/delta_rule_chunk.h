@@ -509,7 +509,8 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
   const int kind = kWaves == 8 ? (wave < 6 ? wave % 3 : 3) : wave;
   const int part = kWaves == 8 ? (wave < 6 ? wave / 3 : wave - 6) : 0;
   constexpr int kShared = kWaves == 8 ? D / 2 : D;
-  float dkk[3], dqk[3];
+  double dkk[3];
+  float dqk[3];
   const bool direct = steep != 0;
   if (!direct) {
     // Blocks (row, column): 0 (0, 0), 1 (1, 1), 2 (1, 0). The key products are summed in
@@ -550,7 +551,9 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
     }
   } else {
     // Direct sums of k_t k_i 2^(G_t - G_i), with the running sums G in FP64 (a chunk may
-    // hold many resets, and FP32 sums of -150 each would lose the small decays between).
+    // hold many resets, and FP32 sums of -150 each would lose the small decays between). The
+    // key products are summed in FP64 as above: the chunk may hold reflections in its other
+    // channels.
     __syncthreads();
     // The decays, from the sums: exact enough again, then summed in FP64 per channel.
     {
@@ -584,7 +587,8 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
     __syncthreads();
     for (int u = 0; u < 3; ++u) {
       const int pair = threadIdx.x + kThreads * u;  // (t, i) with i <= t, 528 in all
-      dkk[u] = dqk[u] = 0.0f;
+      dkk[u] = 0.0;
+      dqk[u] = 0.0f;
       if (pair >= 528) continue;
       int t = 0;
       while ((t + 1) * (t + 2) / 2 <= pair) ++t;
@@ -594,10 +598,11 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
       const char* const qrow =
           R.q + ((first + (t < valid ? t : valid - 1)) * R.q_ts + qk * R.q_hs) * kEB;
       const float fq = t < valid ? qf16[t] : 0.0f;
-      float sk = 0.0f, sq = 0.0f;
+      double sk = 0.0;
+      float sq = 0.0f;
       for (int ch = 0; ch < D; ++ch) {
         const float w = mk[i * kLd + ch] * exp2_hw((float)(gt[ch] - gi[ch]));
-        sk = __builtin_fmaf(mk[t * kLd + ch], w, sk);
+        sk = __builtin_fma((double)mk[t * kLd + ch], (double)w, sk);
         sq = __builtin_fmaf(load_elem<kF>(qrow + ch * kEB) * fq, w, sq);
       }
       dkk[u] = sk;

@@ -53,3 +53,18 @@ def test_strong_gates(lower_bound, lengths, heads, dim):
     kw["lower_bound"] = lower_bound
     args[3] = 2 * args[3]
     compare(args, kw)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("seed", range(8))
+def test_reflections_beside_a_reset_channel(seed, dim):
+    """Equal keys and steps of 2, whose errors grow with the tokens, while a channel without
+    any key is reset in every chunk."""
+    args, kw = log_inputs([97], 1, dim, seed=70 + seed, logits=False)
+    key = args[1][:1].clone()
+    key[..., 5] = 0.0
+    args[1] = key.expand_as(args[1]).contiguous()
+    args[4] = 2 * torch.ones_like(args[4])
+    args[3] = torch.zeros_like(args[3])
+    args[3][3::32, :, 5] = -300.0
+    compare(args, kw)
