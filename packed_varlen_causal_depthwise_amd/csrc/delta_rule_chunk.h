@@ -455,10 +455,14 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
   }
   __syncthreads();
 
-  // Each block of 16 rows takes its decays from its middle (after 8 rows): rows carry
-  // 2^(p - mid), columns 2^(mid - p), whose product is exact to FP32 while both halves of
-  // the block stay within 2^101 (8 tokens of log decay -8.75 each; the bounded gate
-  // reaches -5). Steeper chunks take the direct sums below. Between the blocks lie the decays
+  // Each block of 16 rows takes its decays from its middle (after 8 rows): rows carry 2^d and
+  // columns 2^-d, where d is the log2 decay from the middle to the row. That stays in range
+  // while both halves of the block are within 2^101 (8 tokens of log decay -8.75 each; the
+  // bounded gate reaches -5); steeper chunks take the direct sums below. d is summed from the
+  // middle outwards: rows nearer to the middle than a strong decay do not carry it, and the
+  // product of a row and a column of these is exact to a few 2^-24. Rows beyond it do, and
+  // each addition to a sum of up to 101 is off by up to 2^-18, which the product then is too.
+  // Between the blocks lie the decays
   // of block 0's second half and of block 1's first. Their product may leave FP32's range where
   // neither does, so columns of block 0 carry one and rows of block 1 the other: each scaled
   // operand is at most its vector.
@@ -472,11 +476,13 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
     all[b] = mid[b] + late[b];
     if (mid[b].x < -101.0f || mid[b].y < -101.0f || late[b].x < -101.0f || late[b].y < -101.0f) steep = 1;
   }
-  f32x2 before[kParts], after[kParts];  // log2 decays of the block before and after the group
+  // Log2 decays of the block before and after the group, and between it and the middle.
+  f32x2 before[kParts], after[kParts], inner[kParts];
 #pragma unroll
   for (int j = 0; j < kParts; ++j) {
-    before[j] = after[j] = f32x2{0.0f, 0.0f};
+    before[j] = after[j] = inner[j] = f32x2{0.0f, 0.0f};
     const int b = RW::second(wave, lane, j);
+    if (quad == 0 || quad == 3) inner[j] = *(const f32x2*)&tot[4 * b + (quad == 0 ? 1 : 2)][c];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const f32x2 t = *(const f32x2*)&tot[4 * b + i][c];
@@ -492,8 +498,7 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int r = RW::wave_row(wave, i) + lrow, j = i / 4;
-    const f32x2 m0 = RW::second(wave, lane, j) ? mid[1] : mid[0];
-    const f32x2 d = p[i] + before[j] - m0;
+    const f32x2 d = quad < 2 ? -(rest[i] + inner[j]) : p[i] + inner[j];
     const f32x2 e = {exp2_hw(d.x), exp2_hw(d.y)}, m = {exp2_hw(-d.x), exp2_hw(-d.y)};
     const f32x2 kk = k[i] * ktwo[r];
     *(f32x2*)&mq[r * kLd + c] = q[i] * qf16[r] * e;

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import rule_reference as ref
-from test_gpu_delta_rule import compare
+from test_gpu_delta_rule import compare, run
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +68,18 @@ def test_reflections_beside_a_reset_channel(seed, dim):
     args[3] = torch.zeros_like(args[3])
     args[3][3::32, :, 5] = -300.0
     compare(args, kw)
+
+
+@forms
+def test_weak_decays_beside_a_strong_one(lengths, heads, dim):
+    """A strong decay at the third token of every 16: the rows after it, on the side of the
+    block's middle, meet by sums that do not carry it, exact to a few 2^-24, and so outputs and
+    states to a few times 2^-22, the products' pairs: 2^-20 of the largest. Sums that carry
+    it, about 100, are rounded to 2^-17, and so are their differences."""
+    args, kw = log_inputs(lengths, heads, dim, seed=80)
+    args[3] = torch.full_like(args[3], -0.0123)
+    place = torch.cat([torch.arange(n) % 16 for n in lengths])
+    args[3][place == 3] = -69.0
+    out, st, want, want_st = run(args, kw)
+    for got, exact in ((out.cpu()[place >= 3], want[place >= 3]), (st.cpu(), want_st)):
+        assert (got.double() - exact).abs().max() <= 2.0 ** -20 * exact.abs().max()
