@@ -185,7 +185,7 @@ struct Window {
 };
 
 template <int kF>
-struct Cell;  // loads and stores of one element or a pair
+struct Cell;  // loads of one element or a pair, stores of one
 
 template <>
 struct Cell<kRuleF32> {
@@ -194,10 +194,6 @@ struct Cell<kRuleF32> {
   }
   static __device__ __forceinline__ f32x2 one(const Window& w, uint32_t lane, uint32_t row) {
     return f32x2{__builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(w.r, lane, row * w.stride, 0)), 0.0f};
-  }
-  static __device__ __forceinline__ void store_pair(const Window& w, uint32_t lane, uint32_t row, f32x2 v) {
-    typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
-    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2v, v), w.r, lane, row * w.stride, 0);
   }
   static __device__ __forceinline__ void store_one(const Window& w, uint32_t lane, uint32_t row, float v) {
     __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), w.r, lane, row * w.stride, 0);
@@ -212,17 +208,13 @@ struct Cell {
   static __device__ __forceinline__ uint32_t one(const Window& w, uint32_t lane, uint32_t row) {
     return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(w.r, lane, row * w.stride, 0);
   }
-  static __device__ __forceinline__ uint32_t pack(f32x2 v) {
-    if constexpr (kF == kRuleBF16)
-      return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
-    else
-      return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
-  }
-  static __device__ __forceinline__ void store_pair(const Window& w, uint32_t lane, uint32_t row, f32x2 v) {
-    __builtin_amdgcn_raw_buffer_store_b32(pack(v), w.r, lane, row * w.stride, 0);
-  }
   static __device__ __forceinline__ void store_one(const Window& w, uint32_t lane, uint32_t row, float v) {
-    __builtin_amdgcn_raw_buffer_store_b16((short)pack(f32x2{v, v}), w.r, lane, row * w.stride, 0);
+    uint32_t bits;
+    if constexpr (kF == kRuleBF16)
+      bits = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v, v}, bf16x2));
+    else
+      bits = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v, v}, f16x2));
+    __builtin_amdgcn_raw_buffer_store_b16((short)bits, w.r, lane, row * w.stride, 0);
   }
 };
 
@@ -892,18 +884,18 @@ constexpr float kColLow = 1.0f, kColHigh = 8192.0f;  // columns' largest value s
 constexpr int kColExp = 8;  // and is brought to 2^7 .. 2^8 when it leaves
 constexpr int kMostScale = 118;
 
-// kN column tiles of 16 per wave; lane l owns columns kN (l % 16) + n.
-template <int kM, int kN>
+// 16 columns per wave; lane l holds rows 4 (l / 16) .. + 3 of each 16 of column l % 16.
+template <int kM>
 struct ScanState {
-  f32x4 s[kM][kN];  // times the column's scale
-  float scale[kN], inverse[kN];
+  f32x4 s[kM];  // times the column's scale
+  float scale, inverse;
 
-  __device__ __forceinline__ float largest(int n) const {
+  __device__ __forceinline__ float largest() const {
     float m = 0.0f;
 #pragma unroll
     for (int i = 0; i < kM; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) m = __builtin_fmaxf(m, __builtin_fabsf(s[i][n][r]));
+      for (int r = 0; r < 4; ++r) m = __builtin_fmaxf(m, __builtin_fabsf(s[i][r]));
     return m;
   }
 
@@ -920,21 +912,21 @@ struct ScanState {
   }
 
   // The factor that brings a column whose largest value is m back (m from all its lanes).
-  __device__ __forceinline__ float factor(int n, float m) const {
+  __device__ __forceinline__ float factor(float m) const {
     if (!(m > 0.0f) || !(m < __builtin_huge_valf())) return 1.0f;
     if (m >= kColLow && m < kColHigh) return 1.0f;
     // The scale stays at most 2^kMostScale: a column that fades for long would take it to
     // infinity (its values then go to zero as they are).
-    const int most = kMostScale + 1 - __builtin_amdgcn_frexp_expf(scale[n]);
+    const int most = kMostScale + 1 - __builtin_amdgcn_frexp_expf(scale);
     const int e = kColExp - __builtin_amdgcn_frexp_expf(m);
     return __builtin_amdgcn_ldexpf(1.0f, e < most ? e : most);
   }
 
-  __device__ __forceinline__ void apply(int n, float f) {
+  __device__ __forceinline__ void apply(float f) {
 #pragma unroll
-    for (int i = 0; i < kM; ++i) s[i][n] *= f;
-    scale[n] *= f;
-    inverse[n] *= rcp_hw(f);  // exact for powers of two
+    for (int i = 0; i < kM; ++i) s[i] *= f;
+    scale *= f;
+    inverse *= rcp_hw(f);  // exact for powers of two
   }
 };
 
@@ -956,7 +948,7 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
   constexpr bool kOut = kMode == kScanOut;
   constexpr int kColWaves = D / 16, kWaves = (kOut ? 1 : 2) * kColWaves / kParts;
   constexpr int kEB = elem_bytes<kF>();
-  constexpr int kM = D / 16, kN = D / (16 * kColWaves), kK = D / 32;
+  constexpr int kM = D / 16, kK = D / 32;
   constexpr Slot kSlot{D};
   constexpr int kMatrix = (int)kSlot.matrix();
   __shared__ __attribute__((aligned(16))) char krows[kMatrix];
@@ -987,7 +979,7 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
   // This wave's columns are M's; and which.
   const bool identity = !kOut && (kParts == 2 ? blockIdx.y == 1 : wave >= kColWaves);
   const int cw = wave % kColWaves;
-  const int col = cw * (16 * kN) + kN * n16;
+  const int col = 16 * cw + n16;
   if (kParts == 2 && identity && begin == 0) return;  // nobody needs the first segment's M
   // The segment's end; for outputs the end of the segment before.
   const int move = kOut ? P.move_pieces.first(piece.s, seq.start) + piece.index - 1 : program;
@@ -1010,8 +1002,8 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
   load_rows(slot);
   load_rest(slot);
 
-  ScanState<kM, kN> S;
-  float most[kN];  // the largest magnitude among the lane's values of each column
+  ScanState<kM> S;
+  float most;  // the largest magnitude among the lane's values
   {
     const float* from = nullptr;
     if (begin == 0) {
@@ -1028,40 +1020,23 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
 #pragma unroll
       for (int m = 0; m < kM; ++m)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float* const at = from + (16 * m + 4 * n4 + r) * D + col;
-          if constexpr (kN == 2) {
-            const f32x2 x = *(const f32x2a4*)at;
-            S.s[m][0][r] = x.x;
-            S.s[m][1][r] = x.y;
-          } else {
-            S.s[m][0][r] = *at;
-          }
-        }
+        for (int r = 0; r < 4; ++r) S.s[m][r] = from[(16 * m + 4 * n4 + r) * D + col];
       if (!kOut) {
         float* const copy_to = (float*)(P.moves + cell * move_bytes(D));
 #pragma unroll
         for (int m = 0; m < kM; ++m)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int n = 0; n < kN; ++n) copy_to[(16 * m + 4 * n4 + r) * D + col + n] = S.s[m][n][r];
+          for (int r = 0; r < 4; ++r) copy_to[(16 * m + 4 * n4 + r) * D + col] = S.s[m][r];
       }
     } else {
 #pragma unroll
       for (int m = 0; m < kM; ++m)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int n = 0; n < kN; ++n)
-            S.s[m][n][r] = identity && 16 * m + 4 * n4 + r == col + n ? 1.0f : 0.0f;
+        for (int r = 0; r < 4; ++r) S.s[m][r] = identity && 16 * m + 4 * n4 + r == col ? 1.0f : 0.0f;
     }
-#pragma unroll
-    for (int n = 0; n < kN; ++n) {
-      S.scale[n] = S.inverse[n] = 1.0f;
-      S.apply(n, S.factor(n, column_max(S.largest(n))));
-      most[n] = S.largest(n);
-    }
+    S.scale = S.inverse = 1.0f;
+    S.apply(S.factor(column_max(S.largest())));
+    most = S.largest();
   }
 
   const f16x8* const kq = (const f16x8*)krows;
@@ -1099,17 +1074,13 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
       const uint32_t at = fresh(n4) * (4 * wv.stride) + col * kEB;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int row = 16 * (i / 4) + i % 4;
-        rv[i] = kN == 2 ? Cell<kF>::pair(wv, at, row) : Cell<kF>::one(wv, at, row);
+        rv[i] = Cell<kF>::one(wv, at, 16 * (i / 4) + i % 4);
       }
     }
 
     // ---- Y = (K e^G) S and O = (Q e^G) S
-    f32x4 Y[2][kN], O[2][kN];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int n = 0; n < kN; ++n) Y[t][n] = O[t][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    f32x4 Y[2], O[2];
+    Y[0] = Y[1] = O[0] = O[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     // Steps of (32 channels, 16 rows). A step's left operands are read while the step before
     // runs; the scheduling barriers keep the steps apart.
     f16x8 kh, kl, qh, ql;
@@ -1123,31 +1094,19 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
       }
     };
     read_step(0);
-    Operand b[kN];
+    Operand b;
 #pragma unroll
     for (int step = 0; step < 2 * kK; ++step) {
       const int t = step & 1;
       const f16x8 ch = kh, cl = kl, dh = qh, dl = ql;
       if (step + 1 < 2 * kK) read_step(step + 1);
-      if (t == 0) {
-#pragma unroll
-        for (int n = 0; n < kN; ++n) b[n] = split8(S.s[step][n], S.s[step + 1][n], R.one);
-      }
-#pragma unroll
-      for (int n = 0; n < kN; ++n) {
-        Y[t][n] = mfma16(ch, b[n].hi, Y[t][n]);
-        if (kOut) O[t][n] = mfma16(dh, b[n].hi, O[t][n]);
-      }
-#pragma unroll
-      for (int n = 0; n < kN; ++n) {
-        Y[t][n] = mfma16(ch, b[n].lo, Y[t][n]);
-        if (kOut) O[t][n] = mfma16(dh, b[n].lo, O[t][n]);
-      }
-#pragma unroll
-      for (int n = 0; n < kN; ++n) {
-        Y[t][n] = mfma16(cl, b[n].hi, Y[t][n]);
-        if (kOut) O[t][n] = mfma16(dl, b[n].hi, O[t][n]);
-      }
+      if (t == 0) b = split8(S.s[step], S.s[step + 1], R.one);
+      Y[t] = mfma16(ch, b.hi, Y[t]);
+      if (kOut) O[t] = mfma16(dh, b.hi, O[t]);
+      Y[t] = mfma16(ch, b.lo, Y[t]);
+      if (kOut) O[t] = mfma16(dh, b.lo, O[t]);
+      Y[t] = mfma16(cl, b.hi, Y[t]);
+      if (kOut) O[t] = mfma16(dl, b.hi, O[t]);
       __builtin_amdgcn_sched_barrier(0);
     }
     // This chunk's other operands and values have arrived, and all waves are done with its
@@ -1167,114 +1126,86 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
       for (int i = 0; i < 8; ++i)
         if (identity || 16 * (i / 4) + 4 * n4 + i % 4 >= valid) rv[i] = Pair<kF>::zero();
     }
-    f32x4 X[2][kN];
-    const auto difference = [&](int n) {
+    f32x4 X[2];
+    const auto difference = [&]() {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const f32x4 nt = *(const f32x4*)(factors + kFactorRows + 16 * t + 4 * n4);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const f32x2 v = Pair<kF>::value(rv[4 * t + r]);
-          X[t][n][r] = __builtin_fmaf(v[n], S.scale[n], -nt[r] * Y[t][n][r]);
-        }
+        for (int r = 0; r < 4; ++r)
+          X[t][r] = __builtin_fmaf(Pair<kF>::value(rv[4 * t + r]).x, S.scale, -nt[r] * Y[t][r]);
       }
     };
-    // The columns' range over S and X.
-    float high[kN];
-    const auto range = [&](int n) {
-      float m = most[n];
+    // The column's range over S and X.
+    float high;
+    const auto range = [&]() {
+      high = most;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) m = __builtin_fmaxf(m, __builtin_fabsf(X[t][n][r]));
-      high[n] = m;
+        for (int r = 0; r < 4; ++r) high = __builtin_fmaxf(high, __builtin_fabsf(X[t][r]));
     };
-    bool left = false;
-#pragma unroll
-    for (int n = 0; n < kN; ++n) {
-      difference(n);
-      range(n);
-      left |= S.left(high[n]);
-    }
-    if (left) {
-#pragma unroll
-      for (int n = 0; n < kN; ++n) {
-        // Values beyond a faded column's scale: that goes back to 1 first.
-        if (column_max(high[n]) == __builtin_huge_valf() && S.scale[n] > 1.0f) {
-          const float f = S.inverse[n];
-          S.apply(n, f);
-          most[n] *= f;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            Y[t][n] *= f;
-            O[t][n] *= f;
-          }
-          difference(n);
-          range(n);
-        }
-        const float f = S.factor(n, column_max(high[n]));
-        S.apply(n, f);
+    difference();
+    range();
+    if (S.left(high)) {
+      // Values beyond a faded column's scale: that goes back to 1 first.
+      if (column_max(high) == __builtin_huge_valf() && S.scale > 1.0f) {
+        const float f = S.inverse;
+        S.apply(f);
+        most *= f;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          X[t][n] *= f;
-          O[t][n] *= f;
+          Y[t] *= f;
+          O[t] *= f;
         }
+        difference();
+        range();
+      }
+      const float f = S.factor(column_max(high));
+      S.apply(f);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        X[t] *= f;
+        O[t] *= f;
       }
     }
 
     // ---- U = T X
-    f32x4 U[2][kN];
-    {
+    f32x4 U[2];
+    b = split8(X[0], X[1], R.one);
+    const float us = factors[kFactorRows + 2 * kChunk];
 #pragma unroll
-      for (int n = 0; n < kN; ++n) b[n] = split8(X[0][n], X[1][n], R.one);
-      const float us = factors[kFactorRows + 2 * kChunk];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const f16x8 th = tp[64 * t + lane], tl = tp[128 + 64 * t + lane], tr = tp[256 + 64 * t + lane];
-#pragma unroll
-        for (int n = 0; n < kN; ++n) {
-          f32x4 u = {0.0f, 0.0f, 0.0f, 0.0f};
-          u = mfma16(tr, b[n].hi, u);
-          u = mfma16(tl, b[n].hi, u);
-          u = mfma16(th, b[n].lo, u);
-          u = mfma16(th, b[n].hi, u);
-          U[t][n] = u * us;
-        }
-      }
+    for (int t = 0; t < 2; ++t) {
+      const f16x8 th = tp[64 * t + lane], tl = tp[128 + 64 * t + lane], tr = tp[256 + 64 * t + lane];
+      f32x4 u = {0.0f, 0.0f, 0.0f, 0.0f};
+      u = mfma16(tr, b.hi, u);
+      u = mfma16(tl, b.hi, u);
+      u = mfma16(th, b.lo, u);
+      u = mfma16(th, b.hi, u);
+      U[t] = u * us;
     }
     // (Issued here and not right after the barrier: the products with T then start 300 cycles
     // earlier, and the loads still have the rest of the chunk to arrive.)
     if (chunk + 1 < end) load_rows(slot);
     // U may outgrow X where keys are longer than 1 (S is safe at any smaller scale).
-    left = false;
+    high = 0.0f;
 #pragma unroll
-    for (int n = 0; n < kN; ++n) {
-      float m = 0.0f;
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int r = 0; r < 4; ++r) high = __builtin_fmaxf(high, __builtin_fabsf(U[t][r]));
+    if (__ballot(high >= kColHigh) != 0) {
+      const float m = column_max(high);
+      const float f = m >= kColHigh ? S.factor(m) : 1.0f;
+      S.apply(f);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) m = __builtin_fmaxf(m, __builtin_fabsf(U[t][n][r]));
-      high[n] = m;
-      left |= __ballot(m >= kColHigh) != 0;
-    }
-    if (left) {
-#pragma unroll
-      for (int n = 0; n < kN; ++n) {
-        const float m = column_max(high[n]);
-        const float f = m >= kColHigh ? S.factor(n, m) : 1.0f;
-        S.apply(n, f);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          U[t][n] *= f;
-          O[t][n] *= f;
-        }
+      for (int t = 0; t < 2; ++t) {
+        U[t] *= f;
+        O[t] *= f;
       }
     }
 
     // ---- S <- e^G_end S + K^T U; O += A U
-    Operand u[kN];
-#pragma unroll
-    for (int n = 0; n < kN; ++n) u[n] = split8(U[0][n], U[1][n], R.one);
+    const Operand u = split8(U[0], U[1], R.one);
     f16x8 ah, al;
     f32x4 d;
     const auto read_tile = [&](int m) {
@@ -1288,12 +1219,9 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
       const f16x8 ch = ah, cl = al;
       const f32x4 e = d;
       if (m + 1 < kM) read_tile(m + 1);
-#pragma unroll
-      for (int n = 0; n < kN; ++n) S.s[m][n] = mfma16(ch, u[n].hi, S.s[m][n] * e);
-#pragma unroll
-      for (int n = 0; n < kN; ++n) S.s[m][n] = mfma16(ch, u[n].lo, S.s[m][n]);
-#pragma unroll
-      for (int n = 0; n < kN; ++n) S.s[m][n] = mfma16(cl, u[n].hi, S.s[m][n]);
+      S.s[m] = mfma16(ch, u.hi, S.s[m] * e);
+      S.s[m] = mfma16(ch, u.lo, S.s[m]);
+      S.s[m] = mfma16(cl, u.hi, S.s[m]);
       if (m & 1) __builtin_amdgcn_sched_barrier(0);
     }
     if (kOut) {
@@ -1303,42 +1231,21 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
       for (int t = 0; t < 2; ++t) {
         const f16x8 ah = ap[64 * t + lane], al = ap[128 + 64 * t + lane];
         const f32x4 nq = *(const f32x4*)(factors + kFactorRows + kChunk + 16 * t + 4 * n4);
+        O[t] = mfma16(ah, u.hi, O[t]);
+        O[t] = mfma16(ah, u.lo, O[t]);
+        O[t] = mfma16(al, u.hi, O[t]);
 #pragma unroll
-        for (int n = 0; n < kN; ++n) {
-          O[t][n] = mfma16(ah, u[n].hi, O[t][n]);
-          O[t][n] = mfma16(ah, u[n].lo, O[t][n]);
-          O[t][n] = mfma16(al, u[n].hi, O[t][n]);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float f = nq[r];
-#pragma unroll
-          for (int n = 0; n < kN; ++n) O[t][n][r] *= f * S.inverse[n];
-        }
+        for (int r = 0; r < 4; ++r) O[t][r] *= nq[r] * S.inverse;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int t = i / 4, r = i % 4, row = 16 * t + r;
-        if constexpr (kN == 2)
-          Cell<kF>::store_pair(wo, at, row, f32x2{O[t][0][r], O[t][kN - 1][r]});
-        else
-          Cell<kF>::store_one(wo, at, row, O[t][0][r]);
-      }
+      for (int i = 0; i < 8; ++i) Cell<kF>::store_one(wo, at, 16 * (i / 4) + i % 4, O[i / 4][i % 4]);
     }
-    // The columns' range for the next chunk.
-    left = false;
-#pragma unroll
-    for (int n = 0; n < kN; ++n) {
-      most[n] = S.largest(n);
-      left |= S.left(most[n]);
-    }
-    if (left) {
-#pragma unroll
-      for (int n = 0; n < kN; ++n) {
-        const float f = S.factor(n, column_max(most[n]));
-        S.apply(n, f);
-        most[n] *= f;
-      }
+    // The column's range for the next chunk.
+    most = S.largest();
+    if (S.left(most)) {
+      const float f = S.factor(column_max(most));
+      S.apply(f);
+      most *= f;
     }
     // The next chunk's rows have arrived, and all waves are done with this chunk.
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -1357,13 +1264,7 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
 #pragma unroll
       for (int m = 0; m < kM; ++m)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float* const at = to + (16 * m + 4 * n4 + r) * D + col;
-          if constexpr (kN == 2)
-            *(f32x2a4*)at = f32x2{S.s[m][0][r] * S.inverse[0], S.s[m][1][r] * S.inverse[1]};
-          else
-            *at = S.s[m][0][r] * S.inverse[0];
-        }
+        for (int r = 0; r < 4; ++r) to[(16 * m + 4 * n4 + r) * D + col] = S.s[m][r] * S.inverse;
     }
   }
   if (!kOut && begin > 0) {
@@ -1371,11 +1272,8 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
     // 512.
     float top = 0.0f;
     if (identity) {
-#pragma unroll
-      for (int n = 0; n < kN; ++n) {
-        S.apply(n, S.inverse[n]);
-        top = __builtin_fmaxf(top, S.largest(n));
-      }
+      S.apply(S.inverse);
+      top = S.largest();
 #pragma unroll
       for (int m = 32; m > 0; m >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, m));
       if (lane == 0) part[cw] = top;
@@ -1389,19 +1287,16 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
       e = e > 100 ? 100 : e;
       char* const to = P.moves + cell * move_bytes(D);
       _Float16* const hi = (_Float16*)to;
+      const int pl = place(col % 32);
 #pragma unroll
-      for (int n = 0; n < kN; ++n) {
-        const int cc = col + n, pl = place(cc % 32);
+      for (int m = 0; m < kM; ++m)
 #pragma unroll
-        for (int m = 0; m < kM; ++m)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float x = __builtin_amdgcn_ldexpf(S.s[m][n][r], e);
-            const int at = ((m * kK + cc / 32) * 64 + (pl / 8) * 16 + 4 * n4 + r) * 8 + pl % 8;
-            hi[at] = (_Float16)x;
-            hi[D * D + at] = (_Float16)(x - (float)(_Float16)x);
-          }
-      }
+        for (int r = 0; r < 4; ++r) {
+          const float x = __builtin_amdgcn_ldexpf(S.s[m][r], e);
+          const int at = ((m * kK + col / 32) * 64 + (pl / 8) * 16 + 4 * n4 + r) * 8 + pl % 8;
+          hi[at] = (_Float16)x;
+          hi[D * D + at] = (_Float16)(x - (float)(_Float16)x);
+        }
       if (cw == 0 && lane == 0) *(float*)(to + (int64_t)D * D * 4) = __builtin_amdgcn_ldexpf(1.0f, -e);
     }
   }
