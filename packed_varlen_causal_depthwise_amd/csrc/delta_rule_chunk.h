@@ -32,8 +32,9 @@
 // into a pair of FP16 values (22 bits) and three products: hi hi + hi lo + lo hi, summed
 // in FP32. (One FP32 instruction costs as much as 16 FP16 ones of the same size; pairs of
 // bfloat16 would keep 16 bits, which left the FP32 state 4e-6 off.) FP16's range holds
-// because vectors have unit length, decays are at most 1, and the columns of S, V and U
-// share a power-of-two factor per column that follows their size. T and A come from FP64
+// because vectors have unit length, decays are at most 1, and a column's S and U share a
+// power-of-two factor that follows the larger of them, while X = V - n Y may have one more of
+// its own: with steps near 0 U is far below X, and pairs at X's scale would keep nothing of it. T and A come from FP64
 // and FP32 matrix instructions: their decays e^(G_t - G_i) are products of factors far
 // outside FP16.
 #ifndef KDACONV_DELTA_RULE_CHUNK_H_
@@ -1145,6 +1146,7 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
 #pragma unroll
         for (int r = 0; r < 4; ++r) high = __builtin_fmaxf(high, __builtin_fabsf(X[t][r]));
     };
+    float back = 1.0f;  // what X was divided by
     difference();
     range();
     if (S.left(high)) {
@@ -1161,19 +1163,23 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
         difference();
         range();
       }
-      const float f = S.factor(column_max(high));
-      S.apply(f);
+      // X may be far larger than the U that comes of it (steps near 0, short keys): it is brought
+      // down alone, for its product with T. A column without a state yet comes up as one.
+      const float f = S.factor(column_max(high)), own = f < 1.0f ? f : 1.0f, common = f < 1.0f ? 1.0f : f;
+      back = rcp_hw(own);  // exact for powers of two
+      S.apply(common);
+      most *= common;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         X[t] *= f;
-        O[t] *= f;
+        O[t] *= common;
       }
     }
 
     // ---- U = T X
     f32x4 U[2];
     b = split8(X[0], X[1], R.one);
-    const float us = factors[kFactorRows + 2 * kChunk];
+    const float us = factors[kFactorRows + 2 * kChunk] * back;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const f16x8 th = tp[64 * t + lane], tl = tp[128 + 64 * t + lane], tr = tp[256 + 64 * t + lane];
@@ -1187,15 +1193,14 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
     // (Issued here and not right after the barrier: the products with T then start 300 cycles
     // earlier, and the loads still have the rest of the chunk to arrive.)
     if (chunk + 1 < end) load_rows(slot);
-    // U may outgrow X where keys are longer than 1 (S is safe at any smaller scale).
-    high = 0.0f;
+    // The column's range over S and U: the larger of them keeps its bits.
+    high = most;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) high = __builtin_fmaxf(high, __builtin_fabsf(U[t][r]));
-    if (__ballot(high >= kColHigh) != 0) {
-      const float m = column_max(high);
-      const float f = m >= kColHigh ? S.factor(m) : 1.0f;
+    if (S.left(high)) {
+      const float f = S.factor(column_max(high));
       S.apply(f);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {

@@ -83,3 +83,31 @@ def test_weak_decays_beside_a_strong_one(lengths, heads, dim):
     out, st, want, want_st = run(args, kw)
     for got, exact in ((out.cpu()[place >= 3], want[place >= 3]), (st.cpu(), want_st)):
         assert (got.double() - exact).abs().max() <= 2.0 ** -20 * exact.abs().max()
+
+
+# A state from nothing, in one chunk and over several, token by token, and in segments.
+SIZES = [([40, 200, 3], 64), ([40, 200, 3], 128), ([700], 128)]
+
+
+@pytest.mark.parametrize("lengths,dim", SIZES, ids=str)
+@pytest.mark.parametrize("beta", [1e-2, 1e-3, 1e-4, 1e-6, 1e-10])
+def test_small_steps(beta, lengths, dim):
+    """Updates far below the values that they come from."""
+    args, kw = log_inputs(lengths, 2, dim, seed=90, logits=False,
+                          initial=torch.zeros(len(lengths), dtype=torch.bool))
+    args[4] = args[4] * beta
+    compare(args, kw)
+    args[4][::7] = 0.0
+    args[4][5::50] = 1.0  # and full steps among them
+    compare(args, kw)
+
+
+@pytest.mark.parametrize("lengths,dim", SIZES, ids=str)
+@pytest.mark.parametrize("length", [1e-2, 1e-4, 1e-6, 30.0])
+def test_keys_of_any_length(length, lengths, dim):
+    """Keys as they are, much shorter than 1, and longer."""
+    args, kw = log_inputs(lengths, 2, dim, seed=91, logits=False,
+                          initial=torch.zeros(len(lengths), dtype=torch.bool))
+    args[1] = args[1] / args[1].norm(dim=-1, keepdim=True) * length
+    args[4] = args[4] / max(1.0, length * length)
+    compare(args, kw, qk_l2norm=False)
