@@ -900,17 +900,15 @@ struct ScanState {
     return m;
   }
 
-  // Whether some column's largest value (over lanes holding m) left its range. Zero
-  // columns stay as they are; infinities and NaN count as in range.
-  static __device__ __forceinline__ bool left(float m) {
-    if (__ballot(m >= kColHigh) != 0) return true;
-    uint64_t big = __ballot(m >= kColLow), some = __ballot(m > 0.0f);
+  // Whether some column's values (lanes hold m as their largest) are all below its range.
+  static __device__ __forceinline__ bool below(float m) {
+    uint64_t big = __ballot(m >= kColLow);
     big |= big >> 32;
     big |= big >> 16;
-    some |= some >> 32;
-    some |= some >> 16;
-    return ((some & ~big) & 0xFFFF) != 0;
+    return (big & 0xFFFF) != 0xFFFF;
   }
+
+  static __device__ __forceinline__ bool above(float m) { return __ballot(m >= kColHigh) != 0; }
 
   // The factor that brings a column whose largest value is m back (m from all its lanes).
   __device__ __forceinline__ float factor(float m) const {
@@ -1039,6 +1037,7 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
     S.apply(S.factor(column_max(S.largest())));
     most = S.largest();
   }
+  bool empty = S.below(most);  // some column is
 
   const f16x8* const kq = (const f16x8*)krows;
   const f16x8* const qq = (const f16x8*)qrows;
@@ -1149,7 +1148,7 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
     float back = 1.0f;  // what X was divided by
     difference();
     range();
-    if (S.left(high)) {
+    if (S.above(high) || S.below(high)) {
       // Values beyond a faded column's scale: that goes back to 1 first.
       if (column_max(high) == __builtin_huge_valf() && S.scale > 1.0f) {
         const float f = S.inverse;
@@ -1163,6 +1162,7 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
         difference();
         range();
       }
+      empty = S.below(most);
       // X may be far larger than the U that comes of it (steps near 0, short keys): it is brought
       // down alone, for its product with T. A column without a state yet comes up as one.
       const float f = S.factor(column_max(high)), own = f < 1.0f ? f : 1.0f, common = f < 1.0f ? 1.0f : f;
@@ -1193,13 +1193,14 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
     // (Issued here and not right after the barrier: the products with T then start 300 cycles
     // earlier, and the loads still have the rest of the chunk to arrive.)
     if (chunk + 1 < end) load_rows(slot);
-    // The column's range over S and U: the larger of them keeps its bits.
+    // The column's range over S and U: the larger of them keeps its bits. (S alone is in range
+    // unless the column is empty or has faded.)
     high = most;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) high = __builtin_fmaxf(high, __builtin_fabsf(U[t][r]));
-    if (S.left(high)) {
+    if (S.above(high) || (empty && S.below(high))) {
       const float f = S.factor(column_max(high));
       S.apply(f);
 #pragma unroll
@@ -1247,10 +1248,12 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
     }
     // The column's range for the next chunk.
     most = S.largest();
-    if (S.left(most)) {
+    empty = S.below(most);
+    if (empty || S.above(most)) {
       const float f = S.factor(column_max(most));
       S.apply(f);
       most *= f;
+      empty = S.below(most);
     }
     // The next chunk's rows have arrived, and all waves are done with this chunk.
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
