@@ -1,7 +1,7 @@
 // The gated delta rule in chunks of 32 tokens: the prefill.
 //
 // Mathematics. Inside a chunk let G_t be the running sum of the log decays (per key
-// channel), k^ = k |k|^-1 (or the normalised key), n_t = |k_t| (or 1). With the state S at
+// channel), k^ = k / |k| and n_t = |k_t| (or the normalised key and 1). With the state S at
 // the chunk's start,
 //     L_ti = b_t n_t n_i sum_c k^_tc k^_ic e^(G_tc - G_ic)   for i < t, else 0
 //     T = diag(n) (I + L)^-1 diag(b)
@@ -420,9 +420,16 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
     constexpr int kShare = kLanes / (2 * kRows);  // lanes holding the same sum
     const int l = lane % kLanes, which = l / kShare, r = RW::wave_row(wave, which % kRows) + lrow;
     if (l % kShare == 0) {
+      // Of a row that is 0.7 long or longer after its normalisation the products take it as it is.
+      // Other rows, and those taken without normalisation, enter them at unit length (or 2^118
+      // times themselves, the shortest) and n is the rest: pairs of FP16 values would lose a row
+      // that vanishes beside l2_eps.
       const bool norm = R.l2_eps >= 0.0f;
-      const Factor f = inverse_root(norm ? s + (double)R.l2_eps : s);
-      const float n = norm ? 1.0f : (float)(s * ((double)f.hi + (double)f.lo));
+      const double eps = R.l2_eps, least = 0x1p-236;
+      const bool whole = norm && s >= eps && s >= least;
+      const double own = s < least ? least : s, back = inverse_root_f64(whole ? s + eps : own);
+      const Factor f = two_floats(back);
+      const float n = whole ? 1.0f : (float)(norm ? own * back * inverse_root_f64(s + eps) : own * back);
       if (which < kRows) {
         qf16[r] = kVec * f.hi;
         rows[1][r] = n * R.scale * (1.0f / kVec);
@@ -1241,7 +1248,7 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
         O[t] = mfma16(ah, u.lo, O[t]);
         O[t] = mfma16(al, u.hi, O[t]);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) O[t][r] *= nq[r] * S.inverse;
+        for (int r = 0; r < 4; ++r) O[t][r] = O[t][r] * S.inverse * nq[r];  // (nq * inverse may be subnormal)
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) Cell<kF>::store_one(wo, at, 16 * (i / 4) + i % 4, O[i / 4][i % 4]);

@@ -204,16 +204,22 @@ struct Factor {
   float hi, lo;
 };
 
-__device__ __forceinline__ Factor inverse_root(double x) {
-  Factor f = {0.0f, 0.0f};
-  if (x == 0.0) return f;
+__device__ __forceinline__ double inverse_root_f64(double x) {
+  if (x == 0.0) return 0.0;
   double y = __builtin_amdgcn_rsq(x);
 #pragma unroll
   for (int i = 0; i < 2; ++i) y = __builtin_fma(0.5 * y, __builtin_fma(-x * y, y, 1.0), y);
+  return y;
+}
+
+__device__ __forceinline__ Factor two_floats(double y) {
+  Factor f;
   f.hi = (float)y;
   f.lo = (float)(y - (double)f.hi);
   return f;
 }
+
+__device__ __forceinline__ Factor inverse_root(double x) { return two_floats(inverse_root_f64(x)); }
 
 __device__ __forceinline__ float scaled(float x, Factor f) {
   return __builtin_fmaf(x, f.hi, x * f.lo);

@@ -111,3 +111,46 @@ def test_keys_of_any_length(length, lengths, dim):
     args[1] = args[1] / args[1].norm(dim=-1, keepdim=True) * length
     args[4] = args[4] / max(1.0, length * length)
     compare(args, kw, qk_l2norm=False)
+
+
+@pytest.mark.parametrize("lengths,dim", SIZES, ids=str)
+@pytest.mark.parametrize("operand", ["q", "k"])
+@pytest.mark.parametrize("size", [1e-3, 1e-6, 1e-8, 1e-20, 1e-30])
+def test_short_keys_and_queries(size, operand, lengths, dim):
+    """Lengths that vanish beside the normalisation's 1e-6."""
+    args, kw = log_inputs(lengths, 2, dim, seed=92,
+                          initial=torch.zeros(len(lengths), dtype=torch.bool))
+    args["qk".index(operand)] *= size
+    compare(args, kw)
+    args["qk".index(operand)][1::5] /= size  # and ordinary rows among them
+    compare(args, kw)
+
+
+def shortest(size, operand, dim):
+    args, kw = log_inputs([40, 100, 3], 2, dim, seed=93, logits=False)
+    args[1] = args[1] / args[1].norm(dim=-1, keepdim=True)
+    args["qk".index(operand)] = args["qk".index(operand)] * size
+    args["qk".index(operand)][7] = 0.0
+    return args, kw
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("operand", ["q", "k"])
+@pytest.mark.parametrize("size", [1e-30, 1e-36, 1e-38])
+def test_shortest_keys_and_queries_as_they_are(size, operand, dim):
+    """Lengths whose inverse FP32 cannot hold."""
+    args, kw = shortest(size, operand, dim)
+    compare(args, kw, qk_l2norm=False)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("operand", ["q", "k"])
+def test_subnormal_keys_and_queries_as_they_are(operand, dim):
+    """A length below 2^-118 is taken as 2^-118 with entries of 2^-29 (a pair's last bit over
+    16): of a product with a state's column, whose length is below 2^4 here, that leaves errors
+    below 2^-118 * 2^-29 * sqrt(dim) * 2^4 < 2^-139."""
+    args, kw = shortest(1e-41, operand, dim)
+    out, st, want, want_st = run(args, kw, qk_l2norm=False)
+    for got, exact in ((out, want), (st, want_st)):
+        err = (got.cpu().double() - exact).abs().max()
+        assert err <= ref.ARITHMETIC * exact.abs().max() + 2.0 ** -139
