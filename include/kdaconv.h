@@ -273,6 +273,8 @@ int kdaconv_activation_map(uint32_t first, int64_t count, int activation, int dt
  * from: its line as it is, or zeros there without an initial state. States, sums and norms
  * are held in FP32 or more; matrix products take FP32 values as pairs of FP16 values (22
  * bits) and sum in FP32; only out is rounded to its format.
+ * A value that is not finite reaches what the steps above take it to, tokens from its own on,
+ * and no token before it nor another sequence.
  * A log decay below -104 acts as -104 (its exp is zero in FP32, as is -infinity's). Log
  * decays given as they are (KDACONV_GATE_LOG) are at most 0; positive ones are not looked for
  * and may leave the range of the prefill's FP16 pairs.

@@ -356,6 +356,7 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
   __shared__ float krest[kChunk];
   __shared__ double kfac[kChunk];
   __shared__ int steep;
+  __shared__ int unfinite[kWaves];  // each wave's first row with a value that is not finite
   float* const mq = (float*)shared;
   float* const mk = mq + kMat;
   float* const mc = mq + 2 * kMat;
@@ -384,11 +385,20 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
       rg.load_same(wg, lrow * wg.stride, wave);
   };
 
-  f32x2 q[kRows], k[kRows], p[kRows];  // p: log2 decays, then their running sums
-  f32x2 rest[kRows];  // log2 decay after each row, inside its group of 4
   const Gate gate(R, h);
   f32x2 bias = {0.0f, 0.0f};
   if (R.dt_bias != nullptr) bias = *(const f32x2a4*)(R.dt_bias + h * D + c);
+  // The lane's log2 decays, zeros from row `end` on.
+  const auto read_gates = [&](f32x2 (&g)[kRows], int end) {
+    RawRows<kG, RW> rg;
+    load_gates(rg);
+    rg.values(g, R.g_cs == 0);
+    gate.eval(g, bias);
+    mask_rows<RW>(g, wave, lane, end);
+  };
+
+  f32x2 q[kRows], k[kRows], p[kRows];  // p: log2 decays, then their running sums
+  f32x2 rest[kRows];  // log2 decay after each row, inside its group of 4
   {
     RawRows<kF, RW> rq, rk;
     RawRows<kG, RW> rg;
@@ -403,8 +413,12 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
     gate.eval(p, bias);
     mask_rows<RW>(p, wave, lane, valid);
   }
-  if (threadIdx.x < kChunk)
-    beta[threadIdx.x] = (int)threadIdx.x < valid ? beta_value(R, kF, first + threadIdx.x, h) : 0.0f;
+  int odd = kChunk;  // the first row here with a key or a step that is not finite
+  if (threadIdx.x < kChunk) {
+    const float b = (int)threadIdx.x < valid ? beta_value(R, kF, first + threadIdx.x, h) : 0.0f;
+    beta[threadIdx.x] = b;
+    if (!is_finite(b)) odd = threadIdx.x;
+  }
   if (threadIdx.x == 0) steep = 0;
 
   // Lengths of the rows' queries and keys.
@@ -440,20 +454,58 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
         ktwo[r] = __builtin_amdgcn_ldexpf(1.0f, e);
         krest[r] = __builtin_amdgcn_ldexpf(f.hi, -e);
         kfac[r] = (double)n * __builtin_amdgcn_ldexp((double)f.hi + (double)f.lo, -e);
+        if (!(s < __builtin_huge_val())) odd = odd < r ? odd : r;
       }
     }
   }
   // Running sums inside the groups.
+  const auto running_sums = [&]() {
 #pragma unroll
-  for (int j = 0; j < kParts; ++j) {
-    rest[4 * j + 3] = f32x2{0.0f, 0.0f};
+    for (int j = 0; j < kParts; ++j) {
+      rest[4 * j + 3] = f32x2{0.0f, 0.0f};
 #pragma unroll
-    for (int i = 3; i > 0; --i) rest[4 * j + i - 1] = rest[4 * j + i] + p[4 * j + i];
+      for (int i = 3; i > 0; --i) rest[4 * j + i - 1] = rest[4 * j + i] + p[4 * j + i];
 #pragma unroll
-    for (int i = 1; i < 4; ++i) p[4 * j + i] += p[4 * j + i - 1];
-    *(f32x2*)&tot[4 * RW::second(wave, lane, j) + quad][c] = p[4 * j + 3];
+      for (int i = 1; i < 4; ++i) p[4 * j + i] += p[4 * j + i - 1];
+      *(f32x2*)&tot[4 * RW::second(wave, lane, j) + quad][c] = p[4 * j + 3];
+    }
+  };
+  running_sums();
+  // A key, step or decay that is not finite makes all values from its token on NaN, and none
+  // before: the matrix products would carry it there (0 times NaN). The chunk ends before that
+  // token as far as they are concerned, and n says NaN from there on, which the scans see.
+  {
+    bool any = odd < kChunk;
+#pragma unroll
+    for (int j = 0; j < kParts; ++j) any |= !(is_finite(p[4 * j + 3].x) && is_finite(p[4 * j + 3].y));
+    if (__ballot(any) != 0) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int r = RW::wave_row(wave, i) + lrow;
+        if (!(is_finite(p[i].x) && is_finite(p[i].y))) odd = odd < r ? odd : r;
+      }
+#pragma unroll
+      for (int m = 32; m > 0; m >>= 1) {
+        const int other = __shfl_xor(odd, m);
+        odd = odd < other ? odd : other;
+      }
+    }
+    if (lane == 0) unfinite[wave] = odd;
   }
   __syncthreads();
+  int live = valid;  // rows before it
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) live = live < unfinite[w] ? live : unfinite[w];
+  live = uniform(live);
+  if (live < valid) {
+    read_gates(p, live);
+    running_sums();
+    mask_rows<RW>(k, wave, lane, live);
+    if (threadIdx.x < kChunk && (int)threadIdx.x >= live)
+      beta[threadIdx.x] = kf16[threadIdx.x] = ktwo[threadIdx.x] = krest[threadIdx.x] = rows[0][threadIdx.x] =
+          kfac[threadIdx.x] = 0.0f;
+    __syncthreads();
+  }
 
   // Each block of 16 rows takes its decays from its middle (after 8 rows): rows carry 2^d and
   // columns 2^-d, where d is the log2 decay from the middle to the row. That stays in range
@@ -562,12 +614,8 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
     __syncthreads();
     // The decays, from the sums: exact enough again, then summed in FP64 per channel.
     {
-      RawRows<kG, RW> rg;
-      load_gates(rg);
       f32x2 g[kRows];
-      rg.values(g, R.g_cs == 0);
-      gate.eval(g, bias);
-      mask_rows<RW>(g, wave, lane, valid);
+      read_gates(g, live);
 #pragma unroll
       for (int i = 0; i < kRows; ++i) *(f32x2*)&mk[(RW::wave_row(wave, i) + lrow) * kLd + c] = g[i];
     }
@@ -873,7 +921,9 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
     if (u == 0) df[kFactorRows + 2 * kChunk] = __builtin_amdgcn_ldexpf(1.0f / kVec, -e);
     ((u32q*)(slot + kSlot.a()))[u] = ((const u32q*)sa)[u];
   }
-  if (threadIdx.x < 2 * kChunk) df[kFactorRows + threadIdx.x] = (&rows[0][0])[threadIdx.x];
+  if (threadIdx.x < 2 * kChunk)
+    df[kFactorRows + threadIdx.x] = (int)threadIdx.x >= live && (int)threadIdx.x < valid
+                                        ? __builtin_nanf("") : (&rows[0][0])[threadIdx.x];
 }
 
 // ------------------------------------------------------------------------------- scan
@@ -889,7 +939,9 @@ constexpr int kScanOut = 0;  // outputs and final states
 constexpr int kScanMove = 1;  // a segment's B and M
 
 constexpr float kColLow = 1.0f, kColHigh = 8192.0f;  // columns' largest value stays between
-constexpr int kColExp = 8;  // and is brought to 2^7 .. 2^8 when it leaves
+// And is brought to 2^4 .. 2^5 when it leaves: X is often 2^4 to 2^8 times S and would be above
+// every time if S came to 2^7 .. 2^8 (16384 tokens 378 us against 373).
+constexpr int kColExp = 5;
 constexpr int kMostScale = 118;
 
 // 16 columns per wave; lane l holds rows 4 (l / 16) .. + 3 of each 16 of column l % 16.
@@ -915,7 +967,8 @@ struct ScanState {
     return (big & 0xFFFF) != 0xFFFF;
   }
 
-  static __device__ __forceinline__ bool above(float m) { return __ballot(m >= kColHigh) != 0; }
+  // Whether all columns' values are below its upper end, and none is NaN.
+  static __device__ __forceinline__ bool within(float m) { return __ballot(!(m < kColHigh)) == 0; }
 
   // The factor that brings a column whose largest value is m back (m from all its lanes).
   __device__ __forceinline__ float factor(float m) const {
@@ -1143,21 +1196,26 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
           X[t][r] = __builtin_fmaf(Pair<kF>::value(rv[4 * t + r]).x, S.scale, -nt[r] * Y[t][r]);
       }
     };
-    // The column's range over S and X.
-    float high;
+    // The column's range over S and X; NaN where an X is.
     const auto range = [&]() {
-      high = most;
+      float m = most;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) high = __builtin_fmaxf(high, __builtin_fabsf(X[t][r]));
+        for (int r = 0; r < 4; ++r) m = __builtin_elementwise_maximum(m, __builtin_fabsf(X[t][r]));
+      return m;
     };
     float back = 1.0f;  // what X was divided by
+    int dead = kChunk;  // the column's first row whose X is not finite
+    bool unfinite = false;  // some column has one
     difference();
-    range();
-    if (S.above(high) || S.below(high)) {
+    float high = range();
+    if (!S.within(high) || S.below(high)) {
       // Values beyond a faded column's scale: that goes back to 1 first.
-      if (column_max(high) == __builtin_huge_valf() && S.scale > 1.0f) {
+      bool beyond = false;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) beyond |= __builtin_fabsf(X[i / 4][i % 4]) == __builtin_huge_valf();
+      if (column_max(beyond ? 1.0f : 0.0f) != 0.0f && S.scale > 1.0f) {
         const float f = S.inverse;
         S.apply(f);
         most *= f;
@@ -1167,12 +1225,28 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
           O[t] *= f;
         }
         difference();
-        range();
       }
       empty = S.below(most);
+      // An X that is still not finite would reach all rows of its column (T's zeros times NaN).
+      // By the definition it reaches those from its own on: they are left out here, and O and S
+      // are NaN there at the end.
+#pragma unroll
+      for (int i = 7; i >= 0; --i)
+        if (!is_finite(X[i / 4][i % 4])) dead = 16 * (i / 4) + 4 * n4 + i % 4;
+      unfinite = __ballot(dead < kChunk) != 0;
+      if (unfinite) {
+        int other = __shfl_xor(dead, 16);
+        dead = dead < other ? dead : other;
+        other = __shfl_xor(dead, 32);
+        dead = dead < other ? dead : other;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (16 * (i / 4) + 4 * n4 + i % 4 >= dead) X[i / 4][i % 4] = 0.0f;
+        empty = true;
+      }
       // X may be far larger than the U that comes of it (steps near 0, short keys): it is brought
       // down alone, for its product with T. A column without a state yet comes up as one.
-      const float f = S.factor(column_max(high)), own = f < 1.0f ? f : 1.0f, common = f < 1.0f ? 1.0f : f;
+      const float f = S.factor(column_max(range())), own = f < 1.0f ? f : 1.0f, common = f < 1.0f ? 1.0f : f;
       back = rcp_hw(own);  // exact for powers of two
       S.apply(common);
       most *= common;
@@ -1207,7 +1281,7 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) high = __builtin_fmaxf(high, __builtin_fabsf(U[t][r]));
-    if (S.above(high) || (empty && S.below(high))) {
+    if (!S.within(high) || (empty && S.below(high))) {
       const float f = S.factor(column_max(high));
       S.apply(f);
 #pragma unroll
@@ -1250,13 +1324,24 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
 #pragma unroll
         for (int r = 0; r < 4; ++r) O[t][r] = O[t][r] * S.inverse * nq[r];  // (nq * inverse may be subnormal)
       }
+      if (unfinite) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (16 * (i / 4) + 4 * n4 + i % 4 >= dead) O[i / 4][i % 4] = __builtin_nanf("");
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) Cell<kF>::store_one(wo, at, 16 * (i / 4) + i % 4, O[i / 4][i % 4]);
+    }
+    if (unfinite) {
+      const float nan = __builtin_nanf("");
+#pragma unroll
+      for (int m = 0; m < kM; ++m)
+        if (dead < kChunk) S.s[m] = f32x4{nan, nan, nan, nan};
     }
     // The column's range for the next chunk.
     most = S.largest();
     empty = S.below(most);
-    if (empty || S.above(most)) {
+    if (empty || !S.within(most)) {
       const float f = S.factor(column_max(most));
       S.apply(f);
       most *= f;

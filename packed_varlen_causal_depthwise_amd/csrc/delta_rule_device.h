@@ -81,6 +81,7 @@ __device__ __forceinline__ void store_elem(char* p, float v) {
     *(__bf16*)p = (__bf16)v;
 }
 
+__device__ __forceinline__ bool is_finite(float x) { return __builtin_fabsf(x) < __builtin_huge_valf(); }
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float rcp_hw(float x) { return __builtin_amdgcn_rcpf(x); }
 __device__ __forceinline__ float sigmoid_f(float x) {

@@ -8,7 +8,7 @@ from test_gpu_delta_rule import compare, run
 
 pytestmark = pytest.mark.gpu
 
-F32 = torch.float32
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
 
 # Lengths, heads and head_dim: heads of 64; of 128 with 8 waves per chunk; with 4.
 FORMS = [([100, 40], 3, 64), ([100, 40], 3, 128), ([1100], 16, 128)]
@@ -154,3 +154,56 @@ def test_subnormal_keys_and_queries_as_they_are(operand, dim):
     for got, exact in ((out, want), (st, want_st)):
         err = (got.cpu().double() - exact).abs().max()
         assert err <= ref.ARITHMETIC * exact.abs().max() + 2.0 ** -139
+
+
+def check_finite(got, want, dtype, what):
+    """Finite where the definition is, and those values right."""
+    got, finite = got.cpu(), torch.isfinite(want)
+    differ = (torch.isfinite(got) != finite).sum().item()
+    assert differ == 0, f"{what}: {differ} of {finite.numel()} finite in one alone"
+    ref.check(torch.where(finite, got, torch.zeros_like(got)),
+              torch.where(finite, want, torch.zeros_like(want)), dtype, what)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("steep", [False, True])
+@pytest.mark.parametrize("value", ["inf", "-inf", "nan"])
+@pytest.mark.parametrize("operand", ["q", "k", "v", "g", "beta", "state"])
+def test_values_that_are_not_finite(operand, value, steep, dim):
+    """They reach the tokens after them, and none before: a token of its own per head."""
+    if operand == "g" and value == "-inf":
+        pytest.skip("a reset")
+    tokens = [0, 5, 13, 14, 21, 31, 32, 45, 63, 64, 74]
+    for lengths in ([75, 3], [12, 3]):
+        args, kw = log_inputs(lengths, len(tokens), dim, seed=94, logits=False,
+                              initial=torch.ones(2, dtype=torch.bool))
+        args = [a.contiguous() for a in args]
+        if steep:
+            args[3][4::9, :, 7] = -200.0
+        for h, t in enumerate(tokens):
+            t %= lengths[0]
+            if operand == "state":
+                args[5][int(args[7][0]), h, 3 + h, 2 * h] = float(value)
+            elif operand == "beta":
+                args[4][t, h] = float(value)
+            else:
+                args["qkvg".index(operand)][t, h, 3 * h] = float(value)
+        out, st, want, want_st = run(args, kw)
+        check_finite(out, want, F32, "out")
+        check_finite(st, want_st, F32, "states")
+
+
+@pytest.mark.parametrize("dtype,dim,heads", [(F32, 64, 3), (BF16, 128, 3), (F16, 128, 16)], ids=str)
+@pytest.mark.parametrize("operand", ["q", "k", "v", "g", "beta"])
+def test_values_that_are_not_finite_in_long_sequences(operand, dtype, dim, heads):
+    """Through segments that run side by side, and with gates; the sequence after it is whole."""
+    args, kw = ref.rule_inputs([700, 33], heads=heads, dim=dim, dtype=dtype, seed=95)
+    which = args["q k v g beta".split().index(operand)] = \
+        args["q k v g beta".split().index(operand)].contiguous()
+    if operand == "v":
+        which[333, 0, 0], which[400, 1, 5] = float("nan"), float("inf")
+    else:
+        which[333, 0] = float("nan")
+    out, st, want, want_st = run(args, kw)
+    check_finite(out, want, dtype, "out")
+    check_finite(st, want_st, F32, "states")
