@@ -102,14 +102,14 @@ Plan make_plan(int64_t tokens, int64_t seqs, int64_t heads, int64_t head_dim) {
 }
 
 // Workgroups of the largest launch, of up to 512 threads: a launch may not reach 2^32 threads.
+// (The transitions' have 1024, but moves and joins are at most 3/2 kSegmentCells + heads.)
 constexpr int64_t kMaxGrid = (int64_t)1 << 23;
 
 int64_t largest_grid(const kdaconv_rule_args* a, bool update) {
-  const int64_t heads = std::max<int64_t>(1, a->num_heads);
-  if (update) return a->num_seqs * heads;
+  const int64_t heads = std::max<int64_t>(1, a->num_heads), steps = a->num_seqs * heads;
+  if (update) return steps;
   const Plan p = make_plan(a->num_tokens, a->num_seqs, heads, a->head_dim);
-  // (Moves and joins are at most kSegmentCells + heads.)
-  return std::max(p.chunk_programs, p.segment_programs) * heads;
+  return std::max(p.step ? steps : 0, p.chunks ? std::max(p.chunk_programs, p.segment_programs) * heads : 0);
 }
 
 int validate_rule(const kdaconv_rule_args* a, bool update) {
