@@ -220,14 +220,16 @@ def gated_delta_rule_update(
 
 def gated_delta_rule_supported(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
                                beta: torch.Tensor, states: torch.Tensor) -> bool:
-    """Whether gated_delta_rule_fn and gated_delta_rule_update serve these tensors."""
+    """Whether gated_delta_rule_fn serves these tensors, and gated_delta_rule_update their rows
+    (of up to 2^23 sequences times heads)."""
     try:
         sizes = _heads(q, k, v, g, beta, states)
         lib = _lib.load()
-        lines = torch.empty(sizes[0], dtype=torch.int32, device=v.device)
-        # The output would be a fresh allocation; v stands in for it.
-        args = _pack(q, k, v, g, beta, states, lines, None, None, sizes[0], sizes, None, None, None,
+        one = torch.empty(2, dtype=torch.int32, device=v.device)
+        # As one sequence. The output and the scratch memory would be fresh allocations: v and any
+        # aligned address stand in for them.
+        args = _pack(q, k, v, g, beta, states, one, one, None, 1, sizes, None, None, None,
                      False, True, None, None, v)
     except (ValueError, _lib.LibraryMissing):
         return False
-    return lib.kdaconv_gated_delta_rule_validate(args, 1, None, 0) == _lib.OK
+    return lib.kdaconv_gated_delta_rule_validate(args, 0, 256, 1 << 62) == _lib.OK

@@ -3,6 +3,7 @@
 import pytest
 import torch
 
+import packed_varlen_causal_depthwise_amd as kd
 import rule_reference as ref
 from test_gpu_delta_rule import compare, run
 
@@ -207,3 +208,15 @@ def test_values_that_are_not_finite_in_long_sequences(operand, dtype, dim, heads
     out, st, want, want_st = run(args, kw)
     check_finite(out, want, dtype, "out")
     check_finite(st, want_st, F32, "states")
+
+
+def test_supported_asks_for_a_prefill():
+    """More tokens times heads than an update may have sequences times heads."""
+    one = torch.zeros(1, 64, 128, dtype=BF16, device="cuda")
+    x, beta = one.expand(131072, 64, 128), one[..., 0].expand(131072, 64)
+    states = torch.zeros(1, 64, 128, 128, device="cuda")
+    assert kd.gated_delta_rule_supported(x, x, x, x, beta, states)
+    assert kd.gated_delta_rule_supported(x[:0], x[:0], x[:0], x[:0], beta[:0], states)
+    assert not kd.gated_delta_rule_supported(x, x, x, x.half(), beta, states)
+    wide = torch.empty(3 << 24, dtype=BF16, device="cuda").as_strided((3, 64, 128), (1 << 24, 128, 1))
+    assert not kd.gated_delta_rule_supported(wide, x[:3], x[:3], x[:3], beta[:3], states)
