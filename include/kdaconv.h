@@ -279,7 +279,8 @@ int kdaconv_activation_map(uint32_t first, int64_t count, int activation, int dt
  * decays given as they are (KDACONV_GATE_LOG) are at most 0; positive ones are not looked for
  * and may leave the range of the prefill's FP16 pairs.
  *
- * All strides count elements.
+ * All strides count elements. Those of q, k, v, g and beta are 0 to 2^23 - 1 (else
+ * EUNSUPPORTED); of an axis of one entry they are not looked at.
  */
 typedef enum kdaconv_gate {
   KDACONV_GATE_LOG = 0,

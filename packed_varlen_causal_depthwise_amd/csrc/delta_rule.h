@@ -12,7 +12,7 @@ namespace kdaconv {
 constexpr int kRuleWave = 64;
 
 // One call of the rule. Strides are in elements and bounded by the host checks (a token
-// stride below 2^24), so offsets inside a chunk fit 32 bits.
+// stride below 2^23), so offsets inside a chunk fit 32 bits.
 struct RuleParams {
   const char* q;
   const char* k;

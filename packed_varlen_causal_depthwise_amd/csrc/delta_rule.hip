@@ -3,6 +3,7 @@
 #include "delta_rule.h"
 
 #include <algorithm>
+#include <initializer_list>
 
 namespace kdaconv {
 namespace {
@@ -130,9 +131,16 @@ int validate_rule(const kdaconv_rule_args* a, bool update) {
   if (a->head_dim != 64 && a->head_dim != 128) return KDACONV_EUNSUPPORTED;
   if (a->gate_dtype != a->dtype && a->gate_dtype != KDACONV_F32) return KDACONV_EUNSUPPORTED;
   if (a->beta_dtype != a->dtype && a->beta_dtype != KDACONV_F32) return KDACONV_EUNSUPPORTED;
-  for (int64_t s : {a->q_stride0, a->q_stride1, a->k_stride0, a->k_stride1, a->v_stride0,
-                    a->v_stride1, a->g_stride0, a->g_stride1, a->beta_stride0, a->beta_stride1})
-    if (s < 0 || s >= kMaxStride) return KDACONV_EUNSUPPORTED;
+  // (The stride of an axis of one means nothing.)
+  const struct {
+    int64_t count;
+    std::initializer_list<int64_t> strides;
+  } axes[] = {{a->num_tokens, {a->q_stride0, a->k_stride0, a->v_stride0, a->g_stride0, a->beta_stride0}},
+              {a->num_qk_heads, {a->q_stride1, a->k_stride1}},
+              {a->num_heads, {a->v_stride1, a->g_stride1, a->beta_stride1}}};
+  for (const auto& axis : axes)
+    for (int64_t s : axis.strides)
+      if (axis.count != 1 && (s < 0 || s >= kMaxStride)) return KDACONV_EUNSUPPORTED;
   if (a->state_stride0 < 0 || a->state_stride1 < 0 || a->cache_indices_stride < 0)
     return KDACONV_EUNSUPPORTED;
   // int32 tokens, sequences and workgroups.
@@ -169,17 +177,18 @@ RuleParams rule_params(const kdaconv_rule_args* a, bool update) {
   P.cache_indices = a->cache_indices;
   P.has_init = update ? nullptr : a->has_initial_state;
   P.out = static_cast<char*>(a->out);
-  P.q_ts = a->q_stride0;
-  P.q_hs = a->q_stride1;
-  P.k_ts = a->k_stride0;
-  P.k_hs = a->k_stride1;
-  P.v_ts = a->v_stride0;
-  P.v_hs = a->v_stride1;
-  P.g_ts = a->g_stride0;
-  P.g_hs = a->g_stride1;
+  const int64_t tokens = a->num_tokens != 1, qk_heads = a->num_qk_heads != 1, heads = a->num_heads != 1;
+  P.q_ts = a->q_stride0 * tokens;
+  P.q_hs = a->q_stride1 * qk_heads;
+  P.k_ts = a->k_stride0 * tokens;
+  P.k_hs = a->k_stride1 * qk_heads;
+  P.v_ts = a->v_stride0 * tokens;
+  P.v_hs = a->v_stride1 * heads;
+  P.g_ts = a->g_stride0 * tokens;
+  P.g_hs = a->g_stride1 * heads;
   P.g_cs = (int32_t)a->g_stride2;
-  P.b_ts = a->beta_stride0;
-  P.b_hs = a->beta_stride1;
+  P.b_ts = a->beta_stride0 * tokens;
+  P.b_hs = a->beta_stride1 * heads;
   P.st_line = a->state_stride0;
   P.st_head = a->state_stride1;
   P.num_cache_lines = a->num_cache_lines;

@@ -220,3 +220,25 @@ def test_supported_asks_for_a_prefill():
     assert not kd.gated_delta_rule_supported(x, x, x, x.half(), beta, states)
     wide = torch.empty(3 << 24, dtype=BF16, device="cuda").as_strided((3, 64, 128), (1 << 24, 128, 1))
     assert not kd.gated_delta_rule_supported(wide, x[:3], x[:3], x[:3], beta[:3], states)
+
+
+def test_one_row_of_a_batch_of_one():
+    """One token out of (1, tokens, columns): its token stride is the whole batch."""
+    args, kw = ref.rule_inputs([1], heads=4, dim=128, seed=98, initial=torch.tensor([True]))
+    rows = torch.zeros(1, 4096, 2500, dtype=BF16, device="cuda")
+    row = rows[:, 77]
+    assert row.stride(0) > 1 << 23
+    g = [a.cuda() for a in args]
+    for i in range(4):
+        g[i] = row[:, 512 * i + 3:512 * i + 515].view(1, 4, 128).copy_(args[i])
+    g[4] = row[:, 2100:2104].copy_(args[4])
+    gkw = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in kw.items()}
+    want, want_st = ref.delta_rule(*args, **kw)
+    for update in (False, True):
+        st = args[5].cuda()
+        if update:
+            out = kd.gated_delta_rule_update(*g[:5], st, g[7], **gkw, null_block_id=None)
+        else:
+            out = kd.gated_delta_rule_fn(*g[:5], st, *g[6:], **gkw, null_block_id=None)
+        ref.check(out, want, BF16, "out")
+        ref.check(st, want_st, F32, "states")

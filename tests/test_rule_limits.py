@@ -32,3 +32,18 @@ def test_many_tokens_of_few_sequences():
     assert prefill(T=131072, S=1 << 16, H=64, HK=64) == OK
     assert prefill(T=1 << 22, S=1, H=63, HK=63) == OK
     assert prefill(T=1 << 22, S=1, H=64, HK=64) == EUNSUPPORTED
+
+
+@pytest.mark.parametrize("axis,alone", [(("qs0", "ks0", "vs0", "gs0", "bs0"), dict(T=1)),
+                                        (("qs1", "ks1"), dict(HK=1)),
+                                        (("vs1", "gs1", "bs1"), dict(H=1, HK=1))])
+def test_strides_of_an_axis_of_one_are_not_looked_at(axis, alone):
+    for name in axis:
+        for stride, code in ((1 << 23, EUNSUPPORTED), (-1, EUNSUPPORTED), ((1 << 23) - 1, OK)):
+            assert prefill(**{name: stride}) == code
+            assert update(100, **{name: stride}) == code
+        for stride in (1 << 40, -1):
+            kw = {**alone, name: stride}
+            assert prefill(**{"S": 1, **kw}) == OK
+            tokens = kw.pop("T", 100)
+            assert update(tokens, **kw) == OK
