@@ -70,10 +70,10 @@ __global__ __launch_bounds__(2 * D) void delta_rule_step_kernel(const RuleParams
       Factor rk = {1.0f, 0.0f};
       float rq = P.scale;
       if (P.l2_eps >= 0.0f) {
-        const double x = kk.x, y = kk.y;
+        // (In FP64 the query's square too: in FP32 it would overflow from 2^64 on.)
+        const double x = kk.x, y = kk.y, qx = qq.x, qy = qq.y;
         rk = inverse_root(lane_sum<D / 2>(__builtin_fma(x, x, y * y)) + (double)P.l2_eps);
-        rq = P.scale / __builtin_sqrtf(
-            lane_sum<D / 2>(__builtin_fmaf(qq.x, qq.x, qq.y * qq.y)) + P.l2_eps);
+        rq = (float)(P.scale * inverse_root_f64(lane_sum<D / 2>(__builtin_fma(qx, qx, qy * qy)) + (double)P.l2_eps));
       }
       if (lane < D / 2) {
         *(f32x2*)&sk[buf][wave][c] = f32x2{scaled(kk.x, rk), scaled(kk.y, rk)};

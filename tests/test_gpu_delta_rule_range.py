@@ -242,3 +242,13 @@ def test_one_row_of_a_batch_of_one():
             out = kd.gated_delta_rule_fn(*g[:5], st, *g[6:], **gkw, null_block_id=None)
         ref.check(out, want, BF16, "out")
         ref.check(st, want_st, F32, "states")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=str)
+@pytest.mark.parametrize("operand", ["q", "k"])
+@pytest.mark.parametrize("lengths", [[1, 1, 1], [9, 40]], ids=str)
+def test_long_keys_and_queries(lengths, operand, dtype):
+    """Squares past FP32's range, token by token and in chunks."""
+    args, kw = ref.rule_inputs(lengths, heads=2, dim=128, dtype=dtype, seed=96)
+    args["qk".index(operand)] = (args["qk".index(operand)].double() * 1e25).to(dtype)
+    compare(args, kw)
