@@ -314,8 +314,8 @@ extern "C" int kdaconv_gated_rms_norm(const void* x, int dtype, int64_t num_toke
   if (dim % 8 != 0 || dim > 512) return KDACONV_EUNSUPPORTED;
   if (x_stride0 < 0 || x_stride1 < 0 || gate_stride0 < 0 || gate_stride1 < 0)
     return KDACONV_EUNSUPPORTED;
-  // A launch may not reach 2^32 threads.
-  constexpr int64_t kMaxRows = (int64_t)1 << 28;
+  // A launch may not reach 2^32 threads; a workgroup of 256 takes 16 rows at least.
+  constexpr int64_t kMaxRows = ((int64_t)1 << 28) - 16;
   if (num_tokens > kMaxRows || num_heads > kMaxRows || num_tokens * num_heads > kMaxRows)
     return KDACONV_EUNSUPPORTED;
   if (num_tokens == 0 || num_heads == 0) return KDACONV_OK;

@@ -47,3 +47,10 @@ def test_strides_of_an_axis_of_one_are_not_looked_at(axis, alone):
             assert prefill(**{"S": 1, **kw}) == OK
             tokens = kw.pop("T", 100)
             assert update(tokens, **kw) == OK
+
+
+def test_gated_norm_rows():
+    """2^28 - 15 rows of 512 channels, 16 to a workgroup of 256, would be 2^32 threads."""
+    gated = _lib.load().kdaconv_gated_rms_norm
+    for tokens, heads in (((1 << 28) - 15, 1), (1, 1 << 28), (1 << 14, 1 << 14)):
+        assert gated(A, _lib.BF16, tokens, heads, 512, 0, 0, A, 0, 0, 1, A, 1e-5, A, None) == EUNSUPPORTED
