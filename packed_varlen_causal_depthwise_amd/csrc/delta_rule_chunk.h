@@ -1206,8 +1206,6 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
       return m;
     };
     float back = 1.0f;  // what X was divided by
-    int dead = kChunk;  // the column's first row whose X is not finite
-    bool unfinite = false;  // some column has one
     difference();
     float high = range();
     if (!S.within(high) || S.below(high)) {
@@ -1228,20 +1226,29 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
       }
       empty = S.below(most);
       // An X that is still not finite would reach all rows of its column (T's zeros times NaN).
-      // By the definition it reaches those from its own on: they are left out here, and O and S
-      // are NaN there at the end.
+      // By the definition it reaches those from its own on: they are left out of the products
+      // here, and start O, and S, from NaN.
+      int dead = kChunk;  // the column's first such row
 #pragma unroll
       for (int i = 7; i >= 0; --i)
         if (!is_finite(X[i / 4][i % 4])) dead = 16 * (i / 4) + 4 * n4 + i % 4;
-      unfinite = __ballot(dead < kChunk) != 0;
-      if (unfinite) {
+      if (__ballot(dead < kChunk) != 0) {
         int other = __shfl_xor(dead, 16);
         dead = dead < other ? dead : other;
         other = __shfl_xor(dead, 32);
         dead = dead < other ? dead : other;
+        const float nan = __builtin_nanf("");
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (16 * (i / 4) + 4 * n4 + i % 4 >= dead) X[i / 4][i % 4] = 0.0f;
+          if (16 * (i / 4) + 4 * n4 + i % 4 >= dead) {
+            X[i / 4][i % 4] = 0.0f;
+            O[i / 4][i % 4] = nan;
+          }
+        if (dead < kChunk) {
+#pragma unroll
+          for (int m = 0; m < kM; ++m) S.s[m] = f32x4{nan, nan, nan, nan};
+          most = 0.0f;
+        }
         empty = true;
       }
       // X may be far larger than the U that comes of it (steps near 0, short keys): it is brought
@@ -1324,19 +1331,8 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
 #pragma unroll
         for (int r = 0; r < 4; ++r) O[t][r] = O[t][r] * S.inverse * nq[r];  // (nq * inverse may be subnormal)
       }
-      if (unfinite) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (16 * (i / 4) + 4 * n4 + i % 4 >= dead) O[i / 4][i % 4] = __builtin_nanf("");
-      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) Cell<kF>::store_one(wo, at, 16 * (i / 4) + i % 4, O[i / 4][i % 4]);
-    }
-    if (unfinite) {
-      const float nan = __builtin_nanf("");
-#pragma unroll
-      for (int m = 0; m < kM; ++m)
-        if (dead < kChunk) S.s[m] = f32x4{nan, nan, nan, nan};
     }
     // The column's range for the next chunk.
     most = S.largest();
