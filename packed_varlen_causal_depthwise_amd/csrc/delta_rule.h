@@ -87,8 +87,8 @@ struct Slot {
 };
 
 // In a slot's factors: decays over the chunk (head_dim), then |k| / 16 and the outputs'
-// factors / 16 (kChunk each) and T's factor.
-constexpr int kFactorRows = 128;
+// factors / 16 (kChunk each), T's factor, and 0 if the chunk empties the state (1 if not).
+constexpr int kFactorRows = 128, kFactorT = kFactorRows + 2 * kChunk, kFactorFaded = kFactorT + 1;
 
 // The transition: pairs of FP16 matrices and a scale.
 inline __host__ __device__ int64_t move_bytes(int head_dim) { return (int64_t)head_dim * head_dim * 4 + 256; }

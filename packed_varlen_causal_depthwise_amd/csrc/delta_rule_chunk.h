@@ -33,8 +33,10 @@
 // in FP32. (One FP32 instruction costs as much as 16 FP16 ones of the same size; pairs of
 // bfloat16 would keep 16 bits, which left the FP32 state 4e-6 off.) FP16's range holds
 // because vectors have unit length, decays are at most 1, and a column's S and U share a
-// power-of-two factor that follows the larger of them, while X = V - n Y may have one more of
-// its own: with steps near 0 U is far below X, and pairs at X's scale would keep nothing of it. T and A come from FP64
+// power-of-two factor that follows the larger of them (U alone where a chunk empties S), while
+// X = V - n Y may have one more of its own: with steps near 0 U is far below X, and pairs at X's
+// scale would keep nothing of it. So errors are about 2^-22 of the largest value of a column in a
+// chunk. T and A come from FP64
 // and FP32 matrix instructions: their decays e^(G_t - G_i) are products of factors far
 // outside FP16.
 #ifndef KDACONV_DELTA_RULE_CHUNK_H_
@@ -50,6 +52,7 @@ typedef double f64x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32q __attribute__((ext_vector_type(4)));
 
 constexpr float kVec = 16.0f;  // factor on stored unit vectors (their entries are small)
+constexpr float kFaded = 0x1p-4f;  // a chunk whose decays are all below this empties the state
 
 __device__ __forceinline__ f32x4 mfma16(f16x8 a, f16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -809,9 +812,11 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
         *(f16x4*)&kt[at + 512] = lo;
       }
     }
-    if (wave == 0 && lane < kLanes) {
-      const f32x2 d = all[0] + all[1];
-      *(f32x2*)(slot + kSlot.factors() + 4 * c) = f32x2{exp2_hw(d.x), exp2_hw(d.y)};
+    if (wave == 0) {
+      const f32x2 d = all[0] + all[1], e = {exp2_hw(d.x), exp2_hw(d.y)};
+      if (lane < kLanes) *(f32x2*)(slot + kSlot.factors() + 4 * c) = e;
+      const bool keeps = __ballot(e.x >= kFaded || e.y >= kFaded) != 0;
+      if (lane == 0) ((float*)(slot + kSlot.factors()))[kFactorFaded] = keeps ? 1.0f : 0.0f;
     }
   }
 
@@ -918,7 +923,7 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
     to[256] = lo;
     to[512] = last;
     // U is kept times 1 / 16, so that (16 k^)^T (U / 16) adds to S as it is.
-    if (u == 0) df[kFactorRows + 2 * kChunk] = __builtin_amdgcn_ldexpf(1.0f / kVec, -e);
+    if (u == 0) df[kFactorT] = __builtin_amdgcn_ldexpf(1.0f / kVec, -e);
     ((u32q*)(slot + kSlot.a()))[u] = ((const u32q*)sa)[u];
   }
   if (threadIdx.x < 2 * kChunk)
@@ -977,8 +982,9 @@ struct ScanState {
     // The scale stays at most 2^kMostScale: a column that fades for long would take it to
     // infinity (its values then go to zero as they are).
     const int most = kMostScale + 1 - __builtin_amdgcn_frexp_expf(scale);
-    const int e = kColExp - __builtin_amdgcn_frexp_expf(m);
-    return __builtin_amdgcn_ldexpf(1.0f, e < most ? e : most);
+    int e = kColExp - __builtin_amdgcn_frexp_expf(m);
+    e = e < most ? e : most;
+    return __builtin_amdgcn_ldexpf(1.0f, e < 100 ? e : 100);  // (S itself may be far above m)
   }
 
   __device__ __forceinline__ void apply(float f) {
@@ -1097,7 +1103,6 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
     S.apply(S.factor(column_max(S.largest())));
     most = S.largest();
   }
-  bool empty = S.below(most);  // some column is
 
   const f16x8* const kq = (const f16x8*)krows;
   const f16x8* const qq = (const f16x8*)qrows;
@@ -1196,9 +1201,11 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
           X[t][r] = __builtin_fmaf(Pair<kF>::value(rv[4 * t + r]).x, S.scale, -nt[r] * Y[t][r]);
       }
     };
-    // The column's range over S and X; NaN where an X is.
-    const auto range = [&]() {
-      float m = most;
+    // What the column's values are measured by beside X and U: S, unless this chunk empties it.
+    // Then what X and U hold is all that is left, however far below S it is.
+    float beside = factors[kFactorFaded] != 0.0f ? most : 0.0f;
+    // The column's range over X, NaN where an X is.
+    const auto range = [&](float m) {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -1207,7 +1214,7 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
     };
     float back = 1.0f;  // what X was divided by
     difference();
-    float high = range();
+    float high = range(beside);
     if (!S.within(high) || S.below(high)) {
       // Values beyond a faded column's scale: that goes back to 1 first.
       bool beyond = false;
@@ -1216,7 +1223,7 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
       if (column_max(beyond ? 1.0f : 0.0f) != 0.0f && S.scale > 1.0f) {
         const float f = S.inverse;
         S.apply(f);
-        most *= f;
+        beside *= f;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           Y[t] *= f;
@@ -1224,7 +1231,6 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
         }
         difference();
       }
-      empty = S.below(most);
       // An X that is still not finite would reach all rows of its column (T's zeros times NaN).
       // By the definition it reaches those from its own on: they are left out of the products
       // here, and start O, and S, from NaN.
@@ -1247,27 +1253,24 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
         if (dead < kChunk) {
 #pragma unroll
           for (int m = 0; m < kM; ++m) S.s[m] = f32x4{nan, nan, nan, nan};
-          most = 0.0f;
         }
-        empty = true;
       }
-      // X may be far larger than the U that comes of it (steps near 0, short keys): it is brought
-      // down alone, for its product with T. A column without a state yet comes up as one.
-      const float f = S.factor(column_max(range())), own = f < 1.0f ? f : 1.0f, common = f < 1.0f ? 1.0f : f;
-      back = rcp_hw(own);  // exact for powers of two
-      S.apply(common);
-      most *= common;
+      // X alone, for its product with T: the U that comes of it may be far smaller (steps near
+      // 0, short keys).
+      const float m = column_max(range(0.0f));
+      if (m > 0.0f && (m >= kColHigh || m < kColLow)) {
+        int e = kColExp - __builtin_amdgcn_frexp_expf(m);
+        e = e < 100 ? e : 100;
+        back = __builtin_amdgcn_ldexpf(1.0f, -e);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        X[t] *= f;
-        O[t] *= common;
+        for (int t = 0; t < 2; ++t) X[t] *= __builtin_amdgcn_ldexpf(1.0f, e);
       }
     }
 
     // ---- U = T X
     f32x4 U[2];
     b = split8(X[0], X[1], R.one);
-    const float us = factors[kFactorRows + 2 * kChunk] * back;
+    const float us = factors[kFactorT] * back;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const f16x8 th = tp[64 * t + lane], tl = tp[128 + 64 * t + lane], tr = tp[256 + 64 * t + lane];
@@ -1281,14 +1284,13 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
     // (Issued here and not right after the barrier: the products with T then start 300 cycles
     // earlier, and the loads still have the rest of the chunk to arrive.)
     if (chunk + 1 < end) load_rows(slot);
-    // The column's range over S and U: the larger of them keeps its bits. (S alone is in range
-    // unless the column is empty or has faded.)
-    high = most;
+    // The column's range over U and what S keeps: the larger of them keeps its bits.
+    high = beside;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) high = __builtin_fmaxf(high, __builtin_fabsf(U[t][r]));
-    if (!S.within(high) || (empty && S.below(high))) {
+    if (!S.within(high) || S.below(high)) {
       const float f = S.factor(column_max(high));
       S.apply(f);
 #pragma unroll
@@ -1336,12 +1338,10 @@ __global__ __launch_bounds__((kMode == kScanOut ? 4 : 8) * D / kParts, 4) void d
     }
     // The column's range for the next chunk.
     most = S.largest();
-    empty = S.below(most);
-    if (empty || !S.within(most)) {
+    if (!S.within(most) || S.below(most)) {
       const float f = S.factor(column_max(most));
       S.apply(f);
       most *= f;
-      empty = S.below(most);
     }
     // The next chunk's rows have arrived, and all waves are done with this chunk.
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");

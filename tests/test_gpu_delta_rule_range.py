@@ -252,3 +252,17 @@ def test_long_keys_and_queries(lengths, operand, dtype):
     args, kw = ref.rule_inputs(lengths, heads=2, dim=128, dtype=dtype, seed=96)
     args["qk".index(operand)] = (args["qk".index(operand)].double() * 1e25).to(dtype)
     compare(args, kw)
+
+
+@pytest.mark.parametrize("lengths", [[31], [64, 33], [94, 64, 148, 122]], ids=str)
+@pytest.mark.parametrize("beta", [0.1, 1e-3, 1e-5])
+@pytest.mark.parametrize("most", [3.0, 12.0, 100.0])
+def test_small_steps_after_a_state_that_fades(most, beta, lengths):
+    """Decays that leave nothing of a state within a chunk, and updates far below what it was."""
+    for dim in (64, 128):
+        args, kw = log_inputs(lengths, 2, dim, seed=99, logits=False,
+                              initial=torch.ones(len(lengths), dtype=torch.bool))
+        gen = torch.Generator().manual_seed(7)
+        args[3] = -torch.rand(args[3].shape, generator=gen) * most
+        args[4] = args[4] * beta
+        compare(args, kw)
