@@ -943,10 +943,12 @@ __device__ __forceinline__ float column_max(float x) {
 constexpr int kScanOut = 0;  // outputs and final states
 constexpr int kScanMove = 1;  // a segment's B and M
 
-constexpr float kColLow = 1.0f, kColHigh = 8192.0f;  // columns' largest value stays between
-// And is brought to 2^4 .. 2^5 when it leaves: X is often 2^4 to 2^8 times S and would be above
-// every time if S came to 2^7 .. 2^8 (16384 tokens 378 us against 373).
-constexpr int kColExp = 5;
+// Columns' largest values stay in this range. FP16 ends at 2^16, and its steps at 2^-24: the pairs'
+// errors are 2^-28 of the largest value at its lower end.
+constexpr float kColLow = 8.0f, kColHigh = 32768.0f;
+// And come to 2^6 .. 2^7 when they leave it: X is often 2^4 to 2^8 times S and would be above most
+// times if S came to 2^7 .. 2^8 of a range up to 2^13 (16384 tokens 378 us against 373).
+constexpr int kColExp = 7;
 constexpr int kMostScale = 118;
 
 // 16 columns per wave; lane l holds rows 4 (l / 16) .. + 3 of each 16 of column l % 16.

@@ -266,3 +266,15 @@ def test_small_steps_after_a_state_that_fades(most, beta, lengths):
         args[3] = -torch.rand(args[3].shape, generator=gen) * most
         args[4] = args[4] * beta
         compare(args, kw)
+
+
+@pytest.mark.parametrize("logit", [-5.0, -10.0])
+def test_many_small_updates_of_a_long_memory(logit):
+    """Each about 2^-20 of the state that it is added to, and hardly any decay."""
+    args, kw = ref.rule_inputs([900], heads=20, qk_heads=10, dim=128, dtype=F32, seed=50001)
+    kw["a_log"] = torch.full_like(kw["a_log"], 2.772588722239781)
+    kw["lower_bound"] = -8.0
+    args[3] = 0.3 * args[3]
+    args[4] = args[4] + logit
+    args[1] = args[1] / args[1].norm(dim=-1, keepdim=True) * 0.01
+    compare(args, kw, qk_l2norm=False)
