@@ -272,7 +272,9 @@ int kdaconv_activation_map(uint32_t first, int64_t count, int activation, int dt
  * from zeros and leaves the states alone. A sequence without tokens leaves what it starts
  * from: its line as it is, or zeros there without an initial state. States, sums and norms
  * are held in FP32 or more; matrix products take FP32 values as pairs of FP16 values (22
- * bits) and sum in FP32; only out is rounded to its format.
+ * bits) and sum in FP32; only out is rounded to its format. Errors of the prefill are about
+ * 2^-22 of the largest value that a column of the state, or of v, has within 32 tokens. Keys and
+ * queries taken as they are (l2_eps < 0) lose bits below a length of 2^-118.
  * A value that is not finite reaches what the steps above take it to, tokens from its own on,
  * and no token before it nor another sequence.
  * A log decay below -104 acts as -104 (its exp is zero in FP32, as is -infinity's). Log
@@ -321,8 +323,10 @@ typedef struct kdaconv_rule_args {
 
 /*
  * Bytes of device scratch memory that kdaconv_gated_delta_rule needs for these sizes (0
- * for none; about 60 KB per 32 tokens and head of 128, 35 KB per head of 64). The scratch holds no state between calls; calls that may run at the same
- * time need scratch memories of their own. Aligned to 256 bytes.
+ * for none; about 60 KB per 32 tokens and head of 128, 35 KB per head of 64). It grows with the
+ * call: 0.4 GB for 16384 tokens of 12 heads of 128, 16 GB for 131072 of 64. The scratch holds no
+ * state between calls; calls that may run at the same time need scratch memories of their own.
+ * Aligned to 256 bytes.
  */
 int64_t kdaconv_gated_delta_rule_workspace(int64_t num_tokens, int64_t num_seqs,
                                            int64_t num_heads, int64_t head_dim);
@@ -332,7 +336,9 @@ int64_t kdaconv_gated_delta_rule_workspace(int64_t num_tokens, int64_t num_seqs,
  * multiple of num_qk_heads (else EUNSUPPORTED and EINVAL). Sizes come from the host
  * arguments alone, so a call can be captured in a graph. Preconditions on device data as
  * for kdaconv_packed_causal_conv1d. num_tokens, num_seqs or num_heads of 0: KDACONV_OK
- * with no launch (a call without any token leaves all states alone).
+ * with no launch (a call without any token leaves all states alone). out may not overlap an
+ * input. From (num_tokens / 32 + num_seqs) * num_heads = 2^23 on a call may be refused
+ * (EUNSUPPORTED).
  */
 int kdaconv_gated_delta_rule(const kdaconv_rule_args* args, void* workspace,
                              int64_t workspace_bytes, kdaconv_stream_t stream);
@@ -341,7 +347,7 @@ int kdaconv_gated_delta_rule(const kdaconv_rule_args* args, void* workspace,
  * The rule for one token per sequence (decode): row s of q, k, v, g, beta and out belongs
  * to sequence s, num_seqs equals num_tokens (else EINVAL), and every sequence continues
  * from its stored line (zeros for the null block). query_start_loc and has_initial_state
- * are not read. No scratch memory.
+ * are not read. No scratch memory. Sequences times heads below 2^23 (else EUNSUPPORTED).
  */
 int kdaconv_gated_delta_rule_update(const kdaconv_rule_args* args, kdaconv_stream_t stream);
 
@@ -366,7 +372,8 @@ typedef enum kdaconv_norm_gate {
  * weight    FP32 (dim) contiguous, or NULL for ones.
  * out       format dtype, (num_tokens, num_heads, dim) contiguous; may be x itself when
  *           x is laid out like it.
- * dim       a positive multiple of 8, at most 512 (else EUNSUPPORTED).
+ * dim       a positive multiple of 8, at most 512 (else EUNSUPPORTED, as are more than
+ *           2^28 - 16 tokens times heads).
  */
 int kdaconv_gated_rms_norm(const void* x, int dtype, int64_t num_tokens, int64_t num_heads,
                            int64_t dim, int64_t x_stride0, int64_t x_stride1, const void* gate,
@@ -382,7 +389,7 @@ int kdaconv_gated_rms_norm(const void* x, int dtype, int64_t num_tokens, int64_t
  * x, residual  format dtype; row t at t * stride, columns contiguous.
  * weight       FP32 (hidden) contiguous, or NULL for ones.
  * out          format dtype, (num_tokens, hidden) contiguous.
- * hidden       1 to 16384 (else EUNSUPPORTED).
+ * hidden       1 to 16384 (else EUNSUPPORTED, as are 2^24 tokens and more).
  */
 int kdaconv_residual_rms_norm(const void* x, int dtype, int64_t num_tokens, int64_t hidden,
                               int64_t x_stride, void* residual, int64_t residual_stride,

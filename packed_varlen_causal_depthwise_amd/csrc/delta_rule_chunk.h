@@ -24,8 +24,8 @@
 // A chunk's gates, norms and exponentials are worked out once, by prepare, and handed over
 // as matrix operands (60 KB per chunk and head of 128): the scans were bound by that vector
 // work when they repeated it (5 us per chunk, 0.5 TB/s). One sequence of 16384 tokens, 12
-// heads of 128, bf16 now takes 143 us in prepare, 113 for the transitions, 27 for the join
-// and 96 for the outputs. Its tensors alone, 252 MB, are 50 us; the operands' way through
+// heads of 128, bf16 now takes 147 us in prepare, 113 for the transitions, 27 for the join
+// and 99 for the outputs. Its tensors alone, 252 MB, are 50 us; the operands' way through
 // memory, 1.1 GB of reads and writes more, and the chain from chunk to chunk are the rest.
 //
 // Numbers. Matrix products run on the FP16 matrix instructions with every operand split
@@ -321,14 +321,15 @@ __device__ __forceinline__ double scatter_sum(typename Doubles<N>::type x, int l
 
 // ---------------------------------------------------------------------------- prepare
 
-// With 128 channels 4 or 8 waves: of 8 only two workgroups fit a CU (53 KB of LDS, 112
-// registers), but each is faster; of 4 three do (148 registers). Of 4 one alone takes 24500 cycles:
-// finding its chunk 1600, loads and gates 3900, lengths and sums 1400, operands of the
-// products 2400, products 4400, L and A 1300, operands for the scans 3400, T 4600, the rest
-// its stores. 6144 of them (16384 tokens, 12 heads of 128) take 145 us for 550 MB, 3.8 TB/s,
-// and no single part bounds that: without its stores it takes 130 us, without the products
-// 114, without T 128, without the scans' operands 121. The way through all of them at three
-// workgroups per CU does; a fourth would need 40 KB of LDS and 128 registers.
+// With 128 channels 4 or 8 waves: of 8 only two workgroups fit a CU (53 KB of LDS, 122
+// registers), but each is faster; of 4 three do (162 registers). Of 4 one alone takes about 25000
+// cycles: finding its chunk 1600, loads and gates 3900, lengths and sums 1500, operands of the
+// products 2400, products 4500, L and A 1300, operands for the scans 3400, T 4600, the rest
+// its stores. 6144 of them (16384 tokens, 12 heads of 128) take 147 us for 550 MB, 3.7 TB/s,
+// and no single part bounds that: without its stores it takes 15 us less, without the products
+// 31, without T 17, without the scans' operands 24, without the checks for values that are not
+// finite 2. The way through all of them at three workgroups per CU does; a fourth would need 40 KB
+// of LDS and 128 registers.
 template <int kF, int kG, int D, int kWaves>
 __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_prepare_kernel(const ChunkParams P) {
   typedef Rows<D, kWaves> RW;
@@ -517,10 +518,9 @@ __global__ __launch_bounds__(64 * kWaves, kWaves == 8 ? 4 : 3) void delta_rule_p
   // middle outwards: rows nearer to the middle than a strong decay do not carry it, and the
   // product of a row and a column of these is exact to a few 2^-24. Rows beyond it do, and
   // each addition to a sum of up to 101 is off by up to 2^-18, which the product then is too.
-  // Between the blocks lie the decays
-  // of block 0's second half and of block 1's first. Their product may leave FP32's range where
-  // neither does, so columns of block 0 carry one and rows of block 1 the other: each scaled
-  // operand is at most its vector.
+  // Between the blocks lie the decays of block 0's second half and of block 1's first. Their
+  // product may leave FP32's range where neither does, so columns of block 0 carry one and rows
+  // of block 1 the other: each scaled operand is at most its vector.
   f32x2 all[2], mid[2], late[2];  // of both blocks; late: of their second halves
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
@@ -1006,8 +1006,8 @@ struct ScanState {
 // 14: 20% longer with one sequence of 64 tokens, 5% with many. Two workgroups for the outputs of
 // a segment, half of the columns each, took 37 us against 32 for 96 chains of up to 10 chunks.)
 //
-// 264 output scans of 24 chunks take 96 us: 490 MB, 5 TB/s, what a copy reaches; the matrix
-// units are busy for 37% of it. The 252 transitions take 113 us for half the bytes:
+// 264 output scans of 24 chunks take 99 us: 490 MB, 4.9 TB/s, what a copy reaches; the matrix
+// units are busy for 38% of it. The 252 transitions take 113 us for half the bytes:
 // 16 waves read 640 KB of operands from LDS per chunk, which is 5000 of its 10000 cycles, and
 // the matrix units are busy for 40%.
 template <int kF, int D, int kMode, int kParts>

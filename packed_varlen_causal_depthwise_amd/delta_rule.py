@@ -154,11 +154,13 @@ def gated_delta_rule_fn(
     states (cache lines, heads, head_dim, head_dim) float32 is read and written in place.
     query_start_loc, cache_indices, has_initial_state and null_block_id mean what they mean
     for ``packed_causal_conv1d_fn``; rows no sequence owns are left unwritten, and a sequence
-    without tokens leaves what it starts from (zeros in its line without an initial state). Returns (tokens,
-    heads, head_dim) in v's dtype (``out``, when given). The state and every intermediate hold
-    FP32 or 22-bit pairs; only the output is rounded to its dtype. Takes about 60 KB of scratch
-    memory per 32 tokens and head of 128 from torch's allocator. Queued on the current stream;
-    no synchronisation.
+    without tokens leaves what it starts from (zeros in its line without an initial state, where
+    ``packed_causal_conv1d_fn`` leaves its line alone). A value that is not finite reaches no
+    earlier token. Returns (tokens, heads, head_dim) in v's dtype (``out``, when given; it may not
+    overlap an input). The state and every intermediate hold FP32 or 22-bit pairs; only the output
+    is rounded to its dtype. Takes about 60 KB of scratch memory per 32 tokens and head of 128 from
+    torch's allocator (16 GB for 131072 tokens of 64 heads). Queued on the current stream; no
+    synchronisation.
     """
     sizes = _heads(q, k, v, g, beta, states)
     out = _output(v, out)
