@@ -396,6 +396,88 @@ int kdaconv_residual_rms_norm(const void* x, int dtype, int64_t num_tokens, int6
                               double residual_scale, const float* weight, double eps, void* out,
                               kdaconv_stream_t stream);
 
+/*
+ * Latent attention: the attention layer that alternates with KDA layers. All heads' keys and
+ * values come from one latent vector of latent_dim channels and one rotated vector of rope_dim
+ * channels a token, which are what its cache holds.
+ *
+ * Rotary positions. Channels [offset, offset + rotary) of every head are turned in pairs, pair
+ * i by the angle a_i = positions[t] * inv_freq[i]:
+ *     (u, v) -> (scale * (u cos a_i - v sin a_i), scale * (u sin a_i + v cos a_i))
+ * Pair i is channels (2 i, 2 i + 1) with `interleaved`, else (i, i + rotary / 2), counted from
+ * offset. The angle is taken in FP64 and reduced to a turn there, so far positions keep their
+ * precision; products are FP32, rounded once. The other channels are copied (left alone where
+ * out is x itself, laid out alike).
+ *
+ * x, out     (num_tokens, num_heads, head_dim), element (t, h, c) at t * stride0 +
+ *            h * stride1 + c; format dtype (bf16, fp16 or FP32). out may be x with x's strides;
+ *            it may not overlap x otherwise, nor itself.
+ * positions  (num_tokens) int32, or int64 with positions_64; any value.
+ * inv_freq   (rotary / 2) FP32. rotary is even, 2 to 512 (else EINVAL, EUNSUPPORTED), and
+ *            offset + rotary <= head_dim (else EINVAL).
+ */
+int kdaconv_rotary_embedding(const void* x, int dtype, int64_t num_tokens, int64_t num_heads,
+                             int64_t head_dim, int64_t x_stride0, int64_t x_stride1,
+                             const void* positions, int positions_64, const float* inv_freq,
+                             int64_t rotary, int64_t offset, int interleaved, double scale,
+                             void* out, int64_t out_stride0, int64_t out_stride1,
+                             kdaconv_stream_t stream);
+
+/*
+ * A paged cache. Slot s of it is place s % page_size of page s / page_size. With e4m3 a latent
+ * is held in 8 bits (OCP E4M3) and a scale byte b for each 32 channels stands for 2^(b - 127);
+ * 255 is no scale. rope_dim may be 0. Strides count elements of the tensor they belong to.
+ *
+ * latent_dim is a multiple of 8 (32 with e4m3), 8 to 512, and rope_dim one of 8, 0 to 64 (else
+ * EUNSUPPORTED). Latents and rotated parts lie at multiples of 16 bytes, page for page and slot
+ * for slot (else EUNSUPPORTED). num_pages * page_size is below 2^31 (else EUNSUPPORTED).
+ */
+typedef struct kdaconv_latent_cache {
+  void* latents;   /* (num_pages, page_size, latent_dim): dtype, or e4m3 codes */
+  void* ropes;     /* (num_pages, page_size, rope_dim): dtype */
+  uint8_t* scales; /* (num_pages, page_size, latent_dim / 32) with e4m3, else ignored */
+  int64_t num_pages, page_size, latent_dim, rope_dim;
+  int64_t latents_stride0, latents_stride1, ropes_stride0, ropes_stride1;
+  int64_t scales_stride0, scales_stride1;
+  int32_t dtype; /* KDACONV_BF16 or KDACONV_F16 */
+  int32_t e4m3;
+} kdaconv_latent_cache;
+
+/*
+ * Writes tokens into the cache. Of token t the latent
+ *     y = latent / sqrt(mean(latent^2) + eps) * weight      (y = latent with eps < 0)
+ * and the rotated part (kdaconv_rotary_embedding with one head of rope_dim channels; as it is
+ * without inv_freq) go to slot slots[t]; a slot outside the cache is left out. The norm is
+ * worked out in FP64 and y is its FP32 rounding, so that codes do not depend on the order of a
+ * sum. y is rounded to dtype, or with e4m3 each block of 32 is held as codes of y / 2^e, rounded
+ * to nearest even, where e is the smallest integer >= -100 with max |y| <= 448 * 2^e over the
+ * block's finite values (infinities and NaN become the code NaN).
+ *
+ * latent, rope  (num_tokens, latent_dim) and (num_tokens, rope_dim) of the cache's dtype,
+ *               columns contiguous.
+ * slots         (num_tokens) int32, or int64 with slots_64; slots in the cache are distinct.
+ * weight        FP32 (latent_dim), or NULL for ones.
+ */
+int kdaconv_latent_cache_write(const kdaconv_latent_cache* cache, const void* latent,
+                               int64_t latent_stride, const void* rope, int64_t rope_stride,
+                               int64_t num_tokens, const void* slots, int slots_64,
+                               const float* weight, double eps, const void* positions,
+                               int positions_64, const float* inv_freq, int interleaved,
+                               double rope_scale, kdaconv_stream_t stream);
+
+/*
+ * Reads sequences back out of the cache: row kv_start_loc[s] + i of out (num_tokens,
+ * latent_dim + rope_dim), contiguous, of the cache's dtype, gets token i of sequence s, which
+ * lies in slot block_table[s][i / page_size] * page_size + i % page_size. e4m3 values times
+ * their scale are rounded once. Rows of sequences past num_tokens, and those no sequence owns,
+ * are not written; a token whose page is outside the cache, or past the table's pages_per_seq
+ * columns, reads as zeros. out is aligned to 16 bytes (else EUNSUPPORTED).
+ */
+int kdaconv_latent_cache_read(const kdaconv_latent_cache* cache, const int32_t* block_table,
+                              int64_t table_stride, int64_t pages_per_seq,
+                              const int32_t* kv_start_loc, int64_t num_seqs, int64_t num_tokens,
+                              void* out, kdaconv_stream_t stream);
+
 /* Static English text for a status code. Never NULL. */
 const char* kdaconv_status_string(int status);
 

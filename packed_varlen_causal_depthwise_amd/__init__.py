@@ -19,7 +19,9 @@ from . import _lib
 from ._host import DTYPE_CODES as _DTYPE_CODES
 from ._host import NULL_BLOCK_ID, _on, _ptr, _stream_handle
 from .delta_rule import gated_delta_rule_fn, gated_delta_rule_supported, gated_delta_rule_update
+from .latent import latent_cache_read, latent_cache_write
 from .norms import gated_rms_norm, residual_rms_norm
+from .rotary import rotary_embedding, rotary_frequencies
 
 __all__ = [
     "NULL_BLOCK_ID",
@@ -31,6 +33,10 @@ __all__ = [
     "gated_delta_rule_supported",
     "gated_rms_norm",
     "residual_rms_norm",
+    "rotary_embedding",
+    "rotary_frequencies",
+    "latent_cache_write",
+    "latent_cache_read",
     "activation_map",
     "library_path",
 ]

@@ -17,6 +17,9 @@ NORM_GATE_NONE, NORM_GATE_SIGMOID, NORM_GATE_SILU = 0, 1, 2
 #: kdaconv_rule_args: 12 pointers, 21 integers, 3 doubles, 6 32-bit integers, no padding.
 RULE_ARGS = struct.Struct("=12Q21q3d6i")
 
+#: kdaconv_latent_cache: 3 pointers, 10 integers, 2 32-bit integers, no padding.
+LATENT_CACHE = struct.Struct("=3Q10q2i")
+
 # Every entry point include/kdaconv.h declares.
 EXPORTS = (
     "kdaconv_packed_causal_conv1d",
@@ -30,6 +33,9 @@ EXPORTS = (
     "kdaconv_gated_delta_rule_workspace",
     "kdaconv_gated_rms_norm",
     "kdaconv_residual_rms_norm",
+    "kdaconv_rotary_embedding",
+    "kdaconv_latent_cache_write",
+    "kdaconv_latent_cache_read",
     "kdaconv_status_string",
     "kdaconv_version",
 )
@@ -107,6 +113,23 @@ def load() -> ctypes.CDLL:
         vp, f64, vp, vp,  # weight, eps, out, stream
     ]
     lib.kdaconv_residual_rms_norm.restype = i32
+    lib.kdaconv_rotary_embedding.argtypes = [
+        vp, i32, i64, i64, i64, i64, i64,  # x, dtype, tokens, heads, dim, x strides
+        vp, i32, vp, i64, i64, i32, f64,  # positions, 64 bits, inv_freq, rotary, offset, interleaved, scale
+        vp, i64, i64, vp,  # out, strides, stream
+    ]
+    lib.kdaconv_rotary_embedding.restype = i32
+    lib.kdaconv_latent_cache_write.argtypes = [
+        packed, vp, i64, vp, i64, i64,  # cache, latent, stride, rope, stride, tokens
+        vp, i32, vp, f64,  # slots, 64 bits, weight, eps
+        vp, i32, vp, i32, f64, vp,  # positions, 64 bits, inv_freq, interleaved, scale, stream
+    ]
+    lib.kdaconv_latent_cache_write.restype = i32
+    lib.kdaconv_latent_cache_read.argtypes = [
+        packed, vp, i64, i64,  # cache, block_table, stride, pages per sequence
+        vp, i64, i64, vp, vp,  # kv_start_loc, num_seqs, num_tokens, out, stream
+    ]
+    lib.kdaconv_latent_cache_read.restype = i32
     lib.kdaconv_status_string.argtypes = [i32]
     lib.kdaconv_status_string.restype = ctypes.c_char_p
     lib.kdaconv_version.argtypes = []

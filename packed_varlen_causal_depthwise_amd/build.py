@@ -21,6 +21,7 @@ SOURCES = [PKG / "csrc" / name for name in (
     "delta_rule_f16.hip",
     "delta_rule_f32.hip",
     "norms.hip",
+    "latent_cache.hip",
 )]
 HEADERS = [ROOT / "include" / "kdaconv.h", *sorted((PKG / "csrc").glob("*.h"))]
 LIBRARY = PKG / "libkdaconv.so"
