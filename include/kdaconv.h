@@ -478,6 +478,59 @@ int kdaconv_latent_cache_read(const kdaconv_latent_cache* cache, const int32_t* 
                               const int32_t* kv_start_loc, int64_t num_seqs, int64_t num_tokens,
                               void* out, kdaconv_stream_t stream);
 
+/*
+ * Attention over the paged cache in the absorbed form: queries are already multiplied by the
+ * latents' up-projection, and what comes out is still to be multiplied by the values'. Token i of
+ * the n new tokens of sequence s (rows [qsl[s], qsl[s+1])), whose latents are in the cache, sees
+ * the sequence's first seq_lens[s] - n + i + 1 tokens: for every head
+ *     s_t = scale * (q_latent . latent_t + q_rope . rope_t),   out = sum_t softmax(s)_t latent_t
+ * A token whose page is outside the cache, or past the table's pages_per_seq columns, is not
+ * there; a row that sees none is zero. Rows no sequence owns are not written. Scores, softmax
+ * and sums are FP32; its weights (up to 2^8 before the division by their sum) are rounded to
+ * dtype for the second product, out is rounded once. 8-bit values times their scale are rounded
+ * to dtype, exactly within its range.
+ */
+typedef struct kdaconv_latent_args {
+  kdaconv_latent_cache cache;
+  const void* q_latent; /* (num_tokens, num_heads, latent_dim) of the cache's dtype */
+  const void* q_rope;   /* (num_tokens, num_heads, rope_dim); ignored if rope_dim is 0 */
+  const int32_t* block_table;     /* (num_seqs, pages_per_seq) */
+  const int32_t* seq_lens;        /* (num_seqs), up to 2^30 */
+  const int32_t* query_start_loc; /* (num_seqs + 1); ignored by the update */
+  void* out;                      /* (num_tokens, num_heads, latent_dim), contiguous */
+  int64_t num_tokens, num_seqs, num_heads;
+  int64_t ql_stride0, ql_stride1, qr_stride0, qr_stride1;
+  int64_t table_stride, pages_per_seq;
+  double scale;
+} kdaconv_latent_args;
+
+/*
+ * Bytes of device scratch memory of a call of these sizes: up to 67 MB, 17 MB where sequences
+ * have up to 16 rows (tokens times heads) on average. It holds no state between calls; calls that
+ * may run at the same time need scratch memories of their own. Aligned to 256 bytes.
+ */
+int64_t kdaconv_latent_attention_workspace(int64_t num_tokens, int64_t num_seqs, int64_t num_heads,
+                                           int64_t latent_dim);
+
+/*
+ * New tokens of any number per sequence. The work is split by the lengths on the device: the
+ * launch depends on host sizes alone, and a call can be captured in a graph. num_tokens,
+ * num_seqs or num_heads of 0: KDACONV_OK with no launch. num_tokens * num_heads is below 2^29
+ * (else EUNSUPPORTED).
+ */
+int kdaconv_latent_attention(const kdaconv_latent_args* args, void* workspace,
+                             int64_t workspace_bytes, kdaconv_stream_t stream);
+
+/* One token per sequence (decode): row s belongs to sequence s, num_seqs equals num_tokens (else
+ * EINVAL); query_start_loc is not read. */
+int kdaconv_latent_attention_update(const kdaconv_latent_args* args, void* workspace,
+                                    int64_t workspace_bytes, kdaconv_stream_t stream);
+
+/* The status either call would return before launching (update != 0: the update's). No HIP
+ * call; device pointers are only compared with NULL and tested for alignment. */
+int kdaconv_latent_attention_validate(const kdaconv_latent_args* args, int update,
+                                      const void* workspace, int64_t workspace_bytes);
+
 /* Static English text for a status code. Never NULL. */
 const char* kdaconv_status_string(int status);
 

@@ -19,6 +19,8 @@ RULE_ARGS = struct.Struct("=12Q21q3d6i")
 
 #: kdaconv_latent_cache: 3 pointers, 10 integers, 2 32-bit integers, no padding.
 LATENT_CACHE = struct.Struct("=3Q10q2i")
+#: kdaconv_latent_args after its cache: 6 pointers, 9 integers, 1 double.
+LATENT_ARGS = struct.Struct("=6Q9qd")
 
 # Every entry point include/kdaconv.h declares.
 EXPORTS = (
@@ -36,6 +38,10 @@ EXPORTS = (
     "kdaconv_rotary_embedding",
     "kdaconv_latent_cache_write",
     "kdaconv_latent_cache_read",
+    "kdaconv_latent_attention",
+    "kdaconv_latent_attention_update",
+    "kdaconv_latent_attention_validate",
+    "kdaconv_latent_attention_workspace",
     "kdaconv_status_string",
     "kdaconv_version",
 )
@@ -130,6 +136,13 @@ def load() -> ctypes.CDLL:
         vp, i64, i64, vp, vp,  # kv_start_loc, num_seqs, num_tokens, out, stream
     ]
     lib.kdaconv_latent_cache_read.restype = i32
+    for name in ("kdaconv_latent_attention", "kdaconv_latent_attention_update"):
+        getattr(lib, name).argtypes = [packed, vp, i64, vp]
+        getattr(lib, name).restype = i32
+    lib.kdaconv_latent_attention_validate.argtypes = [packed, i32, vp, i64]
+    lib.kdaconv_latent_attention_validate.restype = i32
+    lib.kdaconv_latent_attention_workspace.argtypes = [i64, i64, i64, i64]
+    lib.kdaconv_latent_attention_workspace.restype = i64
     lib.kdaconv_status_string.argtypes = [i32]
     lib.kdaconv_status_string.restype = ctypes.c_char_p
     lib.kdaconv_version.argtypes = []

@@ -22,6 +22,11 @@ SOURCES = [PKG / "csrc" / name for name in (
     "delta_rule_f32.hip",
     "norms.hip",
     "latent_cache.hip",
+    "latent_attention.hip",
+    "latent_attention_bf16_256.hip",
+    "latent_attention_bf16_512.hip",
+    "latent_attention_f16_256.hip",
+    "latent_attention_f16_512.hip",
 )]
 HEADERS = [ROOT / "include" / "kdaconv.h", *sorted((PKG / "csrc").glob("*.h"))]
 LIBRARY = PKG / "libkdaconv.so"
@@ -40,6 +45,9 @@ FLAGS = [
     "-fno-gpu-flush-denormals-to-zero",
     "-Wall",
 ]
+# Attention's matrix products write ordinary registers: sums that are rescaled now and then
+# would be moved to the accumulation registers and back.
+ATTENTION_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
 
 
 def hipcc() -> str:
@@ -53,7 +61,8 @@ def build(output: pathlib.Path = LIBRARY, extra_flags=()) -> pathlib.Path:
         objects = [pathlib.Path(work) / (src.stem + ".o") for src in SOURCES]
 
         def compile_one(src, obj):
-            subprocess.run([hipcc(), *FLAGS, *extra_flags, "-I", str(ROOT / "include"), "-c",
+            own = ATTENTION_FLAGS if "_attention" in src.stem else []
+            subprocess.run([hipcc(), *FLAGS, *own, *extra_flags, "-I", str(ROOT / "include"), "-c",
                             "-o", str(obj), str(src)], check=True)
 
         with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as pool:

@@ -1,0 +1,54 @@
+// Absorbed latent attention over the paged cache: parameters, and how a call is split.
+#ifndef KDACONV_LATENT_ATTENTION_H_
+#define KDACONV_LATENT_ATTENTION_H_
+
+#include "latent.h"
+
+namespace kdaconv {
+
+struct AttendParams {
+  CacheView C;
+  PageTable T;
+  const char* ql;
+  const char* qr;
+  char* out;  // (tokens, heads, latent), contiguous
+  const int32_t* seq_lens;
+  const int32_t* qsl;  // null: sequence s owns row s
+  float* partial;  // per slot kRows x latent sums, see Partial
+  int32_t* pieces;  // per worker: a split block's sequence, number and pieces
+  int64_t ql_ts, ql_hs, qr_ts, qr_hs;  // bytes
+  int32_t tokens, seqs, workers;
+  Divider heads;
+  float scale;  // times log2(e)
+};
+
+// A call's work is a line of units: for every sequence, for every block of its rows (a row is a
+// head of a token), kBlockUnits for the block itself and one for each tile of keys. The workers
+// (workgroups, one per CU) take equal parts of the line. They work it out for themselves from
+// the lengths on the device, so that a captured call serves any lengths.
+constexpr int kBlockUnits = 2;
+// A part is no shorter than this (unless the line is).
+constexpr int kLeastUnits = 4;
+constexpr int kWorkers = 256;
+
+constexpr int kTileKeys = 32;  // keys that a wave takes at a time
+constexpr int kAttendWaves = 4;
+constexpr int kMostKeys = 1 << 30;  // of a sequence
+
+// A block that several workers share leaves each one's sums in scratch memory, two slots a
+// worker: slot 2 w of the part that ends a block, 2 w + 1 of one that does not.
+struct Partial {
+  int rows, latent;
+  __host__ __device__ constexpr int64_t floats() const { return (int64_t)rows * (latent + 2); }
+  // Sums, then each row's exponent and weight.
+  __host__ __device__ constexpr int64_t exponent() const { return (int64_t)rows * latent; }
+  __host__ __device__ constexpr int64_t weight() const { return (int64_t)rows * (latent + 1); }
+};
+
+// kQ: blocks of 16 rows per workgroup, 1, 2 or 4.
+template <int kF, int kLatent, int kQ, bool kE4m3>
+void launch_attend(const AttendParams& P, hipStream_t st);
+
+}  // namespace kdaconv
+
+#endif  // KDACONV_LATENT_ATTENTION_H_

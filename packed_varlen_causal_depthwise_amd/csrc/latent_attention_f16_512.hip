@@ -1,0 +1,13 @@
+// Absorbed latent attention for f16 queries and latents of up to 512 channels.
+#include "latent_attention_device.h"
+
+namespace kdaconv {
+
+template void launch_attend<kRuleF16, 512, 1, false>(const AttendParams&, hipStream_t);
+template void launch_attend<kRuleF16, 512, 1, true>(const AttendParams&, hipStream_t);
+template void launch_attend<kRuleF16, 512, 2, false>(const AttendParams&, hipStream_t);
+template void launch_attend<kRuleF16, 512, 2, true>(const AttendParams&, hipStream_t);
+template void launch_attend<kRuleF16, 512, 4, false>(const AttendParams&, hipStream_t);
+template void launch_attend<kRuleF16, 512, 4, true>(const AttendParams&, hipStream_t);
+
+}  // namespace kdaconv

@@ -178,3 +178,121 @@ def latent_cache_read(
                kv_start_loc.data_ptr(), seqs, shape[0], out.data_ptr())
     _lib.check(rc, "latent_cache_read")
     return out
+
+
+def _attend(q_latent, q_rope, latents, ropes, scales, block_table, seq_lens, query_start_loc, scale, out):
+    """Checks, then kdaconv_latent_args as bytes, the output and the call's sizes."""
+    cache, dim, rope_dim, dtype, device = _cache(latents, ropes, scales)
+    if (q_latent.dim() != 3 or q_latent.shape[2] != dim
+            or q_rope.shape != (q_latent.shape[0], q_latent.shape[1], rope_dim)):
+        raise ValueError("q_latent must be (tokens, heads, latent_dim) and q_rope (tokens, heads, rope_dim)")
+    tokens, heads, _ = q_latent.shape
+    if q_latent.dtype != dtype or q_rope.dtype != dtype:
+        raise ValueError(f"q_latent and q_rope must have the dtype of ropes, {dtype}")
+    ls, rs = q_latent.stride(), q_rope.stride()
+    if dim > 1 and ls[2] != 1 or rope_dim > 1 and rs[2] != 1:
+        raise ValueError("the last axis of q_latent and q_rope must be contiguous")
+    seqs = tokens
+    if query_start_loc is not None:
+        seqs = max(0, _loc(query_start_loc, device, "query_start_loc"))
+    if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or seq_lens.shape[0] < seqs or (
+            seqs > 1 and seq_lens.stride()[0] != 1):
+        raise ValueError("seq_lens must be a contiguous 1-D int32 tensor with one entry per sequence")
+    table = _table(block_table, seqs, device)
+    if q_latent.get_device() != device or q_rope.get_device() != device or seq_lens.get_device() != device:
+        raise ValueError("all tensors must be on the device of latents")
+    if out is None:
+        out = torch.empty((tokens, heads, dim), dtype=dtype, device=q_latent.device)
+    elif (out.shape != q_latent.shape or out.dtype != dtype or not out.is_contiguous()
+          or out.get_device() != device):
+        raise ValueError(f"out must be a contiguous {dtype} tensor of shape {tuple(q_latent.shape)} on "
+                         f"{latents.device}")
+    args = cache + _lib.LATENT_ARGS.pack(
+        q_latent.data_ptr(), q_rope.data_ptr(), table[0], seq_lens.data_ptr(),
+        0 if query_start_loc is None else query_start_loc.data_ptr(), out.data_ptr(),
+        tokens, seqs, heads, ls[0], ls[1], rs[0], rs[1], table[1], table[2], float(scale))
+    return args, out, device, (tokens, seqs, heads, dim)
+
+
+def _run(name, args, out, device, sizes):
+    if 0 in sizes:
+        return out
+    if device < 0:
+        raise ValueError("latents must be a GPU tensor")
+    lib = _lib.load()
+    # Memory of the current stream: the allocator hands it out again only to work that is
+    # queued behind this call.
+    need = lib.kdaconv_latent_attention_workspace(*sizes)
+    scratch = torch.empty(need, dtype=torch.uint8, device=out.device)
+    rc = _call(device, getattr(lib, "kdaconv_" + name), args, scratch.data_ptr(), need)
+    _lib.check(rc, name)
+    return out
+
+
+def latent_attention_fn(
+    q_latent: torch.Tensor,
+    q_rope: torch.Tensor,
+    latents: torch.Tensor,
+    ropes: torch.Tensor,
+    scales: Optional[torch.Tensor],
+    block_table: torch.Tensor,
+    seq_lens: torch.Tensor,
+    query_start_loc: torch.Tensor,
+    *,
+    scale: float,
+    out: Optional[torch.Tensor] = None,
+) -> torch.Tensor:
+    """Attention of packed new tokens over the paged latent cache, in the absorbed form.
+
+    For every head of token i of the n new tokens of a sequence, over the sequence's tokens t <
+    seq_lens - n + i + 1 (the new ones are in the cache already)::
+
+        s_t = scale * (q_latent . latent_t + q_rope . rope_t)
+        out = sum_t softmax(s)_t latent_t
+
+    q_latent (tokens, heads, latent_dim) is the query times the latents' up-projection for the
+    keys, q_rope (tokens, heads, rope_dim) its turned part, both of ropes' dtype with a contiguous
+    last axis (any token and head strides); the result (tokens, heads, latent_dim) is still to be
+    multiplied by the up-projection for the values. ``scale`` is that of the unabsorbed heads,
+    (key channels + rope_dim) ** -0.5.
+
+    latents, ropes and scales are the cache of ``latent_cache_write``, block_table (sequences,
+    pages per sequence) int32 its pages, seq_lens (sequences,) int32 the tokens of each sequence
+    in it, the new ones included, and query_start_loc (sequences + 1,) int32 the rows of each. A
+    token whose page is outside the cache is not there; a row that sees no token is zero; rows no
+    sequence owns are left unwritten. Scores, softmax and sums are FP32, the weights rounded to
+    the dtype for the second product, the result rounded once. Takes up to 67 MB of scratch memory
+    from torch's allocator. Queued on the current stream; no synchronisation.
+    """
+    return _run("latent_attention", *_attend(q_latent, q_rope, latents, ropes, scales, block_table,
+                                             seq_lens, query_start_loc, scale, out))
+
+
+def latent_attention_update(
+    q_latent: torch.Tensor,
+    q_rope: torch.Tensor,
+    latents: torch.Tensor,
+    ropes: torch.Tensor,
+    scales: Optional[torch.Tensor],
+    block_table: torch.Tensor,
+    seq_lens: torch.Tensor,
+    *,
+    scale: float,
+    out: Optional[torch.Tensor] = None,
+) -> torch.Tensor:
+    """Decode step of ``latent_attention_fn``: row b of q_latent and q_rope is the one new token
+    of sequence b, which sees all seq_lens[b] tokens. Arguments and result as there."""
+    return _run("latent_attention_update", *_attend(q_latent, q_rope, latents, ropes, scales,
+                                                    block_table, seq_lens, None, scale, out))
+
+
+def latent_attention_supported(q_latent: torch.Tensor, q_rope: torch.Tensor, latents: torch.Tensor,
+                               ropes: torch.Tensor, scales: Optional[torch.Tensor] = None) -> bool:
+    """Whether latent_attention_fn and latent_attention_update serve these tensors."""
+    try:
+        one = torch.empty(max(1, q_latent.shape[0]), 1, dtype=torch.int32, device=latents.device)
+        args, _, device, sizes = _attend(q_latent, q_rope, latents, ropes, scales, one, one[:, 0], None, 1.0, None)
+        lib = _lib.load()
+    except (ValueError, _lib.LibraryMissing):
+        return False
+    return device >= 0 and lib.kdaconv_latent_attention_validate(args, 1, 256, 1 << 62) == _lib.OK
