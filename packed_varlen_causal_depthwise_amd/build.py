@@ -45,9 +45,6 @@ FLAGS = [
     "-fno-gpu-flush-denormals-to-zero",
     "-Wall",
 ]
-# Attention's matrix products write ordinary registers: sums that are rescaled now and then
-# would be moved to the accumulation registers and back.
-ATTENTION_FLAGS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
 
 
 def hipcc() -> str:
@@ -61,8 +58,7 @@ def build(output: pathlib.Path = LIBRARY, extra_flags=()) -> pathlib.Path:
         objects = [pathlib.Path(work) / (src.stem + ".o") for src in SOURCES]
 
         def compile_one(src, obj):
-            own = ATTENTION_FLAGS if "_attention" in src.stem else []
-            subprocess.run([hipcc(), *FLAGS, *own, *extra_flags, "-I", str(ROOT / "include"), "-c",
+            subprocess.run([hipcc(), *FLAGS, *extra_flags, "-I", str(ROOT / "include"), "-c",
                             "-o", str(obj), str(src)], check=True)
 
         with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as pool:

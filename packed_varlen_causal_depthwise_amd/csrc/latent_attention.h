@@ -6,6 +6,12 @@
 
 namespace kdaconv {
 
+// A block of rows that several workers share: the first of them and their number (0: none),
+// and which block of which sequence.
+struct Shared {
+  int32_t first, count, s, b;
+};
+
 struct AttendParams {
   CacheView C;
   PageTable T;
@@ -15,24 +21,31 @@ struct AttendParams {
   const int32_t* seq_lens;
   const int32_t* qsl;  // null: sequence s owns row s
   float* partial;  // per slot kRows x latent sums, see Partial
-  int32_t* pieces;  // per worker: a split block's sequence, number and pieces
+  Shared* shared;  // per worker: the block that its part begins inside, and the one it ends inside
   int64_t ql_ts, ql_hs, qr_ts, qr_hs;  // bytes
   int32_t tokens, seqs, workers;
+  int32_t most_keys;  // the table's width in keys, up to kMostKeys
+  int32_t shift;
   Divider heads;
   float scale;  // times log2(e)
 };
 
 // A call's work is a line of units: for every sequence, for every block of its rows (a row is a
-// head of a token), kBlockUnits for the block itself and one for each tile of keys. The workers
-// (workgroups, one per CU) take equal parts of the line. They work it out for themselves from
-// the lengths on the device, so that a captured call serves any lengths.
+// head of a token), kBlockUnits for the block itself and one for each step of keys (2^shift
+// steps, which keeps the line below 2^31 units). The workers (workgroups, one per CU) take equal
+// parts of the line. They work it out for themselves from the lengths on the device, so that a
+// captured call serves any lengths.
 constexpr int kBlockUnits = 2;
 // A part is no shorter than this (unless the line is).
-constexpr int kLeastUnits = 4;
+constexpr int kLeastUnits = 3;
 constexpr int kWorkers = 256;
 
-constexpr int kTileKeys = 32;  // keys that a wave takes at a time
-constexpr int kAttendWaves = 4;
+constexpr int kAttendWaves = 8;
+// Blocks of 16 rows per workgroup, and how it takes keys: a step's keys lie in LDS while
+// kRing - 1 more steps are under way. Few rows leave memory the time that products need not:
+// short steps, many under way. More rows share longer steps.
+constexpr int step_keys(int blocks) { return blocks == 4 ? 64 : 32; }
+constexpr int ring_steps(int blocks) { return blocks == 4 ? 2 : 4; }  // powers of 2 up to 4
 constexpr int kMostKeys = 1 << 30;  // of a sequence
 
 // A block that several workers share leaves each one's sums in scratch memory, two slots a

@@ -7,7 +7,7 @@
 namespace kdaconv {
 namespace {
 
-constexpr int64_t kPiecesBytes = kWorkers * 16;
+constexpr int64_t kSharedBytes = kWorkers * 2 * sizeof(Shared);
 
 bool aligned_to(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
@@ -82,8 +82,8 @@ int attend(const kdaconv_latent_args* a, bool update, void* workspace, int64_t w
   P.out = static_cast<char*>(a->out);
   P.seq_lens = a->seq_lens;
   P.qsl = update ? nullptr : a->query_start_loc;
-  P.pieces = static_cast<int32_t*>(workspace);
-  P.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kPiecesBytes);
+  P.shared = static_cast<Shared*>(workspace);
+  P.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kSharedBytes);
   const int64_t tokens = a->num_tokens > 1, heads = a->num_heads > 1;
   P.ql_ts = a->ql_stride0 * 2 * tokens;
   P.ql_hs = a->ql_stride1 * 2 * heads;
@@ -92,9 +92,14 @@ int attend(const kdaconv_latent_args* a, bool update, void* workspace, int64_t w
   P.tokens = (int32_t)a->num_tokens;
   P.seqs = (int32_t)a->num_seqs;
   P.workers = kWorkers;
+  P.most_keys = (int32_t)std::min<int64_t>(kMostKeys, a->pages_per_seq * a->cache.page_size);
   P.heads = divider_of((uint32_t)a->num_heads);
   P.scale = (float)(a->scale * 1.4426950408889634074);
   const int blocks = blocks_of(a->num_tokens, a->num_seqs, a->num_heads);
+  // What all sequences together can have at most: rows fill at most that many blocks.
+  const int64_t most_blocks = a->num_tokens * a->num_heads / (16 * blocks) + std::min(a->num_tokens, a->num_seqs);
+  P.shift = 0;
+  while (most_blocks * ((P.most_keys >> P.shift) / step_keys(blocks) + 1 + kBlockUnits) > INT32_MAX) ++P.shift;
   if (a->cache.dtype == KDACONV_BF16)
     launch<KDACONV_BF16>(P, (int)a->cache.latent_dim, blocks, a->cache.e4m3 != 0, st);
   else
@@ -111,7 +116,7 @@ extern "C" int64_t kdaconv_latent_attention_workspace(int64_t num_tokens, int64_
                                                       int64_t latent_dim) {
   if (num_tokens <= 0 || num_seqs <= 0 || num_heads <= 0 || latent_dim <= 0) return 0;
   const Partial part{16 * blocks_of(num_tokens, num_seqs, num_heads), (int)latent_dim};
-  return kPiecesBytes + 2 * kWorkers * part.floats() * (int64_t)sizeof(float);
+  return kSharedBytes + 2 * kWorkers * part.floats() * (int64_t)sizeof(float);
 }
 
 extern "C" int kdaconv_latent_attention_validate(const kdaconv_latent_args* args, int update, const void* workspace,

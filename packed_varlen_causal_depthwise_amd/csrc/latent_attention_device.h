@@ -4,12 +4,15 @@
 //     s_t = scale (ql . c_t + qr . r_t),  out = sum_t softmax(s)_t c_t
 // so a token's latent is key and value at once: it goes to LDS once and is read there twice.
 //
-// Products are taken transposed, S^T = K Q^T and O^T = C^T P^T. A matrix product leaves a lane
-// with one column, here one query: its softmax needs no other lane but for the largest score,
-// and the scores are in place as the second product's right operand. (Of 32 keys lane group g
-// holds 4 g .. 4 g + 3 and 16 + 4 g .. ; the left operand takes its keys in that order.) That
-// operand is C transposed, which LDS delivers: ds_read_b64_tr_b16 hands 16 lanes the columns of
-// 4 rows of 16.
+// A workgroup of 8 waves holds kQ blocks of 16 rows and takes the keys in steps. For the scores
+// a wave takes one block's products with 16 or 32 keys over all channels, for the sums all
+// blocks' with its own 64 columns (of 512): between the two the weights go through LDS. So
+// no wave holds more than 64 sums and 72 registers of queries, columns are read once, and two
+// waves share each SIMD.
+//
+// Products are taken transposed, S^T = K Q^T and O^T = C^T P^T: a lane then has one query, whose
+// largest score and rescaling concern no other lane. The left operand C^T is delivered by
+// LDS: ds_read_b64_tr_b16 hands 16 lanes the columns of 4 rows of 16.
 #ifndef KDACONV_LATENT_ATTENTION_DEVICE_H_
 #define KDACONV_LATENT_ATTENTION_DEVICE_H_
 
@@ -43,52 +46,42 @@ __device__ __forceinline__ u32x2 lds_read_columns(const lds_char* p) {
       (__attribute__((address_space(3))) s16x4*)const_cast<lds_char*>(p)));
 }
 
-// 16 bytes per lane from memory to LDS, at the wave's place + 16 times the lane's number.
+// 16 bytes per lane from memory to LDS, at the wave's place + 16 times the lane's number. Not the
+// builtin: the compiler would wait for all such loads before any LDS read that follows. Who
+// reads the bytes waits for them (s_waitcnt vmcnt), and for the barrier if another wave loads.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // m0 is reserved: the compiler sets it before each use
 __device__ __forceinline__ void to_lds16(const char* from, lds_char* wave_to) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
-                                   (__attribute__((address_space(3))) void*)wave_to, 16, 0, 0);
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               :: "v"(from), "s"((uint32_t)(uintptr_t)wave_to) : "memory", "m0");
+}
+// The same at `offset` bytes from an address that all lanes share.
+__device__ __forceinline__ void to_lds16(const char* base, uint32_t offset, lds_char* wave_to) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(offset), "s"(base), "s"((uint32_t)(uintptr_t)wave_to) : "memory", "m0");
+}
+
+#pragma clang diagnostic pop
+
+// A barrier for LDS alone: __syncthreads() would also wait for the loads under way.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Pairs of elements with 0 in the place of infinities and NaN.
+template <int kF>
+__device__ __forceinline__ u32x4 finite_pairs(u32x4 x) {
+  constexpr uint32_t kHigh = kF == kRuleBF16 ? 0x7F800000u : 0x7C000000u, kLow = kHigh >> 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((x[i] & kHigh) == kHigh) x[i] &= 0xFFFFu;
+    if ((x[i] & kLow) == kLow) x[i] &= 0xFFFF0000u;
+  }
+  return x;
 }
 
 // Hides that x is the same in every iteration of a loop. Without it the compiler works out
 // all rows' offsets before the loop, and spills them.
 __device__ __forceinline__ uint32_t fresh(uint32_t x) {
   asm volatile("" : "+v"(x));
-  return x;
-}
-
-// Scheduling of n products and the LDS reads of one operand each (of two halves each): some
-// reads ahead, then one for each product. Left alone the compiler waits for every read.
-template <int kN, int kAhead = 8>
-__device__ __forceinline__ void interleave() {
-  __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
-#pragma unroll
-  for (int i = 0; i < kN - kAhead; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-  }
-  __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
-}
-
-template <int kN, int kAhead = 6>
-__device__ __forceinline__ void interleave_pairs() {
-  __builtin_amdgcn_sched_group_barrier(0x100, 2 * kAhead, 0);
-#pragma unroll
-  for (int i = 0; i < kN - kAhead; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-  }
-  __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
-}
-
-// Pairs of elements with 0 in the place of infinities and NaN.
-template <int kF>
-__device__ __forceinline__ u32x2 finite_pairs(u32x2 x) {
-  constexpr uint32_t kHigh = kF == kRuleBF16 ? 0x7F800000u : 0x7C000000u, kLow = kHigh >> 16;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if ((x[i] & kHigh) == kHigh) x[i] &= 0xFFFFu;
-    if ((x[i] & kLow) == kLow) x[i] &= 0xFFFF0000u;
-  }
   return x;
 }
 
@@ -101,7 +94,7 @@ struct Place {
   __device__ bool before(const Place& o) const { return s < o.s || (s == o.s && (b < o.b || (b == o.b && t < o.t))); }
 };
 
-template <int kRows, int kIter>
+template <int kRows, int kKeys>
 struct Line {
   // The rows, keys and units of a sequence. Offsets out of order or out of range give a
   // sequence without rows.
@@ -116,137 +109,161 @@ struct Line {
     start = a;
     return b - a;
   }
-  static __device__ __forceinline__ int keys(const AttendParams& P, int s) {
-    int64_t most = (int64_t)P.T.width * P.C.page_size.d;
-    most = most < kMostKeys ? most : kMostKeys;
-    const int n = P.seq_lens[s];
-    return n < 0 ? 0 : (n > most ? (int)most : n);
+  static __device__ __forceinline__ int keys(const AttendParams& P, int n) {
+    return n < 0 ? 0 : (n > P.most_keys ? P.most_keys : n);
   }
+  // (Rows are below 2^29 and keys up to 2^30.)
   static __device__ __forceinline__ int blocks(const AttendParams& P, int tokens) {
-    return (int)(((int64_t)tokens * P.heads.d + kRows - 1) / kRows);
+    return (tokens * (int)P.heads.d + kRows - 1) / kRows;
   }
-  static __device__ __forceinline__ int tiles(int keys) { return (int)(((int64_t)keys + kIter - 1) / kIter); }
-  static __device__ __forceinline__ int64_t units(const AttendParams& P, int s) {
-    int start;
-    const int n = tokens(P, s, start);
-    return n > 0 ? (int64_t)blocks(P, n) * (tiles(keys(P, s)) + kBlockUnits) : 0;
+  static __device__ __forceinline__ int tiles(const AttendParams& P, int keys) {
+    const int steps = (int)((uint32_t)(keys + kKeys - 1) / kKeys);
+    return (steps + (1 << P.shift) - 1) >> P.shift;
   }
 };
 
+// Equal parts of a line of `total` units: the first `rest` are one longer than the others.
+struct Parts {
+  int count, each, rest;
+  __device__ __forceinline__ Parts(int total, int most) {
+    count = total < most * kLeastUnits ? total / kLeastUnits : most;
+    count = count < 1 ? 1 : count;
+    each = (int)((uint32_t)total / (uint32_t)count);
+    rest = total - each * count;
+  }
+  __device__ __forceinline__ int begin(int i) const { return each * i + (i < rest ? i : rest); }
+};
+
+// Sum of the lanes up to each, in the vector unit.
+__device__ __forceinline__ int running_sum(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // 1, 2, 4 and 8 lanes down a row of 16
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // a row's last to the next, to rows 1 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);  // lane 31 to rows 2 and 3
+  return x;
+}
+
 // Finds this worker's part of the line. All threads of the workgroup call it; `room` is LDS of
-// 128 bytes. Returns the number of workers that have a part.
-template <int kRows, int kIter>
-__device__ __forceinline__ int find_part(const AttendParams& P, char* room, Place& from, Place& to, int64_t& all) {
-  using L = Line<kRows, kIter>;
-  int64_t* const sums = (int64_t*)room;  // per wave
-  int* const found = (int*)(room + 64);  // from, to
+// 96 bytes.
+template <int kRows, int kKeys>
+__device__ __forceinline__ Parts find_part(const AttendParams& P, char* room, Place& from, Place& to) {
+  using L = Line<kRows, kKeys>;
+  int* const sums = (int*)room;  // per wave, of the first sequences
+  int* const rests = sums + kAttendWaves;  // of the others
+  int* const found = rests + kAttendWaves;  // from, to
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
   constexpr int kThreads = 64 * kAttendWaves;
-  int64_t mine = 0;
-  for (int s = tid; s < P.seqs; s += kThreads) mine += L::units(P, s);
-  mine = lane_sum<64>(mine);
-  if (lane == 0) sums[wave] = mine;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int i = 0; i < kAttendWaves; ++i) total += sums[i];
-  all = total;
-  int64_t workers = total / kLeastUnits;
-  workers = workers < 1 ? 1 : (workers > P.workers ? P.workers : workers);
-  const int w = blockIdx.x;
-  if (w >= workers || total == 0) return (int)workers;
-  const int64_t lo = total * w / workers, hi = total * (w + 1) / workers;
+  int per = 0;  // units of a block
+  const auto units = [&](int s) {
+    if (s >= P.seqs) return 0;
+    int start;
+    const int n = L::tokens(P, s, start);
+    per = L::tiles(P, L::keys(P, P.seq_lens[s])) + kBlockUnits;
+    return L::blocks(P, n) * per;
+  };
+  int u = units(tid), run = running_sum(u);
+  if (lane == 63) sums[wave] = run;
+  const bool many = P.seqs > kThreads;
+  if (many) {
+    const int mine = per;
+    int rest = 0;
+    for (int s = tid + kThreads; s < P.seqs; s += kThreads) rest += units(s);
+    rest = running_sum(rest);
+    if (lane == 63) rests[wave] = rest;
+    per = mine;
+  } else if (lane == 63) {
+    rests[wave] = 0;
+  }
   if (tid < 6) found[tid] = tid % 3 == 0 ? P.seqs : 0;
-  int64_t before = 0;
-  for (int base = 0; base < P.seqs && before <= hi; base += kThreads) {
-    const int s = base + tid;
-    const int64_t u = s < P.seqs ? L::units(P, s) : 0;
-    int64_t run = u;  // inclusive running sum
+  __syncthreads();
+  int first = 0, next = 0, total = 0;  // units before this thread's sequence, before the next thread 0's
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int64_t other = __shfl_up(run, d);
-      run += lane >= d ? other : 0;
-    }
-    __syncthreads();
-    if (lane == 63) sums[wave] = run;
-    __syncthreads();
-    int64_t first = before, chunk = 0;
-#pragma unroll
-    for (int i = 0; i < kAttendWaves; ++i) {
-      if (i < wave) first += sums[i];
-      chunk += sums[i];
-    }
+  for (int i = 0; i < kAttendWaves; ++i) {
+    if (i < wave) first += sums[i];
+    next += sums[i];
+    total += rests[i];
+  }
+  total += next;
+  const Parts parts(total, P.workers);
+  const int w = blockIdx.x, lo = parts.begin(w), hi = parts.begin(w + 1);
+  for (int s = tid;;) {
     first += run - u;
-#pragma unroll
+#pragma unroll 1
     for (int e = 0; e < 2; ++e) {
-      const int64_t at = e == 0 ? lo : hi;
-      if (at >= first && at < first + u) {
-        const int tiles = L::tiles(L::keys(P, s)), per = tiles + kBlockUnits;
-        const int64_t off = at - first;
-        const int b = (int)(off / per), r = (int)(off - (int64_t)b * per);
+      const int off = (e == 0 ? lo : hi) - first;
+      if (off >= 0 && off < u) {
+        const int b = (int)((uint32_t)off / (uint32_t)per), r = off - b * per;
         found[3 * e] = s;
         found[3 * e + 1] = b;
         found[3 * e + 2] = r > kBlockUnits ? r - kBlockUnits : 0;
       }
     }
-    before += chunk;
+    __syncthreads();
+    s += kThreads;
+    if (s - tid >= P.seqs || next > hi) break;
+    u = units(s);
+    run = running_sum(u);
+    if (lane == 63) sums[wave] = run;
+    __syncthreads();
+    first = next;
+#pragma unroll
+    for (int i = 0; i < kAttendWaves; ++i) {
+      if (i < wave) first += sums[i];
+      next += sums[i];
+    }
   }
-  __syncthreads();
   from = Place{uniform(found[0]), uniform(found[1]), uniform(found[2])};
   to = Place{uniform(found[3]), uniform(found[4]), uniform(found[5])};
-  __syncthreads();
-  return (int)workers;
+  if (w >= parts.count) to = from;
+  return parts;
 }
 
-// LDS of one tile: 32 latents, then 32 rotated parts, rows of 16-byte chunks. Chunk c of row r
-// lies at place c ^ f(r) of its row, with f such that neither 16 rows' chunk c (the products'
-// left operand) nor chunks 2 i, 2 i + 1 of 8 rows (columns) share a bank.
-template <int kLatent>
+// LDS of a step's keys: their latents, then their rotated parts, rows of 16-byte chunks. Chunk
+// c of row r lies at place c ^ f(r) of its row, with f such that neither 16 rows' chunk c (the
+// scores' left operand) nor chunks 2 i, 2 i + 1 of rows 0 to 3 and 8 to 11, or 4 to 7 and 12 to 15
+// (columns), share a bank.
+template <int kLatent, int kKeys>
 struct Tile {
   static constexpr int kRow = kLatent * 2, kRope = kRopeMax * 2;
-  static constexpr int kRopes = kTileKeys * kRow;
-  static constexpr int kBytes = kRopes + kTileKeys * kRope;
-  static __device__ __forceinline__ int latent_flip(int row) { return ((row & 7) << 1) | ((row >> 3) & 1); }
+  static constexpr int kRopes = kKeys * kRow;
+  static constexpr int kBytes = kRopes + kKeys * kRope;
+  static __device__ __forceinline__ int latent_flip(int row) {
+    return ((row & 3) << 1) | ((row >> 3 & 1) << 3) | (row >> 2 & 1);
+  }
   static __device__ __forceinline__ int rope_flip(int row) { return (row >> 1) & 7; }
 };
 
-// One tile on its way: keys' addresses, and for 8 bits the codes in registers.
-template <int kF, int kLatent, int kQ, bool kE4m3>
-struct Loader {
-  using T = Tile<kLatent>;
-  static constexpr int kChunks = kLatent / 8;  // 16-byte chunks of 16-bit elements per row
-  static constexpr int kLatentLoads = kE4m3 ? kTileKeys * (kLatent / 16) / 64 / kQ : kTileKeys * kChunks / 64 / kQ;
-  static constexpr int kRopeLoads = kTileKeys / 8 / kQ;  // 8 rows each
-  static constexpr int kScaleLoads = kE4m3 ? kLatentLoads : 1;
-
-  int window = -1;  // page of number window_at + lane of the sequence
-  int window_at = 0, window_of = -1;  // the sequence
-  const char* lat;  // of key `lane % 32`; zeros where there is none
+// Where 64 keys lie: lane i has key i.
+template <bool kE4m3>
+struct Keys {
+  int window = -1;  // page of number window_at + lane of sequence window_of
+  int window_at = 0, window_of = -1;
+  const char* lat;  // zeros where there is no key
   const char* rop;
   const uint8_t* sc;
-  uint32_t mask;  // keys that are there
-
-  u32x4 codes[kE4m3 ? kLatentLoads : 1];
-  uint32_t scales[kScaleLoads];
-  u32x4 ropes[kE4m3 ? kRopeLoads : 1];
+  uint64_t mask;  // keys that are there
 
   // Finds the keys from `first` on. The lanes hold a window of the page table: loads return in
-  // order, so an entry loaded for each tile would wait for all tiles under way.
+  // order, so an entry loaded for each step would wait for all steps under way.
   __device__ __forceinline__ void find(const AttendParams& P, int s, int first, int keys, int lane) {
     lane = (int)fresh(lane);
-    const int end = first + kTileKeys < keys ? first + kTileKeys : keys;
+    const int end = first + 64 < keys ? first + 64 : keys;
     const int low = (int)P.C.page_size((uint32_t)first);
-    if (window_of != s || (end > first && (int)P.C.page_size((uint32_t)(end - 1)) >= window_at + 64)) {
+    if (window_of != s || low < window_at || (end > first && (int)P.C.page_size((uint32_t)(end - 1)) >= window_at + 64)) {
       window_of = s;
       window_at = low;
       window = low + lane < P.T.width ? P.T.table[s * P.T.stride + low + lane] : -1;
+      // (Here and not at its use, which every step would wait for.)
+      asm volatile("s_waitcnt vmcnt(0)" : "+v"(window));
     }
-    const int key = first + lane % kTileKeys;
+    const int key = first + lane;
     const uint32_t p = P.C.page_size((uint32_t)key);
     const int at = key - (int)(p * P.C.page_size.d);
     const int page = __shfl(window, (int)p - window_at);
     const bool ok = key < keys && page >= 0 && page < P.C.num_pages;
-    mask = (uint32_t)__ballot(ok);
+    mask = __ballot(ok);
     lat = ok ? P.C.latents + page * P.C.lat_page + at * P.C.lat_slot : (const char*)kZeros;
     rop = ok ? P.C.ropes + page * P.C.rope_page + at * P.C.rope_slot : (const char*)kZeros;
     if constexpr (kE4m3) sc = ok ? P.C.scales + page * P.C.scale_page + at * P.C.scale_slot : (const uint8_t*)kZeros;
@@ -264,102 +281,104 @@ struct Loader {
     const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)a, row), hi = __builtin_amdgcn_readlane((uint32_t)(a >> 32), row);
     return (const char*)(((uint64_t)hi << 32) | lo);
   }
+};
 
-  // Sends the tile on its way: 16 bits straight to LDS, 8 bits to registers. `part` of the
-  // kQ waves that share it takes its rows.
-  __device__ __forceinline__ void issue(const AttendParams& P, lds_char* to, int part, int lane) {
+// A step from memory to LDS, 16 bits straight, by kLoaders waves in turn: a load takes one row's
+// latent of 512 channels or two of 256, or 8 rows' rotated parts.
+template <int kLatent, int kKeys, int kLoaders>
+struct Direct {
+  using T = Tile<kLatent, kKeys>;
+  static constexpr int kChunks = kLatent / 8, kPer = 64 / kChunks;  // chunks per row, rows per load
+  static constexpr int kLatents = kKeys / kPer, kAll = kLatents + kKeys / 8;  // loads
+  static constexpr int kTurns = (kAll + kLoaders - 1) / kLoaders;
+  static constexpr int kLeast = kLatents / kLoaders;  // of every wave, whatever the sizes
+
+  // `base`: the lane that has the step's first key.
+  static __device__ __forceinline__ void issue(const AttendParams& P, const Keys<false>& K, int base, lds_char* to,
+                                               int loader, int lane) {
     lane = (int)fresh(lane);
-    if constexpr (!kE4m3) {
-      constexpr int kPer = 64 / kChunks;  // rows per load
-      // Flips reach 16 chunks. Where a latent's end is at a multiple of them its lanes are told
-      // by their number alone: those past it read its first chunks (queries are zero there, and
-      // no output is taken).
-      if (P.C.latent % 128 == 0) {
-        const int c = lane % kChunks;
-        const uint32_t at = (c * 8 < P.C.latent ? c : c % 16) * 16;
+    // Flips reach 16 chunks. Where latents end at a multiple of them a lane is past the end by
+    // its number alone: it reads the first chunks (queries are zero there, and no sum is taken).
+    const bool even = P.C.latent % 128 == 0;
+    const int c = lane % kChunks;
+    const uint32_t at = (c * 8 < P.C.latent ? c : c % 16) * 16;
 #pragma unroll
-        for (int i = 0; i < kLatentLoads; ++i) {
-          const int first = (part * kLatentLoads + i) * kPer;
-          if constexpr (kPer == 1) {
-            to_lds16(row_uniform(lat, first) + (at ^ (T::latent_flip(first) * 16)), to + first * T::kRow);
-          } else {
-            const int row = first + lane / kChunks;
-            to_lds16(row_of(lat, row) + (at ^ (T::latent_flip(row) * 16)), to + first * T::kRow);
-          }
+    for (int j = 0; j < kTurns; ++j) {
+      const int i = loader + j * kLoaders;
+      if (i < kLatents) {
+        const int first = i * kPer, row = first + (kPer == 1 ? 0 : lane / kChunks);
+        const uint32_t flip = T::latent_flip(row);
+        if (even) {
+          if constexpr (kPer == 1)
+            to_lds16(K.row_uniform(K.lat, base + first), at ^ (flip * 16), to + first * T::kRow);
+          else
+            to_lds16(K.row_of(K.lat, base + row) + (at ^ (flip * 16)), to + first * T::kRow);
+        } else {
+          const char* const from = K.row_of(K.lat, base + row);
+          const int chunk = c ^ flip;
+          to_lds16(chunk * 8 < P.C.latent ? from + chunk * 16 : (const char*)kZeros, to + first * T::kRow);
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kLatentLoads; ++i) {
-          const int first = (part * kLatentLoads + i) * kPer, row = first + lane / kChunks;
-          const char* const base = row_of(lat, row);
-          const int c = (lane % kChunks) ^ T::latent_flip(row);
-          to_lds16(c * 8 < P.C.latent ? base + c * 16 : (const char*)kZeros, to + first * T::kRow);
-        }
-      }
-      if (P.C.rope > 0) {
-#pragma unroll
-        for (int i = 0; i < kRopeLoads; ++i) {
-          const int first = (part * kRopeLoads + i) * 8, row = first + lane / 8;
-          const char* const base = row_of(rop, row);
-          const int c = (lane % 8) ^ T::rope_flip(row);
-          to_lds16(c * 8 < P.C.rope ? base + c * 16 : (const char*)kZeros, to + T::kRopes + first * T::kRope);
-        }
-      }
-    } else {
-      constexpr int kCodes = kLatent / 16, kPer = 64 / kCodes;  // chunks of 16 codes per row, rows per load
-#pragma unroll
-      for (int i = 0; i < kLatentLoads; ++i) {
-        const int row = (part * kLatentLoads + i) * kPer + lane / kCodes, c = lane % kCodes;
-        const char* const base = row_of(lat, row);
-        const uint8_t* const scale = row_of(sc, row);
-        const bool in = c * 16 < P.C.latent;
-        codes[i] = *(const u32x4*)(in ? base + c * 16 : (const char*)kZeros);
-        scales[i] = in ? scale[c / 2] : 0;
-      }
-      if (P.C.rope > 0) {
-#pragma unroll
-        for (int i = 0; i < kRopeLoads; ++i) {
-          const int row = (part * kRopeLoads + i) * 8 + lane / 8, c = lane % 8;
-          const char* const base = row_of(rop, row);
-          ropes[i] = *(const u32x4*)(c * 8 < P.C.rope ? base + c * 16 : (const char*)kZeros);
-        }
+      } else if (i < kAll && P.C.rope > 0) {
+        const int first = (i - kLatents) * 8, row = first + lane / 8, chunk = lane % 8 ^ T::rope_flip(row);
+        const char* const from = K.row_of(K.rop, base + row);
+        to_lds16(chunk * 8 < P.C.rope ? from + chunk * 16 : (const char*)kZeros, to + T::kRopes + first * T::kRope);
       }
     }
   }
+};
 
-  // 8 bits: from the registers to LDS, as 16-bit values (exact: 4 bits times a power of two).
-  __device__ __forceinline__ void land(const AttendParams& P, lds_char* to, int part, int lane) {
+// 8 bits by way of registers, where they become 16-bit values (exactly, within fp16's range: 4
+// bits times a power of two).
+template <int kF, int kLatent, int kKeys, int kRows>
+struct Staged {
+  using T = Tile<kLatent, kKeys>;
+  static constexpr int kChunks = kLatent / 16, kPer = 64 / kChunks;  // chunks of 16 codes per row, rows per load
+  static constexpr int kLoads = (kRows + kPer - 1) / kPer;
+  u32x4 codes[kLoads], rope;
+  uint32_t scales[kLoads];
+
+  __device__ __forceinline__ void issue(const AttendParams& P, const Keys<true>& K, int first, int wave, int lane) {
     lane = (int)fresh(lane);
-    if constexpr (kE4m3) {
-      constexpr int kCodes = kLatent / 16, kPer = 64 / kCodes;
 #pragma unroll
-      for (int i = 0; i < kLatentLoads; ++i) {
-        const int row = (part * kLatentLoads + i) * kPer + lane / kCodes, c = lane % kCodes;
-        const float f = scale_value(scales[i]);
+    for (int i = 0; i < kLoads; ++i) {
+      const int row = wave * kRows + i * kPer + lane / kChunks, c = lane % kChunks;
+      const char* const base = K.row_of(K.lat, first + row);
+      const uint8_t* const scale = K.row_of(K.sc, first + row);
+      const bool in = c * 16 < P.C.latent;
+      codes[i] = *(const u32x4*)(in ? base + c * 16 : (const char*)kZeros);
+      scales[i] = *(in ? scale + c / 2 : (const uint8_t*)kZeros);
+    }
+    const int row = wave * kRows + lane / 8 % kRows, c = lane % 8;
+    const char* const base = K.row_of(K.rop, first + row);
+    rope = *(const u32x4*)(c * 8 < P.C.rope ? base + c * 16 : (const char*)kZeros);
+  }
+
+  __device__ __forceinline__ void land(lds_char* to, int wave, int lane) const {
+    lane = (int)fresh(lane);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float v[8];
+    for (int i = 0; i < kLoads; ++i) {
+      const int row = wave * kRows + i * kPer + lane / kChunks, c = lane % kChunks;
+      const float f = scale_value(scales[i]);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(codes[i][2 * h + j], false);
-            const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(codes[i][2 * h + j], true);
-            v[4 * j] = f * a.x;
-            v[4 * j + 1] = f * a.y;
-            v[4 * j + 2] = f * b.x;
-            v[4 * j + 3] = f * b.y;
-          }
+      for (int h = 0; h < 2; ++h) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(codes[i][2 * h + j], false);
+          const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(codes[i][2 * h + j], true);
+          v[4 * j] = f * a.x;
+          v[4 * j + 1] = f * a.y;
+          v[4 * j + 2] = f * b.x;
+          v[4 * j + 3] = f * b.y;
+        }
+        if (kRows % kPer == 0 || lane / kChunks < kRows)
           *(__attribute__((address_space(3))) u32x4*)(to + row * T::kRow + ((2 * c + h) ^ T::latent_flip(row)) * 16) =
               pack_eight<kF>(v);
-        }
-      }
-      if (P.C.rope > 0) {
-#pragma unroll
-        for (int i = 0; i < kRopeLoads; ++i) {
-          const int row = (part * kRopeLoads + i) * 8 + lane / 8, c = lane % 8;
-          *(__attribute__((address_space(3))) u32x4*)(to + T::kRopes + row * T::kRope + (c ^ T::rope_flip(row)) * 16) = ropes[i];
-        }
       }
     }
+    const int row = wave * kRows + lane / 8 % kRows, c = lane % 8;
+    if (lane < kRows * 8)
+      *(__attribute__((address_space(3))) u32x4*)(to + T::kRopes + row * T::kRope + (c ^ T::rope_flip(row)) * 16) = rope;
   }
 };
 
@@ -368,42 +387,65 @@ constexpr float kSlack = 8.0f;
 constexpr float kLowest = -3.402823466e38f;
 
 template <int kF, int kLatent, int kQ, bool kE4m3>
-__global__ __launch_bounds__(64 * kAttendWaves, 1) void latent_attend_kernel(AttendParams P) {
-  using T = Tile<kLatent>;
-  constexpr int kSplit = kAttendWaves / kQ;  // waves that share a block of 16 rows, each with its own keys
-  constexpr int kIter = kTileKeys * kSplit, kRows = 16 * kQ;
-  constexpr int kSteps = kLatent / 32, kColumns = kLatent / 16;
-  using L = Line<kRows, kIter>;
-  // Every kQ waves have a ring of kQ tiles: four tiles in all.
-  constexpr int kSumRow = kLatent + 4;  // floats per row of sums, off the banks' period
-  constexpr int kTiles = kAttendWaves * T::kBytes, kSums = kAttendWaves * 16 * kSumRow * 4;
-  __shared__ __attribute__((aligned(16))) char memory[kTiles > kSums ? kTiles : kSums];
-  __shared__ float tops[kAttendWaves][16], totals[kAttendWaves][16];
-  __shared__ __attribute__((aligned(16))) char room[128];
+__global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_eu(2, 2))) void latent_attend_kernel(AttendParams P) {
+  constexpr int kKeys = step_keys(kQ), kRing = ring_steps(kQ), kRows = 16 * kQ;
+  using T = Tile<kLatent, kKeys>;
+  using L = Line<kRows, kKeys>;
+  constexpr int kSteps = kLatent / 32;  // products per score, beside two for the rotated part
+  constexpr int kColumns = kLatent / 16 / kAttendWaves;  // blocks of 16 columns per wave
+  // For the scores, wave w takes row block w % kQ and key blocks of 16 from kPart (w / kQ) on.
+  constexpr int kBlocks = kKeys / 16, kPart = kQ * kBlocks > kAttendWaves ? kQ * kBlocks / kAttendWaves : 1;
+  // Weights: rows of kKeys 16-bit values, chunks flipped as rotated parts are.
+  constexpr int kWeightRow = kKeys * 2, kFlips = kKeys / 8;
+  __shared__ __attribute__((aligned(16))) char memory[kRing * T::kBytes];
+  __shared__ __attribute__((aligned(16))) char weights[kRows * kWeightRow];
+  __shared__ __attribute__((aligned(16))) float tops[kRows][kBlocks];  // a step's largest scores
+  __shared__ __attribute__((aligned(16))) char room[96];
+  __shared__ uint64_t masks[4];  // of the keys of steps under way
 
   const int tid = threadIdx.x, lane = tid % 64, wave = uniform(tid / 64);
-  const int q = wave % kQ, split = wave / kQ, g = lane / 16, n = lane % 16;
+  const int g = lane / 16, n = lane % 16;
+  const int q = wave % kQ, kb = wave / kQ * kPart;
+  const bool scores = kb < kBlocks;  // this wave takes part in them
+  // Where some waves do not, they load (8 bits: four of them, with equal shares).
+  constexpr int kIdle = kAttendWaves - kQ * kBlocks / kPart;
+  constexpr int kLoaders = kIdle == 0 ? kAttendWaves : kE4m3 ? 4 : kIdle, kShare = kKeys / kLoaders;
+  const int loader = wave - (kAttendWaves - kLoaders);
   Place from, to;
-  int64_t all;
-  const int workers = find_part<kRows, kIter>(P, room, from, to, all);
+  const Parts parts = find_part<kRows, kKeys>(P, room, from, to);
   const int w = blockIdx.x;
-  if (tid == 0) P.pieces[4 * w + 2] = 0;
-  if (w >= workers || all == 0) return;
+  if (tid < 2) P.shared[2 * w + tid].count = 0;
+  if (!from.before(to)) return;
 
-  lds_char* const tiles = (lds_char*)memory + split * kQ * T::kBytes;
-  const lds_char* key_at[4];  // chunk 4 k + g of row n, for k % 4
+  const auto flip_weight = [](int row) { return kFlips == 8 ? (row >> 1) & 7 : (row >> 2) & 3; };
+  lds_char* const tiles = (lds_char*)memory;
+  const lds_char* key_at[4];  // chunk 4 k + g of row 16 kb + n, for k % 4
   const lds_char* rope_at[2];
-  const lds_char* column_at[8];  // columns 16 c .. of rows 4 g .. , for c % 8
 #pragma unroll
-  for (int k = 0; k < 4; ++k) key_at[k] = tiles + n * T::kRow + ((4 * k + g) ^ T::latent_flip(n)) * 16;
+  for (int k = 0; k < 4; ++k) key_at[k] = tiles + (16 * kb + n) * T::kRow + ((4 * k + g) ^ T::latent_flip(n)) * 16;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) rope_at[k] = tiles + T::kRopes + n * T::kRope + ((4 * k + g) ^ T::rope_flip(n)) * 16;
+  for (int k = 0; k < 2; ++k)
+    rope_at[k] = tiles + T::kRopes + (16 * kb + n) * T::kRope + ((4 * k + g) ^ T::rope_flip(n)) * 16;
+  // Columns: rows 8 g + n / 4 (the step's first 4 of 8) and 4 more, this wave's first block.
+  const lds_char* column_at[2][kColumns];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const int row = 4 * g + n / 4;
-    column_at[c] = tiles + row * T::kRow + ((2 * c + n % 4 / 2) ^ T::latent_flip(row)) * 16 + n % 2 * 8;
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int c = 0; c < kColumns; ++c) {
+      const int row = 8 * g + 4 * i + n / 4;
+      column_at[i][c] = tiles + row * T::kRow +
+                        ((2 * (wave * kColumns + c) + n % 4 / 2) ^ T::latent_flip(row)) * 16 + n % 2 * 8;
+    }
+
+  // Rotated parts that are never loaded are zeros.
+  if (P.C.rope == 0) {
+    for (int r = 0; r < kRing; ++r)
+      for (int i = tid; i < kKeys * 8; i += 64 * kAttendWaves)
+        *(u32x4*)(memory + r * T::kBytes + T::kRopes + i * 16) = u32x4{0, 0, 0, 0};
+    __syncthreads();
   }
 
+  Keys<kE4m3> find;
   for (Place at = from; at.before(to);) {
     int start;
     const int tokens = L::tokens(P, at.s, start);
@@ -411,23 +453,26 @@ __global__ __launch_bounds__(64 * kAttendWaves, 1) void latent_attend_kernel(Att
       at = Place{at.s + 1, 0, 0};
       continue;
     }
-    const int keys = L::keys(P, at.s), blocks = L::blocks(P, tokens), every = L::tiles(keys);
+    const int length = P.seq_lens[at.s];
+    const int keys = L::keys(P, length), blocks = L::blocks(P, tokens), every = L::tiles(P, keys);
     const bool ends = at.s < to.s || at.b < to.b;
     const int t1 = ends ? every : to.t;
     // The row of this lane's query, its token and how many keys it sees.
     const int rows = tokens * (int)P.heads.d, row = at.b * kRows + q * 16 + n;
     const bool live = row < rows;
     const int token = (int)P.heads(live ? row : 0), head = (live ? row : 0) - token * (int)P.heads.d;
-    const int past = P.seq_lens[at.s] - tokens + 1;  // what token 0 sees
+    const int past = length - tokens + 1;  // what token 0 sees
     const int reach = past + token;
-    const int least = past + (int)P.heads(at.b * kRows + q * 16 < rows ? at.b * kRows + q * 16 : rows - 1);
     const int last_row = (at.b + 1) * kRows < rows ? (at.b + 1) * kRows - 1 : rows - 1;
-    const int most = past + (int)P.heads(last_row);
+    const int least = past + (int)P.heads(at.b * kRows), most = past + (int)P.heads(last_row);
     const int seen = most < 0 ? 0 : (most < keys ? most : keys);
-    const int count = (t1 < L::tiles(seen) ? t1 : L::tiles(seen)) - at.t;  // tiles to go; may be negative
+    // Steps to go; may be negative.
+    const int begin = at.t << P.shift, last = (seen + kKeys - 1) / kKeys;
+    const int count = ((t1 << P.shift) < last ? t1 << P.shift : last) - begin;
+    const int first_key = begin * kKeys;
 
     u32x4 qf[kSteps], qx[2];
-    {
+    if (scores) {
       const char* const a = P.ql + (start + token) * P.ql_ts + head * P.ql_hs;
       const char* const b = P.qr + (start + token) * P.qr_ts + head * P.qr_hs;
       const int c = (int)fresh(g * 8);
@@ -437,281 +482,330 @@ __global__ __launch_bounds__(64 * kAttendWaves, 1) void latent_attend_kernel(Att
 #pragma unroll
       for (int k = 0; k < 2; ++k)
         qx[k] = *(const u32x4_any*)(live && k * 32 + c < P.C.rope ? b + (k * 32 + c) * 2 : (const char*)kZeros);
+      // (They arrive here. Else every step would wait for them, and for the steps under way.)
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) asm volatile("" : "+v"(qf[k]));
+      asm volatile("" : "+v"(qx[0]), "+v"(qx[1]));
     }
-    f32x4 O[kColumns];
+    f32x4 O[kColumns][kQ];
 #pragma unroll
-    for (int c = 0; c < kColumns; ++c) O[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    float top = kLowest, weight = 0.0f;
+    for (int c = 0; c < kColumns; ++c)
+#pragma unroll
+      for (int i = 0; i < kQ; ++i) O[c][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    float top[kQ];  // of rows 16 i + n, the same in every wave
+#pragma unroll
+    for (int i = 0; i < kQ; ++i) top[i] = kLowest;
+    float my_top = kLowest, weight = 0.0f;  // of this lane's query: row q * 16 + n
 
-    const int first_key = at.t * kIter + split * kTileKeys;
-    Loader<kF, kLatent, kQ, kE4m3> load;
-    uint32_t masks[kQ];  // of the tiles under way, the next to be worked on first
-
-    // Works on the tile in ring place `slot`, keys from `key` on.
-    const auto work = [&](int slot, int key, uint32_t mask) {
-      const int off = slot * T::kBytes;
-      f32x4 S[2][2];
+    // One step, in ring place `slot`; everyone's share of it has arrived.
+    const auto work = [&](int step, int slot) {
+      const int off = slot * T::kBytes, key = first_key + step * kKeys;
+      const uint64_t mask = masks[step & 3];
+      float x[kPart][4];
+      const auto weigh = [&]() {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        for (int j = 0; j < 2; ++j) S[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          S[i][k % 2] = mfma_16x16x32<kF>(lds_read16(key_at[k % 4] + off + i * 16 * T::kRow + k / 4 * 256), qf[k], S[i][k % 2]);
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          S[i][k] = mfma_16x16x32<kF>(lds_read16(rope_at[k] + off + i * 16 * T::kRope), qx[k], S[i][k]);
-      interleave<2 * kSteps + 4>();
-      float x[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = (S[i / 4][0][i % 4] + S[i / 4][1][i % 4]) * P.scale;
-      bool unsafe = false;
-      if (mask != 0xFFFFFFFFu || key + kTileKeys > least) {
-        // Rows that do not see a key have weight 0 for it, but 0 times NaN is NaN. A key with a
-        // value that is not finite gives every row such a score.
-        float worst = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) worst += 0.0f * x[i];
-        unsafe = most != least && __ballot(worst != 0.0f) != 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int k = i / 4 * 16 + 4 * g + i % 4;
-          if (!((mask >> k) & 1) || key + k >= reach) x[i] = -__builtin_huge_valf();
+        for (int b = 0; b < kPart; ++b) {
+          const f32x2 lo = {exp2_hw(x[b][0] - my_top), exp2_hw(x[b][1] - my_top)};
+          const f32x2 hi = {exp2_hw(x[b][2] - my_top), exp2_hw(x[b][3] - my_top)};
+          const int r = q * 16 + n, chunk = (kb + b) * 2 + g / 2;
+          char* const p = weights + r * kWeightRow + (chunk ^ flip_weight(r)) * 16 + g % 2 * 8;
+          Pair<kF>::store(p, lo);
+          Pair<kF>::store(p + 4, hi);
+          x[b][0] = lo.x, x[b][1] = lo.y, x[b][2] = hi.x, x[b][3] = hi.y;
         }
-      }
-      float now = x[0];
+      };
+      float raw[kPart][4];
+      if (scores) {
+        f32x4 S[kPart][2];
 #pragma unroll
-      for (int i = 1; i < 8; ++i) now = __builtin_fmaxf(now, x[i]);
-      now = __builtin_fmaxf(now, __shfl_xor(now, 16));
-      now = __builtin_fmaxf(now, __shfl_xor(now, 32));
-      if (__ballot(now > top + kSlack) != 0) {
-        const float next = __builtin_fmaxf(top, now), f = exp2_hw(top - next);
-        top = next;
-        weight *= f;
+        for (int b = 0; b < kPart; ++b)
+          for (int j = 0; j < 2; ++j) S[b][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        // Operands are read a batch ahead of their products. (Left alone the compiler reads one,
+        // waits for it and uses it.)
+        constexpr int kAll = (kSteps + 2) * kPart, kBatch = kQ == 4 || kE4m3 ? 4 : 6;
+        const auto operand = [&](int i) {
+          const int k = i / kPart, b = i % kPart;
+          return k < kSteps ? lds_read16(key_at[k % 4] + off + b * 16 * T::kRow + k / 4 * 256)
+                            : lds_read16(rope_at[k - kSteps] + off + b * 16 * T::kRope);
+        };
+        u32x4 a[2][kBatch];
 #pragma unroll
-        for (int c = 0; c < kColumns; ++c) {
-          O[c] *= f;
-          if (c % 4 == 3) __builtin_amdgcn_sched_barrier(0);
-        }
-      }
-      float p[8];
+        for (int i = 0; i < kBatch; ++i) a[0][i] = operand(i);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        p[i] = exp2_hw(x[i] - top);
-        weight += p[i];
-      }
-      const u32x4 pf = pack_eight<kF>(p);
-      if (unsafe) {
+        for (int j = 0; j < kAll; j += kBatch) {
 #pragma unroll
-        for (int c = 0; c < kColumns; ++c) {
-          const lds_char* const a = column_at[c % 8] + off + c / 8 * 256;
-          const u32x2 u = finite_pairs<kF>(lds_read_columns(a)), v = finite_pairs<kF>(lds_read_columns(a + 16 * T::kRow));
-          O[c] = mfma_16x16x32<kF>(u32x4{u[0], u[1], v[0], v[1]}, pf, O[c]);
+          for (int i = 0; i < kBatch; ++i)
+            if (j + kBatch + i < kAll) a[(j / kBatch + 1) % 2][i] = operand(j + kBatch + i);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            if (j + i >= kAll) break;
+            const int k = (j + i) / kPart, b = (j + i) % kPart;
+            S[b][k % 2] = mfma_16x16x32<kF>(a[j / kBatch % 2][i], k < kSteps ? qf[k] : qx[k - kSteps], S[b][k % 2]);
+          }
           __builtin_amdgcn_sched_barrier(0);
         }
-      } else {
+        float now = -__builtin_huge_valf();
+#pragma unroll
+        for (int b = 0; b < kPart; ++b) {
+          float high = -__builtin_huge_valf();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[b][i] = (S[b][0][i] + S[b][1][i]) * P.scale;
+            const int k = (kb + b) * 16 + 4 * g + i;
+            if (mask != ~0ull >> (64 - kKeys) || key + kKeys > least)
+              x[b][i] = ((mask >> k) & 1) && key + k < reach ? x[b][i] : -__builtin_huge_valf();
+            high = __builtin_fmaxf(high, x[b][i]);
+            raw[b][i] = x[b][i];
+          }
+          high = __builtin_fmaxf(high, __shfl_xor(high, 16));
+          high = __builtin_fmaxf(high, __shfl_xor(high, 32));
+          if (g == 0) tops[q * 16 + n][kb + b] = high;
+          now = __builtin_fmaxf(now, high);
+        }
+        weigh();
+      }
+      lds_barrier();
+      // The step's largest scores: all waves see the same and decide alike.
+      float now[kQ];
+      bool grows = false;
+#pragma unroll
+      for (int i = 0; i < kQ; ++i) {
+        const float* const a = tops[i * 16 + n];
+        now[i] = __builtin_fmaxf(a[0], a[1]);
+        if (kBlocks == 4) now[i] = __builtin_fmaxf(now[i], __builtin_fmaxf(a[2 % kBlocks], a[3 % kBlocks]));
+        grows |= now[i] > top[i] + kSlack;
+      }
+      if (__ballot(grows) != 0) {
+#pragma unroll
+        for (int i = 0; i < kQ; ++i) {
+          const float next = __builtin_fmaxf(top[i], now[i]), f = exp2_hw(top[i] - next);
+          top[i] = next;
+#pragma unroll
+          for (int c = 0; c < kColumns; ++c) O[c][i] *= f;
+        }
+        if (scores) {
+          float next = my_top;
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b) next = __builtin_fmaxf(next, tops[q * 16 + n][b]);
+          weight *= exp2_hw(my_top - next);
+          my_top = next;
+#pragma unroll
+          for (int b = 0; b < kPart; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[b][i] = raw[b][i];
+          weigh();
+        }
+        lds_barrier();
+      }
+      if (scores) {
+#pragma unroll
+        for (int b = 0; b < kPart; ++b) weight += (x[b][0] + x[b][1]) + (x[b][2] + x[b][3]);
+      }
+      // Rows that do not see a key have weight 0 for it, but 0 times NaN is NaN: where rows differ
+      // in what they see, values that are not finite become zeros. (The rows that see one have
+      // a score that is not finite.)
+      if (most != least && key + kKeys > least) {
+        for (int i = tid; i < T::kRopes / 16; i += 64 * kAttendWaves) {
+          u32x4* const a = (u32x4*)(memory + off + i * 16);
+          *a = finite_pairs<kF>(*a);
+        }
+        lds_barrier();
+      }
+#pragma unroll
+      for (int k = 0; k < kKeys / 32; ++k) {
+        u32x4 p[kQ];
+        u32x2 u[kColumns], v[kColumns];
+#pragma unroll
+        for (int i = 0; i < kQ; ++i) {
+          const int r = i * 16 + n;
+          p[i] = *(const u32x4*)(weights + r * kWeightRow + ((4 * k + g) ^ flip_weight(r)) * 16);
+        }
 #pragma unroll
         for (int c = 0; c < kColumns; ++c) {
-          const lds_char* const a = column_at[c % 8] + off + c / 8 * 256;
-          const u32x2 u = lds_read_columns(a), v = lds_read_columns(a + 16 * T::kRow);
-          O[c] = mfma_16x16x32<kF>(u32x4{u[0], u[1], v[0], v[1]}, pf, O[c]);
+          u[c] = lds_read_columns(column_at[0][c] + off + k * 32 * T::kRow);
+          v[c] = lds_read_columns(column_at[1][c] + off + k * 32 * T::kRow);
         }
-        interleave_pairs<kColumns>();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int c = 0; c < kColumns; ++c)
+#pragma unroll
+          for (int i = 0; i < kQ; ++i)
+            O[c][i] = mfma_16x16x32<kF>(u32x4{u[c][0], u[c][1], v[c][0], v[c][1]}, p[i], O[c][i]);
       }
     };
 
-    // Rotated parts that are never loaded are zeros; the last block's sums lay there.
-    if (P.C.rope == 0) {
-      static_assert(T::kBytes - T::kRopes == 16 * 64 * kAttendWaves, "a thread clears 16 bytes of each tile");
-      for (int i = 0; i < kAttendWaves; ++i)
-        ((u32x4*)(memory + i * T::kBytes + T::kRopes))[tid] = u32x4{0, 0, 0, 0};
-      __syncthreads();
-    }
+    // Keys past the end are loaded too, as zeros.
+    const auto find_step = [&](int step) {
+      constexpr int kTimes = 64 / kKeys;  // steps that a search serves
+      const int base = step % kTimes * kKeys;
+      if (base == 0) find.find(P, at.s, first_key + step * kKeys, keys, lane);
+      if (loader == 0 && lane == 0) masks[step & 3] = find.mask << (64 - kKeys - base) >> (64 - kKeys);
+      return base;
+    };
     if (count > 0) {
       if constexpr (kE4m3) {
-        load.find(P, at.s, first_key, keys, lane);
-        load.issue(P, tiles, q, lane);
-        for (int i = 0; i < count; ++i) {
-          const int slot = i % kQ;
-          const uint32_t mask = load.mask;
-          // (The wave's own reads and writes; LDS serves a wave in order.)
-          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-          load.land(P, tiles + slot * T::kBytes, q, lane);
-          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-          if (i + 1 < count) {
-            load.find(P, at.s, first_key + (i + 1) * kIter, keys, lane);
-            load.issue(P, tiles, q, lane);
+        // kSets steps are under way to registers; the next goes to LDS beside the present one.
+        constexpr int kSets = kKeys == 64 ? 1 : 3;
+        Staged<kF, kLatent, kKeys, kShare> set[kSets];
+        for (int base = -kSets; base < count; base += kSets) {
+#pragma unroll
+          for (int j = 0; j < kSets; ++j) {
+            const int i = base + j;
+            if (i >= count) break;
+            if (i >= 0) lds_barrier();  // step i is in LDS, and everyone is done with step i - 1
+            if (loader >= 0) {
+              set[j].issue(P, find, find_step(i + kSets), loader, lane);
+              if (kSets > 1 && i >= -1) set[(j + 1) % kSets].land(tiles + ((i + 1) & 1) * T::kBytes, loader, lane);
+            }
+            if (i >= 0) work(i, i & 1);
+            if (kSets == 1 && loader >= 0) set[0].land(tiles + ((i + 1) & 1) * T::kBytes, loader, lane);
           }
-          if (kQ > 1) __syncthreads();
-          work(slot, first_key + i * kIter, mask);
-        }
-      } else if constexpr (kQ == 1) {
-        load.find(P, at.s, first_key, keys, lane);
-        load.issue(P, tiles, q, lane);
-        for (int i = 0; i < count; ++i) {
-          const uint32_t mask = load.mask;
-          if (i + 1 < count) load.find(P, at.s, first_key + (i + 1) * kIter, keys, lane);
-          asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-          work(0, first_key + i * kIter, mask);
-          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-          if (i + 1 < count) load.issue(P, tiles, q, lane);
         }
       } else {
-#pragma unroll
-        for (int i = 0; i < kQ - 1; ++i) {
-          if (i < count) {
-            load.find(P, at.s, first_key + i * kIter, keys, lane);
-            load.issue(P, tiles + i * T::kBytes, q, lane);
-            masks[i] = load.mask;
+        using D = Direct<kLatent, kKeys, kLoaders>;
+        for (int i = 1 - kRing; i < count; ++i) {
+          if (i >= 0) {
+            // This wave's share of step i has arrived; after the barrier everyone's has, and
+            // everyone is done with step i - 1, whose place is free.
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kRing - 2) * D::kLeast) : "memory");
+            lds_barrier();
           }
-        }
-        int slot = 0;
-        for (int i = 0; i < count; ++i) {
-          // This wave's part of tile i has arrived; after the barrier everyone's has, and
-          // everyone is done with tile i - 1.
-          if (i + kQ - 1 < count + 1)
-            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kQ - 2) * Loader<kF, kLatent, kQ, kE4m3>::kLatentLoads) : "memory");
-          else
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-          __syncthreads();
-          const uint32_t mask = masks[0];
-#pragma unroll
-          for (int j = 0; j + 1 < kQ - 1; ++j) masks[j] = masks[j + 1];
-          if (i + kQ - 1 < count) {
-            load.find(P, at.s, first_key + (i + kQ - 1) * kIter, keys, lane);
-            load.issue(P, tiles + (slot == 0 ? kQ - 1 : slot - 1) * T::kBytes, q, lane);
-            masks[kQ - 2] = load.mask;
+          if (loader >= 0) {
+            const int ahead = i + kRing - 1;
+            D::issue(P, find, find_step(ahead), tiles + (ahead & (kRing - 1)) * T::kBytes, loader, lane);
           }
-          work(slot, first_key + i * kIter, mask);
-          slot = slot + 1 == kQ ? 0 : slot + 1;
+          if (i >= 0) work(i, i & (kRing - 1));
         }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       }
     }
+
+    // Each row's weight: this wave's lanes of it, then the waves that share it.
     weight += __shfl_xor(weight, 16);
     weight += __shfl_xor(weight, 32);
-
-    // The waves' sums of a row come together in LDS, and go out.
-    if (g == 0) {
-      tops[wave][n] = top;
-      totals[wave][n] = weight;
-    }
-    __syncthreads();  // tiles are no longer read
-    float high = tops[q][n];
-#pragma unroll
-    for (int i = 1; i < kSplit; ++i) high = __builtin_fmaxf(high, tops[i * kQ + q][n]);
-    float f = exp2_hw(top - high), total = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kSplit; ++i) total = __builtin_fmaf(totals[i * kQ + q][n], exp2_hw(tops[i * kQ + q][n] - high), total);
+    __syncthreads();  // everyone has read the last step's largest scores
+    if (scores && g == 0) tops[q * 16 + n][wave / kQ] = weight;
+    __syncthreads();
+    constexpr int kSums = kBlocks / kPart;
     const bool whole = at.t == 0 && t1 == every;
-    if (whole) f *= total == 0.0f ? 0.0f : 1.0f / total;
-    float* const sums = (float*)memory;
-#pragma unroll
-    for (int c = 0; c < kColumns; ++c) *(f32x4*)(sums + (wave * 16 + n) * kSumRow + 16 * c + 4 * g) = f * O[c];
     const Partial part{kRows, P.C.latent};
     float* const mine = P.partial + part.floats() * (2 * w + (ends ? 0 : 1));
-    if (!whole && split == 0 && g == 0) {
-      mine[part.exponent() + q * 16 + n] = high;
-      mine[part.weight() + q * 16 + n] = total;
-    }
-    __syncthreads();
-    constexpr int kEights = kLatent / 8;
-    for (int i = tid; i < kRows * kEights; i += 64 * kAttendWaves) {
-      const int r = i / kEights, c = i % kEights * 8;
-      if (c >= P.C.latent || at.b * kRows + r >= rows) continue;
-      float v[8] = {};
 #pragma unroll
-      for (int k = 0; k < kSplit; ++k) {
-        const float* const a = sums + ((k * kQ + r / 16) * 16 + r % 16) * kSumRow + c;
+    for (int i = 0; i < kQ; ++i) {
+      const int r = i * 16 + n;
+      float total = tops[r][0];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += a[j];
+      for (int j = 1; j < kSums; ++j) total += tops[r][j];
+      if (!whole && wave == 0 && g == 0) {
+        mine[part.exponent() + r] = top[i];
+        mine[part.weight() + r] = total;
       }
-      if (whole) {
-        const int64_t to_row = (int64_t)start * P.heads.d + at.b * kRows + r;
-        store_eight<kF>(P.out + (to_row * P.C.latent + c) * 2, v);
-      } else {
-        *(f32x4*)(mine + (int64_t)r * P.C.latent + c) = f32x4{v[0], v[1], v[2], v[3]};
-        *(f32x4*)(mine + (int64_t)r * P.C.latent + c + 4) = f32x4{v[4], v[5], v[6], v[7]};
+      const float f = total == 0.0f ? 0.0f : 1.0f / total;
+      if (at.b * kRows + r < rows) {
+#pragma unroll
+        for (int c = 0; c < kColumns; ++c) {
+          const int column = (wave * kColumns + c) * 16 + 4 * g;
+          if (column >= P.C.latent) break;
+          if (whole) {
+            const f32x4 v = f * O[c][i];
+            char* const o = P.out + (((int64_t)start * P.heads.d + at.b * kRows + r) * P.C.latent + column) * 2;
+            Pair<kF>::store(o, f32x2{v[0], v[1]});
+            Pair<kF>::store(o + 4, f32x2{v[2], v[3]});
+          } else {
+            *(f32x4*)(mine + (int64_t)r * P.C.latent + column) = O[c][i];
+          }
+        }
       }
     }
-    // The worker that begins a shared block says how many have a part of it.
-    if (tid == 0 && at.t == 0 && !ends) {
-      // Units up to the block's end: this worker's part ends to.t + kBlockUnits units into it.
-      const int64_t end = all * (w + 1) / workers - (to.t + kBlockUnits) + every + kBlockUnits;
-      const int64_t last = (end * workers + all - 1) / all;  // the first worker that begins at or past it
-      P.pieces[4 * w] = at.s;
-      P.pieces[4 * w + 1] = at.b;
-      P.pieces[4 * w + 2] = (int)(last - w);
+    // Who else has a part of this block: the last worker to begin at or before its first key (the
+    // line's units count kBlockUnits before it) and those that begin after it, before its end.
+    if (wave == 0 && !whole) {
+      const int zero = at.t > 0 ? parts.begin(w) - at.t : parts.begin(w + 1) - to.t, end = zero + every;
+      int before = 0, all = 0;
+      for (int i = lane; __ballot(i < parts.count) != 0; i += 64) {
+        const int at_unit = parts.begin(i);
+        before += __builtin_popcountll(__ballot(i < parts.count && at_unit <= zero));
+        all += __builtin_popcountll(__ballot(i < parts.count && at_unit < end));
+      }
+      if (lane == 0) P.shared[2 * w + (ends ? 0 : 1)] = Shared{before - 1, all - (before - 1), at.s, at.b};
     }
     __syncthreads();
     at = at.b + 1 < blocks ? Place{at.s, at.b + 1, 0} : Place{at.s + 1, 0, 0};
   }
 }
 
-// Joins the parts of shared blocks: one wave per row.
+// Joins the parts of shared blocks. Each worker that has a part joins its share of the block's
+// rows and columns, 8 columns of a row at a time by as many lanes as take kJoinParts parts each.
+constexpr int kJoinThreads = 512, kJoinParts = 8;
+
 template <int kF, int kRows>
-__global__ __launch_bounds__(256) void latent_join_kernel(AttendParams P) {
-  const int w = blockIdx.x, lane = threadIdx.x % 64;
-  const int count = P.pieces[4 * w + 2];
-  if (count == 0) return;
-  const int s = P.pieces[4 * w], b = P.pieces[4 * w + 1];
-  int start;
-  const int tokens = Line<kRows, 1>::tokens(P, s, start);
-  const int r = blockIdx.y * 4 + uniform(threadIdx.x / 64);
-  if (b * kRows + r >= tokens * (int)P.heads.d) return;
+__global__ __launch_bounds__(kJoinThreads) void latent_join_kernel(AttendParams P) {
+  // The block that this worker's part begins inside, or the one that it ends inside.
+  const int x = blockIdx.x, tid = threadIdx.x;
   const Partial part{kRows, P.C.latent};
+  const Shared share = P.shared[2 * x + blockIdx.y];
+  const int count = uniform(share.count), w = uniform(share.first);
+  if (count == 0) return;
+  int start;
+  const int tokens = Line<kRows, 1>::tokens(P, uniform(share.s), start);
+  int rows = tokens * (int)P.heads.d - uniform(share.b) * kRows;
+  rows = rows < kRows ? rows : kRows;
+  const int chunks = P.C.latent / 8, all = rows * chunks;
+  const int from = (int)((uint32_t)(all * (x - w)) / (uint32_t)count), to = (int)((uint32_t)(all * (x - w + 1)) / (uint32_t)count);
+  char* const out = P.out + ((int64_t)start * P.heads.d + uniform(share.b) * kRows) * P.C.latent * 2;
   const auto slot = [&](int i) { return P.partial + part.floats() * (2 * (w + i) + (i + 1 < count)); };
-  float high = kLowest;
-  for (int i = lane; i < count; i += 64) high = __builtin_fmaxf(high, slot(i)[part.exponent() + r]);
+  int lanes = 1, log = 0;  // (at most 32: there are 256 workers)
+  while (lanes * kJoinParts < count) lanes *= 2, ++log;
+  const int turn = tid & (lanes - 1);
+  for (int base = from; base < to; base += kJoinThreads >> log) {
+    const int i = base + (tid >> log);
+    const bool mine = i < to;
+    const int r = (int)((uint32_t)(mine ? i : from) / (uint32_t)chunks), c = (mine ? i : from) - r * chunks;
+    float e[kJoinParts], l[kJoinParts], high = kLowest, total = 0.0f;
+    f32x4 a[kJoinParts][2], v[2] = {};
 #pragma unroll
-  for (int m = 32; m > 0; m >>= 1) high = __builtin_fmaxf(high, __shfl_xor(high, m));
-  const int c = lane * 8;
-  const bool mine = c < P.C.latent;
-  float total = 0.0f, v[8] = {};
-  for (int base = 0; base < count; base += 64) {
-    float f = 0.0f, l = 0.0f;
-    if (base + lane < count) {
-      const float* const a = slot(base + lane);
-      f = exp2_hw(a[part.exponent() + r] - high);
-      l = f * a[part.weight() + r];
+    for (int k = 0; k < kJoinParts; ++k) {
+      if (k * lanes >= count) break;
+      const int number = turn + k * lanes;
+      const float* const p = slot(number < count ? number : 0);
+      e[k] = number < count ? p[part.exponent() + r] : kLowest;
+      l[k] = p[part.weight() + r];
+      const f32x4* const q = (const f32x4*)(p + (int64_t)r * P.C.latent + c * 8);
+      a[k][0] = q[0];
+      a[k][1] = q[1];
     }
-    total += lane_sum<64>(l);
-    const int here = count - base < 64 ? count - base : 64;
-    // Four parts' loads at a time.
-    for (int i = 0; i < here; i += 4) {
-      f32x4 lo[4], hi[4];
-      float fs[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int at = i + k < here ? i + k : here - 1;
-        fs[k] = i + k < here ? __shfl(f, at) : 0.0f;
-        const f32x4* const a = (const f32x4*)(slot(base + at) + (int64_t)r * P.C.latent + (mine ? c : 0));
-        lo[k] = a[0];
-        hi[k] = a[1];
-      }
+    for (int k = 0; k < kJoinParts; ++k)
+      if (k * lanes < count) high = __builtin_fmaxf(high, e[k]);
+    for (int m = lanes / 2; m > 0; m >>= 1) high = __builtin_fmaxf(high, __shfl_xor(high, m));
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (i + k >= here) break;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[j] = __builtin_fmaf(fs[k], lo[k][j], v[j]);
-          v[4 + j] = __builtin_fmaf(fs[k], hi[k][j], v[4 + j]);
-        }
-      }
+    for (int k = 0; k < kJoinParts; ++k) {
+      if (turn + k * lanes >= count) break;
+      const float f = exp2_hw(e[k] - high);
+      total = __builtin_fmaf(f, l[k], total);
+      v[0] += f * a[k][0];
+      v[1] += f * a[k][1];
     }
+    float o[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = v[j / 4][j % 4];
+    for (int m = lanes / 2; m > 0; m >>= 1) {
+      total += __shfl_xor(total, m);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] += __shfl_xor(o[j], m);
+    }
+    const float f = total == 0.0f ? 0.0f : 1.0f / total;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] *= f;
+    if (mine && turn == 0) store_eight<kF>(out + ((int64_t)r * chunks + c) * 16, o);
   }
-  const float f = total == 0.0f ? 0.0f : 1.0f / total;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] *= f;
-  if (mine) store_eight<kF>(P.out + (((int64_t)start * P.heads.d + b * kRows + r) * P.C.latent + c) * 2, v);
 }
 
 template <int kF, int kLatent, int kQ, bool kE4m3>
 void launch_attend(const AttendParams& P, hipStream_t st) {
   hipLaunchKernelGGL((latent_attend_kernel<kF, kLatent, kQ, kE4m3>), dim3(P.workers), dim3(64 * kAttendWaves), 0, st, P);
-  hipLaunchKernelGGL((latent_join_kernel<kF, 16 * kQ>), dim3(P.workers, 4 * kQ), dim3(256), 0, st, P);
+  hipLaunchKernelGGL((latent_join_kernel<kF, 16 * kQ>), dim3(P.workers, 2), dim3(kJoinThreads), 0, st, P);
 }
 
 }  // namespace kdaconv
