@@ -531,6 +531,46 @@ int kdaconv_latent_attention_update(const kdaconv_latent_args* args, void* works
 int kdaconv_latent_attention_validate(const kdaconv_latent_args* args, int update,
                                       const void* workspace, int64_t workspace_bytes);
 
+/*
+ * Attention of packed sequences in the expanded form: every head has keys and values of its own
+ * (a latent's up-projection), beside the rotated part of the keys that all heads share. Row i of
+ * the n queries of sequence s, rows [qsl[s], qsl[s+1]), sees the first m - n + i + 1 of its m
+ * keys, rows [ksl[s], ksl[s+1]) of k, k_rope and v, or all of them without `causal`:
+ *     s_t = scale * (q[:key_dim] . k_t + q[key_dim:] . k_rope_t),   out = sum_t softmax(s)_t v_t
+ * A row that sees none is zero; rows no sequence owns are not written. Scores, softmax and sums
+ * are FP32; its weights (up to 2^8 before the division by their sum) are rounded to dtype for the
+ * second product, out is rounded once. A key or value that is not finite reaches no row that does
+ * not see it.
+ *
+ * key_dim and value_dim are multiples of 8 up to 128, rope_dim is one of 8, 0 to 64 (else
+ * EUNSUPPORTED); up to 64, 64 and 32 a smaller kernel serves. k, v and k_rope lie at multiples of
+ * 16 bytes, token for token and head for head (else EUNSUPPORTED). Strides count elements, 0 to
+ * 2^23 - 1 (else EUNSUPPORTED); of an axis of one entry they are not looked at.
+ */
+typedef struct kdaconv_expanded_args {
+  const void* q;      /* (num_tokens, num_heads, key_dim + rope_dim), last axis contiguous */
+  const void* k;      /* (num_keys, num_heads, key_dim), last axis contiguous */
+  const void* k_rope; /* (num_keys, rope_dim), columns contiguous; ignored if rope_dim is 0 */
+  const void* v;      /* (num_keys, num_heads, value_dim), last axis contiguous */
+  const int32_t* query_start_loc; /* (num_seqs + 1) */
+  const int32_t* kv_start_loc;    /* (num_seqs + 1) */
+  void* out;          /* (num_tokens, num_heads, value_dim), contiguous */
+  int64_t num_tokens, num_keys, num_seqs, num_heads, key_dim, rope_dim, value_dim;
+  int64_t q_stride0, q_stride1, k_stride0, k_stride1, kr_stride0, v_stride0, v_stride1;
+  double scale;
+  int32_t dtype; /* KDACONV_BF16 or KDACONV_F16 */
+  int32_t causal;
+} kdaconv_expanded_args;
+
+/* The launch depends on host sizes alone, so a call can be captured in a graph. num_tokens,
+ * num_seqs or num_heads of 0: KDACONV_OK with no launch. (num_tokens / 128 + num_seqs) *
+ * num_heads is below 2^23 (else EUNSUPPORTED). No scratch memory. */
+int kdaconv_expanded_attention(const kdaconv_expanded_args* args, kdaconv_stream_t stream);
+
+/* The status the call would return before launching. No HIP call; device pointers are only
+ * compared with NULL and tested for alignment. */
+int kdaconv_expanded_attention_validate(const kdaconv_expanded_args* args);
+
 /* Static English text for a status code. Never NULL. */
 const char* kdaconv_status_string(int status);
 

@@ -19,6 +19,7 @@ from . import _lib
 from ._host import DTYPE_CODES as _DTYPE_CODES
 from ._host import NULL_BLOCK_ID, _on, _ptr, _stream_handle
 from .delta_rule import gated_delta_rule_fn, gated_delta_rule_supported, gated_delta_rule_update
+from .expanded import expanded_attention_fn, expanded_attention_supported
 from .latent import (latent_attention_fn, latent_attention_supported, latent_attention_update,
                      latent_cache_read, latent_cache_write)
 from .norms import gated_rms_norm, residual_rms_norm
@@ -41,6 +42,8 @@ __all__ = [
     "latent_attention_fn",
     "latent_attention_update",
     "latent_attention_supported",
+    "expanded_attention_fn",
+    "expanded_attention_supported",
     "activation_map",
     "library_path",
 ]

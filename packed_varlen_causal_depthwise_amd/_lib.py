@@ -21,6 +21,8 @@ RULE_ARGS = struct.Struct("=12Q21q3d6i")
 LATENT_CACHE = struct.Struct("=3Q10q2i")
 #: kdaconv_latent_args after its cache: 6 pointers, 9 integers, 1 double.
 LATENT_ARGS = struct.Struct("=6Q9qd")
+#: kdaconv_expanded_args: 7 pointers, 14 integers, 1 double, 2 32-bit integers, no padding.
+EXPANDED_ARGS = struct.Struct("=7Q14qd2i")
 
 # Every entry point include/kdaconv.h declares.
 EXPORTS = (
@@ -42,6 +44,8 @@ EXPORTS = (
     "kdaconv_latent_attention_update",
     "kdaconv_latent_attention_validate",
     "kdaconv_latent_attention_workspace",
+    "kdaconv_expanded_attention",
+    "kdaconv_expanded_attention_validate",
     "kdaconv_status_string",
     "kdaconv_version",
 )
@@ -143,6 +147,10 @@ def load() -> ctypes.CDLL:
     lib.kdaconv_latent_attention_validate.restype = i32
     lib.kdaconv_latent_attention_workspace.argtypes = [i64, i64, i64, i64]
     lib.kdaconv_latent_attention_workspace.restype = i64
+    lib.kdaconv_expanded_attention.argtypes = [packed, vp]
+    lib.kdaconv_expanded_attention.restype = i32
+    lib.kdaconv_expanded_attention_validate.argtypes = [packed]
+    lib.kdaconv_expanded_attention_validate.restype = i32
     lib.kdaconv_status_string.argtypes = [i32]
     lib.kdaconv_status_string.restype = ctypes.c_char_p
     lib.kdaconv_version.argtypes = []

@@ -27,6 +27,9 @@ SOURCES = [PKG / "csrc" / name for name in (
     "latent_attention_bf16_512.hip",
     "latent_attention_f16_256.hip",
     "latent_attention_f16_512.hip",
+    "expanded_attention.hip",
+    "expanded_attention_bf16.hip",
+    "expanded_attention_f16.hip",
 )]
 HEADERS = [ROOT / "include" / "kdaconv.h", *sorted((PKG / "csrc").glob("*.h"))]
 LIBRARY = PKG / "libkdaconv.so"

@@ -1,0 +1,36 @@
+// Expanded attention over packed sequences: parameters shared by the host code and the kernels.
+#ifndef KDACONV_EXPANDED_ATTENTION_H_
+#define KDACONV_EXPANDED_ATTENTION_H_
+
+#include "latent.h"
+
+namespace kdaconv {
+
+constexpr int kExpandKeys = 64;  // keys per step
+constexpr int kWaveRows = 32;  // queries per wave
+
+struct ExpandParams {
+  const char* q;
+  const char* k;
+  const char* kr;
+  const char* v;
+  char* out;  // (tokens, heads, value channels), contiguous
+  const int32_t* qsl;
+  const int32_t* ksl;
+  int64_t q_ts, q_hs, k_ts, k_hs, kr_ts, v_ts, v_hs;  // bytes
+  int32_t tokens, keys, seqs, heads;
+  int32_t dim, rope, vdim;
+  int32_t programs;  // blocks of rows: sequence s owns v(s) = s + start of s / rows up to v(s + 1)
+  int32_t search_top;  // 64^(levels - 1), 64^levels >= seqs
+  float scale;  // times log2(e), not negative
+  uint32_t flip;  // the queries' sign bits, where the scale was
+  bool causal;
+  bool plain;  // all channels are there: dim, rope and vdim are the kernel's
+};
+
+template <int kF, int kDim, int kRope, int kWaves>
+void launch_expanded(const ExpandParams& P, hipStream_t st);
+
+}  // namespace kdaconv
+
+#endif  // KDACONV_EXPANDED_ATTENTION_H_

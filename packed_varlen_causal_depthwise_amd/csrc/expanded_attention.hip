@@ -1,0 +1,126 @@
+// Expanded attention: checks of arguments and the C entry point. include/kdaconv.h states the
+// operator.
+#include "expanded_attention.h"
+
+#include <algorithm>
+#include <cmath>
+
+namespace kdaconv {
+namespace {
+
+// A step's 64 rows stay below 2^31 bytes.
+constexpr int64_t kMaxStride = (int64_t)1 << 23;
+
+bool aligned_to(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+// Workgroups take 256 rows where sequences are as long on average, else 128.
+int waves_of(int64_t tokens, int64_t seqs) { return tokens >= 256 * seqs ? 8 : 4; }
+
+int64_t programs_of(int64_t tokens, int64_t seqs) {
+  return tokens / (kWaveRows * waves_of(tokens, seqs)) + seqs;
+}
+
+int validate_expanded(const kdaconv_expanded_args* a) {
+  if (a == nullptr) return KDACONV_EINVAL;
+  if (a->num_tokens < 0 || a->num_keys < 0 || a->num_seqs < 0 || a->num_heads < 0 || a->key_dim <= 0 ||
+      a->rope_dim < 0 || a->value_dim <= 0 || std::isnan(a->scale))
+    return KDACONV_EINVAL;
+  if (a->dtype != KDACONV_BF16 && a->dtype != KDACONV_F16 && a->dtype != KDACONV_F32) return KDACONV_EINVAL;
+  if (a->dtype == KDACONV_F32) return KDACONV_EUNSUPPORTED;
+  if (a->key_dim % 8 != 0 || a->key_dim > 128 || a->value_dim % 8 != 0 || a->value_dim > 128 ||
+      a->rope_dim % 8 != 0 || a->rope_dim > kRopeMax)
+    return KDACONV_EUNSUPPORTED;
+  // Strides of axes of one entry mean nothing. Keys and values move in pieces of 16 bytes.
+  const struct {
+    int64_t count, stride;
+    bool pieces;
+  } axes[] = {{a->num_tokens, a->q_stride0, false}, {a->num_heads, a->q_stride1, false},
+              {a->num_keys, a->k_stride0, true},    {a->num_heads, a->k_stride1, true},
+              {a->num_keys, a->v_stride0, true},    {a->num_heads, a->v_stride1, true},
+              {a->rope_dim > 0 ? a->num_keys : 0, a->kr_stride0, true}};
+  for (const auto& axis : axes)
+    if (axis.count > 1 && (axis.stride < 0 || axis.stride >= kMaxStride || (axis.pieces && axis.stride % 8 != 0)))
+      return KDACONV_EUNSUPPORTED;
+  if (a->num_tokens > INT32_MAX / 4 || a->num_keys > INT32_MAX / 4 || a->num_seqs > INT32_MAX / 4 || a->num_heads > 65535)
+    return KDACONV_EUNSUPPORTED;
+  // 2^32 threads.
+  if (programs_of(a->num_tokens, a->num_seqs) * a->num_heads >= (int64_t)1 << 23) return KDACONV_EUNSUPPORTED;
+  if (a->num_tokens == 0 || a->num_seqs == 0 || a->num_heads == 0) return KDACONV_OK;
+  if (!a->q || !a->out || !a->query_start_loc || !a->kv_start_loc) return KDACONV_EINVAL;
+  if (a->num_keys > 0 && (!a->k || !a->v || (a->rope_dim > 0 && !a->k_rope))) return KDACONV_EINVAL;
+  if (!aligned_to(a->q, 2) || !aligned_to(a->out, 2) || !aligned_to(a->k, 16) || !aligned_to(a->v, 16) ||
+      (a->rope_dim > 0 && !aligned_to(a->k_rope, 16)) || !aligned_to(a->query_start_loc, 4) || !aligned_to(a->kv_start_loc, 4))
+    return KDACONV_EUNSUPPORTED;
+  return KDACONV_OK;
+}
+
+template <int kF, int kDim, int kRope>
+void launch(const ExpandParams& P, int waves, hipStream_t st) {
+  if (waves == 8)
+    launch_expanded<kF, kDim, kRope, 8>(P, st);
+  else
+    launch_expanded<kF, kDim, kRope, 4>(P, st);
+}
+
+template <int kF>
+void launch(const ExpandParams& P, bool wide, bool rope, int waves, hipStream_t st) {
+  if (wide && rope)
+    launch<kF, 128, 64>(P, waves, st);
+  else if (wide)
+    launch<kF, 128, 32>(P, waves, st);
+  else if (rope)
+    launch<kF, 64, 64>(P, waves, st);
+  else
+    launch<kF, 64, 32>(P, waves, st);
+}
+
+}  // namespace
+}  // namespace kdaconv
+
+using namespace kdaconv;
+
+extern "C" int kdaconv_expanded_attention_validate(const kdaconv_expanded_args* args) { return validate_expanded(args); }
+
+extern "C" int kdaconv_expanded_attention(const kdaconv_expanded_args* a, kdaconv_stream_t stream) {
+  const int rc = validate_expanded(a);
+  if (rc != KDACONV_OK || a->num_tokens == 0 || a->num_seqs == 0 || a->num_heads == 0) return rc;
+  ExpandParams P;
+  P.q = static_cast<const char*>(a->q);
+  P.k = static_cast<const char*>(a->k);
+  P.kr = static_cast<const char*>(a->k_rope);
+  P.v = static_cast<const char*>(a->v);
+  P.out = static_cast<char*>(a->out);
+  P.qsl = a->query_start_loc;
+  P.ksl = a->kv_start_loc;
+  const int64_t tokens = a->num_tokens > 1, keys = a->num_keys > 1, heads = a->num_heads > 1;
+  P.q_ts = a->q_stride0 * 2 * tokens;
+  P.q_hs = a->q_stride1 * 2 * heads;
+  P.k_ts = a->k_stride0 * 2 * keys;
+  P.k_hs = a->k_stride1 * 2 * heads;
+  P.kr_ts = a->kr_stride0 * 2 * keys;
+  P.v_ts = a->v_stride0 * 2 * keys;
+  P.v_hs = a->v_stride1 * 2 * heads;
+  P.tokens = (int32_t)a->num_tokens;
+  P.keys = (int32_t)a->num_keys;
+  P.seqs = (int32_t)a->num_seqs;
+  P.heads = (int32_t)a->num_heads;
+  P.dim = (int32_t)a->key_dim;
+  P.rope = (int32_t)a->rope_dim;
+  P.vdim = (int32_t)a->value_dim;
+  const int waves = waves_of(a->num_tokens, a->num_seqs);
+  P.programs = (int32_t)programs_of(a->num_tokens, a->num_seqs);
+  int64_t reach = 64;
+  while (reach < a->num_seqs) reach *= 64;
+  P.search_top = (int32_t)(reach / 64);
+  P.scale = (float)(std::fabs(a->scale) * 1.4426950408889634074);
+  P.flip = a->scale < 0 ? 0x80008000u : 0u;
+  P.causal = a->causal != 0;
+  const bool wide = std::max(a->key_dim, a->value_dim) > 64, rope = a->rope_dim > 32;
+  P.plain = P.dim == (wide ? 128 : 64) && P.vdim == P.dim && P.rope == (rope ? 64 : 32);
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (a->dtype == KDACONV_BF16)
+    launch<KDACONV_BF16>(P, wide, rope, waves, st);
+  else
+    launch<KDACONV_F16>(P, wide, rope, waves, st);
+  return hipGetLastError() == hipSuccess ? KDACONV_OK : KDACONV_ELAUNCH;
+}
