@@ -17,7 +17,7 @@ struct ExpandParams {
   char* out;  // (tokens, heads, value channels), contiguous
   const int32_t* qsl;
   const int32_t* ksl;
-  int64_t q_ts, q_hs, k_ts, k_hs, kr_ts, v_ts, v_hs;  // bytes
+  int64_t q_ts, q_hs, k_ts, k_hs, kr_ts, v_ts, v_hs;  // bytes; kr_ts is k_ts if rope is 0
   int32_t tokens, keys, seqs, heads;
   int32_t dim, rope, vdim;
   int32_t programs;  // blocks of rows: sequence s owns v(s) = s + start of s / rows up to v(s + 1)
@@ -25,7 +25,6 @@ struct ExpandParams {
   float scale;  // times log2(e), not negative
   uint32_t flip;  // the queries' sign bits, where the scale was
   bool causal;
-  bool plain;  // all channels are there: dim, rope and vdim are the kernel's
 };
 
 template <int kF, int kDim, int kRope, int kWaves>

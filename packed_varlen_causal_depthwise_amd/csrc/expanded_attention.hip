@@ -97,7 +97,7 @@ extern "C" int kdaconv_expanded_attention(const kdaconv_expanded_args* a, kdacon
   P.q_hs = a->q_stride1 * 2 * heads;
   P.k_ts = a->k_stride0 * 2 * keys;
   P.k_hs = a->k_stride1 * 2 * heads;
-  P.kr_ts = a->kr_stride0 * 2 * keys;
+  P.kr_ts = (a->rope_dim > 0 ? a->kr_stride0 : a->k_stride0) * 2 * keys;
   P.v_ts = a->v_stride0 * 2 * keys;
   P.v_hs = a->v_stride1 * 2 * heads;
   P.tokens = (int32_t)a->num_tokens;
@@ -116,7 +116,6 @@ extern "C" int kdaconv_expanded_attention(const kdaconv_expanded_args* a, kdacon
   P.flip = a->scale < 0 ? 0x80008000u : 0u;
   P.causal = a->causal != 0;
   const bool wide = std::max(a->key_dim, a->value_dim) > 64, rope = a->rope_dim > 32;
-  P.plain = P.dim == (wide ? 128 : 64) && P.vdim == P.dim && P.rope == (rope ? 64 : 32);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   if (a->dtype == KDACONV_BF16)
     launch<KDACONV_BF16>(P, wide, rope, waves, st);
