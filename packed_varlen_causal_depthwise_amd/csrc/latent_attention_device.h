@@ -267,10 +267,11 @@ struct Staged {
   using T = Tile<kLatent, kKeys>;
   static constexpr int kChunks = kLatent / 16, kPer = 64 / kChunks;  // chunks of 16 codes per row, rows per load
   static constexpr int kLoads = (kRows + kPer - 1) / kPer;
-  u32x4 codes[kLoads], rope;
-  uint32_t scales[kLoads];
+  // A step's registers: codes, the rotated part, scales.
+  static constexpr int kRegisters = kLoads + 1 + (kLoads + 3) / 4;
 
-  __device__ __forceinline__ void issue(const AttendParams& P, const Keys<true>& K, int first, int wave, int lane) {
+  static __device__ __forceinline__ void issue(const AttendParams& P, const Keys<true>& K, int first, int wave, int lane,
+                                               u32x4* set) {
     lane = (int)fresh(lane);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
@@ -278,40 +279,35 @@ struct Staged {
       const char* const base = K.row_of(K.lat, first + row);
       const uint8_t* const scale = K.row_of(K.sc, first + row);
       const bool in = c * 16 < P.C.latent;
-      codes[i] = *(const u32x4*)(in ? base + c * 16 : (const char*)kZeros);
-      scales[i] = *(in ? scale + c / 2 : (const uint8_t*)kZeros);
+      set[i] = *(const u32x4*)(in ? base + c * 16 : (const char*)kZeros);
+      set[kLoads + 1 + i / 4][i % 4] = *(in ? scale + c / 2 : (const uint8_t*)kZeros);
     }
     const int row = wave * kRows + lane / 8 % kRows, c = lane % 8;
     const char* const base = K.row_of(K.rop, first + row);
-    rope = *(const u32x4*)(c * 8 < P.C.rope ? base + c * 16 : (const char*)kZeros);
+    set[kLoads] = *(const u32x4*)(c * 8 < P.C.rope ? base + c * 16 : (const char*)kZeros);
   }
 
-  __device__ __forceinline__ void land(lds_char* to, int wave, int lane) const {
+  static __device__ __forceinline__ void land(lds_char* to, int wave, int lane, const u32x4* set) {
     lane = (int)fresh(lane);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int row = wave * kRows + i * kPer + lane / kChunks, c = lane % kChunks;
-      const float f = scale_value(scales[i]);
+      const float f = scale_value(set[kLoads + 1 + i / 4][i % 4]);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float v[8];
+        u32x4 v;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(codes[i][2 * h + j], false);
-          const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(codes[i][2 * h + j], true);
-          v[4 * j] = f * a.x;
-          v[4 * j + 1] = f * a.y;
-          v[4 * j + 2] = f * b.x;
-          v[4 * j + 3] = f * b.y;
+          v[2 * j] = scaled_pair<kF, false>(set[i][2 * h + j], f);
+          v[2 * j + 1] = scaled_pair<kF, true>(set[i][2 * h + j], f);
         }
         if (kRows % kPer == 0 || lane / kChunks < kRows)
-          *(__attribute__((address_space(3))) u32x4*)(to + row * T::kRow + ((2 * c + h) ^ T::latent_flip(row)) * 16) =
-              pack_eight<kF>(v);
+          *(__attribute__((address_space(3))) u32x4*)(to + row * T::kRow + ((2 * c + h) ^ T::latent_flip(row)) * 16) = v;
       }
     }
     const int row = wave * kRows + lane / 8 % kRows, c = lane % 8;
     if (lane < kRows * 8)
-      *(__attribute__((address_space(3))) u32x4*)(to + T::kRopes + row * T::kRope + (c ^ T::rope_flip(row)) * 16) = rope;
+      *(__attribute__((address_space(3))) u32x4*)(to + T::kRopes + row * T::kRope + (c ^ T::rope_flip(row)) * 16) = set[kLoads];
   }
 };
 
@@ -326,7 +322,8 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
   constexpr int kBlocks = kKeys / 16, kPart = kQ * kBlocks > kAttendWaves ? kQ * kBlocks / kAttendWaves : 1;
   // Weights: rows of kKeys 16-bit values, chunks flipped as rotated parts are.
   constexpr int kWeightRow = kKeys * 2, kFlips = kKeys / 8;
-  __shared__ __attribute__((aligned(16))) char memory[kRing * T::kBytes];
+  __shared__ __attribute__((aligned(1024))) char memory[kRing * T::kBytes];
+  static_assert(T::kBytes % 1024 == 0 && T::kRow % 256 == 0 && kColumns <= 4);
   __shared__ __attribute__((aligned(16))) char weights[kRows * kWeightRow];
   __shared__ __attribute__((aligned(16))) float tops[kRows][kBlocks];  // a step's largest scores
   __shared__ __attribute__((aligned(16))) char room[96];
@@ -340,6 +337,11 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
   constexpr int kIdle = kAttendWaves - kQ * kBlocks / kPart;
   constexpr int kLoaders = kIdle == 0 ? kAttendWaves : kE4m3 ? 4 : kIdle, kShare = kKeys / kLoaders;
   const int loader = wave - (kAttendWaves - kLoaders);
+  // Of 8-bit keys kSets steps are under way to registers, of waves that hold no queries where
+  // there are such.
+  using Load = Staged<kF, kLatent, kKeys, kShare>;
+  constexpr int kSets = kKeys == 64 ? 1 : 3, kSetsHold = kE4m3 ? kSets * Load::kRegisters : 0;
+  constexpr int kHold = kIdle > 0 ? (kSetsHold > kSteps + 2 ? kSetsHold : kSteps + 2) : kSteps + 2 + kSetsHold;
   Place from, to;
   const Parts parts = find_part<kRows, kKeys>(P, room, from, to);
   const int w = blockIdx.x;
@@ -348,23 +350,19 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
 
   const auto flip_weight = [](int row) { return kFlips == 8 ? (row >> 1) & 7 : (row >> 2) & 3; };
   lds_char* const tiles = (lds_char*)memory;
-  const lds_char* key_at[4];  // chunk 4 k + g of row 16 kb + n, for k % 4
-  const lds_char* rope_at[2];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) key_at[k] = tiles + (16 * kb + n) * T::kRow + ((4 * k + g) ^ T::latent_flip(n)) * 16;
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    rope_at[k] = tiles + T::kRopes + (16 * kb + n) * T::kRope + ((4 * k + g) ^ T::rope_flip(n)) * 16;
+  // (A flip and a chunk's number are joined by xor, and tiles begin at multiples of 1024 bytes: so
+  // chunk 4 k + g of a row is at (place of chunk g) ^ 64 k, and block c of columns at (place of
+  // the wave's first) ^ 32 c.)
+  const uint32_t key_at = (16 * kb + n) * T::kRow + (g ^ T::latent_flip(n)) * 16;
+  const uint32_t rope_at = T::kRopes + (16 * kb + n) * T::kRope + (g ^ T::rope_flip(n)) * 16;
   // Columns: rows 8 g + n / 4 (the step's first 4 of 8) and 4 more, this wave's first block.
-  const lds_char* column_at[2][kColumns];
+  uint32_t column_at[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int c = 0; c < kColumns; ++c) {
-      const int row = 8 * g + 4 * i + n / 4;
-      column_at[i][c] = tiles + row * T::kRow +
-                        ((2 * (wave * kColumns + c) + n % 4 / 2) ^ T::latent_flip(row)) * 16 + n % 2 * 8;
-    }
+  for (int i = 0; i < 2; ++i) {
+    const int row = 8 * g + 4 * i + n / 4;
+    column_at[i] = row * T::kRow + ((2 * wave * kColumns + n % 4 / 2) ^ T::latent_flip(row)) * 16 + n % 2 * 8;
+  }
+  const auto flipped = [&](uint32_t at, uint32_t by) { return tiles + (at ^ by); };
 
   // Rotated parts that are never loaded are zeros.
   if (P.C.rope == 0) {
@@ -400,22 +398,22 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
     const int count = ((t1 << P.shift) < last ? t1 << P.shift : last) - begin;
     const int first_key = begin * kKeys;
 
-    u32x4 qf[kSteps], qx[2];
+    u32x4 held[kHold];  // queries: chunks of 32 channels, then two of the rotated part
     if (scores) {
       const char* const a = P.ql + (start + token) * P.ql_ts + head * P.ql_hs;
       const char* const b = P.qr + (start + token) * P.qr_ts + head * P.qr_hs;
       const int c = (int)fresh(g * 8);
 #pragma unroll
       for (int k = 0; k < kSteps; ++k)
-        qf[k] = *(const u32x4_any*)(live && k * 32 + c < P.C.latent ? a + (k * 32 + c) * 2 : (const char*)kZeros);
+        held[k] = *(const u32x4_any*)(live && k * 32 + c < P.C.latent ? a + (k * 32 + c) * 2 : (const char*)kZeros);
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        qx[k] = *(const u32x4_any*)(live && k * 32 + c < P.C.rope ? b + (k * 32 + c) * 2 : (const char*)kZeros);
+        held[kSteps + k] = *(const u32x4_any*)(live && k * 32 + c < P.C.rope ? b + (k * 32 + c) * 2 : (const char*)kZeros);
       // (They arrive here. Else every step would wait for them, and for the steps under way.)
 #pragma unroll
-      for (int k = 0; k < kSteps; ++k) asm volatile("" : "+v"(qf[k]));
-      asm volatile("" : "+v"(qx[0]), "+v"(qx[1]));
+      for (int k = 0; k < kSteps + 2; ++k) asm volatile("" : "+v"(held[k]));
     }
+    u32x4* const set = held + (kIdle > 0 ? 0 : kSteps + 2);
     f32x4 O[kColumns][kQ];
 #pragma unroll
     for (int c = 0; c < kColumns; ++c)
@@ -430,8 +428,9 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
     const auto work = [&](int step, int slot) {
       const int off = slot * T::kBytes, key = first_key + step * kKeys;
       const uint64_t mask = masks[step & 3];
-      float x[kPart][4];
+      float x[kPart][4], sum;
       const auto weigh = [&]() {
+        sum = 0.0f;
 #pragma unroll
         for (int b = 0; b < kPart; ++b) {
           const f32x2 lo = {exp2_hw(x[b][0] - my_top), exp2_hw(x[b][1] - my_top)};
@@ -440,22 +439,22 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
           char* const p = weights + r * kWeightRow + (chunk ^ flip_weight(r)) * 16 + g % 2 * 8;
           Pair<kF>::store(p, lo);
           Pair<kF>::store(p + 4, hi);
-          x[b][0] = lo.x, x[b][1] = lo.y, x[b][2] = hi.x, x[b][3] = hi.y;
+          sum += (lo.x + lo.y) + (hi.x + hi.y);
         }
       };
-      float raw[kPart][4];
       if (scores) {
-        f32x4 S[kPart][2];
+        constexpr int kChains = kPart == 1 ? 2 : 1;  // (products that follow one another wait)
+        f32x4 S[kPart][kChains];
 #pragma unroll
         for (int b = 0; b < kPart; ++b)
-          for (int j = 0; j < 2; ++j) S[b][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          for (int j = 0; j < kChains; ++j) S[b][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         // Operands are read a batch ahead of their products. (Left alone the compiler reads one,
         // waits for it and uses it.)
         constexpr int kAll = (kSteps + 2) * kPart, kBatch = kQ == 4 || kE4m3 ? 4 : 6;
         const auto operand = [&](int i) {
           const int k = i / kPart, b = i % kPart;
-          return k < kSteps ? lds_read16(key_at[k % 4] + off + b * 16 * T::kRow + k / 4 * 256)
-                            : lds_read16(rope_at[k - kSteps] + off + b * 16 * T::kRope);
+          return k < kSteps ? lds_read16(flipped(key_at + off, k % 4 * 64) + b * 16 * T::kRow + k / 4 * 256)
+                            : lds_read16(flipped(rope_at + off, (k - kSteps) * 64) + b * 16 * T::kRope);
         };
         u32x4 a[2][kBatch];
 #pragma unroll
@@ -470,7 +469,7 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
           for (int i = 0; i < kBatch; ++i) {
             if (j + i >= kAll) break;
             const int k = (j + i) / kPart, b = (j + i) % kPart;
-            S[b][k % 2] = mfma_16x16x32<kF>(a[j / kBatch % 2][i], k < kSteps ? qf[k] : qx[k - kSteps], S[b][k % 2]);
+            S[b][k % kChains] = mfma_16x16x32<kF>(a[j / kBatch % 2][i], held[k], S[b][k % kChains]);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -480,12 +479,11 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
           float high = -__builtin_huge_valf();
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            x[b][i] = (S[b][0][i] + S[b][1][i]) * P.scale;
+            x[b][i] = (kChains == 1 ? S[b][0][i] : S[b][0][i] + S[b][kChains - 1][i]) * P.scale;
             const int k = (kb + b) * 16 + 4 * g + i;
             if (mask != ~0ull >> (64 - kKeys) || key + kKeys > least)
               x[b][i] = ((mask >> k) & 1) && key + k < reach ? x[b][i] : -__builtin_huge_valf();
             high = __builtin_fmaxf(high, x[b][i]);
-            raw[b][i] = x[b][i];
           }
           high = __builtin_fmaxf(high, __shfl_xor(high, 16));
           high = __builtin_fmaxf(high, __shfl_xor(high, 32));
@@ -519,18 +517,11 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
           for (int b = 0; b < kBlocks; ++b) next = __builtin_fmaxf(next, tops[q * 16 + n][b]);
           weight *= exp2_hw(my_top - next);
           my_top = next;
-#pragma unroll
-          for (int b = 0; b < kPart; ++b)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[b][i] = raw[b][i];
           weigh();
         }
         lds_barrier();
       }
-      if (scores) {
-#pragma unroll
-        for (int b = 0; b < kPart; ++b) weight += (x[b][0] + x[b][1]) + (x[b][2] + x[b][3]);
-      }
+      if (scores) weight += sum;
       // Rows that do not see a key have weight 0 for it, but 0 times NaN is NaN: where rows differ
       // in what they see, values that are not finite become zeros. (The rows that see one have
       // a score that is not finite.)
@@ -552,8 +543,8 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
         }
 #pragma unroll
         for (int c = 0; c < kColumns; ++c) {
-          u[c] = lds_read_columns(column_at[0][c] + off + k * 32 * T::kRow);
-          v[c] = lds_read_columns(column_at[1][c] + off + k * 32 * T::kRow);
+          u[c] = lds_read_columns(flipped(column_at[0] + off, c * 32) + k * 32 * T::kRow);
+          v[c] = lds_read_columns(flipped(column_at[1] + off, c * 32) + k * 32 * T::kRow);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -575,8 +566,6 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
     if (count > 0) {
       if constexpr (kE4m3) {
         // kSets steps are under way to registers; the next goes to LDS beside the present one.
-        constexpr int kSets = kKeys == 64 ? 1 : 3;
-        Staged<kF, kLatent, kKeys, kShare> set[kSets];
         for (int base = -kSets; base < count; base += kSets) {
 #pragma unroll
           for (int j = 0; j < kSets; ++j) {
@@ -584,11 +573,12 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
             if (i >= count) break;
             if (i >= 0) lds_barrier();  // step i is in LDS, and everyone is done with step i - 1
             if (loader >= 0) {
-              set[j].issue(P, find, find_step(i + kSets), loader, lane);
-              if (kSets > 1 && i >= -1) set[(j + 1) % kSets].land(tiles + ((i + 1) & 1) * T::kBytes, loader, lane);
+              Load::issue(P, find, find_step(i + kSets), loader, lane, set + j * Load::kRegisters);
+              if (kSets > 1 && i >= -1) 
+                Load::land(tiles + ((i + 1) & 1) * T::kBytes, loader, lane, set + (j + 1) % kSets * Load::kRegisters);
             }
             if (i >= 0) work(i, i & 1);
-            if (kSets == 1 && loader >= 0) set[0].land(tiles + ((i + 1) & 1) * T::kBytes, loader, lane);
+            if (kSets == 1 && loader >= 0) Load::land(tiles + ((i + 1) & 1) * T::kBytes, loader, lane, set);
           }
         }
       } else {

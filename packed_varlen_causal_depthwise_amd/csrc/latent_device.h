@@ -92,6 +92,16 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
   return __builtin_bit_cast(float, byte == 255 ? 0x7FC00000u : byte == 0 ? 0x00400000u : byte << 23);
 }
 
+// Two e4m3 codes, the lower or upper half of a word, times a scale: what scale_value(byte) times
+// the code's value is when rounded once to 16 bits, for all codes and bytes.
+template <int kF, bool kHigh>
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t codes, float scale) {
+  if constexpr (kF == kRuleBF16)
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, kHigh));
+  else
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, scale, kHigh));
+}
+
 }  // namespace kdaconv
 
 #endif  // KDACONV_LATENT_DEVICE_H_
