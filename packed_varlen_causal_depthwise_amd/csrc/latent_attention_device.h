@@ -612,7 +612,7 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
     float* const mine = P.partial + part.floats() * (2 * w + (ends ? 0 : 1));
 #pragma unroll
     for (int i = 0; i < kQ; ++i) {
-      const int r = i * 16 + n;
+      const int r = i * 16 + (kQ == 4 ? (int)fresh(n) : n);
       float total = tops[r][0];
 #pragma unroll
       for (int j = 1; j < kSums; ++j) total += tops[r][j];
@@ -624,7 +624,7 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
       if (at.b * kRows + r < rows) {
 #pragma unroll
         for (int c = 0; c < kColumns; ++c) {
-          const int column = (wave * kColumns + c) * 16 + 4 * g;
+          const int column = (wave * kColumns + c) * 16 + 4 * (kQ == 4 ? (int)fresh(g) : g);
           if (column >= P.C.latent) break;
           if (whole) {
             const f32x4 v = f * O[c][i];
