@@ -261,37 +261,39 @@ struct Direct {
 };
 
 // 8 bits by way of registers, where they become 16-bit values (exactly, within fp16's range: 4
-// bits times a power of two).
-template <int kF, int kLatent, int kKeys, int kRows>
+// bits times a power of two). A wave takes 8 rows, of each 8 lanes every eighth chunk of 16 codes:
+// a row's addresses are found once, and the chunks' flips are the same for all of a lane's.
+template <int kF, int kLatent, int kKeys>
 struct Staged {
   using T = Tile<kLatent, kKeys>;
-  static constexpr int kChunks = kLatent / 16, kPer = 64 / kChunks;  // chunks of 16 codes per row, rows per load
-  static constexpr int kLoads = (kRows + kPer - 1) / kPer;
+  static constexpr int kRows = 8, kLoads = kLatent / 128;
   // A step's registers: codes, the rotated part, scales.
   static constexpr int kRegisters = kLoads + 1 + (kLoads + 3) / 4;
+  template <class X>
+  using Global = const __attribute__((address_space(1))) X*;
 
   static __device__ __forceinline__ void issue(const AttendParams& P, const Keys<true>& K, int first, int wave, int lane,
                                                u32x4* set) {
-    lane = (int)fresh(lane);
+    const uint32_t at = fresh(lane), c = at % 8, row = first + wave * kRows + at / 8;
+    const auto codes = (Global<char>)K.row_of(K.lat, row), rope = (Global<char>)K.row_of(K.rop, row);
+    const auto scales = (Global<uint8_t>)K.row_of(K.sc, row);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int row = wave * kRows + i * kPer + lane / kChunks, c = lane % kChunks;
-      const char* const base = K.row_of(K.lat, first + row);
-      const uint8_t* const scale = K.row_of(K.sc, first + row);
-      const bool in = c * 16 < P.C.latent;
-      set[i] = *(const u32x4*)(in ? base + c * 16 : (const char*)kZeros);
-      set[kLoads + 1 + i / 4][i % 4] = *(in ? scale + c / 2 : (const uint8_t*)kZeros);
+      // (Past the end the first chunk: queries are zero there, and no sum is taken.)
+      const uint32_t chunk = (c + 8 * i) * 16 < (uint32_t)P.C.latent ? c + 8 * i : 0;
+      set[i] = *(Global<u32x4>)(codes + chunk * 16);
+      set[kLoads + 1 + i / 4][i % 4] = scales[chunk / 2];
     }
-    const int row = wave * kRows + lane / 8 % kRows, c = lane % 8;
-    const char* const base = K.row_of(K.rop, first + row);
-    set[kLoads] = *(const u32x4*)(c * 8 < P.C.rope ? base + c * 16 : (const char*)kZeros);
+    const auto zeros = (Global<char>)(const char*)kZeros;
+    set[kLoads] = *(Global<u32x4>)(c * 8 < (uint32_t)P.C.rope ? rope + c * 16 : zeros);
   }
 
   static __device__ __forceinline__ void land(lds_char* to, int wave, int lane, const u32x4* set) {
-    lane = (int)fresh(lane);
+    typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+    const uint32_t at = fresh(lane), c = at % 8, row = wave * kRows + at / 8;
+    const uint32_t even = row * T::kRow + ((2 * c) ^ T::latent_flip(row)) * 16;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int row = wave * kRows + i * kPer + lane / kChunks, c = lane % kChunks;
       const float f = scale_value(set[kLoads + 1 + i / 4][i % 4]);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -301,13 +303,10 @@ struct Staged {
           v[2 * j] = scaled_pair<kF, false>(set[i][2 * h + j], f);
           v[2 * j + 1] = scaled_pair<kF, true>(set[i][2 * h + j], f);
         }
-        if (kRows % kPer == 0 || lane / kChunks < kRows)
-          *(__attribute__((address_space(3))) u32x4*)(to + row * T::kRow + ((2 * c + h) ^ T::latent_flip(row)) * 16) = v;
+        *(lds_u32x4*)(to + (even ^ (h * 16)) + i * 256) = v;
       }
     }
-    const int row = wave * kRows + lane / 8 % kRows, c = lane % 8;
-    if (lane < kRows * 8)
-      *(__attribute__((address_space(3))) u32x4*)(to + T::kRopes + row * T::kRope + (c ^ T::rope_flip(row)) * 16) = set[kLoads];
+    *(lds_u32x4*)(to + T::kRopes + row * T::kRope + (c ^ T::rope_flip(row)) * 16) = set[kLoads];
   }
 };
 
@@ -335,11 +334,12 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
   const bool scores = kb < kBlocks;  // this wave takes part in them
   // Where some waves do not, they load (8 bits: four of them, with equal shares).
   constexpr int kIdle = kAttendWaves - kQ * kBlocks / kPart;
-  constexpr int kLoaders = kIdle == 0 ? kAttendWaves : kE4m3 ? 4 : kIdle, kShare = kKeys / kLoaders;
+  constexpr int kLoaders = kIdle == 0 ? kAttendWaves : kE4m3 ? 4 : kIdle;
   const int loader = wave - (kAttendWaves - kLoaders);
   // Of 8-bit keys kSets steps are under way to registers, of waves that hold no queries where
   // there are such.
-  using Load = Staged<kF, kLatent, kKeys, kShare>;
+  using Load = Staged<kF, kLatent, kKeys>;
+  static_assert(!kE4m3 || kKeys == kLoaders * Load::kRows);
   constexpr int kSets = kKeys == 64 ? 1 : 3, kSetsHold = kE4m3 ? kSets * Load::kRegisters : 0;
   constexpr int kHold = kIdle > 0 ? (kSetsHold > kSteps + 2 ? kSetsHold : kSteps + 2) : kSteps + 2 + kSetsHold;
   Place from, to;
