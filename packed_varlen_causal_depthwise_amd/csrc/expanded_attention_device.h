@@ -110,7 +110,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(kWa
     for (int k = 0; k < kAll; ++k) {
       const int c = (k < kOwn ? k : k - kOwn) * 16 + 8 * h;
       const bool there = live && c < (k < kOwn ? P.dim : P.rope);
-      qf[k] = *(const u32x4_any*)(there ? q + (k < kOwn ? c : P.dim + c) * 2 : (const char*)kZeros);
+      qf[k] = *(Global<u32x4_any>)(there ? q + (k < kOwn ? c : P.dim + c) * 2 : (const char*)kZeros);
     }
 #pragma unroll
     for (int k = 0; k < kAll; ++k)

@@ -269,8 +269,6 @@ struct Staged {
   static constexpr int kRows = 8, kLoads = kLatent / 128;
   // A step's registers: codes, the rotated part, scales.
   static constexpr int kRegisters = kLoads + 1 + (kLoads + 3) / 4;
-  template <class X>
-  using Global = const __attribute__((address_space(1))) X*;
 
   static __device__ __forceinline__ void issue(const AttendParams& P, const Keys<true>& K, int first, int wave, int lane,
                                                u32x4* set) {
@@ -405,10 +403,10 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
       const int c = (int)fresh(g * 8);
 #pragma unroll
       for (int k = 0; k < kSteps; ++k)
-        held[k] = *(const u32x4_any*)(live && k * 32 + c < P.C.latent ? a + (k * 32 + c) * 2 : (const char*)kZeros);
+        held[k] = *(Global<u32x4_any>)(live && k * 32 + c < P.C.latent ? a + (k * 32 + c) * 2 : (const char*)kZeros);
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        held[kSteps + k] = *(const u32x4_any*)(live && k * 32 + c < P.C.rope ? b + (k * 32 + c) * 2 : (const char*)kZeros);
+        held[kSteps + k] = *(Global<u32x4_any>)(live && k * 32 + c < P.C.rope ? b + (k * 32 + c) * 2 : (const char*)kZeros);
       // (They arrive here. Else every step would wait for them, and for the steps under way.)
 #pragma unroll
       for (int k = 0; k < kSteps + 2; ++k) asm volatile("" : "+v"(held[k]));
