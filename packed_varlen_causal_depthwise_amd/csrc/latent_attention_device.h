@@ -226,10 +226,9 @@ struct Direct {
   static constexpr int kTurns = (kAll + kLoaders - 1) / kLoaders;
   static constexpr int kLeast = kLatents / kLoaders;  // of every wave, whatever the sizes
 
-  // `base`: the lane that has the step's first key.
+  // Turns `begin` to `end` of this wave. `base`: the lane that has the step's first key.
   static __device__ __forceinline__ void issue(const AttendParams& P, const Keys<false>& K, int base, lds_char* to,
-                                               int loader, int lane) {
-    lane = (int)fresh(lane);
+                                               int loader, int lane, int begin, int end) {
     // Flips reach 16 chunks. Where latents end at a multiple of them a lane is past the end by
     // its number alone: it reads the first chunks (queries are zero there, and no sum is taken).
     const bool even = P.C.latent % 128 == 0;
@@ -237,6 +236,7 @@ struct Direct {
     const uint32_t at = (c * 8 < P.C.latent ? c : c % 16) * 16;
 #pragma unroll
     for (int j = 0; j < kTurns; ++j) {
+      if (j < begin || j >= end) continue;
       const int i = loader + j * kLoaders;
       if (i < kLatents) {
         const int first = i * kPer, row = first + (kPer == 1 ? 0 : lane / kChunks);
@@ -422,8 +422,10 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
     for (int i = 0; i < kQ; ++i) top[i] = kLowest;
     float my_top = kLowest, weight = 0.0f;  // of this lane's query: row q * 16 + n
 
+    constexpr int kAll = (kSteps + 2) * kPart, kBatch = kQ == 4 ? 3 : kE4m3 ? 4 : 6, kBatches = (kAll + kBatch - 1) / kBatch;
     // One step, in ring place `slot`; everyone's share of it has arrived.
-    const auto work = [&](int step, int slot) {
+    // `send(j)`, for j below kBatches, is called along the scores.
+    const auto work = [&](int step, int slot, auto send) {
       const int off = slot * T::kBytes, key = first_key + step * kKeys;
       const uint64_t mask = masks[step & 3];
       float x[kPart][4], sum;
@@ -448,7 +450,6 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
           for (int j = 0; j < kChains; ++j) S[b][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         // Operands are read a batch ahead of their products. (Left alone the compiler reads one,
         // waits for it and uses it.)
-        constexpr int kAll = (kSteps + 2) * kPart, kBatch = kQ == 4 || kE4m3 ? 4 : 6;
         const auto operand = [&](int i) {
           const int k = i / kPart, b = i % kPart;
           return k < kSteps ? lds_read16(flipped(key_at + off, k % 4 * 64) + b * 16 * T::kRow + k / 4 * 256)
@@ -459,6 +460,7 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
         for (int i = 0; i < kBatch; ++i) a[0][i] = operand(i);
 #pragma unroll
         for (int j = 0; j < kAll; j += kBatch) {
+          send(j / kBatch);
 #pragma unroll
           for (int i = 0; i < kBatch; ++i)
             if (j + kBatch + i < kAll) a[(j / kBatch + 1) % 2][i] = operand(j + kBatch + i);
@@ -575,7 +577,7 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
               if (kSets > 1 && i >= -1) 
                 Load::land(tiles + ((i + 1) & 1) * T::kBytes, loader, lane, set + (j + 1) % kSets * Load::kRegisters);
             }
-            if (i >= 0) work(i, i & 1);
+            if (i >= 0) work(i, i & 1, [](int) {});
             if (kSets == 1 && loader >= 0) Load::land(tiles + ((i + 1) & 1) * T::kBytes, loader, lane, set);
           }
         }
@@ -588,11 +590,24 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
             asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kRing - 2) * D::kLeast) : "memory");
             lds_barrier();
           }
-          if (loader >= 0) {
-            const int ahead = i + kRing - 1;
-            D::issue(P, find, find_step(ahead), tiles + (ahead & (kRing - 1)) * T::kBytes, loader, lane);
+          const int ahead = i + kRing - 1;
+          lds_char* const to = tiles + (ahead & (kRing - 1)) * T::kBytes;
+          if constexpr (kIdle > 0) {
+            if (loader >= 0) D::issue(P, find, find_step(ahead), to, loader, (int)fresh(lane), 0, D::kTurns);
+            if (i >= 0) work(i, i & (kRing - 1), [](int) {});
+          } else {
+            // A wave that sends faster than the loads are taken (1 KB in some 45 cycles of a CU)
+            // stands: waves that have scores to do send along them.
+            const int base = find_step(ahead), anew = (int)fresh(lane);
+            const auto send = [&](int batch) {
+              D::issue(P, find, base, to, loader, anew, (batch * D::kTurns + kBatches - 1) / kBatches,
+                       ((batch + 1) * D::kTurns + kBatches - 1) / kBatches);
+            };
+            if (i >= 0)
+              work(i, i & (kRing - 1), send);
+            else
+              D::issue(P, find, base, to, loader, anew, 0, D::kTurns);
           }
-          if (i >= 0) work(i, i & (kRing - 1));
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       }
