@@ -564,12 +564,20 @@ typedef struct kdaconv_expanded_args {
 
 /* The launch depends on host sizes alone, so a call can be captured in a graph. num_tokens,
  * num_seqs or num_heads of 0: KDACONV_OK with no launch. (num_tokens / 128 + num_seqs) *
- * num_heads is below 2^23 (else EUNSUPPORTED). No scratch memory. */
-int kdaconv_expanded_attention(const kdaconv_expanded_args* args, kdaconv_stream_t stream);
+ * num_heads is below 2^23 (else EUNSUPPORTED). workspace is device memory of at least
+ * kdaconv_expanded_attention_workspace bytes, none where that is 0 (else EINVAL), aligned to 256
+ * bytes (else EUNSUPPORTED); it holds nothing between calls, but no two calls in flight share it. */
+int kdaconv_expanded_attention(const kdaconv_expanded_args* args, void* workspace,
+                               int64_t workspace_bytes, kdaconv_stream_t stream);
+
+/* Bytes of scratch memory: 0 but for few rows over many keys, whose keys are split. */
+int64_t kdaconv_expanded_attention_workspace(int64_t num_tokens, int64_t num_keys, int64_t num_seqs,
+                                             int64_t num_heads, int64_t value_dim);
 
 /* The status the call would return before launching. No HIP call; device pointers are only
  * compared with NULL and tested for alignment. */
-int kdaconv_expanded_attention_validate(const kdaconv_expanded_args* args);
+int kdaconv_expanded_attention_validate(const kdaconv_expanded_args* args, const void* workspace,
+                                        int64_t workspace_bytes);
 
 /* Static English text for a status code. Never NULL. */
 const char* kdaconv_status_string(int status);

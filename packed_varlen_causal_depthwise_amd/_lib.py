@@ -46,6 +46,7 @@ EXPORTS = (
     "kdaconv_latent_attention_workspace",
     "kdaconv_expanded_attention",
     "kdaconv_expanded_attention_validate",
+    "kdaconv_expanded_attention_workspace",
     "kdaconv_status_string",
     "kdaconv_version",
 )
@@ -147,9 +148,11 @@ def load() -> ctypes.CDLL:
     lib.kdaconv_latent_attention_validate.restype = i32
     lib.kdaconv_latent_attention_workspace.argtypes = [i64, i64, i64, i64]
     lib.kdaconv_latent_attention_workspace.restype = i64
-    lib.kdaconv_expanded_attention.argtypes = [packed, vp]
+    lib.kdaconv_expanded_attention.argtypes = [packed, vp, i64, vp]
     lib.kdaconv_expanded_attention.restype = i32
-    lib.kdaconv_expanded_attention_validate.argtypes = [packed]
+    lib.kdaconv_expanded_attention_workspace.argtypes = [i64, i64, i64, i64, i64]
+    lib.kdaconv_expanded_attention_workspace.restype = i64
+    lib.kdaconv_expanded_attention_validate.argtypes = [packed, vp, i64]
     lib.kdaconv_expanded_attention_validate.restype = i32
     lib.kdaconv_status_string.argtypes = [i32]
     lib.kdaconv_status_string.restype = ctypes.c_char_p

@@ -25,6 +25,16 @@ struct ExpandParams {
   float scale;  // times log2(e), not negative
   uint32_t flip;  // the queries' sign bits, where the scale was
   bool causal;
+  int32_t splits;  // parts of a block's keys, each a workgroup's
+  float* partial;  // if there are several: per program, head and part an ExpandPartial
+};
+
+// A part's sums, then each row's exponent and weight.
+struct ExpandPartial {
+  int rows, channels;
+  __host__ __device__ constexpr int64_t floats() const { return (int64_t)rows * (channels + 2); }
+  __host__ __device__ constexpr int64_t exponent() const { return (int64_t)rows * channels; }
+  __host__ __device__ constexpr int64_t weight() const { return (int64_t)rows * (channels + 1); }
 };
 
 template <int kF, int kDim, int kRope, int kWaves>

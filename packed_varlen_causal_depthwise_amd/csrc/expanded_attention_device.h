@@ -52,6 +52,30 @@ struct Step {
   static constexpr int kShare = 2, kRopeShare = kRope == 64 ? 2 : 1;
 };
 
+// The sequence and block of a program: the largest s with v(s) <= program.
+template <int kRows>
+__device__ __forceinline__ bool find_program(const ExpandParams& P, int program, int lane, int& sequence, int& block) {
+  int s = 0, v = 0;
+  for (int stride = P.search_top; stride > 0; stride >>= 6) {
+    const int i = s + lane * stride;
+    int at = 0;
+    bool ok = i < P.seqs;
+    if (ok) {
+      int a = P.qsl[i];
+      a = a < 0 ? 0 : (a > P.tokens ? P.tokens : a);
+      at = i + a / kRows;
+      ok = at <= program;
+    }
+    const int found = __builtin_popcountll(__ballot(ok));
+    if (found == 0) return false;
+    s += (found - 1) * stride;
+    v = __shfl(at, found - 1);
+  }
+  sequence = uniform(s);
+  block = program - uniform(v);
+  return block >= 0;
+}
+
 template <int kF, int kDim, int kRope, int kWaves>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(kWaves / 4, kWaves / 4))) void expanded_kernel(ExpandParams P) {
   using T = Step<kDim, kRope>;
@@ -67,35 +91,27 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(kWa
   // Long blocks first: they come last in their sequence.
   const int program = P.programs - 1 - (int)(blockIdx.x / (uint32_t)P.heads), head = blockIdx.x % (uint32_t)P.heads;
 
-  // The sequence and block of the program: the largest s with v(s) <= program.
-  int s = 0, v = 0;
-  for (int stride = P.search_top; stride > 0; stride >>= 6) {
-    const int i = s + lane * stride;
-    int at = 0;
-    bool ok = i < P.seqs;
-    if (ok) {
-      int a = P.qsl[i];
-      a = a < 0 ? 0 : (a > P.tokens ? P.tokens : a);
-      at = i + a / kRows;
-      ok = at <= program;
-    }
-    const int found = __builtin_popcountll(__ballot(ok));
-    if (found == 0) return;
-    s += (found - 1) * stride;
-    v = __shfl(at, found - 1);
-  }
-  s = uniform(s);
-  const int block = program - uniform(v);
+  int s, block;
+  if (!find_program<kRows>(P, program, lane, s, block)) return;
   const auto bound = [](int x, int low, int high) { return x < low ? low : (x > high ? high : x); };
   const int start = bound(P.qsl[s], 0, P.tokens), rows = bound(P.qsl[s + 1], start, P.tokens) - start;
-  const int kstart = bound(P.ksl[s], 0, P.keys), keys = bound(P.ksl[s + 1], kstart, P.keys) - kstart;
-  if (block < 0 || block * kRows >= rows) return;
+  int kstart = bound(P.ksl[s], 0, P.keys), keys = bound(P.ksl[s + 1], kstart, P.keys) - kstart;
+  if (block * kRows >= rows) return;
 
   // What rows see: all keys, or those up to the row's own place, counted from the end.
   const int row = block * kRows + wave * kWaveRows + n;
   const bool live = row < rows;
-  const int past = P.causal ? keys - rows + 1 : keys;
+  int past = P.causal ? keys - rows + 1 : keys;
   const auto reach_of = [&](int r) { return P.causal ? bound(past + r, 0, keys) : keys; };
+  if (P.splits > 1) {
+    // This workgroup's part of the block's keys, as though they were all.
+    const int end = reach_of((block + 1) * kRows < rows ? (block + 1) * kRows - 1 : rows - 1);
+    const int64_t all = (end + kExpandKeys - 1) / kExpandKeys;
+    const int from = (int)(all * blockIdx.y / P.splits) * kExpandKeys, to = (int)(all * (blockIdx.y + 1) / P.splits) * kExpandKeys;
+    kstart += from;
+    past -= from;
+    keys = (to < keys ? to : keys) - from;
+  }
   const int reach = reach_of(live ? row : rows - 1);
   const int wave_row = block * kRows + wave * kWaveRows;
   const int least = reach_of(wave_row), most = reach_of(wave_row + kWaveRows < rows ? wave_row + kWaveRows - 1 : rows - 1);
@@ -354,6 +370,29 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(kWa
   const float f = weight == 0.0f ? 0.0f : 1.0f / weight;
   __syncthreads();  // all values that are not finite are known
   if (!live) return;
+  if (P.splits > 1) {
+    const ExpandPartial part{kRows, P.vdim};
+    float* const mine = P.partial + part.floats() * (((int64_t)program * P.heads + head) * P.splits + blockIdx.y);
+    const int r = wave * kWaveRows + n;
+    if (h == 0) {
+      mine[part.exponent() + r] = top;
+      mine[part.weight() + r] = weight;
+    }
+    if (weight == 0.0f) return;  // (its sums are not looked at)
+#pragma unroll
+    for (int c = 0; c < kColumns; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int column = 32 * c + 8 * i + 4 * h;
+        if (column >= P.vdim) continue;
+        f32x4 x = {O[c][4 * i], O[c][4 * i + 1], O[c][4 * i + 2], O[c][4 * i + 3]};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (bad[column + j] < reach) x[j] = __builtin_nanf("");
+        *(f32x4*)(mine + (int64_t)r * P.vdim + column) = x;
+      }
+    return;
+  }
   char* const out = P.out + (((int64_t)(start + row) * P.heads + head) * P.vdim) * 2;
 #pragma unroll
   for (int c = 0; c < kColumns; ++c)
@@ -370,10 +409,51 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(kWa
     }
 }
 
+// Joins the parts of a block's keys: a workgroup per block and head, 8 channels of a row at a time.
+constexpr int kExpandJoinThreads = 256;
+
+template <int kF, int kRows>
+__global__ __launch_bounds__(kExpandJoinThreads) void expanded_join_kernel(ExpandParams P) {
+  const int tid = threadIdx.x, head = blockIdx.x % (uint32_t)P.heads, program = blockIdx.x / (uint32_t)P.heads;
+  int s, block;
+  if (!find_program<kRows>(P, program, tid % 64, s, block)) return;
+  const auto bound = [](int x, int low, int high) { return x < low ? low : (x > high ? high : x); };
+  const int start = bound(P.qsl[s], 0, P.tokens), all = bound(P.qsl[s + 1], start, P.tokens) - start;
+  const int rows = all - block * kRows < kRows ? all - block * kRows : kRows, chunks = P.vdim / 8;
+  const ExpandPartial part{kRows, P.vdim};
+  const float* const parts = P.partial + part.floats() * ((int64_t)blockIdx.x * P.splits);
+  for (int i = blockIdx.y * kExpandJoinThreads + tid; i < rows * chunks; i += kExpandJoinThreads * gridDim.y) {
+    const int r = (int)((uint32_t)i / (uint32_t)chunks), c = i - r * chunks;
+    float high = kLowest, total = 0.0f;
+    for (int k = 0; k < P.splits; ++k) {
+      const float* const p = parts + part.floats() * k;
+      if (p[part.weight() + r] != 0.0f) high = __builtin_fmaxf(high, p[part.exponent() + r]);
+    }
+    f32x4 v[2] = {};
+    for (int k = 0; k < P.splits; ++k) {
+      const float* const p = parts + part.floats() * k;
+      const float l = p[part.weight() + r];
+      if (l == 0.0f) continue;  // no key of this part
+      const float f = exp2_hw(p[part.exponent() + r] - high);
+      const f32x4* const q = (const f32x4*)(p + (int64_t)r * P.vdim + c * 8);
+      total = __builtin_fmaf(f, l, total);
+      v[0] += f * q[0];
+      v[1] += f * q[1];
+    }
+    const float f = total == 0.0f ? 0.0f : 1.0f / total;
+    float o[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = f * v[j / 4][j % 4];
+    store_eight<kF>(P.out + ((((int64_t)start + block * kRows + r) * P.heads + head) * P.vdim + c * 8) * 2, o);
+  }
+}
+
 template <int kF, int kDim, int kRope, int kWaves>
 void launch_expanded(const ExpandParams& P, hipStream_t st) {
-  hipLaunchKernelGGL((expanded_kernel<kF, kDim, kRope, kWaves>), dim3((unsigned)((int64_t)P.programs * P.heads)),
-                     dim3(64 * kWaves), 0, st, P);
+  const unsigned blocks = (unsigned)((int64_t)P.programs * P.heads);
+  hipLaunchKernelGGL((expanded_kernel<kF, kDim, kRope, kWaves>), dim3(blocks, P.splits), dim3(64 * kWaves), 0, st, P);
+  if (P.splits > 1)
+    hipLaunchKernelGGL((expanded_join_kernel<kF, kWaveRows * kWaves>), dim3(blocks, kWaves), dim3(kExpandJoinThreads), 0, st, P);
 }
 
 }  // namespace kdaconv

@@ -7,12 +7,12 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._host import DTYPE_CODES, _call
+from ._host import DTYPE_CODES, _call, _ptr
 from .latent import _loc
 
 
 def _expand(q, k, k_rope, v, query_start_loc, kv_start_loc, scale, causal, out):
-    """Checks, then kdaconv_expanded_args as bytes, the output and whether there is work."""
+    """Checks, then kdaconv_expanded_args as bytes, the output and the call's sizes."""
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or k.shape[:2] != v.shape[:2] or q.shape[1] != k.shape[1]:
         raise ValueError("q must be (tokens, heads, key_dim + rope_dim), k (keys, heads, key_dim) and "
                          "v (keys, heads, value_dim)")
@@ -52,7 +52,7 @@ def _expand(q, k, k_rope, v, query_start_loc, kv_start_loc, scale, causal, out):
         tokens, keys, max(0, seqs), heads, key_dim, rope_dim, value_dim,
         qs[0], qs[1], ks[0], ks[1], rs[0], vs[0], vs[1],
         width ** -0.5 if scale is None else float(scale), DTYPE_CODES[dtype], int(causal))
-    return args, out, tokens > 0 and seqs > 0 and heads > 0
+    return args, out, (tokens, keys, seqs, heads, value_dim)
 
 
 def expanded_attention_fn(
@@ -87,15 +87,21 @@ def expanded_attention_fn(
     A row that sees no key is zero, rows no sequence owns are left unwritten, and a value that is
     not finite reaches no row that does not see it. Scores, softmax and sums are FP32, the weights
     rounded to the dtype for the second product, the result (tokens, heads, value_dim) once.
-    Queued on the current stream; no synchronisation.
+    Few rows over many keys take up to 35 MB of scratch memory from torch's allocator. Queued on the current stream; no synchronisation.
     """
-    args, out, work = _expand(q, k, k_rope, v, query_start_loc, kv_start_loc, scale, causal, out)
-    if not work:
+    args, out, sizes = _expand(q, k, k_rope, v, query_start_loc, kv_start_loc, scale, causal, out)
+    tokens, _, seqs, heads, _ = sizes
+    if tokens == 0 or seqs <= 0 or heads == 0:
         return out
     device = q.get_device()
     if device < 0:
         raise ValueError("q must be a GPU tensor")
-    _lib.check(_call(device, _lib.load().kdaconv_expanded_attention, args), "expanded_attention_fn")
+    lib = _lib.load()
+    need, scratch = lib.kdaconv_expanded_attention_workspace(*sizes), None
+    if need:  # memory of the current stream, as the attention over the cache takes it
+        scratch = torch.empty(need, dtype=torch.uint8, device=out.device)
+    rc = _call(device, lib.kdaconv_expanded_attention, args, _ptr(scratch), need)
+    _lib.check(rc, "expanded_attention_fn")
     return out
 
 
@@ -108,4 +114,4 @@ def expanded_attention_supported(q: torch.Tensor, k: torch.Tensor, k_rope: Optio
         lib = _lib.load()
     except (ValueError, _lib.LibraryMissing):
         return False
-    return q.get_device() >= 0 and lib.kdaconv_expanded_attention_validate(args) == _lib.OK
+    return q.get_device() >= 0 and lib.kdaconv_expanded_attention_validate(args, 256, 1 << 62) == _lib.OK

@@ -5,6 +5,7 @@ import torch
 
 import latent_reference as ref
 import packed_varlen_causal_depthwise_amd as kd
+from packed_varlen_causal_depthwise_amd import _lib
 
 pytestmark = pytest.mark.gpu
 
@@ -188,3 +189,90 @@ def test_empty():
     assert kd.expanded_attention_fn(q[:0], k, kr, v, loc, kv_loc).shape == (0, 2, 64)
     assert kd.expanded_attention_fn(q, k, kr, v, loc[:1], kv_loc[:1]).shape == (3, 2, 64)
     assert kd.expanded_attention_supported(q, k, kr, v) and not kd.expanded_attention_supported(q.cpu(), k, kr, v)
+
+
+def parts(new, lens, heads):
+    """Whether the call splits its keys."""
+    return _lib.load().kdaconv_expanded_attention_workspace(sum(new), sum(lens), len(new), heads, 64) > 0
+
+
+@DTYPES
+@pytest.mark.parametrize("new,lens,heads,sizes", [
+    ([1], [5000], 2, (128, 64, 128)), ([1], [513], 1, (8, 8, 8)), ([33, 1, 0, 128, 7], [5000, 1, 0, 900, 64], 3, (128, 64, 128)),
+    ([300], [6000], 3, (128, 32, 128)), ([400, 300], [400, 7000], 1, (64, 64, 64)), ([129] * 3, [1100, 130, 3000], 4, (40, 0, 104)),
+    ([90, 5], [60, 2000], 2, (64, 32, 64)), ([2] * 60, [700] * 60, 2, (64, 16, 32))])
+@pytest.mark.parametrize("causal", [True, False])
+def test_few_rows_over_many_keys(new, lens, heads, sizes, causal, dtype):
+    """Keys split among workgroups: parts that end inside a block's reach, or see nothing."""
+    assert parts(new, lens, heads)
+    compare(inputs(new, lens, heads, *sizes, dtype), dtype, (new, lens), causal=causal)
+
+
+def test_split_rows_without_keys():
+    new, lens = [5, 3, 40, 2], [2, 0, 5000, 0]
+    assert parts(new, lens, 2)
+    q, k, kr, v, loc, kv_loc = inputs(new, lens, 2, 64, 32, 64, BF16)
+    out = torch.full((q.shape[0] + 3, 2, 64), 7.0, dtype=BF16, device="cuda")
+    got = run((torch.cat([q[:2], q, q[:1]]), k, kr, v, loc + 2, kv_loc), out=out, scale=0.1)
+    assert (got[:2] == 7).all() and (got[-1:] == 7).all()
+    check(got[2:-1], ref.expanded(q, k, kr, v, loc, kv_loc, 0.1), BF16, v.double().abs().max(), "rows")
+    assert (got[2:5] == 0).all() and (got[7:10] == 0).all() and (got[50:52] == 0).all()
+
+
+@DTYPES
+@pytest.mark.parametrize("scale", [2.0, -2.0])
+def test_split_large_scores(scale, dtype):
+    """Scores that rise or fall by 700 along the keys: of most parts nothing is left."""
+    m = 2100
+    q, k, kr, v, loc, kv_loc = inputs([40], [m], 1, 64, 32, 64, dtype)
+    q, k, kr = torch.zeros_like(q), torch.zeros_like(k), kr * 0
+    q[..., 0] = 1.0
+    k[:, 0, 0] = ((torch.arange(m) - m // 2) // 6).to(dtype)  # up to 175, exact
+    q[..., 70], kr[:, 6] = 0.5, normal(m, seed=9, dtype=dtype)
+    compare((q, k, kr, v, loc, kv_loc), dtype, scale, scale=scale)
+
+
+def test_split_values_that_are_not_finite():
+    """In parts before, at and behind what rows see."""
+    n, m = 70, 3000
+    assert parts([n], [m], 2)
+    q, k, kr, v, loc, kv_loc = inputs([n], [m], 2, 128, 64, 128, BF16)
+    clean = run((q, k, kr, v, loc, kv_loc))
+    for key in (0, 1000, 2929, 2930, 2931, 2960, 2999):
+        at = max(0, key - (m - n))  # the first row that sees it
+        for what in ("k", "v", "inf"):
+            t = (k if what == "k" else v).clone()
+            t[key, 1, 5] = float("inf") if what == "inf" else float("nan")
+            got = run((q, t, kr, v, loc, kv_loc) if what == "k" else (q, k, kr, t, loc, kv_loc))
+            assert torch.equal(got[:at], clean[:at]) and torch.equal(got[:, 0], clean[:, 0]), (key, what)
+            if what == "k":
+                assert torch.isnan(got[at:, 1]).all(), key
+            else:
+                assert not torch.isfinite(got[at:, 1, 5]).any(), (key, what)
+                got[at:, 1, 5] = clean[at:, 1, 5]
+                assert torch.equal(got, clean), (key, what)
+
+
+def test_split_graph_and_streams():
+    """Two captured calls and eager ones on another stream, each with scratch memory of its own."""
+    new, lens = [20, 1], [2000, 600]
+    assert parts(new, lens, 4)
+    args = ref.on_gpu(*inputs(new, lens, 4, 128, 64, 128, BF16))
+    other = torch.cuda.Stream()
+    graphs, outs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    torch.cuda.synchronize()
+    for graph in graphs:
+        with torch.cuda.graph(graph):
+            outs.append(kd.expanded_attention_fn(*args))
+    for seed, change, keys in ((4, new, lens), (5, [1, 20], [0, 2600]), (6, [10, 11], [1300, 1300])):
+        args[0].copy_(normal(*args[0].shape, seed=seed, dtype=BF16))
+        args[4].copy_(ref.starts(change))
+        args[5].copy_(ref.starts(keys))
+        want = kd.expanded_attention_fn(*args)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(other):
+            graphs[1].replay()
+            again = [kd.expanded_attention_fn(*args) for _ in range(3)]
+        graphs[0].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, want) for a in outs + again), seed

@@ -89,11 +89,12 @@ def test_workspace():
         assert size(tokens, seqs, heads, 512) == shared + 2 * 256 * rows * 514 * 4
 
 
-def expanded_code(**kw):
+def expanded_code(workspace=0, size=0, **kw):
     a = dict(q=A, k=A, kr=A, v=A, qsl=A, ksl=A, out=A, tokens=9, keys=20, seqs=2, heads=12, key=128, rope=64, value=128,
              q0=12 * 192, q1=192, k0=12 * 256, k1=256, kr0=64, v0=12 * 256, v1=256, scale=0.1, dt=_lib.F16, causal=1)
     assert set(kw) <= set(a)
-    return _lib.load().kdaconv_expanded_attention_validate(_lib.EXPANDED_ARGS.pack(*{**a, **kw}.values()))
+    return _lib.load().kdaconv_expanded_attention_validate(
+        _lib.EXPANDED_ARGS.pack(*{**a, **kw}.values()), workspace, size)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -115,8 +116,22 @@ def test_expanded_codes(kw, code):
 
 def test_expanded_null():
     lib = _lib.load()
-    assert lib.kdaconv_expanded_attention_validate(None) == EINVAL
-    assert lib.kdaconv_expanded_attention(None, None) == EINVAL
+    assert lib.kdaconv_expanded_attention_validate(None, A, 1 << 40) == EINVAL
+    assert lib.kdaconv_expanded_attention(None, A, 1 << 40, None) == EINVAL
+
+
+def test_expanded_workspace():
+    size = _lib.load().kdaconv_expanded_attention_workspace
+    assert size(9, 20, 2, 12, 128) == size(0, 9999, 1, 1, 8) == size(1, 0, 1, 1, 8) == size(1, 9999, 0, 1, 8) == 0
+    # Blocks of 128 rows, 2 sequences of 3 heads, at most 256 / 6 parts of 4 steps of 64 keys.
+    assert size(9, 2 * 64 * 4 * 2, 2, 3, 40) == 2 * 3 * 2 * 128 * 42 * 4
+    assert size(9, 1 << 20, 2, 3, 40) == 2 * 3 * 42 * 128 * 42 * 4
+    assert size(9, 1 << 20, 2, 65, 40) == 0 and size(9, 2 * 64 * 8 - 1, 2, 3, 40) == 0
+    # Of 256 rows, where sequences are as long.
+    assert size(600, 1 << 16, 2, 3, 40) == 4 * 3 * 21 * 256 * 42 * 4
+    kw = dict(keys=2048, seqs=2)
+    assert expanded_code(**kw) == EINVAL and expanded_code(A, 1 << 30, **kw) == OK
+    assert expanded_code(A + 16, 1 << 30, **kw) == EUNSUPPORTED and expanded_code(A, 9999, **kw) == EINVAL
 
 
 def rotary_code(**kw):
