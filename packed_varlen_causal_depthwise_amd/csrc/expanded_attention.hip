@@ -13,22 +13,32 @@ constexpr int64_t kMaxStride = (int64_t)1 << 23;
 
 bool aligned_to(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
-// Workgroups take 256 rows where sequences are as long on average, else 128: few rows leave more
-// CUs something to do, many read keys less often.
-int waves_of(int64_t tokens, int64_t seqs) { return tokens >= 256 * seqs ? 8 : 4; }
+constexpr int kCus = 256;
 
-int64_t programs_of(int64_t tokens, int64_t seqs) {
-  return tokens / (kWaveRows * waves_of(tokens, seqs)) + seqs;
+int64_t blocks_of(int64_t tokens, int64_t seqs, int waves) { return tokens / (kWaveRows * waves) + seqs; }
+
+// Workgroups take 128 rows where these are no more blocks than CUs, or sequences are shorter; else
+// 256, which read keys half as often, and so where every block has 2048 keys and more. 12 heads, in
+// us with 256 and 128: 8 prompts of 200 rows 21.2 and 18.5, 16 of them 22.6 and 33.5; 4 of 512 rows
+// 28.9 and 26.2, 16 of them 60 and 77; 20 of 64 rows 20.7 and 12.0; 3 of 300 rows over 5000 keys
+// 78 and 93.
+int waves_of(int64_t tokens, int64_t keys, int64_t seqs, int64_t heads) {
+  const bool many = tokens >= 128 * seqs && blocks_of(tokens, seqs, 4) * heads > kCus;
+  return many || (tokens >= 256 * seqs && keys >= 2048 * seqs) ? 8 : 4;
+}
+
+int64_t programs_of(int64_t tokens, int64_t keys, int64_t seqs, int64_t heads) {
+  return blocks_of(tokens, seqs, waves_of(tokens, keys, seqs, heads));
 }
 
 // Parts of a block's keys: where blocks are fewer than half the CUs, as many as give each CU one, of
 // kLeastSteps steps on average or more. 12 heads of 128 + 64 channels, in us, with and without:
 // 1 row over 16000 keys 53 and 451, 300 over 8000 65 and 216, 128 of 2 sequences over 2200 26 and
 // 42, over 1024 20.3 and 22.9. Twice as many parts as CUs: 78, 96, 26, 20.
-constexpr int kCus = 256, kLeastSteps = 4, kMostSplits = 64;
+constexpr int kLeastSteps = 4, kMostSplits = 64;
 int splits_of(int64_t tokens, int64_t keys, int64_t seqs, int64_t heads) {
   if (tokens <= 0 || keys <= 0 || seqs <= 0 || heads <= 0) return 1;
-  const int64_t fill = kCus / (programs_of(tokens, seqs) * heads), long_enough = keys / (seqs * kExpandKeys * kLeastSteps);
+  const int64_t fill = kCus / (programs_of(tokens, keys, seqs, heads) * heads), long_enough = keys / (seqs * kExpandKeys * kLeastSteps);
   return (int)std::max<int64_t>(1, std::min<int64_t>({fill, long_enough, kMostSplits}));
 }
 
@@ -56,7 +66,7 @@ int validate_expanded(const kdaconv_expanded_args* a) {
   if (a->num_tokens > INT32_MAX / 4 || a->num_keys > INT32_MAX / 4 || a->num_seqs > INT32_MAX / 4 || a->num_heads > 65535)
     return KDACONV_EUNSUPPORTED;
   // 2^32 threads.
-  if (programs_of(a->num_tokens, a->num_seqs) * a->num_heads >= (int64_t)1 << 23) return KDACONV_EUNSUPPORTED;
+  if (programs_of(a->num_tokens, a->num_keys, a->num_seqs, a->num_heads) * a->num_heads >= (int64_t)1 << 23) return KDACONV_EUNSUPPORTED;
   if (a->num_tokens == 0 || a->num_seqs == 0 || a->num_heads == 0) return KDACONV_OK;
   if (!a->q || !a->out || !a->query_start_loc || !a->kv_start_loc) return KDACONV_EINVAL;
   if (a->num_keys > 0 && (!a->k || !a->v || (a->rope_dim > 0 && !a->k_rope))) return KDACONV_EINVAL;
@@ -95,8 +105,8 @@ extern "C" int64_t kdaconv_expanded_attention_workspace(int64_t num_tokens, int6
                                                         int64_t num_heads, int64_t value_dim) {
   const int splits = splits_of(num_tokens, num_keys, num_seqs, num_heads);
   if (splits == 1 || value_dim <= 0) return 0;
-  const ExpandPartial part{kWaveRows * waves_of(num_tokens, num_seqs), (int)value_dim};
-  return programs_of(num_tokens, num_seqs) * num_heads * splits * part.floats() * (int64_t)sizeof(float);
+  const ExpandPartial part{kWaveRows * waves_of(num_tokens, num_keys, num_seqs, num_heads), (int)value_dim};
+  return programs_of(num_tokens, num_keys, num_seqs, num_heads) * num_heads * splits * part.floats() * (int64_t)sizeof(float);
 }
 
 extern "C" int kdaconv_expanded_attention_validate(const kdaconv_expanded_args* args, const void* workspace,
@@ -137,8 +147,8 @@ extern "C" int kdaconv_expanded_attention(const kdaconv_expanded_args* a, void* 
   P.dim = (int32_t)a->key_dim;
   P.rope = (int32_t)a->rope_dim;
   P.vdim = (int32_t)a->value_dim;
-  const int waves = waves_of(a->num_tokens, a->num_seqs);
-  P.programs = (int32_t)programs_of(a->num_tokens, a->num_seqs);
+  const int waves = waves_of(a->num_tokens, a->num_keys, a->num_seqs, a->num_heads);
+  P.programs = (int32_t)programs_of(a->num_tokens, a->num_keys, a->num_seqs, a->num_heads);
   int64_t reach = 64;
   while (reach < a->num_seqs) reach *= 64;
   P.search_top = (int32_t)(reach / 64);

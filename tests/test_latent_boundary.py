@@ -127,8 +127,11 @@ def test_expanded_workspace():
     assert size(9, 2 * 64 * 4 * 2, 2, 3, 40) == 2 * 3 * 2 * 128 * 42 * 4
     assert size(9, 1 << 20, 2, 3, 40) == 2 * 3 * 42 * 128 * 42 * 4
     assert size(9, 1 << 20, 2, 65, 40) == 0 and size(9, 2 * 64 * 8 - 1, 2, 3, 40) == 0
-    # Of 256 rows, where sequences are as long.
-    assert size(600, 1 << 16, 2, 3, 40) == 4 * 3 * 21 * 256 * 42 * 4
+    assert size(600, 4095, 2, 3, 40) == 6 * 3 * 7 * 128 * 42 * 4
+    # Of 256 rows over 2048 keys or more.
+    assert size(600, 4096, 2, 3, 40) == 4 * 3 * 8 * 256 * 42 * 4
+    assert size(2000, 1 << 16, 1, 16, 40) == 8 * 16 * 2 * 256 * 42 * 4
+    assert size(2000, 1 << 16, 1, 17, 40) == 0
     kw = dict(keys=2048, seqs=2)
     assert expanded_code(**kw) == EINVAL and expanded_code(A, 1 << 30, **kw) == OK
     assert expanded_code(A + 16, 1 << 30, **kw) == EUNSUPPORTED and expanded_code(A, 9999, **kw) == EINVAL
