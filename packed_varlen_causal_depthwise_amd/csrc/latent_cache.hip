@@ -217,17 +217,20 @@ struct ReadParams {
   char* out;
   int32_t tokens, seqs, search_top;
   int32_t row_chunks;  // of 8 channels
+  int32_t per;  // rows of a wave, up to 64
   Divider chunks;
 };
 
-constexpr int kReadTokens = 16, kReadWaves = 4;
+constexpr int kReadWaves = 4, kReadAhead = 2;
 
-// A wave reads kReadTokens neighbouring rows of the output: its lanes first find each row's
-// sequence and slot, then copy 8 channels at a time.
+// A wave reads some neighbouring rows of the output: its lanes first find each row's sequence and
+// slot, then copy 8 channels at a time, kReadAhead loads before the first is waited for. Memory
+// bounds it: 131072 rows of 512 8-bit and 64 16-bit channels take 49 us, 237 MB at 4.8 TB/s (one
+// load at a time 63 us, six 67: registers then leave fewer waves).
 template <int kF, bool kE4m3>
 __global__ __launch_bounds__(kWave * kReadWaves) void latent_read_kernel(ReadParams P) {
   const int lane = threadIdx.x % kWave;
-  const int first = uniform((blockIdx.x * kReadWaves + threadIdx.x / kWave) * kReadTokens);
+  const int first = uniform((blockIdx.x * kReadWaves + threadIdx.x / kWave) * P.per);
   if (first >= P.tokens) return;
   // The last sequence that starts at or before the first row; 64-way search, a ballot a level.
   int s = 0;
@@ -241,7 +244,7 @@ __global__ __launch_bounds__(kWave * kReadWaves) void latent_read_kernel(ReadPar
   // Row `lane` of the wave's: its slot, -1 for zeros, -2 for a row that no sequence owns.
   int64_t slot = -2;
   const int row = first + lane;
-  if (lane < kReadTokens && row < P.tokens) {
+  if (lane < P.per && row < P.tokens) {
     int mine = s;
     while (mine < P.seqs && P.starts[mine + 1] <= row) ++mine;
     if (mine < P.seqs && P.starts[mine] <= row) {
@@ -253,34 +256,44 @@ __global__ __launch_bounds__(kWave * kReadWaves) void latent_read_kernel(ReadPar
       }
     }
   }
-  const int latent_chunks = P.C.latent / 8, total = kReadTokens * P.row_chunks;
-  for (int i = lane; i < total; i += kWave) {
-    const int t = P.chunks(i), c = i - t * P.row_chunks;
-    const int at = __shfl((int)slot, t);
-    if (at == -2) continue;
-    u32x4 v = {0, 0, 0, 0};
-    if (at >= 0) {
-      const uint32_t page = P.C.page_size((uint32_t)at), place = (uint32_t)at - page * P.C.page_size.d;
-      if (c >= latent_chunks) {
-        v = *(const u32x4*)(P.C.ropes + page * P.C.rope_page + place * P.C.rope_slot + (c - latent_chunks) * 16);
-      } else if constexpr (!kE4m3) {
-        v = *(const u32x4*)(P.C.latents + page * P.C.lat_page + place * P.C.lat_slot + c * 16);
-      } else {
-        const u32x2 q = *(const u32x2*)(P.C.latents + page * P.C.lat_page + place * P.C.lat_slot + c * 8);
-        const float f = scale_value(P.C.scales[page * P.C.scale_page + place * P.C.scale_slot + c / 4]);
-        float x[8];
+  const int latent_chunks = P.C.latent / 8, total = P.per * P.row_chunks;
+  for (int base = lane; base < total; base += kWave * kReadAhead) {
+    u32x4 v[kReadAhead];
+    uint32_t scales[kReadAhead];
+    char* to[kReadAhead];
+    bool codes[kReadAhead];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(q[j], false), b = __builtin_amdgcn_cvt_pk_f32_fp8(q[j], true);
-          x[4 * j] = f * a.x;
-          x[4 * j + 1] = f * a.y;
-          x[4 * j + 2] = f * b.x;
-          x[4 * j + 3] = f * b.y;
+    for (int u = 0; u < kReadAhead; ++u) {
+      const int i = base + u * kWave;
+      const int t = P.chunks(i), c = i - t * P.row_chunks;
+      const int at = i < total ? __shfl((int)slot, t) : -2;
+      v[u] = u32x4{0, 0, 0, 0};
+      scales[u] = 127;
+      to[u] = at == -2 ? nullptr : P.out + ((int64_t)(first + t) * P.row_chunks + c) * 16;
+      codes[u] = kE4m3 && c < latent_chunks;
+      if (at >= 0) {
+        const uint32_t page = P.C.page_size((uint32_t)at), place = (uint32_t)at - page * P.C.page_size.d;
+        if (c >= latent_chunks) {
+          v[u] = *(const u32x4*)(P.C.ropes + page * P.C.rope_page + place * P.C.rope_slot + (c - latent_chunks) * 16);
+        } else if constexpr (!kE4m3) {
+          v[u] = *(const u32x4*)(P.C.latents + page * P.C.lat_page + place * P.C.lat_slot + c * 16);
+        } else {
+          const u32x2 q = *(const u32x2*)(P.C.latents + page * P.C.lat_page + place * P.C.lat_slot + c * 8);
+          v[u][0] = q[0], v[u][1] = q[1];
+          scales[u] = P.C.scales[page * P.C.scale_page + place * P.C.scale_slot + c / 4];
         }
-        v = pack_eight<kF>(x);
       }
     }
-    *(u32x4*)(P.out + ((int64_t)(first + t) * P.row_chunks + c) * 16) = v;
+#pragma unroll
+    for (int u = 0; u < kReadAhead; ++u) {
+      if (kE4m3 && codes[u]) {
+        const float f = scale_value(scales[u]);
+        const uint32_t lo = v[u][0], hi = v[u][1];
+        v[u] = u32x4{scaled_pair<kF, false>(lo, f), scaled_pair<kF, true>(lo, f),
+                     scaled_pair<kF, false>(hi, f), scaled_pair<kF, true>(hi, f)};
+      }
+      if (to[u] != nullptr) *(u32x4*)to[u] = v[u];
+    }
   }
 }
 
@@ -491,7 +504,10 @@ extern "C" int kdaconv_latent_cache_read(const kdaconv_latent_cache* cache, cons
   P.search_top = (int32_t)(reach / kWave);
   P.row_chunks = (int32_t)((cache->latent_dim + cache->rope_dim) / 8);
   P.chunks = divider_of((uint32_t)P.row_chunks);
-  const int64_t per = kReadTokens * kReadWaves, blocks = (num_tokens + per - 1) / per;
+  // 16 rows a wave, or 4 where that leaves CUs without 4 waves: 4004 rows, written and read, 10.4 us
+  // in a graph and 21.9 with 16; 131072 rows 67 and 60.
+  P.per = num_tokens >= 256 * 4 * 16 ? 16 : 4;
+  const int64_t per = P.per * kReadWaves, blocks = (num_tokens + per - 1) / per;
   if (blocks >= (int64_t)1 << 24) return KDACONV_EUNSUPPORTED;  // 2^32 threads
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   const dim3 grid((unsigned)blocks), block(kWave * kReadWaves);
