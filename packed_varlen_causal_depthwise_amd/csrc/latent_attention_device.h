@@ -555,11 +555,13 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
       }
     };
 
-    // Keys past the end are loaded too, as zeros.
+    // Steps past the part's end are loaded too, but as zeros: its keys are another worker's.
+    const int64_t part_end = (int64_t)first_key + (int64_t)count * kKeys;
+    const int there = part_end < keys ? (int)part_end : keys;
     const auto find_step = [&](int step) {
       constexpr int kTimes = 64 / kKeys;  // steps that a search serves
       const int base = step % kTimes * kKeys;
-      if (base == 0) find.find(P, at.s, first_key + step * kKeys, keys, lane);
+      if (base == 0) find.find(P, at.s, first_key + step * kKeys, there, lane);
       if (loader == 0 && lane == 0) masks[step & 3] = find.mask << (64 - kKeys - base) >> (64 - kKeys);
       return base;
     };
