@@ -2,10 +2,12 @@
 
 Python face of libkdaconv (include/kdaconv.h): the two functions of the page
 "vllm.models.kimi_k3.nvidia.ops.kda_conv", ``packed_causal_conv1d_fn`` and
-``packed_causal_conv1d_supported``, with the same arguments; the decode step; and what
+``packed_causal_conv1d_supported``, with the same arguments; the decode step; what
 follows the convolution in a KDA layer: the gated delta rule over its planes (prefill and
-single tokens) and the norms around it. PyTorch supplies the device memory and the current stream; every step of the computation runs in the
-HIP kernels of libkdaconv. There is no CPU path: if the library is not built,
+single tokens) and the norms around it; and what the latent attention layers between KDA layers
+run: rotary positions, the paged latent cache and attention over it, absorbed and expanded.
+PyTorch supplies the device memory and the current stream; every step of the computation runs in
+the HIP kernels of libkdaconv. There is no CPU path: if the library is not built,
 importing the functions still works but calling them raises.
 """
 

@@ -8,8 +8,10 @@
 // the products. Of 8 waves two share each SIMD, and the matrix unit and the vector unit would
 // take turns if they kept step: both products, then both softmaxes. So waves 4 to 7 run half a
 // step behind: while one wave of a SIMD multiplies (values of the last step, keys of the next),
-// the other one weighs its scores. Barriers keep them so. (One prompt of 16384 tokens, 12 heads:
-// 1067 us in step.) Products are taken transposed, S^T = K Q^T and O^T = V^T P^T, so a lane
+// the other one weighs its scores. Barriers keep them so. One prompt of 16384 tokens, 12 heads of
+// 128 + 64 channels, takes 925 us so (1115 TFLOP/s, where a library product of 8192^3 reaches 1242)
+// and took 1067 in step. The matrix unit is busy 62% of the time, at the clock that its power
+// leaves. Products are taken transposed, S^T = K Q^T and O^T = V^T P^T, so a lane
 // has one query and its softmax needs no other lane but for the largest score; and the scores'
 // registers are the second product's right operand as they are: of 16 keys lane half h holds 4 h
 // .. 4 h + 3 and 8 + 4 h .., and the left operand takes its keys in that order. That operand is V

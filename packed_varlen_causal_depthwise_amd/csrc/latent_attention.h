@@ -36,14 +36,16 @@ struct AttendParams {
 // parts of the line. They work it out for themselves from the lengths on the device, so that a
 // captured call serves any lengths.
 constexpr int kBlockUnits = 2;
-// A part is no shorter than this (unless the line is).
+// A part is no shorter than this (unless the line is). One sequence of 16000 keys, 502 units, in us:
+// parts of 2 units and more 26.7, 3 23.7, 4 25.4, 6 25.5 (the join's reads against the longest part).
 constexpr int kLeastUnits = 3;
 constexpr int kWorkers = 256;
 
 constexpr int kAttendWaves = 8;
 // Blocks of 16 rows per workgroup, and how it takes keys: a step's keys lie in LDS while
 // kRing - 1 more steps are under way. Few rows leave memory the time that products need not:
-// short steps, many under way. More rows share longer steps.
+// short steps, many under way. More rows share longer steps. (LDS holds 4 steps of 32 keys, or 2
+// of 64 beside the weights.)
 constexpr int step_keys(int blocks) { return blocks == 4 ? 64 : 32; }
 constexpr int ring_steps(int blocks) { return blocks == 4 ? 2 : 4; }  // powers of 2 up to 4
 constexpr int kMostKeys = 1 << 30;  // of a sequence

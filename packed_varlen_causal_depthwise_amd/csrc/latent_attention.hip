@@ -11,7 +11,8 @@ constexpr int64_t kSharedBytes = kWorkers * 2 * sizeof(Shared);
 
 bool aligned_to(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
-// Blocks of 16 rows per workgroup: as many as a sequence fills on average, up to 4.
+// Blocks of 16 rows per workgroup: as many as a sequence fills on average, up to 4. Every block
+// reads the sequence's keys once; 8 blocks' sums and queries are more than the registers hold.
 int blocks_of(int64_t tokens, int64_t seqs, int64_t heads) {
   const int64_t rows = tokens * heads;
   return rows <= 16 * seqs ? 1 : rows <= 32 * seqs ? 2 : 4;

@@ -29,7 +29,8 @@ constexpr int kRotaryThreads = 256, kAngles = 256;
 
 // A workgroup's tokens share one table of angles, which its threads work out first: the sine
 // and cosine in FP64 reduction cost some 150 instructions, once per token and pair rather than
-// once per head. Then a thread turns `units` of kV channels (kV = 8: 16 bytes a load).
+// once per head. Then a thread turns `units` of kV channels (kV = 8: 16 bytes a load). 16384 tokens
+// of 12 heads, 64 channels turned in place: 9.6 us, 5.3 TB/s of the 64; 37 tokens 4 us, a launch.
 template <int kF, int kV>
 __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(RotaryParams P) {
   __shared__ f32x2 table[kAngles];
@@ -134,6 +135,8 @@ struct WriteParams {
 constexpr int kWriteWaves = 4;
 
 // One wave per token, 8 channels of the latent per lane. A block of 32 channels is four lanes.
+// 16384 tokens of 512 + 64 bf16 channels take 11.4 us (3.3 TB/s; a wave's norm waits for its whole
+// row, and a launch's first and last microseconds weigh), 37 tokens 4 us, a launch.
 template <int kF, bool kE4m3>
 __global__ __launch_bounds__(kWave * kWriteWaves) void latent_write_kernel(WriteParams P) {
   const int lane = threadIdx.x % kWave;
