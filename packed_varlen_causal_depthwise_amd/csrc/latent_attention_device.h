@@ -669,7 +669,9 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
         before += __builtin_popcountll(__ballot(i < parts.count && at_unit <= zero));
         all += __builtin_popcountll(__ballot(i < parts.count && at_unit < end));
       }
-      if (lane == 0) P.shared[2 * w + (ends ? 0 : 1)] = Shared{before - 1, all - (before - 1), at.s, at.b};
+      // (Offsets that give rows to several sequences may wrap the line: still, all stays in range.)
+      const int first = before > 0 ? before - 1 : 0;
+      if (lane == 0) P.shared[2 * w + (ends ? 0 : 1)] = Shared{first, all > first ? all - first : 0, at.s, at.b};
     }
     __syncthreads();
     at = at.b + 1 < blocks ? Place{at.s, at.b + 1, 0} : Place{at.s + 1, 0, 0};
@@ -689,7 +691,7 @@ __global__ __launch_bounds__(kJoinThreads) void latent_join_kernel(AttendParams 
   const Partial part{kRows, P.C.latent};
   const Shared share = P.shared[2 * x + blockIdx.y];
   const int count = uniform(share.count), w = uniform(share.first);
-  if (count == 0) return;
+  if (count == 0 || x < w || x - w >= count) return;
   int start;
   const int tokens = Line<kRows, 1>::tokens(P, uniform(share.s), start);
   int rows = tokens * (int)P.heads.d - uniform(share.b) * kRows;

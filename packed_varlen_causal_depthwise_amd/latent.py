@@ -16,15 +16,16 @@ SCALE_BLOCK = 32
 
 def _cache(latents, ropes, scales):
     """Checks a cache's tensors; returns kdaconv_latent_cache as bytes and its sizes."""
-    if latents.dim() != 3 or ropes.dim() != 3 or latents.shape[:2] != ropes.shape[:2]:
+    size, rope_size = latents.shape, ropes.shape
+    if len(size) != 3 or len(rope_size) != 3 or size[0] != rope_size[0] or size[1] != rope_size[1]:
         raise ValueError("latents must be (pages, page_size, latent_dim) and ropes (pages, page_size, "
                          "rope_dim)")
-    pages, page_size, latent = latents.shape
-    rope, dtype = ropes.shape[2], ropes.dtype
-    if dtype not in (torch.bfloat16, torch.float16):
+    pages, page_size, latent = size
+    rope, dtype, kind = rope_size[2], ropes.dtype, latents.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise ValueError("ropes must be bfloat16 or float16")
-    e4m3 = latents.dtype == torch.float8_e4m3fn
-    if not e4m3 and latents.dtype != dtype:
+    e4m3 = kind is not dtype
+    if e4m3 and kind is not torch.float8_e4m3fn:
         raise ValueError("latents must have the dtype of ropes, or float8_e4m3fn")
     ls, rs, ss = latents.stride(), ropes.stride(), (0, 0)
     if latent > 1 and ls[2] != 1 or rope > 1 and rs[2] != 1:
@@ -45,7 +46,7 @@ def _cache(latents, ropes, scales):
     packed = _lib.LATENT_CACHE.pack(
         latents.data_ptr(), ropes.data_ptr(), 0 if scales is None else scales.data_ptr(),
         pages, page_size, latent, rope, ls[0], ls[1], rs[0], rs[1], ss[0], ss[1],
-        DTYPE_CODES[dtype], int(e4m3))
+        DTYPE_CODES[dtype], e4m3)
     return packed, latent, rope, dtype, device
 
 
@@ -85,10 +86,11 @@ def latent_cache_write(
     synchronisation.
     """
     cache, dim, rope_dim, dtype, device = _cache(latents, ropes, scales)
-    if latent.dim() != 2 or latent.shape[1] != dim or rope.shape != (latent.shape[0], rope_dim):
+    size = latent.shape
+    if len(size) != 2 or size[1] != dim or rope.shape != (size[0], rope_dim):
         raise ValueError("latent must be (tokens, latent_dim) and rope (tokens, rope_dim)")
-    tokens = latent.shape[0]
-    if latent.dtype != dtype or rope.dtype != dtype:
+    tokens = size[0]
+    if latent.dtype is not dtype or rope.dtype is not dtype:
         raise ValueError(f"latent and rope must have the dtype of ropes, {dtype}")
     xs, rs = latent.stride(), rope.stride()
     if dim > 1 and xs[1] != 1 or rope_dim > 1 and rs[1] != 1:
@@ -101,7 +103,7 @@ def latent_cache_write(
             raise ValueError("weight belongs to the norm: give eps")
     elif not eps >= 0:
         raise ValueError("eps must not be negative")
-    if weight is not None and (weight.dtype != torch.float32 or weight.shape != (dim,)
+    if weight is not None and (weight.dtype is not torch.float32 or weight.shape != (dim,)
                                or not weight.is_contiguous() or weight.get_device() != device):
         raise ValueError(f"weight must be a contiguous float32 ({dim},) tensor on the device of latents")
     far = 0
@@ -124,22 +126,24 @@ def latent_cache_write(
 
 
 def _table(block_table, seqs, device):
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] < seqs:
+    size = block_table.shape
+    if block_table.dtype is not torch.int32 or len(size) != 2 or size[0] < seqs:
         raise ValueError("block_table must be int32 (sequences, pages per sequence)")
     ts = block_table.stride()
-    if block_table.shape[1] > 1 and ts[1] != 1:
+    if size[1] > 1 and ts[1] != 1:
         raise ValueError("the columns of block_table must be contiguous")
     if block_table.get_device() != device:
         raise ValueError("all tensors must be on the device of latents")
-    return block_table.data_ptr(), ts[0], block_table.shape[1]
+    return block_table.data_ptr(), ts[0], size[1]
 
 
 def _loc(loc, device, what):
-    if loc.dtype != torch.int32 or loc.dim() != 1 or not loc.is_contiguous():
+    size = loc.shape
+    if loc.dtype is not torch.int32 or len(size) != 1 or not loc.is_contiguous():
         raise ValueError(f"{what} must be a contiguous 1-D int32 tensor")
     if loc.get_device() != device:
         raise ValueError("all tensors must be on one device")
-    return loc.shape[0] - 1
+    return size[0] - 1
 
 
 def latent_cache_read(
@@ -183,11 +187,11 @@ def latent_cache_read(
 def _attend(q_latent, q_rope, latents, ropes, scales, block_table, seq_lens, query_start_loc, scale, out):
     """Checks, then kdaconv_latent_args as bytes, the output and the call's sizes."""
     cache, dim, rope_dim, dtype, device = _cache(latents, ropes, scales)
-    if (q_latent.dim() != 3 or q_latent.shape[2] != dim
-            or q_rope.shape != (q_latent.shape[0], q_latent.shape[1], rope_dim)):
+    size = q_latent.shape
+    if len(size) != 3 or size[2] != dim or q_rope.shape != (size[0], size[1], rope_dim):
         raise ValueError("q_latent must be (tokens, heads, latent_dim) and q_rope (tokens, heads, rope_dim)")
-    tokens, heads, _ = q_latent.shape
-    if q_latent.dtype != dtype or q_rope.dtype != dtype:
+    tokens, heads, _ = size
+    if q_latent.dtype is not dtype or q_rope.dtype is not dtype:
         raise ValueError(f"q_latent and q_rope must have the dtype of ropes, {dtype}")
     ls, rs = q_latent.stride(), q_rope.stride()
     if dim > 1 and ls[2] != 1 or rope_dim > 1 and rs[2] != 1:
@@ -195,7 +199,8 @@ def _attend(q_latent, q_rope, latents, ropes, scales, block_table, seq_lens, que
     seqs = tokens
     if query_start_loc is not None:
         seqs = max(0, _loc(query_start_loc, device, "query_start_loc"))
-    if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or seq_lens.shape[0] < seqs or (
+    lens = seq_lens.shape
+    if seq_lens.dtype is not torch.int32 or len(lens) != 1 or lens[0] < seqs or (
             seqs > 1 and seq_lens.stride()[0] != 1):
         raise ValueError("seq_lens must be a contiguous 1-D int32 tensor with one entry per sequence")
     table = _table(block_table, seqs, device)
@@ -203,7 +208,7 @@ def _attend(q_latent, q_rope, latents, ropes, scales, block_table, seq_lens, que
         raise ValueError("all tensors must be on the device of latents")
     if out is None:
         out = torch.empty((tokens, heads, dim), dtype=dtype, device=q_latent.device)
-    elif (out.shape != q_latent.shape or out.dtype != dtype or not out.is_contiguous()
+    elif (out.shape != size or out.dtype != dtype or not out.is_contiguous()
           or out.get_device() != device):
         raise ValueError(f"out must be a contiguous {dtype} tensor of shape {tuple(q_latent.shape)} on "
                          f"{latents.device}")

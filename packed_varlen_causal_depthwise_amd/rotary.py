@@ -46,19 +46,21 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, factor: float 
 
 def _positions(positions, tokens, device, what="positions"):
     """Checks a vector with one index per token; returns whether it is 64 bits wide."""
-    if (positions.dtype not in (torch.int32, torch.int64) or positions.shape != (tokens,)
+    kind, size = positions.dtype, positions.shape
+    if (kind is not torch.int32 and kind is not torch.int64 or len(size) != 1 or size[0] != tokens
             or not positions.is_contiguous() or positions.get_device() != device):
         raise ValueError(f"{what} must be a contiguous int32 or int64 ({tokens},) tensor on the "
                          "device of the other tensors")
-    return int(positions.dtype == torch.int64)
+    return int(kind is torch.int64)
 
 
 def _frequencies(inv_freq, device):
-    if (inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous()
+    size = inv_freq.shape
+    if (inv_freq.dtype is not torch.float32 or len(size) != 1 or not inv_freq.is_contiguous()
             or inv_freq.get_device() != device):
         raise ValueError("inv_freq must be a contiguous 1-D float32 tensor on the device of the "
                          "other tensors")
-    return 2 * inv_freq.shape[0]
+    return 2 * size[0]
 
 
 def rotary_embedding(
@@ -82,11 +84,12 @@ def rotary_embedding(
     channels are read and written. Otherwise it may not overlap x. Queued on the current stream;
     no synchronisation.
     """
-    if x.dim() != 3:
+    size, dtype = x.shape, x.dtype
+    if len(size) != 3:
         raise ValueError("x must be (tokens, heads, head_dim)")
-    tokens, heads, dim = x.shape
-    if x.dtype not in DTYPE_CODES:
-        raise ValueError(f"x must be bfloat16, float16 or float32 (got {x.dtype})")
+    tokens, heads, dim = size
+    if dtype not in DTYPE_CODES:
+        raise ValueError(f"x must be bfloat16, float16 or float32 (got {dtype})")
     xs = x.stride()
     if dim > 1 and xs[2] != 1:
         raise ValueError("the last axis of x must be contiguous")
@@ -95,17 +98,17 @@ def rotary_embedding(
     rotary = _frequencies(inv_freq, device)
     if out is None:
         out = _fresh_like(x)
-    elif (out.shape != x.shape or out.dtype != x.dtype or out.get_device() != device
+    elif out is not x and (out.shape != size or out.dtype is not dtype or out.get_device() != device
           or dim > 1 and out.stride()[2] != 1):
-        raise ValueError(f"out must be a {x.dtype} tensor of shape {tuple(x.shape)} on {x.device} "
+        raise ValueError(f"out must be a {dtype} tensor of shape {tuple(size)} on {x.device} "
                          "with a contiguous last axis")
     if tokens == 0 or heads == 0:
         return out
     if device < 0:
         raise ValueError("x must be a GPU tensor")
-    os = out.stride()
+    os = xs if out is x else out.stride()
     rc = _call(device, _lib.load().kdaconv_rotary_embedding,
-               x.data_ptr(), DTYPE_CODES[x.dtype], tokens, heads, dim, xs[0], xs[1],
+               x.data_ptr(), DTYPE_CODES[dtype], tokens, heads, dim, xs[0], xs[1],
                positions.data_ptr(), wide, inv_freq.data_ptr(), rotary, int(offset),
                int(interleaved), float(scale), out.data_ptr(), os[0], os[1])
     _lib.check(rc, "rotary_embedding")
