@@ -275,7 +275,8 @@ struct Staged {
   using T = Tile<kLatent, kKeys>;
   static constexpr int kRows = 8, kLoads = kLatent / 128;
   // A step's registers: codes, the rotated part, scales.
-  static constexpr int kRegisters = kLoads + 1 + (kLoads + 3) / 4;
+  static constexpr int kRegisters = kLoads + 2;
+  static_assert(kLoads <= 4);
 
   static __device__ __forceinline__ void issue(const AttendParams& P, const Keys<true>& K, int first, int wave, int lane,
                                                u32x4* set) {
@@ -287,7 +288,19 @@ struct Staged {
       // (Past the end the first chunk: queries are zero there, and no sum is taken.)
       const uint32_t chunk = (c + 8 * i) * 16 < (uint32_t)P.C.latent ? c + 8 * i : 0;
       set[i] = *(Global<u32x4>)(codes + chunk * 16);
-      set[kLoads + 1 + i / 4][i % 4] = scales[chunk / 2];
+    }
+    // Chunk c + 8 i has scale c / 2 + 4 i: that byte of word i.
+    if (P.C.latent == kLatent) {
+      typedef uint32_t words __attribute__((ext_vector_type(kLoads), aligned(1)));
+      const words w = *(Global<words>)scales;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) set[kLoads + 1][i] = w[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const uint32_t chunk = (c + 8 * i) * 16 < (uint32_t)P.C.latent ? c + 8 * i : 0;
+        set[kLoads + 1][i] = scales[chunk / 2] << (c / 2 * 8);
+      }
     }
     const auto zeros = (Global<char>)(const char*)kZeros;
     set[kLoads] = *(Global<u32x4>)(c * 8 < (uint32_t)P.C.rope ? rope + c * 16 : zeros);
@@ -299,7 +312,7 @@ struct Staged {
     const uint32_t even = row * T::kRow + ((2 * c) ^ T::latent_flip(row)) * 16;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const float f = scale_value(set[kLoads + 1 + i / 4][i % 4]);
+      const float f = scale_value(set[kLoads + 1][i] >> (c / 2 * 8) & 255);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         u32x4 v;

@@ -232,3 +232,22 @@ def test_empty():
     assert kd.latent_attention_update(g[0][:0], g[1][:0], *g[2:7], scale=1.0).shape == (0, 2, 64)
     assert kd.latent_attention_fn(g[0][:0], g[1][:0], *g[2:7], g[7][:1], scale=1.0).shape == (0, 2, 64)
     assert kd.latent_attention_supported(*g[:5]) and not kd.latent_attention_supported(ql, qr, *cache)
+
+
+@pytest.mark.parametrize("latent", [512, 480, 256])
+def test_scales_at_odd_addresses(latent):
+    """Scales that lie at no multiple of anything, among other bytes."""
+    lens = [70, 3, 200]
+    table, pages = ref.tables(lens, 8)
+    c, r, s = ref.on_gpu(*ref.cache(pages, 8, latent, 64, torch.bfloat16, e4m3=True))
+    among = torch.full((pages, 8, latent // 32 + 3), 255, dtype=torch.uint8, device="cuda")
+    odd = among[..., 1:1 + latent // 32]
+    odd.copy_(s)
+    g = torch.Generator().manual_seed(3)
+    for heads in (12, 40):
+        q = torch.randn(3, heads, latent, generator=g).bfloat16().cuda()
+        qr = torch.randn(3, heads, 64, generator=g).bfloat16().cuda()
+        rest = (table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"))
+        want = kd.latent_attention_update(q, qr, c, r, s, *rest, scale=0.05)
+        assert torch.isfinite(want).all()
+        assert torch.equal(kd.latent_attention_update(q, qr, c, r, odd, *rest, scale=0.05), want)
