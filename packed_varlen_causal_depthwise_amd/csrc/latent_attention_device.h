@@ -544,7 +544,7 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
       if (scores) weight += sum;
       // Rows that do not see a key have weight 0 for it, but 0 times NaN is NaN: where rows differ
       // in what they see, values that are not finite become zeros. (The rows that see one have
-      // a score that is not finite.)
+      // a score that is not finite. What no row sees is not loaded.)
       if (most != least && key + kKeys > least) {
         for (int i = tid; i < T::kRopes / 16; i += 64 * kAttendWaves) {
           u32x4* const a = (u32x4*)(memory + off + i * 16);
@@ -575,9 +575,10 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
       }
     };
 
-    // Steps past the part's end are loaded too, but as zeros: its keys are another worker's.
+    // Keys past the part's end, which are another worker's, and past what any row sees are loaded
+    // as zeros: the latter have weight 0, but their values may be NaN.
     const int64_t part_end = (int64_t)first_key + (int64_t)count * kKeys;
-    const int there = part_end < keys ? (int)part_end : keys;
+    const int there = part_end < seen ? (int)part_end : seen;
     const auto find_step = [&](int step) {
       constexpr int kTimes = 64 / kKeys;  // steps that a search serves
       const int base = step % kTimes * kKeys;
