@@ -345,6 +345,7 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
   __shared__ __attribute__((aligned(16))) float tops[kRows][kBlocks];  // a step's largest scores
   __shared__ __attribute__((aligned(16))) char room[96];
   __shared__ uint64_t masks[4];  // of the keys of steps under way
+  __shared__ __attribute__((aligned(16))) int bad[kLatent];  // a channel's first key that is not finite, of those made 0
 
   const int tid = threadIdx.x, lane = tid % 64, wave = uniform(tid / 64);
   const int g = lane / 16, n = lane % 16;
@@ -411,6 +412,9 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
     const int last_row = (at.b + 1) * kRows < rows ? (at.b + 1) * kRows - 1 : rows - 1;
     const int least = past + (int)P.heads(at.b * kRows), most = past + (int)P.heads(last_row);
     const int seen = most < 0 ? 0 : (most < keys ? most : keys);
+    const bool differ = most != least;
+    static_assert(kLatent <= 64 * kAttendWaves);
+    if (differ && tid < kLatent) bad[tid] = INT32_MAX;
     // Steps to go; may be negative.
     const int begin = at.t << P.shift, last = (seen + kKeys - 1) / kKeys;
     const int count = ((t1 << P.shift) < last ? t1 << P.shift : last) - begin;
@@ -543,12 +547,22 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
       }
       if (scores) weight += sum;
       // Rows that do not see a key have weight 0 for it, but 0 times NaN is NaN: where rows differ
-      // in what they see, values that are not finite become zeros. (The rows that see one have
-      // a score that is not finite. What no row sees is not loaded.)
-      if (most != least && key + kKeys > least) {
-        for (int i = tid; i < T::kRopes / 16; i += 64 * kAttendWaves) {
+      // in what they see, values that are not finite become zeros. The rows that see one have a
+      // score that is not finite; if that is -inf their weight is 0 too, and they get their NaN at
+      // the end. (What no row sees is not loaded.)
+      if (differ && key + kKeys > least) {
+        for (int i = (int)fresh(tid); i < T::kRopes / 16; i += 64 * kAttendWaves) {
           u32x4* const a = (u32x4*)(memory + off + i * 16);
-          *a = finite_pairs<kF>(*a);
+          const u32x4 had = *a, has = finite_pairs<kF>(had);
+          uint32_t change = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) change |= had[j] ^ has[j];
+          if (change != 0) {
+            *a = has;
+            const int r = i / (kLatent / 8), c = (i % (kLatent / 8) ^ T::latent_flip(r)) * 8;
+            for (int j = 0; j < 8; ++j)
+              if (((had[j / 2] ^ has[j / 2]) >> (j % 2 * 16)) & 0xFFFF) atomicMin(&bad[c + j], key + r);
+          }
         }
         lds_barrier();
       }
@@ -658,10 +672,16 @@ __global__ __launch_bounds__(64 * kAttendWaves) __attribute__((amdgpu_waves_per_
       }
       const float f = total == 0.0f ? 0.0f : 1.0f / total;
       if (at.b * kRows + r < rows) {
+        const int sees = differ ? past + (int)P.heads(at.b * kRows + r) : 0;
 #pragma unroll
         for (int c = 0; c < kColumns; ++c) {
           const int column = (wave * kColumns + c) * 16 + 4 * (kQ == 4 ? (int)fresh(g) : g);
           if (column >= P.C.latent) break;
+          if (differ) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (bad[column + j] < sees) O[c][i][j] = __builtin_nanf("");
+          }
           if (whole) {
             const f32x4 v = f * O[c][i];
             char* const o = P.out + (((int64_t)start * P.heads.d + at.b * kRows + r) * P.C.latent + column) * 2;
