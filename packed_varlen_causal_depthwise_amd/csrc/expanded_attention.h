@@ -22,8 +22,9 @@ struct ExpandParams {
   int32_t dim, rope, vdim;
   int32_t programs;  // blocks of rows: sequence s owns v(s) = s + start of s / rows up to v(s + 1)
   int32_t search_top;  // 64^(levels - 1), 64^levels >= seqs
-  float scale;  // times log2(e), not negative
-  uint32_t flip;  // the queries' sign bits, where the scale was
+  float scale;  // times log2(e), positive; 1 if `vanish`
+  bool vanish;  // the scale is 0, or too small for FP32
+  uint32_t flip;  // the queries' sign bits, where the scale was negative
   bool causal;
   int32_t splits;  // parts of a block's keys, each a workgroup's
   float* partial;  // if there are several: per program, head and part an ExpandPartial

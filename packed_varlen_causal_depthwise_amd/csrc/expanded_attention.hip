@@ -153,6 +153,8 @@ extern "C" int kdaconv_expanded_attention(const kdaconv_expanded_args* a, void* 
   while (reach < a->num_seqs) reach *= 64;
   P.search_top = (int32_t)(reach / 64);
   P.scale = (float)(std::fabs(a->scale) * 1.4426950408889634074);
+  P.vanish = P.scale == 0.0f;
+  if (P.vanish) P.scale = 1.0f;
   P.flip = a->scale < 0 ? 0x80008000u : 0u;
   P.causal = a->causal != 0;
   P.splits = splits_of(a->num_tokens, a->num_keys, a->num_seqs, a->num_heads);

@@ -134,6 +134,17 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(kWa
     for (int k = 0; k < kAll; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) qf[k][i] ^= P.flip;
+    // A scale of 0 is taken by the queries: the scores of keys that are not seen are -inf, and that
+    // times 0 would be NaN. (Elements that are not finite become NaN: their exponent's last bit
+    // moves to the mantissa's first.)
+    if (P.vanish) {
+      constexpr uint32_t kLast = kF == kRuleBF16 ? 0x00800080u : 0x04000400u;
+#pragma unroll
+      for (int k = 0; k < kAll; ++k) {
+        qf[k] ^= finite_pairs<kF>(qf[k]);
+        qf[k] |= (qf[k] & kLast) >> 1;
+      }
+    }
     // (They arrive here. Else every step would wait for them, and for the step under way.)
 #pragma unroll
     for (int k = 0; k < kAll; ++k) asm volatile("" : "+v"(qf[k]));

@@ -1,0 +1,39 @@
+"""Expanded attention at the ends of its arguments: scales of zero and next to it, heads far apart,
+rows past 2^32 bytes, parts of the keys that weigh nothing."""
+
+import pytest
+import torch
+
+import latent_reference as ref
+import packed_varlen_causal_depthwise_amd as kd
+from test_gpu_expanded_attention import BF16, DTYPES, F16, check, compare, inputs, normal, parts, run
+
+pytestmark = pytest.mark.gpu
+
+
+@DTYPES
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("scale", [0.0, -0.0, 2.0 ** -140, 2.0 ** -160, -2.0 ** -160, 2.0 ** -1074])
+@pytest.mark.parametrize("new,lens", [([70, 3], [70, 200]), ([300], [333]), ([40, 1], [5000, 900]), ([5, 3], [2, 0])])
+def test_scale_zero(new, lens, scale, causal, dtype):
+    """No score differs from another: the mean of the values that a row sees."""
+    compare(inputs(new, lens, 2, 128, 64, 128, dtype), dtype, (new, scale), scale=scale, causal=causal)
+
+
+def test_scale_zero_times_infinity():
+    """0 times a score that is not finite is NaN, as in its definition: where the row sees it."""
+    n = 100
+    q, k, kr, v, loc, kv_loc = inputs([n], [n], 2, 64, 32, 64, BF16)
+    clean = run((q, k, kr, v, loc, kv_loc), scale=0.0)
+    k[40, 1, 3] = float("inf")
+    got = run((q, k, kr, v, loc, kv_loc), scale=0.0)
+    assert torch.equal(got[:40], clean[:40]) and torch.equal(got[:, 0], clean[:, 0])
+    assert torch.isnan(got[40:, 1]).all()
+    for value in (float("inf"), -float("inf"), float("nan")):
+        bad = q.clone()
+        bad[30, 0, 7] = value  # a channel of its own part, of head 0
+        bad[31, 0, 70] = value
+        got = run((bad, k, kr, v, loc, kv_loc), scale=0.0)[:40]
+        assert torch.isnan(got[30:32, 0]).all()
+        got[30:32, 0] = clean[30:32, 0]
+        assert torch.equal(got, clean[:40])
