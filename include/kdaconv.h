@@ -544,8 +544,9 @@ int kdaconv_latent_attention_validate(const kdaconv_latent_args* args, int updat
  *
  * key_dim and value_dim are multiples of 8 up to 128, rope_dim is one of 8, 0 to 64 (else
  * EUNSUPPORTED); up to 64, 64 and 32 a smaller kernel serves. k, v and k_rope lie at multiples of
- * 16 bytes, token for token and head for head (else EUNSUPPORTED). Strides count elements, 0 to
- * 2^23 - 1 (else EUNSUPPORTED); of an axis of one entry they are not looked at.
+ * 16 bytes, token for token and head for head (else EUNSUPPORTED). Strides count elements and are
+ * not negative, those of the tokens of k, k_rope and v below 2^23 (else EUNSUPPORTED); of an axis
+ * of one entry they are not looked at.
  */
 typedef struct kdaconv_expanded_args {
   const void* q;      /* (num_tokens, num_heads, key_dim + rope_dim), last axis contiguous */

@@ -8,8 +8,9 @@
 namespace kdaconv {
 namespace {
 
-// A step's 64 rows stay below 2^31 bytes.
-constexpr int64_t kMaxStride = (int64_t)1 << 23;
+// Keys' and values' rows are counted from a step's first in 32 bits, a row times a stride of up to 24
+// bits in bytes.
+constexpr int64_t kMaxTokenStride = (int64_t)1 << 23;
 
 bool aligned_to(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
@@ -53,16 +54,16 @@ int validate_expanded(const kdaconv_expanded_args* a) {
       a->rope_dim % 8 != 0 || a->rope_dim > kRopeMax)
     return KDACONV_EUNSUPPORTED;
   // Strides of axes of one entry mean nothing. Keys and values move in pieces of 16 bytes.
+  const bool tokens = a->num_tokens > 1, keys = a->num_keys > 1, heads = a->num_heads > 1;
+  if ((tokens && a->q_stride0 < 0) || (heads && a->q_stride1 < 0)) return KDACONV_EUNSUPPORTED;
   const struct {
-    int64_t count, stride;
-    bool pieces;
-  } axes[] = {{a->num_tokens, a->q_stride0, false}, {a->num_heads, a->q_stride1, false},
-              {a->num_keys, a->k_stride0, true},    {a->num_heads, a->k_stride1, true},
-              {a->num_keys, a->v_stride0, true},    {a->num_heads, a->v_stride1, true},
-              {a->rope_dim > 0 ? a->num_keys : 0, a->kr_stride0, true}};
+    bool counts;
+    int64_t stride, limit;
+  } axes[] = {{keys, a->k_stride0, kMaxTokenStride},  {heads, a->k_stride1, INT64_MAX},
+              {keys, a->v_stride0, kMaxTokenStride},  {heads, a->v_stride1, INT64_MAX},
+              {keys && a->rope_dim > 0, a->kr_stride0, kMaxTokenStride}};
   for (const auto& axis : axes)
-    if (axis.count > 1 && (axis.stride < 0 || axis.stride >= kMaxStride || (axis.pieces && axis.stride % 8 != 0)))
-      return KDACONV_EUNSUPPORTED;
+    if (axis.counts && (axis.stride < 0 || axis.stride >= axis.limit || axis.stride % 8 != 0)) return KDACONV_EUNSUPPORTED;
   if (a->num_tokens > INT32_MAX / 4 || a->num_keys > INT32_MAX / 4 || a->num_seqs > INT32_MAX / 4 || a->num_heads > 65535)
     return KDACONV_EUNSUPPORTED;
   // 2^32 threads.

@@ -77,8 +77,9 @@ def expanded_attention_fn(
         out = sum_t softmax(s)_t v_t
 
     q (tokens, heads, key_dim + rope_dim), k (keys, heads, key_dim) and v (keys, heads, value_dim)
-    are bfloat16 or float16 with a contiguous last axis and any token and head strides: k and v
-    may be slices of one up-projection's rows. k_rope (keys, rope_dim), a slice of
+    are bfloat16 or float16 with a contiguous last axis and any token and head strides (a token of
+    k, k_rope and v below 2^23 elements from the next): k and v may be slices of one
+    up-projection's rows. k_rope (keys, rope_dim), a slice of
     ``latent_cache_read``'s rows say, is the part of the keys that all heads share, or None.
     scale defaults to (key_dim + rope_dim) ** -0.5. key_dim and value_dim are multiples of 8 up to
     128, rope_dim up to 64; k, k_rope and v lie at multiples of 16 bytes, row for row and head for

@@ -37,3 +37,21 @@ def test_scale_zero_times_infinity():
         assert torch.isnan(got[30:32, 0]).all()
         got[30:32, 0] = clean[30:32, 0]
         assert torch.equal(got, clean[:40])
+
+
+@DTYPES
+def test_heads_far_apart(dtype):
+    """Head-major queries, keys and values: strides of heads past 2^23 elements."""
+    heads, new, lens = 3, [5, 2], [65700, 100]
+    q, k, kr, v, loc, kv_loc = inputs(new, lens, heads, 128, 64, 128, dtype)
+    want = ref.expanded(q, k, kr, v, loc, kv_loc, 0.05)
+    major = [torch.empty(heads, n, d, dtype=dtype, device="cuda").transpose(0, 1)
+             for n, d in ((50000, 192), (sum(lens), 128), (sum(lens), 128))]
+    major[0][:7].copy_(q)
+    major[1].copy_(k)
+    major[2].copy_(v)
+    assert min(t.stride()[1] for t in major) >= 1 << 23
+    out = torch.zeros(50000, heads, 128, dtype=dtype, device="cuda")
+    kd.expanded_attention_fn(major[0], major[1], kr.cuda(), major[2], loc.cuda(), kv_loc.cuda(), scale=0.05, out=out)
+    check(out[:7], want, dtype, v.double().abs().max(), "head-major")
+    assert (out[7:] == 0).all()
