@@ -54,6 +54,10 @@ struct Step {
   static constexpr int kShare = 2, kRopeShare = kRope == 64 ? 2 : 1;
 };
 
+// In the place of a row's weight in a part of the keys of which it sees none. (Where it sees one of
+// score -inf the weight is 0, but 0 times its value may be NaN.)
+constexpr float kUnseen = -1.0f;
+
 // The sequence and block of a program: the largest s with v(s) <= program.
 template <int kRows>
 __device__ __forceinline__ bool find_program(const ExpandParams& P, int program, int lane, int& sequence, int& block) {
@@ -389,9 +393,9 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(kWa
     const int r = wave * kWaveRows + n;
     if (h == 0) {
       mine[part.exponent() + r] = top;
-      mine[part.weight() + r] = weight;
+      mine[part.weight() + r] = reach > 0 ? weight : kUnseen;
     }
-    if (weight == 0.0f) return;  // (its sums are not looked at)
+    if (reach <= 0) return;  // (its sums are not looked at)
 #pragma unroll
     for (int c = 0; c < kColumns; ++c)
 #pragma unroll
@@ -440,13 +444,13 @@ __global__ __launch_bounds__(kExpandJoinThreads) void expanded_join_kernel(Expan
     float high = kLowest, total = 0.0f;
     for (int k = 0; k < P.splits; ++k) {
       const float* const p = parts + part.floats() * k;
-      if (p[part.weight() + r] != 0.0f) high = __builtin_fmaxf(high, p[part.exponent() + r]);
+      high = __builtin_fmaxf(high, p[part.exponent() + r]);  // (the lowest, of a part without weight)
     }
     f32x4 v[2] = {};
     for (int k = 0; k < P.splits; ++k) {
       const float* const p = parts + part.floats() * k;
       const float l = p[part.weight() + r];
-      if (l == 0.0f) continue;  // no key of this part
+      if (l == kUnseen) continue;
       const float f = exp2_hw(p[part.exponent() + r] - high);
       const f32x4* const q = (const f32x4*)(p + (int64_t)r * P.vdim + c * 8);
       total = __builtin_fmaf(f, l, total);

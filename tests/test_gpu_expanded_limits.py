@@ -55,3 +55,24 @@ def test_heads_far_apart(dtype):
     kd.expanded_attention_fn(major[0], major[1], kr.cuda(), major[2], loc.cuda(), kv_loc.cuda(), scale=0.05, out=out)
     check(out[:7], want, dtype, v.double().abs().max(), "head-major")
     assert (out[7:] == 0).all()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_weightless_parts(value):
+    """Of a row's part of the keys only one is seen, with a score of -inf: its weight is 0, and 0
+    times a value that is not finite is NaN."""
+    new, lens = [100, 1], [150, 9000]  # 17 parts; the first sequence's hold a step of 64 keys or none
+    assert parts(new, lens, 1)
+    q, k, kr, v, loc, kv_loc = inputs(new, lens, 1, 128, 64, 128, BF16)
+    q[..., 5] = -1.0
+    for key in (64, 128):
+        weak, bad = k.clone(), v.clone()
+        weak[key, 0, 5] = float("inf")
+        bad[key, 0, 7] = value
+        want = run((q, weak, kr, v, loc, kv_loc))
+        got = run((q, weak, kr, bad, loc, kv_loc))
+        assert torch.isfinite(want).all()
+        first = key - 50
+        assert torch.isnan(got[first:100, 0, 7]).all() if value != value else not torch.isfinite(got[first:100, 0, 7]).any()
+        got[first:100, 0, 7] = want[first:100, 0, 7]
+        assert torch.equal(got, want), key
