@@ -11,8 +11,8 @@ from ._host import DTYPE_CODES, _call, _ptr
 from .latent import _loc
 
 
-def _expand(q, k, k_rope, v, query_start_loc, kv_start_loc, scale, causal, out):
-    """Checks, then kdaconv_expanded_args as bytes, the output and the call's sizes."""
+def _inputs(q, k, k_rope, v):
+    """Checks them; returns kdaconv_expanded_args' sizes and strides."""
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or k.shape[:2] != v.shape[:2] or q.shape[1] != k.shape[1]:
         raise ValueError("q must be (tokens, heads, key_dim + rope_dim), k (keys, heads, key_dim) and "
                          "v (keys, heads, value_dim)")
@@ -33,25 +33,39 @@ def _expand(q, k, k_rope, v, query_start_loc, kv_start_loc, scale, causal, out):
             or rope_dim > 1 and rs[1] != 1):
         raise ValueError("the last axis of q, k, k_rope and v must be contiguous")
     device = q.get_device()
+    if k.get_device() != device or v.get_device() != device or (
+            k_rope is not None and k_rope.get_device() != device):
+        raise ValueError("all tensors must be on the device of q")
+    return ((tokens, keys, heads, key_dim, rope_dim, value_dim),
+            (qs[0], qs[1], ks[0], ks[1], rs[0], vs[0], vs[1]))
+
+
+def _pack(q, k, k_rope, v, loc, kv_loc, out, seqs, sizes, strides, scale, causal):
+    """kdaconv_expanded_args as bytes; loc, kv_loc and out are addresses."""
+    tokens, keys, heads, key_dim, rope_dim, value_dim = sizes
+    return _lib.EXPANDED_ARGS.pack(
+        q.data_ptr(), k.data_ptr(), 0 if k_rope is None else k_rope.data_ptr(), v.data_ptr(), loc, kv_loc, out,
+        tokens, keys, max(0, seqs), heads, key_dim, rope_dim, value_dim, *strides,
+        (key_dim + rope_dim) ** -0.5 if scale is None else float(scale), DTYPE_CODES[q.dtype], int(causal))
+
+
+def _expand(q, k, k_rope, v, query_start_loc, kv_start_loc, scale, causal, out):
+    """Checks, then kdaconv_expanded_args as bytes, the output and the call's sizes."""
+    sizes, strides = _inputs(q, k, k_rope, v)
+    tokens, keys, heads, _, _, value_dim = sizes
+    dtype, device = q.dtype, q.get_device()
     seqs = _loc(query_start_loc, device, "query_start_loc")
     if kv_start_loc is None:
         kv_start_loc = query_start_loc
     elif _loc(kv_start_loc, device, "kv_start_loc") != seqs:
         raise ValueError("kv_start_loc must have as many entries as query_start_loc")
-    if k.get_device() != device or v.get_device() != device or (
-            k_rope is not None and k_rope.get_device() != device):
-        raise ValueError("all tensors must be on the device of q")
     shape = (tokens, heads, value_dim)
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=q.device)
     elif out.shape != shape or out.dtype != dtype or not out.is_contiguous() or out.get_device() != device:
         raise ValueError(f"out must be a contiguous {dtype} tensor of shape {shape} on {q.device}")
-    args = _lib.EXPANDED_ARGS.pack(
-        q.data_ptr(), k.data_ptr(), 0 if k_rope is None else k_rope.data_ptr(), v.data_ptr(),
-        query_start_loc.data_ptr(), kv_start_loc.data_ptr(), out.data_ptr(),
-        tokens, keys, max(0, seqs), heads, key_dim, rope_dim, value_dim,
-        qs[0], qs[1], ks[0], ks[1], rs[0], vs[0], vs[1],
-        width ** -0.5 if scale is None else float(scale), DTYPE_CODES[dtype], int(causal))
+    args = _pack(q, k, k_rope, v, query_start_loc.data_ptr(), kv_start_loc.data_ptr(), out.data_ptr(), seqs, sizes,
+                 strides, scale, causal)
     return args, out, (tokens, keys, seqs, heads, value_dim)
 
 
@@ -110,9 +124,10 @@ def expanded_attention_supported(q: torch.Tensor, k: torch.Tensor, k_rope: Optio
                                  v: torch.Tensor) -> bool:
     """Whether expanded_attention_fn serves these tensors."""
     try:
-        two = torch.zeros(2, dtype=torch.int32, device=q.device)
-        args, _, _ = _expand(q, k, k_rope, v, two, two, None, True, None)
+        sizes, strides = _inputs(q, k, k_rope, v)
         lib = _lib.load()
     except (ValueError, _lib.LibraryMissing):
         return False
+    # What a call has beside these is aligned: any such address will do.
+    args = _pack(q, k, k_rope, v, 256, 256, 256, 1, sizes, strides, 1.0, True)
     return q.get_device() >= 0 and lib.kdaconv_expanded_attention_validate(args, 256, 1 << 62) == _lib.OK

@@ -184,18 +184,26 @@ def latent_cache_read(
     return out
 
 
-def _attend(q_latent, q_rope, latents, ropes, scales, block_table, seq_lens, query_start_loc, scale, out):
-    """Checks, then kdaconv_latent_args as bytes, the output and the call's sizes."""
-    cache, dim, rope_dim, dtype, device = _cache(latents, ropes, scales)
+def _queries(q_latent, q_rope, dim, rope_dim, dtype, device):
+    """Checks the queries; returns (tokens, heads, latent_dim) and both tensors' strides."""
     size = q_latent.shape
     if len(size) != 3 or size[2] != dim or q_rope.shape != (size[0], size[1], rope_dim):
         raise ValueError("q_latent must be (tokens, heads, latent_dim) and q_rope (tokens, heads, rope_dim)")
-    tokens, heads, _ = size
     if q_latent.dtype is not dtype or q_rope.dtype is not dtype:
         raise ValueError(f"q_latent and q_rope must have the dtype of ropes, {dtype}")
     ls, rs = q_latent.stride(), q_rope.stride()
     if dim > 1 and ls[2] != 1 or rope_dim > 1 and rs[2] != 1:
         raise ValueError("the last axis of q_latent and q_rope must be contiguous")
+    if q_latent.get_device() != device or q_rope.get_device() != device:
+        raise ValueError("all tensors must be on the device of latents")
+    return size, ls, rs
+
+
+def _attend(q_latent, q_rope, latents, ropes, scales, block_table, seq_lens, query_start_loc, scale, out):
+    """Checks, then kdaconv_latent_args as bytes, the output and the call's sizes."""
+    cache, dim, rope_dim, dtype, device = _cache(latents, ropes, scales)
+    size, ls, rs = _queries(q_latent, q_rope, dim, rope_dim, dtype, device)
+    tokens, heads, _ = size
     seqs = tokens
     if query_start_loc is not None:
         seqs = max(0, _loc(query_start_loc, device, "query_start_loc"))
@@ -204,7 +212,7 @@ def _attend(q_latent, q_rope, latents, ropes, scales, block_table, seq_lens, que
             seqs > 1 and seq_lens.stride()[0] != 1):
         raise ValueError("seq_lens must be a contiguous 1-D int32 tensor with one entry per sequence")
     table = _table(block_table, seqs, device)
-    if q_latent.get_device() != device or q_rope.get_device() != device or seq_lens.get_device() != device:
+    if seq_lens.get_device() != device:
         raise ValueError("all tensors must be on the device of latents")
     if out is None:
         out = torch.empty((tokens, heads, dim), dtype=dtype, device=q_latent.device)
@@ -295,9 +303,12 @@ def latent_attention_supported(q_latent: torch.Tensor, q_rope: torch.Tensor, lat
                                ropes: torch.Tensor, scales: Optional[torch.Tensor] = None) -> bool:
     """Whether latent_attention_fn and latent_attention_update serve these tensors."""
     try:
-        one = torch.empty(max(1, q_latent.shape[0]), 1, dtype=torch.int32, device=latents.device)
-        args, _, device, sizes = _attend(q_latent, q_rope, latents, ropes, scales, one, one[:, 0], None, 1.0, None)
+        cache, dim, rope_dim, dtype, device = _cache(latents, ropes, scales)
+        (tokens, heads, _), ls, rs = _queries(q_latent, q_rope, dim, rope_dim, dtype, device)
         lib = _lib.load()
     except (ValueError, _lib.LibraryMissing):
         return False
+    # What a call has beside these is aligned: any such address will do.
+    args = cache + _lib.LATENT_ARGS.pack(q_latent.data_ptr(), q_rope.data_ptr(), 256, 256, 0, 256, tokens, tokens, heads,
+                                         ls[0], ls[1], rs[0], rs[1], 1, 1, 1.0)
     return device >= 0 and lib.kdaconv_latent_attention_validate(args, 1, 256, 1 << 62) == _lib.OK

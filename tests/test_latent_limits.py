@@ -1,7 +1,10 @@
 """Limits of the latent attention operators on the host: what is refused, and what is not."""
 
 import pytest
+import torch
 
+import latent_reference as ref
+import packed_varlen_causal_depthwise_amd as kd
 from packed_varlen_causal_depthwise_amd._lib import EUNSUPPORTED, OK
 from test_latent_boundary import expanded_code
 
@@ -20,3 +23,18 @@ FAR = 1 << 40
 ])
 def test_expanded_strides(kw, code):
     assert expanded_code(**kw) == code
+
+
+def test_supported_allocates_nothing(monkeypatch):
+    """Queries of support look at the tensors alone."""
+    bf = torch.bfloat16
+    cache = ref.cache(4, 8, 64, 16, bf)
+    q, r = torch.zeros(3, 2, 64, dtype=bf), torch.zeros(3, 2, 16, dtype=bf)
+    k, v, kr = torch.zeros(9, 2, 64, dtype=bf), torch.zeros(9, 2, 64, dtype=bf), torch.zeros(9, 16, dtype=bf)
+    long = torch.cat((q, r), -1)
+    for name in ("empty", "zeros", "ones", "full", "empty_like", "tensor"):
+        monkeypatch.setattr(torch, name, None)
+    assert not kd.latent_attention_supported(q, r, *cache)  # not on a GPU
+    assert not kd.latent_attention_supported(q, r[:, :1], *cache)
+    assert not kd.expanded_attention_supported(long, k, kr, v)
+    assert not kd.expanded_attention_supported(long, k, None, v)
