@@ -46,7 +46,7 @@ def _pack(q, k, k_rope, v, loc, kv_loc, out, seqs, sizes, strides, scale, causal
     return _lib.EXPANDED_ARGS.pack(
         q.data_ptr(), k.data_ptr(), 0 if k_rope is None else k_rope.data_ptr(), v.data_ptr(), loc, kv_loc, out,
         tokens, keys, max(0, seqs), heads, key_dim, rope_dim, value_dim, *strides,
-        (key_dim + rope_dim) ** -0.5 if scale is None else float(scale), DTYPE_CODES[q.dtype], int(causal))
+        (key_dim + rope_dim or 1) ** -0.5 if scale is None else float(scale), DTYPE_CODES[q.dtype], int(causal))
 
 
 def _expand(q, k, k_rope, v, query_start_loc, kv_start_loc, scale, causal, out):

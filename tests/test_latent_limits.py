@@ -38,3 +38,10 @@ def test_supported_allocates_nothing(monkeypatch):
     assert not kd.latent_attention_supported(q, r[:, :1], *cache)
     assert not kd.expanded_attention_supported(long, k, kr, v)
     assert not kd.expanded_attention_supported(long, k, None, v)
+
+
+def test_expanded_without_channels():
+    """Refused as any other width, by ValueError."""
+    q, v, loc = torch.zeros(5, 2, 0, dtype=torch.bfloat16), torch.zeros(5, 2, 8, dtype=torch.bfloat16), torch.tensor([0, 5]).int()
+    with pytest.raises(ValueError):
+        kd.expanded_attention_fn(q, q, None, v, loc)
