@@ -76,3 +76,16 @@ def test_weightless_parts(value):
         assert torch.isnan(got[first:100, 0, 7]).all() if value != value else not torch.isfinite(got[first:100, 0, 7]).any()
         got[first:100, 0, 7] = want[first:100, 0, 7]
         assert torch.equal(got, want), key
+
+
+def test_rows_past_4_gb():
+    """Keys and values at the largest stride of tokens: the last ones lie past 2^32 bytes."""
+    n, stride = 300, (1 << 23) - 8  # elements, 16 MB
+    assert (n - 1) * stride * 2 > 1 << 32
+    buf = torch.empty((n - 1) * stride + 256, dtype=BF16, device="cuda")
+    q, k, kr, v, loc, kv_loc = inputs([n], [n], 1, 128, 64, 128, BF16)
+    far = buf.as_strided((n, 1, 256), (stride, 256, 1))
+    far[..., :128].copy_(k)
+    far[..., 128:].copy_(v)
+    got = kd.expanded_attention_fn(q.cuda(), far[..., :128], kr.cuda(), far[..., 128:], loc.cuda())
+    assert torch.equal(got, run((q, k, kr, v, loc, kv_loc)))
