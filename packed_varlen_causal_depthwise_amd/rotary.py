@@ -20,8 +20,10 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, factor: float 
     With ``factor`` above 1 the context is stretched that many times beyond ``original_length``
     as in YaRN (Peng et al., 2023): pairs that turn ``beta_fast`` times or more within the
     original length keep their frequency, those that turn at most ``beta_slow`` times have it
-    divided by the factor, and between lies a linear ramp in the pair's number; the second
-    result is then 0.1 ln(factor) + 1, else 1. Computed in FP64; the frequencies are float32.
+    divided by the factor, and between lies a linear ramp in the pair's number, from the first
+    pair at the earliest to where a pair would turn ``beta_slow`` times, past the last one too;
+    the second result is then 0.1 ln(factor) + 1, else 1. Computed in FP64; the frequencies are
+    float32.
     """
     if rotary_dim <= 0 or rotary_dim % 2:
         raise ValueError("rotary_dim must be a positive even number")
@@ -38,7 +40,7 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, factor: float 
         return rotary_dim * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
 
     low = max(0.0, math.floor(pair(beta_fast)))
-    high = min(rotary_dim / 2 - 1.0, math.ceil(pair(beta_slow)))
+    high = math.ceil(pair(beta_slow))
     stretched = ((i - low) / max(high - low, 1e-3)).clamp(0, 1)
     freq = freq * (1 - stretched) + freq / factor * stretched
     return freq.float().to(device), 0.1 * math.log(factor) + 1.0

@@ -1,5 +1,7 @@
 """Limits of the latent attention operators on the host: what is refused, and what is not."""
 
+import math
+
 import pytest
 import torch
 
@@ -45,3 +47,29 @@ def test_expanded_without_channels():
     q, v, loc = torch.zeros(5, 2, 0, dtype=torch.bfloat16), torch.zeros(5, 2, 8, dtype=torch.bfloat16), torch.tensor([0, 5]).int()
     with pytest.raises(ValueError):
         kd.expanded_attention_fn(q, q, None, v, loc)
+
+
+@pytest.mark.parametrize("dim,base,length", [(64, 1e4, 4096), (64, 1e4, 32768), (64, 1e4, 65536), (64, 1e4, 131072), (64, 1e4, 262144),
+                                             (32, 1e4, 65536), (128, 1e6, 40960), (128, 5e5, 1 << 24), (64, 1e4, 200)])
+@pytest.mark.parametrize("factor,fast,slow", [(4.0, 32.0, 1.0), (40.0, 32.0, 1.0), (8.0, 16.0, 2.0)])
+def test_stretched_frequencies(dim, base, length, factor, fast, slow):
+    """Each pair by itself: a frequency between base^(-2 i / dim) and that over the factor, by where
+    the pair lies between those that would turn fast and slow times, which need not exist."""
+    f, m = kd.rotary_frequencies(dim, base, factor=factor, original_length=length, beta_fast=fast, beta_slow=slow, device="cpu")
+
+    def number(turns):  # of turns: base^(-2 i / dim) length / (2 pi) of pair i
+        return dim / 2 * math.log(length / (2 * math.pi * turns)) / math.log(base)
+
+    low, high = max(0, math.floor(number(fast))), math.ceil(number(slow))
+    for i in range(dim // 2):
+        plain = base ** (-2 * i / dim)
+        part = min(1.0, max(0.0, (i - low) / (high - low)))
+        want = plain * (1 - part) + plain / factor * part
+        # FP64 to a few units in the last place, then one rounding to FP32.
+        assert abs(f[i].item() - want) <= want * (2.0 ** -24 + 2.0 ** -48), (i, part)
+        turns = plain * length / (2 * math.pi)
+        if turns >= fast * (1 + 1e-12):
+            assert f[i].item() == torch.tensor(plain).item()
+        assert turns > slow or abs(f[i].item() * factor / plain - 1) < 2.0 ** -23
+        assert turns <= slow * (1 + 1e-12) or f[i].item() > plain / factor  # it turns more often: not all divided
+    assert m == 0.1 * math.log(factor) + 1
