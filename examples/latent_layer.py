@@ -52,8 +52,10 @@ class LatentLayer:
         self.out_proj = normal(heads * head_dim, hidden, scale=(heads * head_dim) ** -0.5)
         self.norm_weight = (1 + 0.1 * torch.randn(hidden, generator=gen)).to(device)
         self.latent_weight = (1 + 0.1 * torch.randn(latent, generator=gen)).to(device)
-        self.inv_freq, self.rope_scale = kd.rotary_frequencies(rope_dim, factor=factor, device=device)
-        self.scale = (head_dim + rope_dim) ** -0.5
+        # The factor of a stretched context is one on queries and on keys, all of their channels: it
+        # goes into the scale, for only a part of a head is turned.
+        self.inv_freq, temper = kd.rotary_frequencies(rope_dim, factor=factor, device=device)
+        self.scale = (head_dim + rope_dim) ** -0.5 * temper ** 2
         self.ropes = torch.zeros(pages, page_size, rope_dim, dtype=dtype, device=device)
         kind = torch.float8_e4m3fn if e4m3 else dtype
         self.latents = torch.zeros(pages, page_size, latent, dtype=dtype, device=device).to(kind)
@@ -73,9 +75,9 @@ class LatentLayer:
         rows = kd.residual_rms_norm(x, residual, self.norm_weight, eps=self.EPS) @ self.in_proj
         q = rows[:, :self.query].view(-1, self.heads, self.head_dim + self.rope_dim)
         latent, rope = rows[:, self.query:].split([self.latent, self.rope_dim], 1)
-        kd.rotary_embedding(q, positions, self.inv_freq, offset=self.head_dim, scale=self.rope_scale, out=q)
+        kd.rotary_embedding(q, positions, self.inv_freq, offset=self.head_dim, out=q)
         kd.latent_cache_write(latent, rope, *self.cache, slots, weight=self.latent_weight, eps=self.EPS,
-                              positions=positions, inv_freq=self.inv_freq, rope_scale=self.rope_scale)
+                              positions=positions, inv_freq=self.inv_freq)
         return q
 
     def _absorbed(self, q):

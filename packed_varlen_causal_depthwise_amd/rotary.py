@@ -14,16 +14,18 @@ from ._host import DTYPE_CODES, _call, _fresh_like
 def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, factor: float = 1.0,
                        original_length: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0,
                        device="cuda") -> Tuple[torch.Tensor, float]:
-    """Angles per position of ``rotary_dim // 2`` pairs, base ** (-2 i / rotary_dim), and the
-    factor on cosines and sines, for ``rotary_embedding`` and ``latent_cache_write``.
+    """Angles per position of ``rotary_dim // 2`` pairs, base ** (-2 i / rotary_dim), for
+    ``rotary_embedding`` and ``latent_cache_write``, and the factor on queries and on keys.
 
     With ``factor`` above 1 the context is stretched that many times beyond ``original_length``
     as in YaRN (Peng et al., 2023): pairs that turn ``beta_fast`` times or more within the
     original length keep their frequency, those that turn at most ``beta_slow`` times have it
     divided by the factor, and between lies a linear ramp in the pair's number, from the first
     pair at the earliest to where a pair would turn ``beta_slow`` times, past the last one too;
-    the second result is then 0.1 ln(factor) + 1, else 1. Computed in FP64; the frequencies are
-    float32.
+    the second result is then 0.1 ln(factor) + 1, else 1. It belongs to all channels of a score:
+    as ``scale`` of ``rotary_embedding`` where all of a head's channels are turned; where a part
+    is, as in latent attention, its square goes into the attention's ``scale`` instead. Computed
+    in FP64; the frequencies are float32.
     """
     if rotary_dim <= 0 or rotary_dim % 2:
         raise ValueError("rotary_dim must be a positive even number")
