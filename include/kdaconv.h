@@ -412,7 +412,8 @@ int kdaconv_residual_rms_norm(const void* x, int dtype, int64_t num_tokens, int6
  * x, out     (num_tokens, num_heads, head_dim), element (t, h, c) at t * stride0 +
  *            h * stride1 + c; format dtype (bf16, fp16 or FP32). out may be x with x's strides;
  *            it may not overlap x otherwise, nor itself.
- * positions  (num_tokens) int32, or int64 with positions_64; any value.
+ * positions  (num_tokens) int32, or int64 with positions_64; any value. Angles are off by 2^-26 of a
+ *            turn at most up to 2^53 (beyond, positions round to FP64).
  * inv_freq   (rotary / 2) FP32. rotary is even, 2 to 512 (else EINVAL, EUNSUPPORTED), and
  *            offset + rotary <= head_dim (else EINVAL).
  */

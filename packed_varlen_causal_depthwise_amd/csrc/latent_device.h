@@ -60,15 +60,19 @@ __device__ __forceinline__ int64_t load_index(const void* p, int64_t i, bool wid
   return wide ? ((const int64_t*)p)[i] : (int64_t)((const int32_t*)p)[i];
 }
 
-// Cosine and sine of position * frequency. The product is exact in FP64 up to positions of
-// 2^29; it is counted in turns, with 1 / (2 pi) in two parts, and what is left, at most half a
-// turn, rounds to FP32: off by 2^-26 of a turn at most, however far the position.
+// Cosine and sine of position * frequency, for positions up to 2^53. The product is taken in FP64 with
+// its rounding's error beside it (0 up to positions of 2^29), and counted in turns, with 1 / (2 pi)
+// in two parts. What is left, at most half a turn, rounds to FP32: off by 2^-26 of a turn at
+// most, however far the position.
 __device__ __forceinline__ f32x2 turn(int64_t position, float frequency) {
   constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
   const double a = (double)position * (double)frequency;
+  const double low = __builtin_fma((double)position, (double)frequency, -a);
   const double turns = a * kHi;
-  const double rest = __builtin_fma(a, kLo, __builtin_fma(a, kHi, -turns));
-  const float t = (float)((turns - __builtin_rint(turns)) + rest);
+  const double rest = __builtin_fma(low, kHi, __builtin_fma(a, kLo, __builtin_fma(a, kHi, -turns)));
+  const double left = (turns - __builtin_rint(turns)) + rest;
+  // (Turns from 2^50 on are counted in quarters, and the rest is up to an eighth.)
+  const float t = (float)(left - __builtin_rint(left));
   float s, c;
   sincospif(2.0f * t, &s, &c);
   return f32x2{c, s};

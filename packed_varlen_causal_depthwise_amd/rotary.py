@@ -83,10 +83,10 @@ def rotary_embedding(
     token and head strides). Pair i, channels (2 i, 2 i + 1) counted from offset with
     ``interleaved`` and (i, i + len(inv_freq)) without, is turned by positions[t] * inv_freq[i]
     and multiplied by ``scale``. positions (tokens,) is int32 or int64; the angle is reduced in
-    FP64, so far positions turn as exactly as near ones. The other channels are copied. ``out``,
-    of x's shape and dtype with a contiguous last axis, may be x itself: then only the turned
-    channels are read and written. Otherwise it may not overlap x. Queued on the current stream;
-    no synchronisation.
+    FP64, so far positions, up to 2^53, turn as exactly as near ones. The other channels are
+    copied. ``out``, of x's shape and dtype with a contiguous last axis, may be x itself: then
+    only the turned channels are read and written. Otherwise it may not overlap x. Queued on the
+    current stream; no synchronisation.
     """
     size, dtype = x.shape, x.dtype
     if len(size) != 3:
