@@ -415,7 +415,8 @@ int kdaconv_residual_rms_norm(const void* x, int dtype, int64_t num_tokens, int6
  * positions  (num_tokens) int32, or int64 with positions_64; any value. Angles are off by 2^-26 of a
  *            turn at most up to 2^53 (beyond, positions round to FP64).
  * inv_freq   (rotary / 2) FP32. rotary is even, 2 to 512 (else EINVAL, EUNSUPPORTED), and
- *            offset + rotary <= head_dim (else EINVAL).
+ *            offset + rotary <= head_dim (else EINVAL). num_heads is below 2^16, head_dim at most
+ *            2^16 and their product below 2^31 - 256 (else EUNSUPPORTED).
  */
 int kdaconv_rotary_embedding(const void* x, int dtype, int64_t num_tokens, int64_t num_heads,
                              int64_t head_dim, int64_t x_stride0, int64_t x_stride1,

@@ -407,8 +407,8 @@ extern "C" int kdaconv_rotary_embedding(const void* x, int dtype, int64_t num_to
   // four per CU.
   const int64_t most = std::max<int64_t>(1, kAngles / (rotary / 2));
   P.per_block = (int32_t)std::max<int64_t>(1, std::min(most, num_tokens / 1024));
-  // A workgroup's units are counted in 31 bits.
-  if (P.per_block * num_heads * std::max(units, copies) > INT32_MAX) return KDACONV_EUNSUPPORTED;
+  // A workgroup's units are counted in 31 bits, a stride past their end too.
+  if (P.per_block * num_heads * std::max(units, copies) > INT32_MAX - kRotaryThreads) return KDACONV_EUNSUPPORTED;
   P.pairs = divider_of((uint32_t)(rotary / 2));
   P.units = divider_of((uint32_t)units);
   P.head_units = divider_of((uint32_t)(units * num_heads));

@@ -8,7 +8,7 @@ import torch
 import latent_reference as ref
 import packed_varlen_causal_depthwise_amd as kd
 from packed_varlen_causal_depthwise_amd._lib import EUNSUPPORTED, OK
-from test_latent_boundary import expanded_code
+from test_latent_boundary import expanded_code, rotary_code
 
 FAR = 1 << 40
 
@@ -73,3 +73,11 @@ def test_stretched_frequencies(dim, base, length, factor, fast, slow):
         assert turns > slow or abs(f[i].item() * factor / plain - 1) < 2.0 ** -23
         assert turns <= slow * (1 + 1e-12) or f[i].item() > plain / factor  # it turns more often: not all divided
     assert m == 0.1 * math.log(factor) + 1
+
+
+def test_rotary_units():
+    """A workgroup counts a token's heads times other channels, and its threads' stride past them,
+    in 31 bits: 49981 * 42966 is 2^31 - 2."""
+    assert 49981 * 42966 == (1 << 31) - 2
+    kw = dict(tokens=1, heads=49981, dim=42968, x1=42968, o1=42968, rotary=2, offset=0)
+    assert rotary_code(**kw) == EUNSUPPORTED
