@@ -443,6 +443,9 @@ extern "C" int kdaconv_latent_cache_write(const kdaconv_latent_cache* cache, con
   if ((places && cache->latents_stride1 < cache->latent_dim) || (pages && cache->latents_stride0 < cache->latent_dim) ||
       (places && cache->ropes_stride1 < cache->rope_dim) || (pages && cache->ropes_stride0 < cache->rope_dim))
     return KDACONV_EINVAL;
+  const int64_t blocks_of_scales = cache->latent_dim / kScaleBlock;
+  if (cache->e4m3 && ((places && cache->scales_stride1 < blocks_of_scales) || (pages && cache->scales_stride0 < blocks_of_scales)))
+    return KDACONV_EINVAL;
   if (num_tokens == 0 || cache->num_pages == 0) return KDACONV_OK;
   if (!latent || (cache->rope_dim > 0 && !rope) || !slots || (inv_freq && !positions)) return KDACONV_EINVAL;
   if (!aligned_to(latent, 2) || !aligned_to(rope, 2) || !aligned_to(weight, 4) || !aligned_to(inv_freq, 4) ||

@@ -7,8 +7,8 @@ import torch
 
 import latent_reference as ref
 import packed_varlen_causal_depthwise_amd as kd
-from packed_varlen_causal_depthwise_amd._lib import EUNSUPPORTED, OK
-from test_latent_boundary import expanded_code, rotary_code
+from packed_varlen_causal_depthwise_amd._lib import EINVAL, EUNSUPPORTED, OK
+from test_latent_boundary import A, expanded_code, rotary_code, write_code
 
 FAR = 1 << 40
 
@@ -81,3 +81,14 @@ def test_rotary_units():
     assert 49981 * 42966 == (1 << 31) - 2
     kw = dict(tokens=1, heads=49981, dim=42968, x1=42968, o1=42968, rotary=2, offset=0)
     assert rotary_code(**kw) == EUNSUPPORTED
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(s0=256, s1=16, pages=0), OK), (dict(s0=256, s1=0), EINVAL), (dict(s0=256, s1=15), EINVAL), (dict(s0=0, s1=16), EINVAL),
+    (dict(s0=15, s1=9 * 16), EINVAL), (dict(s0=0, s1=0), EINVAL),
+    # Strides of an axis of one entry mean nothing.
+    (dict(s0=0, s1=15, pages=1), EINVAL), (dict(s0=15, s1=0, page=1), EINVAL), (dict(s0=0, s1=16, pages=0, page=1), OK),
+])
+def test_scales_that_overlap(kw, code):
+    """Each token's scales are written, as its latent is: a broadcast cache of scales is refused."""
+    assert write_code(cache=dict(e4m3=1, scales=A, **kw)) == code
