@@ -487,7 +487,8 @@ int kdaconv_latent_cache_read(const kdaconv_latent_cache* cache, const int32_t* 
  * the sequence's first seq_lens[s] - n + i + 1 tokens: for every head
  *     s_t = scale * (q_latent . latent_t + q_rope . rope_t),   out = sum_t softmax(s)_t latent_t
  * A token whose page is outside the cache, or past the table's pages_per_seq columns, is not
- * there; a row that sees none is zero. Rows no sequence owns are not written. Scores, softmax
+ * there; a row that sees none is zero, and so is one whose scores are all -inf. A latent that is
+ * not finite reaches no row that does not see it. Rows no sequence owns are not written. Scores, softmax
  * and sums are FP32; its weights (up to 2^8 before the division by their sum) are rounded to
  * dtype for the second product, out is rounded once. 8-bit values times their scale are rounded
  * to dtype, exactly within its range.
@@ -539,10 +540,10 @@ int kdaconv_latent_attention_validate(const kdaconv_latent_args* args, int updat
  * the n queries of sequence s, rows [qsl[s], qsl[s+1]), sees the first m - n + i + 1 of its m
  * keys, rows [ksl[s], ksl[s+1]) of k, k_rope and v, or all of them without `causal`:
  *     s_t = scale * (q[:key_dim] . k_t + q[key_dim:] . k_rope_t),   out = sum_t softmax(s)_t v_t
- * A row that sees none is zero; rows no sequence owns are not written. Scores, softmax and sums
- * are FP32; its weights (up to 2^8 before the division by their sum) are rounded to dtype for the
+ * A row that sees none is zero, and so is one whose scores are all -inf; rows no sequence owns are
+ * not written. Scores, softmax and sums are FP32; its weights (up to 2^8 before the division by their sum) are rounded to dtype for the
  * second product, out is rounded once. A key or value that is not finite reaches no row that does
- * not see it.
+ * not see it; a channel of the rows that see such a value is NaN or infinite.
  *
  * key_dim and value_dim are multiples of 8 up to 128, rope_dim is one of 8, 0 to 64 (else
  * EUNSUPPORTED); up to 64, 64 and 32 a smaller kernel serves. k, v and k_rope lie at multiples of

@@ -79,11 +79,11 @@ __device__ __forceinline__ uint32_t fresh(uint32_t x) {
   return x;
 }
 
-// What a key outside the sequence, and channels past a latent's, read.
 // Memory that a load need not take for LDS: waits for such flat loads are waits for all of them.
 template <class X>
 using Global = const __attribute__((address_space(1))) X*;
 
+// What a key outside the sequence, and channels past a latent's, read.
 static __device__ const uint32_t kZeros[kLatentMax / 2] = {};
 
 // A row's largest score may grow by this (in powers of two) before its sums are rescaled.

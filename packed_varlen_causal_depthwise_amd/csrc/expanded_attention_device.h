@@ -9,8 +9,8 @@
 // take turns if they kept step: both products, then both softmaxes. So waves 4 to 7 run half a
 // step behind: while one wave of a SIMD multiplies (values of the last step, keys of the next),
 // the other one weighs its scores. Barriers keep them so. One prompt of 16384 tokens, 12 heads of
-// 128 + 64 channels, takes 925 us so (1115 TFLOP/s, where a library product of 8192^3 reaches 1242)
-// and took 1067 in step. The matrix unit is busy 62% of the time, at the clock that its power
+// 128 + 64 channels, takes 925 to 970 us so from card to card (1115 to 1065 TFLOP/s, where a library
+// product of 8192^3 reaches 1242), and 1067 in step where it took 925. The matrix unit is busy 62% of the time, at the clock that its power
 // leaves. Products are taken transposed, S^T = K Q^T and O^T = V^T P^T, so a lane
 // has one query and its softmax needs no other lane but for the largest score; and the scores'
 // registers are the second product's right operand as they are: of 16 keys lane half h holds 4 h
@@ -327,8 +327,8 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(kWa
   };
 
   // Rows that do not see a key have weight 0 for it, but 0 times NaN is NaN: where rows differ in
-  // what they see, values that are not finite become zeros, and their rows NaN at the end. And where
-  // keys end the last one's values stand for missing ones.
+  // what they see, values that are not finite become zeros, and rows that see one get NaN in that
+  // channel at the end. And where keys end the last one's values stand for missing ones.
   const auto clean = [&](int step, int place) {
     const int key = step * kExpandKeys;
     if (key + kExpandKeys <= (block_most == block_least ? keys : block_least)) return;

@@ -12,7 +12,9 @@ constexpr int64_t kSharedBytes = kWorkers * 2 * sizeof(Shared);
 bool aligned_to(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
 // Blocks of 16 rows per workgroup: as many as a sequence fills on average, up to 4. Every block
-// reads the sequence's keys once; 8 blocks' sums and queries are more than the registers hold.
+// reads the sequence's keys once; 8 blocks' sums and queries are more than the registers hold. The
+// average serves unlike sequences too (12 heads, 4096 keys each): 255 decode rows take 226 us, a chunk
+// of 512 tokens 103, both in one call 319, though its decode rows are in blocks of 64.
 int blocks_of(int64_t tokens, int64_t seqs, int64_t heads) {
   const int64_t rows = tokens * heads;
   return rows <= 16 * seqs ? 1 : rows <= 32 * seqs ? 2 : 4;
@@ -64,6 +66,9 @@ void launch(const AttendParams& P, int blocks, bool e4m3, hipStream_t st) {
     launch<kF, kLatent, 4>(P, e4m3, st);
 }
 
+// Two sizes of kernel: registers and LDS of 512 channels serve all above 256, whose products are the
+// channels' that are not there too. 37 decode steps over 90001 keys, 12 heads: 256 channels 30 us,
+// 384 35, 512 37.
 template <int kF>
 void launch(const AttendParams& P, int latent, int blocks, bool e4m3, hipStream_t st) {
   if (latent <= 256)

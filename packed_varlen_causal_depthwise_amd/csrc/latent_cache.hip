@@ -135,8 +135,9 @@ struct WriteParams {
 constexpr int kWriteWaves = 4;
 
 // One wave per token, 8 channels of the latent per lane. A block of 32 channels is four lanes.
-// 16384 tokens of 512 + 64 bf16 channels take 11.4 us (3.3 TB/s; a wave's norm waits for its whole
-// row, and a launch's first and last microseconds weigh), 37 tokens 4 us, a launch.
+// Latency bounds it: a wave's row, then an FP64 sum over six lane exchanges, a division and a root,
+// then the stores, with nothing else of the wave's to do meanwhile. 16384 tokens of 512 + 64 bf16
+// channels take 11.5 to 12 us (3.2 TB/s) and 13 into 8 bits (2.2 TB/s), 37 tokens 4 us, a launch.
 template <int kF, bool kE4m3>
 __global__ __launch_bounds__(kWave * kWriteWaves) void latent_write_kernel(WriteParams P) {
   const int lane = threadIdx.x % kWave;
@@ -228,8 +229,9 @@ constexpr int kReadWaves = 4, kReadAhead = 2;
 
 // A wave reads some neighbouring rows of the output: its lanes first find each row's sequence and
 // slot, then copy 8 channels at a time, kReadAhead loads before the first is waited for. Memory
-// bounds it: 131072 rows of 512 8-bit and 64 16-bit channels take 49 us, 237 MB at 4.8 TB/s (one
-// load at a time 63 us, six 67: registers then leave fewer waves).
+// bounds it: 131072 rows of 512 8-bit and 64 16-bit channels take 46 to 49 us among calls of their
+// kind, 237 MB at 5 TB/s, and 62 us after other work has filled the caches (one load at a time 63 us
+// where this took 49, six 67: registers then leave fewer waves); 16-bit rows, 302 MB, take 54 us.
 template <int kF, bool kE4m3>
 __global__ __launch_bounds__(kWave * kReadWaves) void latent_read_kernel(ReadParams P) {
   const int lane = threadIdx.x % kWave;

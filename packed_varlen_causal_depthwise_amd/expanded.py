@@ -93,16 +93,18 @@ def expanded_attention_fn(
     q (tokens, heads, key_dim + rope_dim), k (keys, heads, key_dim) and v (keys, heads, value_dim)
     are bfloat16 or float16 with a contiguous last axis and any token and head strides (a token of
     k, k_rope and v below 2^23 elements from the next): k and v may be slices of one
-    up-projection's rows. k_rope (keys, rope_dim), a slice of
-    ``latent_cache_read``'s rows say, is the part of the keys that all heads share, or None.
-    scale defaults to (key_dim + rope_dim) ** -0.5. key_dim and value_dim are multiples of 8 up to
+    up-projection's rows. k_rope (keys, rope_dim), a slice of ``latent_cache_read``'s rows say, is
+    the part of the keys that all heads share, or None. scale defaults to
+    (key_dim + rope_dim) ** -0.5; 0 is allowed. key_dim and value_dim are multiples of 8 up to
     128, rope_dim up to 64; k, k_rope and v lie at multiples of 16 bytes, row for row and head for
     head.
 
-    A row that sees no key is zero, rows no sequence owns are left unwritten, and a value that is
-    not finite reaches no row that does not see it. Scores, softmax and sums are FP32, the weights
-    rounded to the dtype for the second product, the result (tokens, heads, value_dim) once.
-    Few rows over many keys take up to 35 MB of scratch memory from torch's allocator. Queued on the current stream; no synchronisation.
+    A row that sees no key, or only scores of -inf, is zero, rows no sequence owns are left
+    unwritten, and a value that is not finite reaches no row that does not see it (that channel of
+    those that do is NaN or infinite). Scores, softmax and sums are FP32, the weights rounded to
+    the dtype for the second product, the result (tokens, heads, value_dim) once. Few rows over
+    many keys take up to 35 MB of scratch memory from torch's allocator. Queued on the current
+    stream; no synchronisation.
     """
     args, out, sizes = _expand(q, k, k_rope, v, query_start_loc, kv_start_loc, scale, causal, out)
     tokens, _, seqs, heads, _ = sizes

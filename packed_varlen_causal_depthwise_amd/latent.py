@@ -272,9 +272,10 @@ def latent_attention_fn(
     latents, ropes and scales are the cache of ``latent_cache_write``, block_table (sequences,
     pages per sequence) int32 its pages, seq_lens (sequences,) int32 the tokens of each sequence
     in it, the new ones included, and query_start_loc (sequences + 1,) int32 the rows of each. A
-    token whose page is outside the cache is not there; a row that sees no token is zero; rows no
-    sequence owns are left unwritten. Scores, softmax and sums are FP32, the weights rounded to
-    the dtype for the second product, the result rounded once. Takes up to 67 MB of scratch memory
+    token whose page is outside the cache is not there; a row that sees no token, or only scores
+    of -inf, is zero; rows no sequence owns are left unwritten; a latent that is not finite reaches
+    no row that does not see it. Scores, softmax and sums are FP32, the weights rounded to the
+    dtype for the second product, the result rounded once. Takes up to 67 MB of scratch memory
     from torch's allocator. Queued on the current stream; no synchronisation.
     """
     return _run("latent_attention", *_attend(q_latent, q_rope, latents, ropes, scales, block_table,
