@@ -10,8 +10,9 @@
 // step behind: while one wave of a SIMD multiplies (values of the last step, keys of the next),
 // the other one weighs its scores. Barriers keep them so. One prompt of 16384 tokens, 12 heads of
 // 128 + 64 channels, takes 925 to 970 us so from card to card (1115 to 1065 TFLOP/s, where a library
-// product of 8192^3 reaches 1242), and 1067 in step where it took 925. The matrix unit is busy 62% of the time, at the clock that its power
-// leaves. Products are taken transposed, S^T = K Q^T and O^T = V^T P^T, so a lane
+// product of 8192^3 reaches 1242), and 1067 in step where it took 925. The matrix unit is busy 62% of
+// the time, at the clock that its power leaves. Products are taken transposed, S^T = K Q^T and O^T =
+// V^T P^T, so a lane
 // has one query and its softmax needs no other lane but for the largest score; and the scores'
 // registers are the second product's right operand as they are: of 16 keys lane half h holds 4 h
 // .. 4 h + 3 and 8 + 4 h .., and the left operand takes its keys in that order. That operand is V

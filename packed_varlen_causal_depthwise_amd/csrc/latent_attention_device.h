@@ -15,8 +15,9 @@
 // of 32 keys 2450 cycles, in which LDS takes its 36 KB at 1 KB in some 45 cycles. With 64 rows memory
 // still: 24 chunks of 500 tokens in all, 8 heads, 70007 keys take 78 us, 330 TFLOP/s. Blocks of one
 // sequence are at different keys at any one time, so keys come three times (272 MB read and 35 MB
-// of sums written: 62 us at a copy's rate); LDS reads of 420 KB a step take some 18. With few keys latency: some 3000 cycles until a worker
-// has found its part, 6000 more until the first keys are there.
+// of sums written: 62 us at a copy's rate); LDS reads of 420 KB a step take some 18. With few keys
+// latency: some 3000 cycles until a worker has found its part, 6000 more until the first keys are
+// there.
 //
 // Products are taken transposed, S^T = K Q^T and O^T = C^T P^T: a lane then has one query, whose
 // largest score and rescaling concern no other lane. The left operand C^T is delivered by
